@@ -57,12 +57,21 @@ class VocabLayout(ctypes.Structure):
                 ("n_pairs", ctypes.c_int32), ("pairs", ctypes.POINTER(ctypes.c_int16)), ("off_id", ctypes.c_int32)]
 
 
+class SharedContext(ctypes.Structure):
+    _fields_ = [("prefix_store", ctypes.c_void_p), ("prefix_cap", ctypes.c_int32), ("prefix_len", ctypes.c_void_p),
+                ("kv_store", ctypes.c_void_p), ("t_cap", ctypes.c_int32), ("ctx_len", ctypes.c_void_p),
+                ("pos_offset", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("prefix_weights", ctypes.c_void_p),
+                ("accumulate", ctypes.c_int32)]
+
+
 _lib = None
 _EXPORTS = ["fpd_model_create", "fpd_model_destroy", "fpd_kv_store_bytes", "fpd_workspace_bytes",
             "fpd_prepare_context", "fpd_prepare_context_rows", "fpd_draft_block", "fpd_constrain_argmax",
             "fpd_constrain_argmax_noalloc", "fpd_verify", "fpd_verify_prefix", "fpd_sd_advance", "fpd_grid_to_text",
             "fpd_model_enable_fp8", "fpd_model_fp8_enabled", "fpd_quantize_fp8", "fpd_last_error",
-            "fpd_kernel_launches", "fpd_device_status"]
+            "fpd_kernel_launches", "fpd_device_status", "fpd_shared_attention", "fpd_shared_attention_workspace_bytes",
+            "fpd_context_weights", "fpd_evict_context", "fpd_evict_workspace_bytes", "fpd_prepare_context_at",
+            "fpd_draft_block_shared", "fpd_shared_workspace_bytes"]
 
 
 def lib():
@@ -104,9 +113,21 @@ def lib():
         l.fpd_model_fp8_enabled.argtypes = [vp]
         l.fpd_model_fp8_enabled.restype = ctypes.c_int32
         l.fpd_quantize_fp8.argtypes = [vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, vp, vp, vp]
+        ci = ctypes.c_int
+        l.fpd_shared_attention.argtypes = [ci] * 6 + [vp] * 4 + [ci, vp, vp, ci, vp, vp, vp, vp, sz, vp]
+        l.fpd_shared_attention_workspace_bytes.argtypes = [ci] * 7
+        l.fpd_context_weights.argtypes = [ci] * 6 + [vp, vp, vp, ci, vp, vp, ci, vp]
+        l.fpd_evict_context.argtypes = [ci] * 6 + [vp, ci, vp, vp, vp, ci, vp, vp, vp, vp, vp, sz, vp]
+        l.fpd_evict_workspace_bytes.argtypes = [ci] * 4
+        l.fpd_prepare_context_at.argtypes = [vp, ci, ci, vp, vp, vp, vp, ctypes.POINTER(vp), vp, ci, vp, sz, vp]
+        l.fpd_draft_block_shared.argtypes = [vp, ci, ci, ctypes.POINTER(SharedContext), vp, i32, vp, vp, vp, sz, vp]
+        l.fpd_shared_workspace_bytes.argtypes = [vp] + [ci] * 4
+        for f in ("fpd_shared_attention_workspace_bytes", "fpd_evict_workspace_bytes", "fpd_shared_workspace_bytes"):
+            getattr(l, f).restype = sz
         for f in ("fpd_model_create", "fpd_model_enable_fp8", "fpd_quantize_fp8", "fpd_prepare_context", "fpd_prepare_context_rows", "fpd_draft_block",
                   "fpd_constrain_argmax", "fpd_constrain_argmax_noalloc", "fpd_verify", "fpd_sd_advance",
-                  "fpd_grid_to_text", "fpd_verify_prefix",
+                  "fpd_grid_to_text", "fpd_verify_prefix", "fpd_shared_attention", "fpd_context_weights",
+                  "fpd_evict_context", "fpd_prepare_context_at", "fpd_draft_block_shared",
                   "fpd_device_status"):
             getattr(l, f).restype = ctypes.c_int
         _lib = l
@@ -243,6 +264,102 @@ def fpd_verify_prefix(batch, block_len, draft, margin, tau, layout, rule, pad_id
                                    _stream(stream)), "fpd_verify_prefix")
 
 
+# ---- operators on a context store (sizes and layouts: include/fpd.h) -------------------------------------------
+
+def _arg(t, dtype, n, what):
+    """Device address of a tensor that must be contiguous, of `dtype` ("bfloat16", "float32", "int32", "uint8"), on the
+    current device and hold at least n elements; an int address or None is passed on."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype is not getattr(torch, dtype):
+        raise ValueError(f"{what} must be torch.{dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous (row-major)")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.numel() < n:
+        raise ValueError(f"{what} holds {t.numel()} elements, the call needs {n}")
+    return t.data_ptr()
+
+
+def fpd_shared_attention_workspace_bytes(batch, block_len, n_q_heads, n_kv_heads, head_dim, prefix_cap, t_cap) -> int:
+    return int(lib().fpd_shared_attention_workspace_bytes(batch, block_len, n_q_heads, n_kv_heads, head_dim, prefix_cap,
+                                                          t_cap))
+
+
+def fpd_shared_attention(batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, q, k_blk, v_blk, prefix_store,
+                         prefix_cap, prefix_len, kv_store, t_cap, ctx_len, out, lse, workspace, workspace_bytes,
+                         stream=None):
+    """Attention of a batch over [shared prefix ; own context ; block] of one layer; out and lse are written."""
+    n, bf = batch * block_len * n_q_heads, "bfloat16"
+    blk, pos = batch * n_kv_heads * block_len * head_dim, 2 * n_kv_heads * head_dim
+    _check(lib().fpd_shared_attention(
+        batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, _arg(q, bf, n * head_dim, "q"),
+        _arg(k_blk, bf, blk, "k_blk"), _arg(v_blk, bf, blk, "v_blk"),
+        _arg(prefix_store, bf, (layer + 1) * prefix_cap * pos, "prefix_store"), prefix_cap,
+        _arg(prefix_len, "int32", 1, "prefix_len"),
+        _arg(kv_store, bf, (layer + 1) * batch * t_cap * pos, "kv_store"), t_cap, _arg(ctx_len, "int32", batch, "ctx_len"),
+        _arg(out, bf, n * head_dim, "out"), _arg(lse, "float32", n, "lse"),
+        _arg(workspace, "uint8", workspace_bytes, "workspace"), workspace_bytes, _stream(stream)), "fpd_shared_attention")
+
+
+def fpd_context_weights(batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, q, lse, kv_store, t_cap, ctx_len,
+                        weights, accumulate=False, stream=None):
+    """weights[layer] (+)= the attention weight every context position collects from the rows of q."""
+    n, at = batch * block_len * n_q_heads, (layer + 1) * batch * n_kv_heads * t_cap
+    _check(lib().fpd_context_weights(
+        batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, _arg(q, "bfloat16", n * head_dim, "q"),
+        _arg(lse, "float32", n, "lse"), _arg(kv_store, "bfloat16", at * 2 * head_dim, "kv_store"), t_cap,
+        _arg(ctx_len, "int32", batch, "ctx_len"), _arg(weights, "float32", at, "weights"), int(bool(accumulate)),
+        _stream(stream)), "fpd_context_weights")
+
+
+def fpd_evict_workspace_bytes(n_layers, batch, n_kv_heads, budget) -> int:
+    return int(lib().fpd_evict_workspace_bytes(n_layers, batch, n_kv_heads, budget))
+
+
+def fpd_evict_context(n_layers, batch, n_kv_heads, head_dim, budget, recent, kv_store, t_cap, weights, ctx_len, out_store,
+                      out_cap, out_weights, out_len, pos_offset, kept, workspace, workspace_bytes, stream=None):
+    """Keeps the last `recent` positions and those with the largest weights, `budget` in all, of every request."""
+    heads, bf = n_layers * batch * n_kv_heads, "bfloat16"
+    _check(lib().fpd_evict_context(
+        n_layers, batch, n_kv_heads, head_dim, budget, recent, _arg(kv_store, bf, heads * 2 * t_cap * head_dim, "kv_store"),
+        t_cap, _arg(weights, "float32", heads * t_cap, "weights"), _arg(ctx_len, "int32", batch, "ctx_len"),
+        _arg(out_store, bf, heads * 2 * out_cap * head_dim, "out_store"), out_cap,
+        _arg(out_weights, "float32", heads * out_cap, "out_weights"), _arg(out_len, "int32", batch, "out_len"),
+        _arg(pos_offset, "int32", batch, "pos_offset"), _arg(kept, "int32", heads * budget, "kept"),
+        _arg(workspace, "uint8", workspace_bytes, "workspace"), workspace_bytes, _stream(stream)), "fpd_evict_context")
+
+
+def fpd_prepare_context_at(model, batch, total_rows, row_off, row_cnt, pos_start, pos_offset, feats, kv_store, t_cap,
+                           workspace, workspace_bytes, stream=None):
+    arr = (ctypes.c_void_p * len(feats))(*[_ptr(f) for f in feats])
+    _check(lib().fpd_prepare_context_at(model, batch, total_rows, _ptr(row_off), _ptr(row_cnt), _ptr(pos_start),
+                                        _ptr(pos_offset), arr, _ptr(kv_store), t_cap, _ptr(workspace), workspace_bytes,
+                                        _stream(stream)), "fpd_prepare_context_at")
+
+
+def fpd_shared_workspace_bytes(model, batch, max_block_len, prefix_cap, t_cap) -> int:
+    return int(lib().fpd_shared_workspace_bytes(model, batch, max_block_len, prefix_cap, t_cap))
+
+
+def shared_context(prefix_store=None, prefix_cap=0, prefix_len=None, kv_store=None, t_cap=0, ctx_len=None, pos_offset=None,
+                   weights=None, prefix_weights=None, accumulate=False) -> SharedContext:
+    """Build an fpd_shared_context; it keeps its tensors alive."""
+    c = SharedContext(_ptr(prefix_store), prefix_cap, _ptr(prefix_len), _ptr(kv_store), t_cap, _ptr(ctx_len),
+                      _ptr(pos_offset), _ptr(weights), _ptr(prefix_weights), int(bool(accumulate)))
+    c._keep = (prefix_store, prefix_len, kv_store, ctx_len, pos_offset, weights, prefix_weights)
+    return c
+
+
+def fpd_draft_block_shared(model, batch, block_len, ctx: SharedContext, anchor, mask_id, hidden_out, layer_hidden,
+                           workspace, workspace_bytes, stream=None):
+    _check(lib().fpd_draft_block_shared(model, batch, block_len, ctypes.byref(ctx), _ptr(anchor), int(mask_id),
+                                        _ptr(hidden_out), _ptr(layer_hidden), _ptr(workspace), workspace_bytes,
+                                        _stream(stream)), "fpd_draft_block_shared")
+
+
 def grid_format(digit_ids, plus_id, minus_id, pad_id, n_axes=3, width=5, axis_sep=",", point_sep=";") -> GridFormat:
     f = GridFormat()
     for k, t in enumerate(digit_ids):
@@ -282,4 +399,4 @@ def fpd_device_status(stream=None) -> int:
     return int(code.value)
 
 
-from .drafter import Drafter  # noqa: E402  (convenience wrapper over the calls above)
+from .drafter import Drafter, SharedDraft  # noqa: E402  (convenience wrapper over the calls above)

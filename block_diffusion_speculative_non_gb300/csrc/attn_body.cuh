@@ -79,8 +79,9 @@ struct Smem {
 // One tile of NK keys (64, or 16 for a short last tile: a quarter of the products) of the online softmax for one
 // warp's 16 query rows (rows lane/4 and lane/4 + 8 of its m16 fragment): S = Q K^T on mma.sync from the swizzled K
 // tile at ks, keys at or past k_end masked, running maximum (m0, m1) and sum (l0, l1) in base 2, O += (P_hi + P_lo)
-// V from the V tile at vs.  k0: the tile's first key.
-template <int H, int NK = KT>
+// V from the V tile at vs.  k0: the tile's first key.  SAFE: a row whose valid scores are all -inf so far keeps weight
+// 0 instead of 2^(-inf + inf) = NaN, and a tile may hold no valid key at all.
+template <int H, int NK = KT, bool SAFE = false>
 __device__ __forceinline__ void attn_tile_math(uint32_t ks, uint32_t vs, const uint32_t (&qf)[H / 16][4],
                                                float (&o)[H / 8][4], float& m0, float& m1, float& l0, float& l1,
                                                int k0, int k_end, int lane, float sl2) {
@@ -131,7 +132,7 @@ __device__ __forceinline__ void attn_tile_math(uint32_t ks, uint32_t vs, const u
   m0 = mn0;
   m1 = mn1;
   float ps0 = 0.f, ps1 = 0.f;
-  const float n0 = -mn0, n1 = -mn1;
+  const float n0 = SAFE && mn0 == -INFINITY ? 0.f : -mn0, n1 = SAFE && mn1 == -INFINITY ? 0.f : -mn1;
 #pragma unroll
   for (int n = 0; n < NK / 8; n++) {
     s[n][0] = ex2_approx(fmaf(s[n][0], sl2, n0));

@@ -2,7 +2,6 @@
 // carving, and the order of kernel launches of each call.  Every entry point validates all of its arguments
 // before it launches anything and returns an fpd_status; nothing here synchronises, allocates or copies
 // between host and device except fpd_model_create / fpd_model_destroy / fpd_device_status.
-#include <nvtx3/nvToolsExt.h>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -11,7 +10,9 @@
 #include <string>
 #include <vector>
 
+#include "fpd_context.cuh"
 #include "fpd_kernels.cuh"
+#include "fpd_scope.cuh"
 
 namespace fpd {
 std::atomic<uint64_t> g_launches{0};
@@ -313,28 +314,6 @@ fpd_status set_last_error(fpd_status s, const char* msg) {
   return s;
 }
 size_t argmax_scratch_bytes(const fpd_model* m, int batch, int block_len) { return ws_argmax_bytes(*m, batch, block_len); }
-
-// NVTX range over one entry point; with FPD_DEBUG the call's kernels are also waited for and checked.
-struct ApiScope {
-  const char* name;
-  cudaStream_t st;
-  ApiScope(const char* n, void* s) : name(n), st((cudaStream_t)s) { nvtxRangePushA(n); }
-  ~ApiScope() { nvtxRangePop(); }
-  fpd_status done(fpd_status r) const {
-#ifdef FPD_DEBUG
-    if (r != FPD_OK) return r;
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) return r;
-    cudaError_t e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return set_last_error(FPD_ERR_CUDA, (std::string(name) + ": " + cudaGetErrorString(e)).c_str());
-    int32_t code = 0;
-    if (cudaMemcpyFromSymbol(&code, g_device_check, sizeof(code)) == cudaSuccess && code != 0)
-      return set_last_error(FPD_ERR_DEVICE_CHECK, (std::string(name) + ": device check " + std::to_string(code)).c_str());
-#endif
-    return r;
-  }
-};
 }  // namespace fpd
 
 extern "C" {
@@ -390,6 +369,7 @@ fpd_status fpd_model_create(const fpd_model_desc* desc, const fpd_weights* w, fp
       if (init_err == cudaSuccess) init_err = stream_init_attributes();
       if (init_err == cudaSuccess) init_err = attn_tc_init_attributes();
       if (init_err == cudaSuccess) init_err = attn_short_init_attributes();
+      if (init_err == cudaSuccess) init_err = context_ops_init();
     });
     if (init_err != cudaSuccess) return cuda_fail(init_err, "kernel attributes");
   }
@@ -534,12 +514,13 @@ fpd_status fpd_prepare_context(fpd_model* m, int batch, int total_rows, const in
 }
 
 static fpd_status prepare_rows_impl(fpd_model* m, int batch, int total_rows, const int32_t* row_off,
-                                    const int32_t* row_cnt, const int32_t* pos_start, const void* const* feats,
-                                    void* kv_store, int t_cap, void* workspace, size_t ws_bytes, void* stream) {
+                                    const int32_t* row_cnt, const int32_t* pos_start, const int32_t* pos_offset,
+                                    const void* const* feats, void* kv_store, int t_cap, void* workspace,
+                                    size_t ws_bytes, void* stream) {
   if (!m) return fail(FPD_ERR_INVALID_ARG, "model is null");
   const auto& d = m->d;
   if (batch < 1 || total_rows < 0 || t_cap < 1) return fail(FPD_ERR_SHAPE, "batch %d, total_rows %d, t_cap %d", batch, total_rows, t_cap);
-  if (t_cap > d.max_pos) return fail(FPD_ERR_CAPACITY, "t_cap %d exceeds max_pos %d", t_cap, d.max_pos);
+  if (!pos_offset && t_cap > d.max_pos) return fail(FPD_ERR_CAPACITY, "t_cap %d exceeds max_pos %d", t_cap, d.max_pos);
   if ((long long)total_rows > (long long)batch * t_cap) return fail(FPD_ERR_CAPACITY, "total_rows %d exceeds batch * t_cap", total_rows);
   if (!row_off || !feats || !kv_store || !workspace) return fail(FPD_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned16(kv_store) || !aligned16(workspace)) return fail(FPD_ERR_INVALID_ARG, "kv_store/workspace not 16-byte aligned");
@@ -593,6 +574,7 @@ static fpd_status prepare_rows_impl(fpd_model* m, int batch, int total_rows, con
       kg.row_off = row_off;
       kg.row_cnt = row_cnt;
       kg.pos_start = pos_start;
+      kg.pos_offset = pos_offset;
       FPD_CUDA(launch_tc_kvctx(kg, m->num_sms, st), "context K/V GEMM + store epilogue");
       continue;
     }
@@ -613,7 +595,8 @@ static fpd_status prepare_rows_impl(fpd_model* m, int batch, int total_rows, con
       k.k_split = pk.k_split;
       FPD_CUDA(launch_tc_gemm(k, pk, st), "context K/V GEMM");
       FPD_CUDA(launch_kv_post((bf16*)kv_store, w.part, pk.splits, k.c_split_stride, (const bf16*)m->w.k_norm[l],
-                              m->rope, row_off, row_cnt, pos_start, batch, l, t_cap, r0, R, nkv, h, d.rms_eps, st),
+                              m->rope, row_off, row_cnt, pos_start, pos_offset, d.max_pos, batch, l, t_cap, r0, R, nkv,
+                              h, d.rms_eps, st),
                "context K/V epilogue");
     }
   }
@@ -621,13 +604,64 @@ static fpd_status prepare_rows_impl(fpd_model* m, int batch, int total_rows, con
 }
 
 // ---- a3..a7 -------------------------------------------------------------------------------------------------
+// Scratch of a block pass over a shared context, behind the block pass's own.
+struct SharedWs {
+  SharedPlan plan;
+  int32_t* base;     // rotary position of every request's first block slot
+  float* lse;
+  float* o_part;
+  float2* ml;
+};
+
+static SharedWs carve_shared(const Model& m, Carver& c, int B, int L, int p_cap, int t_cap) {
+  SharedWs w{};
+  const auto& d = m.d;
+  w.plan = shared_attn_plan(B, L, L, d.n_q_heads, d.n_kv_heads, d.head_dim, p_cap, t_cap, m.num_sms);
+  const size_t n_out = (size_t)B * L * d.n_q_heads;
+  w.base = c.take<int32_t>(B);
+  w.lse = c.take<float>(n_out);
+  w.o_part = c.take<float>(n_out * w.plan.splits() * d.head_dim);
+  w.ml = c.take<float2>(n_out * w.plan.splits());
+  return w;
+}
+
+size_t fpd_shared_workspace_bytes(const fpd_model* m, int batch, int max_block_len, int prefix_cap, int t_cap) {
+  if (!m || batch < 1 || max_block_len < 2 || prefix_cap < 0 || t_cap < 0) return 0;
+  size_t best = 0;   // calls may use any smaller batch and block length: the maximum over all of them
+  for (int b = 1; b <= batch; b++)
+    for (int l = 2; l <= max_block_len; l++) {
+      size_t own = ws_draft_bytes(*m, b, l, 1);
+      Carver c;
+      carve_shared(*m, c, b, l, prefix_cap, t_cap);
+      best = std::max(best, own + c.off);
+    }
+  return best + 512;
+}
+
 static fpd_status draft_block_impl(fpd_model* m, int batch, int L, const void* kv_store, int t_cap,
                                    const int32_t* ctx_len, const int32_t* anchor, int32_t mask_id, void* hidden_out,
-                                   void* layer_hidden, void* workspace, size_t ws_bytes, void* stream) {
+                                   void* layer_hidden, void* workspace, size_t ws_bytes, void* stream,
+                                   const fpd_shared_context* sc = nullptr) {
   if (!m) return fail(FPD_ERR_INVALID_ARG, "model is null");
   const auto& d = m->d;
+  if (sc) {
+    if (batch < 1 || L < 2 || sc->prefix_cap < 0 || sc->t_cap < 0 || sc->prefix_cap > kMaxStoreCap || sc->t_cap > kMaxStoreCap)
+      return fail(FPD_ERR_SHAPE, "batch %d, block_len %d, prefix_cap %d, t_cap %d", batch, L, sc->prefix_cap, sc->t_cap);
+    if (L > d.max_pos) return fail(FPD_ERR_CAPACITY, "block_len %d exceeds max_pos %d", L, d.max_pos);
+    if ((sc->prefix_cap > 0) != (sc->prefix_store && sc->prefix_len) || (sc->t_cap > 0) != (sc->kv_store && sc->ctx_len))
+      return fail(FPD_ERR_INVALID_ARG, "a store with a capacity needs its pointer and its length, one without neither");
+    if ((sc->weights && !sc->t_cap) || (sc->prefix_weights && !sc->prefix_cap))
+      return fail(FPD_ERR_INVALID_ARG, "weights without the store they belong to");
+    if (!aligned16(sc->prefix_store)) return fail(FPD_ERR_INVALID_ARG, "prefix_store not 16-byte aligned");
+    if ((long long)batch * L * d.n_q_heads > kMaxAttnRows)
+      return fail(FPD_ERR_SHAPE, "batch * block_len * n_q_heads exceeds %lld", kMaxAttnRows);
+    kv_store = sc->kv_store ? sc->kv_store : sc->prefix_store;
+    if (!kv_store) kv_store = workspace;   // no context at all: never read
+    ctx_len = sc->ctx_len ? sc->ctx_len : anchor;   // placeholder for the checks below; replaced by the rotary base
+    t_cap = 1;
+  }
   if (batch < 1 || L < 2 || t_cap < 1) return fail(FPD_ERR_SHAPE, "batch %d, block_len %d, t_cap %d", batch, L, t_cap);
-  if ((long long)t_cap + L > d.max_pos) return fail(FPD_ERR_CAPACITY, "t_cap + block_len %d exceeds max_pos %d", t_cap + L, d.max_pos);
+  if (!sc && (long long)t_cap + L > d.max_pos) return fail(FPD_ERR_CAPACITY, "t_cap + block_len %d exceeds max_pos %d", t_cap + L, d.max_pos);
   if (mask_id < 0 || mask_id >= d.vocab) return fail(FPD_ERR_SHAPE, "mask_id %d outside [0, %d)", mask_id, d.vocab);
   if (!kv_store || !ctx_len || !anchor || !hidden_out || !workspace) return fail(FPD_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned16(kv_store) || !aligned16(hidden_out) || !aligned16(workspace) || (layer_hidden && !aligned16(layer_hidden)))
@@ -637,6 +671,8 @@ static fpd_status draft_block_impl(fpd_model* m, int batch, int L, const void* k
   Carver c;
   c.base = (char*)workspace;
   DraftWs w = carve_draft(*m, c, batch, L, t_cap, m->fp8);
+  SharedWs sw{};
+  if (sc) sw = carve_shared(*m, c, batch, L, sc->prefix_cap, sc->t_cap);
   if (c.off > ws_bytes) return fail(FPD_ERR_CAPACITY, "workspace %zu < %zu bytes", ws_bytes, c.off);
   cudaStream_t st = (cudaStream_t)stream;
   const int M = batch * L, dm = d.d_model, h = d.head_dim, nq = d.n_q_heads, nkv = d.n_kv_heads, F = d.d_ff;
@@ -659,6 +695,70 @@ static fpd_status draft_block_impl(fpd_model* m, int batch, int L, const void* k
   a.rows = M;
   a.splits = w.att_splits;
   a.chunk = w.att_chunk;
+  // Over a shared context: rotary positions come from the offsets (the QKV kernels see them as context lengths, bounded
+  // so that a block stays inside the rotary table), and the attention reads both stores and leaves the collected weights.
+  auto attend_shared = [&](int l) -> cudaError_t {
+    SharedAttn s{};
+    const size_t pre_layer = (size_t)2 * nkv * sc->prefix_cap * h, own_layer = (size_t)batch * 2 * nkv * sc->t_cap * h;
+    s.q = w.q;
+    if (sc->prefix_cap) {
+      s.pk = (const bf16*)sc->prefix_store + l * pre_layer;
+      s.pv = s.pk + pre_layer / 2;
+    }
+    if (sc->t_cap) {
+      s.ck = (const bf16*)sc->kv_store + l * own_layer;
+      s.cv = s.ck + (size_t)nkv * sc->t_cap * h;
+    }
+    s.kblk = w.kblk;
+    s.vblk = w.vblk;
+    s.prefix_len = sc->prefix_len;
+    s.ctx_len = sc->ctx_len;
+    s.out = w.o;
+    s.lse = sc->weights || sc->prefix_weights ? sw.lse : nullptr;
+    s.o_part = sw.o_part;
+    s.ml = sw.ml;
+    s.batch = batch;
+    s.L = s.lb = L;
+    s.nq = nq;
+    s.nkv = nkv;
+    s.h = h;
+    s.p_cap = sc->prefix_cap;
+    s.t_cap = sc->t_cap;
+    s.rows = M;
+    cudaError_t e = launch_shared_attention(s, sw.plan, st);
+    CtxWeights cw{};
+    cw.q = w.q;
+    cw.lse = sw.lse;
+    cw.nq = nq;
+    cw.nkv = nkv;
+    cw.h = h;
+    cw.accumulate = sc->accumulate;
+    if (e == cudaSuccess && sc->weights) {
+      cw.ck = s.ck;
+      cw.ctx_len = sc->ctx_len;
+      cw.weights = sc->weights + (size_t)l * batch * nkv * sc->t_cap;
+      cw.batch = batch;
+      cw.L = L;
+      cw.t_cap = sc->t_cap;
+      e = launch_ctx_weights(cw, m->num_sms, st);
+    }
+    if (e == cudaSuccess && sc->prefix_weights) {
+      cw.ck = s.pk;
+      cw.ctx_len = sc->prefix_len;
+      cw.weights = sc->prefix_weights + (size_t)l * nkv * sc->prefix_cap;
+      cw.batch = 1;
+      cw.L = M;
+      cw.t_cap = sc->prefix_cap;
+      e = launch_ctx_weights(cw, m->num_sms, st);
+    }
+    return e;
+  };
+  if (sc) {
+    FPD_CUDA(launch_rope_base(sw.base, sc->ctx_len, sc->prefix_len, sc->pos_offset, batch, sc->t_cap, sc->prefix_cap, st),
+             "rotary positions");
+    ctx_len = sw.base;
+    t_cap = d.max_pos - L;
+  }
   if (w.stream) {
     // few-token path: 5 kernels per layer, norms applied on load, split-K reduced inside the GEMMs, attention
     // splits merged inside the attention kernel
@@ -703,7 +803,8 @@ static fpd_status draft_block_impl(fpd_model* m, int batch, int L, const void* k
       g.h = h;
       FPD_CUDA(launch_stream_gemm(g, st), "QKV GEMM + q/k norm + RoPE");
       a.layer = l;
-      FPD_CUDA(short_attn ? launch_attention_short(a, w.o, st) : launch_attention(a, w.o, st), "attention");
+      FPD_CUDA(sc ? attend_shared(l) : short_attn ? launch_attention_short(a, w.o, st) : launch_attention(a, w.o, st),
+               "attention");
       // O projection + residual
       StreamGemm o = g;
       o.epi = SEPI_RESID;
@@ -788,7 +889,8 @@ static fpd_status draft_block_impl(fpd_model* m, int batch, int L, const void* k
       g.eps = d.rms_eps;
       FPD_CUDA(launch_tc_tok(g, w.p_qkv, st), "QKV GEMM + q/k norm + RoPE");
       a.layer = l;
-      FPD_CUDA(w.att_tc ? launch_attention_tc(a, w.o, st) : launch_attention(a, w.o, st), "attention");
+      FPD_CUDA(sc ? attend_shared(l) : w.att_tc ? launch_attention_tc(a, w.o, st) : launch_attention(a, w.o, st),
+               "attention");
       TokGemm r{};
       r.qkv = false;
       r.x = w.o;
@@ -841,7 +943,7 @@ static fpd_status draft_block_impl(fpd_model* m, int batch, int L, const void* k
                              L, nq, nkv, h, d.rms_eps, st),
              "q/k norm + RoPE");
     a.layer = l;
-    FPD_CUDA(launch_attention(a, w.o, st), "attention");
+    FPD_CUDA(sc ? attend_shared(l) : launch_attention(a, w.o, st), "attention");
     FPD_CUDA(gemm(w.o, nq * h, m->w.wo[l], dm, w.p_o), "O GEMM");
     FPD_CUDA(launch_residual_norm(x, w.xn, w.part, w.p_o.splits, (size_t)M * dm, (const bf16*)m->w.mlp_norm[l], M, dm,
                                   d.rms_eps, st),
@@ -1001,8 +1103,18 @@ fpd_status fpd_prepare_context_rows(fpd_model* m, int batch, int total_rows, con
                                     const int32_t* row_cnt, const int32_t* pos_start, const void* const* feats,
                                     void* kv_store, int t_cap, void* workspace, size_t ws_bytes, void* stream) {
   ApiScope scope("fpd_prepare_context", stream);
-  return scope.done(prepare_rows_impl(m, batch, total_rows, row_off, row_cnt, pos_start, feats, kv_store, t_cap,
+  return scope.done(prepare_rows_impl(m, batch, total_rows, row_off, row_cnt, pos_start, nullptr, feats, kv_store, t_cap,
                                       workspace, ws_bytes, stream));
+}
+
+fpd_status fpd_prepare_context_at(fpd_model* m, int batch, int total_rows, const int32_t* row_off,
+                                  const int32_t* row_cnt, const int32_t* pos_start, const int32_t* pos_offset,
+                                  const void* const* feats, void* kv_store, int t_cap, void* workspace, size_t ws_bytes,
+                                  void* stream) {
+  ApiScope scope("fpd_prepare_context_at", stream);
+  if (!pos_offset) return fail(FPD_ERR_INVALID_ARG, "pos_offset is null");
+  return scope.done(prepare_rows_impl(m, batch, total_rows, row_off, row_cnt, pos_start, pos_offset, feats, kv_store,
+                                      t_cap, workspace, ws_bytes, stream));
 }
 
 fpd_status fpd_draft_block(fpd_model* m, int batch, int L, const void* kv_store, int t_cap, const int32_t* ctx_len,
@@ -1011,6 +1123,15 @@ fpd_status fpd_draft_block(fpd_model* m, int batch, int L, const void* kv_store,
   ApiScope scope("fpd_draft_block", stream);
   return scope.done(draft_block_impl(m, batch, L, kv_store, t_cap, ctx_len, anchor, mask_id, hidden_out, layer_hidden,
                                      workspace, ws_bytes, stream));
+}
+
+fpd_status fpd_draft_block_shared(fpd_model* m, int batch, int L, const fpd_shared_context* ctx, const int32_t* anchor,
+                                  int32_t mask_id, void* hidden_out, void* layer_hidden, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  ApiScope scope("fpd_draft_block_shared", stream);
+  if (!ctx) return fail(FPD_ERR_INVALID_ARG, "context is null");
+  return scope.done(draft_block_impl(m, batch, L, nullptr, 0, nullptr, anchor, mask_id, hidden_out, layer_hidden,
+                                     workspace, ws_bytes, stream, ctx));
 }
 
 fpd_status fpd_constrain_argmax(fpd_model* m, int batch, int L, const void* hidden, const fpd_vocab_layout* layout,

@@ -45,6 +45,7 @@ struct KvCtxGemm {
   bf16* store;                      // [layers][batch][K|V][H_kv][t_cap][h]
   int batch, t_cap, row0;
   const int32_t *row_off, *row_cnt, *pos_start;
+  const int32_t* pos_offset;        // [batch] or null: rotary position of slot 0
 };
 bool kvctx_supported(const fpd_model_desc& d);
 cudaError_t launch_tc_kvctx(const KvCtxGemm& g, int num_sms, cudaStream_t st);
@@ -136,8 +137,8 @@ cudaError_t launch_qkv_post(bf16* q, bf16* kblk, bf16* vblk, const float* part, 
                             int t_cap, int B, int L, int nq, int nkv, int h, float eps, cudaStream_t st);
 cudaError_t launch_kv_post(bf16* store, const float* part, int nsplit, size_t split_stride, const bf16* k_norm,
                            const float2* rope, const int32_t* row_off, const int32_t* row_cnt, const int32_t* pos_start,
-                           int batch, int layer, int t_cap, int row0, int rows, int nkv, int h, float eps,
-                           cudaStream_t st);
+                           const int32_t* pos_offset, int max_pos, int batch, int layer, int t_cap, int row0, int rows,
+                           int nkv, int h, float eps, cudaStream_t st);
 cudaError_t launch_residual_norm(bf16* x, bf16* xn, const float* part, int nsplit, size_t split_stride, const bf16* g,
                                  int rows, int d, float eps, cudaStream_t st);
 cudaError_t launch_embed_norm(bf16* x, bf16* xn, const bf16* embed, const int32_t* anchor, int32_t mask_id,

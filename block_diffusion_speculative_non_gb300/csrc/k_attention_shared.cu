@@ -1,0 +1,298 @@
+// k_attention_shared.cu — attention of a batch of blocks whose requests share a long context prefix:
+//   out_r = sum_t exp(s_rt - lse_r) v_t,   s_rt = q_r . k_t / sqrt(h),   lse_r = log sum_t exp(s_rt)
+// with t over [prefix ; the request's own context ; its block].
+//
+// The prefix is one request's K/V, so the query rows of ALL requests that use a kv head form the rows of one product:
+// each prefix key is read once per kv head and row tile instead of once per request.  The own context and the block
+// are the ordinary attention of one request.  Both parts leave unnormalised partials (o, m, l) per split of their keys;
+// the softmax of a row is put together from them in split order (deterministic, no atomics).
+#include "attn_body.cuh"
+#include "fpd_context.cuh"
+
+namespace fpd {
+
+namespace {
+using namespace attn;
+
+// ---- work units -------------------------------------------------------------------------------------------------
+// Unit u of the prefix part: (split, kv head, row tile), row tiles fastest, so that the CTAs which read the same keys
+// run next to one another.  Own part: (split, request, kv head, row tile).
+struct Unit {
+  int b, g, qt, split;     // split: index among all partials of a row
+  int n0, nrows;           // first row of the part in [rows], rows (position, head) of the part and kv head
+  int T, n_keys;           // keys from the store, all keys
+  int k_begin, k_end;
+  const bf16 *kc, *vc, *kb, *vb;
+};
+
+// Cuts n_keys into `splits` runs of whole tiles as evenly as the tile count allows.
+__device__ __forceinline__ void split_range(int n_keys, int splits, int s, int tile, int& k0, int& k1) {
+  const long long nt = (n_keys + tile - 1) / tile;
+  k0 = (int)(s * nt / splits) * tile;
+  k1 = min(n_keys, (int)((s + 1) * nt / splits) * tile);
+}
+
+template <int H>
+__device__ __forceinline__ Unit decode_unit(const SharedAttn& a, const SharedPlan& pl, bool prefix, int u, int tile) {
+  Unit w;
+  if (prefix) {
+    w.qt = u % pl.pre_tiles;
+    u /= pl.pre_tiles;
+    w.g = u % a.nkv;
+    const int s = u / a.nkv;
+    w.b = 0;
+    w.split = s;
+    w.n0 = 0;
+    w.nrows = a.rows * (a.nq / a.nkv);
+    w.T = w.n_keys = clamp_ctx(a.prefix_len[0], a.p_cap);
+    w.kc = a.pk + (size_t)w.g * a.p_cap * H;
+    w.vc = a.pv + (size_t)w.g * a.p_cap * H;
+    w.kb = w.vb = nullptr;
+    split_range(w.n_keys, pl.pre_splits, s, tile, w.k_begin, w.k_end);
+  } else {
+    w.qt = u % pl.own_tiles;
+    u /= pl.own_tiles;
+    w.g = u % a.nkv;
+    u /= a.nkv;
+    w.b = u % a.batch;
+    const int s = u / a.batch;
+    w.split = pl.pre_splits + s;
+    w.n0 = w.b * a.L;
+    w.nrows = a.L * (a.nq / a.nkv);
+    w.T = a.ck ? clamp_ctx(a.ctx_len[w.b], a.t_cap) : 0;
+    w.n_keys = w.T + a.lb;
+    const size_t off = ((size_t)w.b * 2 * a.nkv + w.g) * a.t_cap * H;
+    w.kc = a.ck + off;
+    w.vc = a.cv + off;
+    const size_t boff = ((size_t)w.b * a.nkv + w.g) * a.lb * H;
+    w.kb = a.kblk + boff;
+    w.vb = a.vblk + boff;
+    split_range(w.n_keys, pl.own_splits, s, tile, w.k_begin, w.k_end);
+  }
+  return w;
+}
+
+// One 64-row tile over one split on mma.sync (the tile math of attn_body.cuh).
+template <int H>
+__global__ void __launch_bounds__(NWARP * 32) shared_mma_kernel(const __grid_constant__ SharedAttn a, const __grid_constant__ SharedPlan pl,
+                                                                int pre_units) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  constexpr int CH = H / 8, NKS = H / 16, NOT = H / 8;
+  Smem<H>& sm = *reinterpret_cast<Smem<H>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool prefix = (int)blockIdx.x < pre_units;
+  const Unit w = decode_unit<H>(a, pl, prefix, prefix ? blockIdx.x : blockIdx.x - pre_units, KT);
+  const int grp = a.nq / a.nkv;
+  const float sl2 = rsqrtf((float)H) * 1.4426950408889634f;
+
+  const uint32_t q_s = smem_addr(sm.q);
+  for (int idx = tid; idx < QT * CH; idx += NWARP * 32) {
+    const int r = idx / CH, c = idx % CH, qi = w.qt * QT + r;
+    const bool ok = qi < w.nrows;
+    const bf16* src = a.q;
+    if (ok) src = a.q + ((size_t)(w.n0 + qi / grp) * a.nq + w.g * grp + qi % grp) * H + c * 8;
+    cp_async16(swz<H>(q_s, r, c), src, ok);
+  }
+  cp_async_commit();
+  auto load_kv = [&](int buf, int k0) {
+    const uint32_t ks = smem_addr(sm.k[buf]), vs = smem_addr(sm.v[buf]);
+    for (int idx = tid; idx < KT * CH; idx += NWARP * 32) {
+      const int r = idx / CH, c = idx % CH, t = k0 + r;
+      const bool ok = t < w.k_end;
+      const bf16 *ksrc = a.q, *vsrc = a.q;   // any mapped address: zero bytes are read when !ok
+      if (ok) {
+        ksrc = t < w.T ? w.kc + (size_t)t * H + c * 8 : w.kb + (size_t)(t - w.T) * H + c * 8;
+        vsrc = t < w.T ? w.vc + (size_t)t * H + c * 8 : w.vb + (size_t)(t - w.T) * H + c * 8;
+      }
+      cp_async16(swz<H>(ks, r, c), ksrc, ok);
+      cp_async16(swz<H>(vs, r, c), vsrc, ok);
+    }
+    cp_async_commit();
+  };
+  const int n_tiles = w.k_end > w.k_begin ? (w.k_end - w.k_begin + KT - 1) / KT : 0;
+  if (n_tiles > 0) load_kv(0, w.k_begin);
+
+  float o[NOT][4];
+#pragma unroll
+  for (int n = 0; n < NOT; n++) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  uint32_t qf[NKS][4];
+  if (n_tiles > 0)
+    cp_async_wait<1>();
+  else
+    cp_async_wait<0>();
+  __syncthreads();
+  {
+    const int r = warp * 16 + (lane & 15);
+#pragma unroll
+    for (int kk = 0; kk < NKS; kk++) ldsm_x4(swz<H>(q_s, r, kk * 2 + (lane >> 4)), qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3]);
+  }
+  for (int it = 0; it < n_tiles; it++) {
+    const int buf = it & 1, k0 = w.k_begin + it * KT;
+    if (it + 1 < n_tiles) {
+      load_kv(buf ^ 1, k0 + KT);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncthreads();
+    attn_tile_math<H, KT, true>(smem_addr(sm.k[buf]), smem_addr(sm.v[buf]), qf, o, m0, m1, l0, l1, k0, w.k_end, lane, sl2);
+    __syncthreads();
+  }
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    const int qi = w.qt * QT + warp * 16 + (lane >> 2) + half * 8;
+    if (qi >= w.nrows) continue;
+    const size_t orow = (size_t)(w.n0 + qi / grp) * a.nq + w.g * grp + qi % grp;
+    const size_t prow = (size_t)w.split * a.rows * a.nq + orow;
+    const float m = half ? m1 : m0, l = half ? l1 : l0;
+    if (n_tiles > 0) {
+      float* dst = a.o_part + prow * H + (lane & 3) * 2;
+#pragma unroll
+      for (int n = 0; n < NOT; n++) *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][half * 2], o[n][half * 2 + 1]);
+    }
+    if ((lane & 3) == 0) a.ml[prow] = make_float2(m, l);
+  }
+}
+
+// The softmax of one (row, head) from its partials, one warp: M = max m_s over the partials that hold a key
+// (l_s != 0; a NaN sum counts, so that it reaches the output), den = sum l_s 2^(m_s - M), out = sum o_s 2^(m_s - M) / den,
+// lse = (M + log2 den) ln 2.  Partials in split order: bit-reproducible.
+template <int H>
+__global__ void __launch_bounds__(256) shared_merge_kernel(bf16* __restrict__ out, float* __restrict__ lse,
+                                                           const float* __restrict__ o_part, const float2* __restrict__ ml,
+                                                           int nsplit, int n_out) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int DPL = H / 32;
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= n_out) return;
+  float mx = -INFINITY;
+  for (int s0 = 0; s0 < nsplit; s0 += 32) {
+    const int s = s0 + lane;
+    const float2 v = s < nsplit ? __ldcg(ml + (size_t)s * n_out + r) : make_float2(-INFINITY, 0.f);
+    mx = fmaxf(mx, warp_max(v.y == 0.f ? -INFINITY : v.x));
+  }
+  float den = 0.f, num[DPL];
+#pragma unroll
+  for (int e = 0; e < DPL; e++) num[e] = 0.f;
+  for (int s0 = 0; s0 < nsplit; s0 += 8) {
+    float t[8][DPL], wgt[8];
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      const int s = s0 + u;
+      wgt[u] = 0.f;
+#pragma unroll
+      for (int e = 0; e < DPL; e++) t[u][e] = 0.f;
+      if (s < nsplit) {
+        const float2 v = __ldcg(ml + (size_t)s * n_out + r);
+        if (v.y != 0.f) {
+          wgt[u] = exp2f(v.x - mx);
+          den += v.y * wgt[u];
+          const float* op = o_part + ((size_t)s * n_out + r) * H + lane * DPL;
+          if constexpr (DPL == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(op));
+            t[u][0] = f.x;
+            t[u][1] = f.y;
+            t[u][2] = f.z;
+            t[u][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(op));
+            t[u][0] = f.x;
+            t[u][1] = f.y;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; u++)
+#pragma unroll
+      for (int e = 0; e < DPL; e++) num[e] += wgt[u] != 0.f ? t[u][e] * wgt[u] : 0.f;
+  }
+  const bool none = den == 0.f;   // no key at all (or every score -inf): output 0, lse -inf
+  bf16* dst = out + (size_t)r * H + lane * DPL;
+#pragma unroll
+  for (int e = 0; e < DPL; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + e) =
+        __floats2bfloat162_rn(none ? 0.f : num[e] / den, none ? 0.f : num[e + 1] / den);
+  if (lse && lane == 0) lse[r] = none ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
+}
+
+__global__ void rope_base_kernel(int32_t* base, const int32_t* ctx_len, const int32_t* prefix_len, const int32_t* pos_offset,
+                                 int batch, int t_cap, int p_cap) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= batch) return;
+  const int off = pos_offset ? pos_offset[b] : (prefix_len ? clamp_ctx(prefix_len[0], p_cap) : 0);
+  const int cl = ctx_len ? clamp_ctx(ctx_len[b], t_cap) : 0;
+  base[b] = (off < 0 || off > INT32_MAX - cl) ? -1 : off + cl;
+}
+
+}  // namespace
+
+// Splits: with `base` row tiles times heads and n key tiles each, a part has base * s CTAs of about n / s tiles.  The
+// total time of both parts is close to waves * (tiles per CTA + c) where c is what a CTA pays besides its tiles (Q,
+// the partial out, its share of the merge); the smallest such cost over tile counts per CTA wins, ties to fewer splits.
+SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms) {
+  SharedPlan pl{};
+  const int grp = nq / nkv, rows = batch * L;
+  const int pre_kt = ceil_div(p_cap, KT), own_kt = ceil_div(t_cap + lb, KT);
+  pl.pre_tiles = p_cap ? ceil_div(rows * grp, QT) : 0;
+  pl.own_tiles = t_cap + lb ? ceil_div(L * grp, QT) : 0;
+  const long pre_base = (long)pl.pre_tiles * nkv, own_base = (long)pl.own_tiles * nkv * batch;
+  const int slots = 2 * num_sms, most = std::max(pre_kt, own_kt);
+  double best = 0;
+  int best_w = std::max(most, 1);
+  for (int w = most; w >= 1; w = w > 16 ? w - std::max(1, w / 16) : w - 1) {
+    const long sp = ceil_div(pre_kt, w), so = ceil_div(own_kt, w);
+    if (sp > 128 || so > 128) break;
+    const long units = pre_base * sp + own_base * so;
+    const double waves = units <= slots ? 1.0 : (double)units / slots;
+    const double cost = waves * (w + 2);
+    if (w == most || cost < best) {
+      best = cost;
+      best_w = w;
+    }
+  }
+  pl.pre_splits = pl.pre_tiles ? ceil_div(pre_kt, best_w) : 0;
+  pl.own_splits = pl.own_tiles ? ceil_div(own_kt, best_w) : 0;
+  return pl;
+}
+
+cudaError_t shared_attn_init_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(shared_mma_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(Smem<128>));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(shared_mma_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<64>));
+  return e;
+}
+
+cudaError_t launch_shared_attention(const SharedAttn& a, const SharedPlan& pl, cudaStream_t st) {
+  const int pre_units = pl.pre_tiles * a.nkv * pl.pre_splits;
+  const int units = pre_units + pl.own_tiles * a.nkv * a.batch * pl.own_splits;
+  cudaError_t e = cudaSuccess;
+  if (units > 0)
+    e = a.h == 128 ? launch_k(shared_mma_kernel<128>, units, NWARP * 32, sizeof(Smem<128>), st, a, pl, pre_units)
+                   : launch_k(shared_mma_kernel<64>, units, NWARP * 32, sizeof(Smem<64>), st, a, pl, pre_units);
+  if (e != cudaSuccess) return e;
+  const int n_out = a.rows * a.nq, blocks = ceil_div(n_out, 8);
+  return a.h == 128 ? launch_k(shared_merge_kernel<128>, blocks, 256, 0, st, a.out, a.lse, (const float*)a.o_part,
+                               (const float2*)a.ml, pl.splits(), n_out)
+                    : launch_k(shared_merge_kernel<64>, blocks, 256, 0, st, a.out, a.lse, (const float*)a.o_part,
+                               (const float2*)a.ml, pl.splits(), n_out);
+}
+
+cudaError_t launch_rope_base(int32_t* base, const int32_t* ctx_len, const int32_t* prefix_len, const int32_t* pos_offset,
+                             int batch, int t_cap, int p_cap, cudaStream_t st) {
+  return launch_k(rope_base_kernel, ceil_div(batch, 128), 128, 0, st, base, ctx_len, prefix_len, pos_offset, batch, t_cap,
+                  p_cap);
+}
+
+}  // namespace fpd

@@ -1,0 +1,133 @@
+// k_context_weights.cu — the attention weight that each stored context position collects from a block's queries:
+//   weights[b][g][t] (+)= sum over the rows r of request b in kv head g of exp(q_r . k_t / sqrt(h) - lse_r)
+// with lse_r the attention's own log-sum-exp, so that every row hands out a total weight of 1 over all its keys.
+//
+// The sum runs over the query rows of one key, so keys take the product's row side: a warp holds 16 keys as A
+// fragments for the whole kernel and streams the query rows past them; the exponentials of a key stay in the quad of
+// lanes that owns it, and no intermediate leaves the registers.  One CTA owns its keys: no atomics, a fixed order.
+#include "attn_body.cuh"
+#include "fpd_context.cuh"
+
+namespace fpd {
+
+namespace {
+using namespace attn;
+
+template <int H>
+struct WeightSmem {
+  bf16 k[KT * H];
+  bf16 q[2][QT * H];
+  float l2[2][QT];   // lse log2(e) of the rows, +inf for rows that hold no key and past the last row: weight 0
+};
+
+template <int H>
+__global__ void __launch_bounds__(NWARP * 32) weights_mma_kernel(const __grid_constant__ CtxWeights a, int key_tiles) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  constexpr int CH = H / 8, NKS = H / 16;
+  WeightSmem<H>& sm = *reinterpret_cast<WeightSmem<H>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bg = blockIdx.x / key_tiles, k0 = (int)(blockIdx.x % key_tiles) * KT;
+  const int b = bg / a.nkv, g = bg % a.nkv, grp = a.nq / a.nkv, nrows = a.L * grp;
+  const int T = clamp_ctx(a.ctx_len[b], a.t_cap);
+  if (k0 >= T) return;
+  const float log2e = 1.4426950408889634f, sl2 = rsqrtf((float)H) * log2e;
+  const bf16* kc = a.ck + ((size_t)b * 2 * a.nkv + g) * a.t_cap * H;
+  for (int idx = tid; idx < KT * CH; idx += NWARP * 32) {
+    const int r = idx / CH, c = idx % CH;
+    const bool ok = k0 + r < T;
+    cp_async16(swz<H>(smem_addr(sm.k), r, c), ok ? kc + (size_t)(k0 + r) * H + c * 8 : kc, ok);
+  }
+  auto load_q = [&](int buf, int r0) {
+    for (int idx = tid; idx < QT * CH; idx += NWARP * 32) {
+      const int r = idx / CH, c = idx % CH, qi = r0 + r;
+      const bool ok = qi < nrows;
+      const bf16* src = a.q;
+      if (ok) src = a.q + (((size_t)b * a.L + qi / grp) * a.nq + g * grp + qi % grp) * H + c * 8;
+      cp_async16(swz<H>(smem_addr(sm.q[buf]), r, c), src, ok);
+    }
+    if (tid < QT) {
+      const int qi = r0 + tid;
+      float v = INFINITY;
+      if (qi < nrows) {
+        v = a.lse[((size_t)b * a.L + qi / grp) * a.nq + g * grp + qi % grp];
+        v = v == -INFINITY ? INFINITY : v * log2e;
+      }
+      sm.l2[buf][tid] = v;
+    }
+    cp_async_commit();
+  };
+  load_q(0, 0);
+  const int nt = ceil_div(nrows, QT);
+  uint32_t kf[NKS][4];
+  float w0 = 0.f, w1 = 0.f;   // keys warp * 16 + lane / 4 and + 8: this lane's columns
+  for (int it = 0; it < nt; it++) {
+    const int buf = it & 1;
+    if (it + 1 < nt) {
+      load_q(buf ^ 1, (it + 1) * QT);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncthreads();
+    if (it == 0) {
+      const int r = warp * 16 + (lane & 15);
+#pragma unroll
+      for (int kk = 0; kk < NKS; kk++)
+        ldsm_x4(swz<H>(smem_addr(sm.k), r, kk * 2 + (lane >> 4)), kf[kk][0], kf[kk][1], kf[kk][2], kf[kk][3]);
+    }
+    float t0 = 0.f, t1 = 0.f;   // this tile's share first: the long sum has one term per tile
+#pragma unroll
+    for (int np = 0; np < QT / 16; np++) {
+      float s[2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < NKS; kk++) {
+        const int row = np * 16 + (lane & 7) + ((lane >> 4) << 3), c = kk * 2 + ((lane >> 3) & 1);
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(swz<H>(smem_addr(sm.q[buf]), row, c), b0, b1, b2, b3);
+        mma_bf16(s[0], kf[kk][0], kf[kk][1], kf[kk][2], kf[kk][3], b0, b1);
+        mma_bf16(s[1], kf[kk][0], kf[kk][1], kf[kk][2], kf[kk][3], b2, b3);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const float2 l = *reinterpret_cast<const float2*>(&sm.l2[buf][np * 16 + e * 8 + (lane & 3) * 2]);
+        t0 += ex2_approx(fmaf(s[e][0], sl2, -l.x)) + ex2_approx(fmaf(s[e][1], sl2, -l.y));
+        t1 += ex2_approx(fmaf(s[e][2], sl2, -l.x)) + ex2_approx(fmaf(s[e][3], sl2, -l.y));
+      }
+    }
+    w0 += t0;
+    w1 += t1;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    w0 += __shfl_xor_sync(0xffffffffu, w0, o);
+    w1 += __shfl_xor_sync(0xffffffffu, w1, o);
+  }
+  if ((lane & 3) == 0) {
+    float* dst = a.weights + ((size_t)b * a.nkv + g) * a.t_cap;
+    const int t = k0 + warp * 16 + (lane >> 2);
+    if (t < T) dst[t] = a.accumulate ? dst[t] + w0 : w0;
+    if (t + 8 < T) dst[t + 8] = a.accumulate ? dst[t + 8] + w1 : w1;
+  }
+}
+
+}  // namespace
+
+cudaError_t ctx_weights_init_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(weights_mma_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(WeightSmem<128>));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(weights_mma_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(WeightSmem<64>));
+  return e;
+}
+
+cudaError_t launch_ctx_weights(const CtxWeights& a, int num_sms, cudaStream_t st) {
+  const int key_tiles = ceil_div(a.t_cap, KT);
+  const int grid = a.batch * a.nkv * key_tiles;
+  return a.h == 128 ? launch_k(weights_mma_kernel<128>, grid, NWARP * 32, sizeof(WeightSmem<128>), st, a, key_tiles)
+                    : launch_k(weights_mma_kernel<64>, grid, NWARP * 32, sizeof(WeightSmem<64>), st, a, key_tiles);
+}
+
+}  // namespace fpd

@@ -79,7 +79,8 @@ struct TcParams {
   bf16* store;
   const bf16* k_norm_l[FPD_MAX_LAYERS];
   const int32_t *row_off, *row_cnt, *pos_start;
-  int batch, row0;
+  const int32_t* pos_offset;   // [batch] or null: rotary position of slot 0
+  int max_pos, batch, row0;
 };
 
 // A pipeline stage holds KS consecutive 64-element K atoms of both operands: [A atoms][B atoms].  Several
@@ -436,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
         const int grow = p.row0 + m;
         bool ok = m < p.M;
         int b = 0, pos = 0;
+        long long rpos = 0;   // rotary position of slot pos
         if (ok) {
           int lo = 0, hi = p.batch;
           while (hi - lo > 1) {
@@ -447,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
             ok = false;
           } else {
             pos = (p.pos_start ? p.pos_start[b] : 0) + grow - p.row_off[b];
-            if (pos < 0 || pos >= p.t_cap) {
+            rpos = (long long)pos + (p.pos_offset ? p.pos_offset[b] : 0);
+            if (pos < 0 || pos >= p.t_cap || rpos < 0 || rpos >= p.max_pos) {
               record_check(kCheckBadPosition);
               ok = false;
             }
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
         }
         const int layer = w.b_row0 / p.kv_cols;
         const int hh = p.hd / 2;
-        const float2* rope_row = p.rope + (size_t)(ok ? pos : 0) * hh;
+        const float2* rope_row = p.rope + (size_t)(ok ? rpos : 0) * hh;
         const bf16* gain = p.k_norm_l[layer];
 #pragma unroll 1
         for (int h0 = 0; h0 < BN; h0 += p.hd) {
@@ -855,6 +858,8 @@ cudaError_t launch_tc_kvctx(const KvCtxGemm& g, int num_sms, cudaStream_t st) {
   p.row_off = g.row_off;
   p.row_cnt = g.row_cnt;
   p.pos_start = g.pos_start;
+  p.pos_offset = g.pos_offset;
+  p.max_pos = d.max_pos;
   p.batch = g.batch;
   p.row0 = g.row0;
   p.t_cap = g.t_cap;

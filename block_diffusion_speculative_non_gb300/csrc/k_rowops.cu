@@ -156,8 +156,8 @@ template <int H>
 __global__ void kv_post_kernel(bf16* __restrict__ store, const float* __restrict__ part, int nsplit,
                                size_t split_stride, const bf16* __restrict__ k_norm, const float2* __restrict__ rope,
                                const int32_t* __restrict__ row_off, const int32_t* __restrict__ row_cnt,
-                               const int32_t* __restrict__ pos_start, int batch, int layer, int t_cap, int row0, int nkv,
-                               float eps) {
+                               const int32_t* __restrict__ pos_start, const int32_t* __restrict__ pos_offset, int max_pos,
+                               int batch, int layer, int t_cap, int row0, int nkv, float eps) {
   pdl_trigger();
   pdl_wait();
   constexpr int NV = H / 32;
@@ -171,7 +171,8 @@ __global__ void kv_post_kernel(bf16* __restrict__ store, const float* __restrict
   const int b = lo;
   if (grow >= row_off[batch] || (row_cnt && grow - row_off[b] >= row_cnt[b])) return;   // rows past the count
   const int pos = (pos_start ? pos_start[b] : 0) + grow - row_off[b];
-  if (pos < 0 || pos >= t_cap) {                // caller contract violated: skip the store, record it
+  const long long rpos = (long long)pos + (pos_offset ? pos_offset[b] : 0);   // rotary position of slot pos
+  if (pos < 0 || pos >= t_cap || rpos < 0 || rpos >= max_pos) {   // caller contract violated: skip the store, record it
     if (lane == 0 && hd == 0) record_check(kCheckBadPosition);
     return;
   }
@@ -184,7 +185,7 @@ __global__ void kv_post_kernel(bf16* __restrict__ store, const float* __restrict
     v[k] = a;
   }
   const int is_v = hd >= nkv, g = is_v ? hd - nkv : hd;
-  if (!is_v) head_norm_rope<H>(v, k_norm, eps, rope + (size_t)pos * (H / 2), true, true);
+  if (!is_v) head_norm_rope<H>(v, k_norm, eps, rope + (size_t)rpos * (H / 2), true, true);
   bf16* dst = store + (((((size_t)layer * batch + b) * 2 + is_v) * nkv + g) * (size_t)t_cap + pos) * H;
 #pragma unroll
   for (int k = 0; k < NV; k++) dst[lane + 32 * k] = __float2bfloat16_rn(v[k]);
@@ -192,15 +193,15 @@ __global__ void kv_post_kernel(bf16* __restrict__ store, const float* __restrict
 
 cudaError_t launch_kv_post(bf16* store, const float* part, int nsplit, size_t split_stride, const bf16* k_norm,
                            const float2* rope, const int32_t* row_off, const int32_t* row_cnt, const int32_t* pos_start,
-                           int batch, int layer, int t_cap, int row0, int rows, int nkv, int h, float eps,
-                           cudaStream_t st) {
+                           const int32_t* pos_offset, int max_pos, int batch, int layer, int t_cap, int row0, int rows,
+                           int nkv, int h, float eps, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   dim3 grid(rows, 2 * nkv);
   if (h == 128)
     return launch_k(kv_post_kernel<128>, grid, 32, 0, st, store, part, nsplit, split_stride, k_norm, rope, row_off,
-                    row_cnt, pos_start, batch, layer, t_cap, row0, nkv, eps);
+                    row_cnt, pos_start, pos_offset, max_pos, batch, layer, t_cap, row0, nkv, eps);
   return launch_k(kv_post_kernel<64>, grid, 32, 0, st, store, part, nsplit, split_stride, k_norm, rope, row_off,
-                  row_cnt, pos_start, batch, layer, t_cap, row0, nkv, eps);
+                  row_cnt, pos_start, pos_offset, max_pos, batch, layer, t_cap, row0, nkv, eps);
 }
 
 // ---- residual add fused with the next RMSNorm: one block per row ------------------------------------------------

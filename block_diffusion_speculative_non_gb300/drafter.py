@@ -9,10 +9,11 @@ import numpy as np
 import torch
 
 from . import (FPD_VERIFY_SCHEMA, FPD_VERIFY_TEXT, MAX_LAYERS, ModelDesc, Weights, fpd_constrain_argmax,
-               fpd_draft_block, fpd_kv_store_bytes, fpd_model_create, fpd_model_destroy, fpd_model_enable_fp8,
-               fpd_prepare_context,
-               fpd_prepare_context_rows, fpd_sd_advance, fpd_verify, fpd_verify_prefix, fpd_workspace_bytes,
-               make_layout)
+               fpd_draft_block, fpd_draft_block_shared, fpd_evict_context, fpd_evict_workspace_bytes,
+               fpd_kv_store_bytes, fpd_model_create, fpd_model_destroy, fpd_model_enable_fp8,
+               fpd_prepare_context, fpd_prepare_context_at,
+               fpd_prepare_context_rows, fpd_sd_advance, fpd_shared_workspace_bytes, fpd_verify, fpd_verify_prefix,
+               fpd_workspace_bytes, make_layout, shared_context)
 
 _LAYER_KEYS = ("attn_norm", "wqkv", "q_norm", "k_norm", "wo", "mlp_norm", "w_gate_up", "w_down")
 
@@ -27,9 +28,11 @@ def to_device_bf16(a, device) -> torch.Tensor:
 class Drafter:
     """One drafter model on one GPU, sized for up to `max_batch` requests of `t_cap` context positions and
     blocks of up to `max_block_len` positions.  fp8=True adds the 8-bit copies of the streamed matrices
-    (fpd_model_enable_fp8): calls of at most 16 positions then run on them."""
+    (fpd_model_enable_fp8): calls of at most 16 positions then run on them.  max_pos: rotary positions, when contexts go
+    on past t_cap (behind a shared prefix, or after evictions); t_cap + max_block_len by default."""
 
-    def __init__(self, shape, weights, max_batch: int, max_block_len: int, t_cap: int, device="cuda", fp8=False):
+    def __init__(self, shape, weights, max_batch: int, max_block_len: int, t_cap: int, device="cuda", fp8=False,
+                 max_pos=None):
         self.shape = shape
         self.device = torch.device(device)
         self.max_batch, self.max_block_len, self.t_cap = max_batch, max_block_len, t_cap
@@ -37,7 +40,8 @@ class Drafter:
                                                                        "lm_head")}
         self.layers = [{k: to_device_bf16(lw[k], self.device) for k in _LAYER_KEYS} for lw in weights["layers"]]
         desc = ModelDesc(shape.n_layers, shape.d_model, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, shape.d_ff,
-                         shape.vocab, shape.n_feat, t_cap + max_block_len, shape.rms_eps, shape.rope_theta)
+                         shape.vocab, shape.n_feat, max(max_pos or 0, t_cap + max_block_len), shape.rms_eps,
+                         shape.rope_theta)
         W = Weights()
         for k, t in self.w.items():
             setattr(W, k, t.data_ptr())
@@ -111,6 +115,10 @@ class Drafter:
         valid = torch.empty(batch, dtype=torch.int32, device=dev)
         fpd_verify_prefix(batch, block_len, draft, margin, tau, layout, rule, pad_id, accept, committed, valid, stream)
         return accept, committed, valid
+
+    def shared(self, batch, block_len, t_cap, prefix_cap=0, collect=False):
+        """Buffers and calls for a batch of requests behind one shared prefix (see SharedDraft)."""
+        return SharedDraft(self, batch, block_len, t_cap, prefix_cap, collect)
 
     def spec_state(self, batch, block_len, ctx_len, anchor):
         """Device buffers of a text speculative loop (see spec_step), starting from ctx_len / anchor."""
@@ -191,3 +199,89 @@ class SpecState:
     def after_verify(self, stream=None):
         for h in self.hooks:   # callers record per-step results here (e.g. copies into a history buffer)
             h(self)
+
+
+class SharedDraft:
+    """A batch of requests that go on from one shared prefix: the prefix's store (batch 1), the requests' own stores and
+    lengths, the rotary offset of each own store's slot 0, and a workspace for every call below.  collect=True keeps the
+    attention weight that each position has collected over the draft calls, which evict() and evict_prefix() go by.
+
+    Everything runs on torch's current stream, without host synchronisation; the buffers stay where they are, so the
+    calls can be captured in a CUDA graph.  Objects share nothing but the drafter's weights.  Positions reach up to the
+    Drafter's max_pos."""
+
+    def __init__(self, dr, batch, block_len, t_cap, prefix_cap=0, collect=False):
+        s, dev = dr.shape, dr.device
+        self.dr, self.batch, self.block_len, self.t_cap, self.prefix_cap = dr, batch, block_len, t_cap, prefix_cap
+        i32 = dict(dtype=torch.int32, device=dev)
+
+        def store(b, cap):
+            return torch.zeros(s.n_layers, b, 2, s.n_kv_heads, cap, s.head_dim, dtype=torch.bfloat16, device=dev)
+
+        def collected(b, cap):
+            return torch.zeros(s.n_layers, b, s.n_kv_heads, cap, device=dev) if collect and cap else None
+
+        self.kv, self.weights = (store(batch, t_cap) if t_cap else None), collected(batch, t_cap)
+        self.prefix_kv, self.prefix_weights = (store(1, prefix_cap) if prefix_cap else None), collected(1, prefix_cap)
+        self.ctx_len = torch.zeros(batch, **i32)
+        self.pos_offset = torch.zeros(batch, **i32)
+        self.prefix_len, self.prefix_offset = torch.zeros(1, **i32), torch.zeros(1, **i32)
+        n = fpd_shared_workspace_bytes(dr.handle, batch, block_len, prefix_cap, t_cap)
+        for b, cap in ((batch, t_cap), (1, prefix_cap)):
+            if cap:
+                n = max(n, fpd_workspace_bytes(dr.handle, b, 2, cap), fpd_evict_workspace_bytes(s.n_layers, b, s.n_kv_heads, cap))
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        self.context = shared_context(
+            self.prefix_kv, prefix_cap, self.prefix_len if prefix_cap else None, self.kv, t_cap,
+            self.ctx_len if t_cap else None, self.pos_offset, self.weights, self.prefix_weights, accumulate=True)
+
+    def prepare_prefix(self, feats):
+        """Appends target features [rows, d] to the prefix; the requests' positions move behind it.  Call it before the
+        requests have context of their own."""
+        fd = [to_device_bf16(f, self.dr.device) for f in feats]
+        rows = int(fd[0].shape[0])
+        off = torch.tensor([0, rows], dtype=torch.int32, device=self.dr.device)
+        fpd_prepare_context_at(self.dr.handle, 1, rows, off, None, self.prefix_len, self.prefix_offset, fd, self.prefix_kv,
+                               self.prefix_cap, self.workspace, self.workspace.numel())
+        self.prefix_len.add_(rows)
+        self.pos_offset.add_(rows)
+
+    def append(self, row_off, feats):
+        """Appends packed target features to the requests' own contexts: request b's rows are [row_off[b], row_off[b + 1])
+        of every feature tensor (row_off: host sequence)."""
+        fd = [to_device_bf16(f, self.dr.device) for f in feats]
+        off = np.asarray(row_off, np.int32)
+        off_d = torch.from_numpy(off.copy()).to(self.dr.device)
+        self.append_rows(int(off[-1]), off_d, None, self.ctx_len, fd)
+        self.ctx_len.add_(off_d[1:] - off_d[:-1])
+
+    def append_rows(self, total_rows, row_off_d, row_cnt_d, pos_start_d, feats_d):
+        """fpd_prepare_context_at on device arrays, into the own stores at slots pos_start_d (lengths are the caller's to
+        advance, e.g. by fpd_sd_advance)."""
+        fpd_prepare_context_at(self.dr.handle, self.batch, total_rows, row_off_d, row_cnt_d, pos_start_d, self.pos_offset,
+                               feats_d, self.kv, self.t_cap, self.workspace, self.workspace.numel())
+
+    def draft_block(self, anchor, mask_id, hidden_out=None, layer_hidden=None):
+        """One block pass of every request over [prefix ; own context ; block] -> hidden_out [batch * block_len, d]."""
+        if hidden_out is None:
+            hidden_out = torch.empty(self.batch * self.block_len, self.dr.shape.d_model, dtype=torch.bfloat16,
+                                     device=self.dr.device)
+        fpd_draft_block_shared(self.dr.handle, self.batch, self.block_len, self.context, anchor, mask_id, hidden_out,
+                               layer_hidden, self.workspace, self.workspace.numel())
+        return hidden_out
+
+    def _evict(self, batch, cap, kv, weights, lens, offset, budget, recent, kept):
+        if weights is None:
+            raise ValueError("eviction needs the weights that collect=True keeps")
+        s = self.dr.shape
+        fpd_evict_context(s.n_layers, batch, s.n_kv_heads, s.head_dim, budget, recent, kv, cap, weights, lens, kv, cap,
+                          weights, lens, offset, kept, self.workspace, self.workspace.numel())
+
+    def evict(self, budget, recent, kept=None):
+        """Shrinks every own context to at most `budget` positions, in place."""
+        self._evict(self.batch, self.t_cap, self.kv, self.weights, self.ctx_len, self.pos_offset, budget, recent, kept)
+
+    def evict_prefix(self, budget, recent, kept=None):
+        """Shrinks the shared prefix to at most `budget` positions, in place."""
+        self._evict(1, self.prefix_cap, self.prefix_kv, self.prefix_weights, self.prefix_len, self.prefix_offset, budget,
+                    recent, kept)

@@ -334,6 +334,104 @@ typedef struct fpd_grid_format {
 fpd_status fpd_grid_to_text(int batch, int block_len, const int32_t* committed, const int32_t* accept,
                             const fpd_grid_format* fmt, char* out, size_t out_bytes, size_t* offsets);
 
+/* ---- a batch behind a shared prefix, and a context store that stays inside a budget --------------------------------
+ * Several blocks are often drafted for one scene: the requests' contexts start with the same positions (the scene) and
+ * go on differently.  A prefix store holds the common part once ([layer][1][K|V][kv_head][prefix_cap][head_dim], written
+ * by fpd_prepare_context with batch 1); each request's own store holds what follows.  And a store that grows with every
+ * accepted block fills up: each position's collected attention weight tells which positions the blocks still look at,
+ * and eviction keeps those.  After either, a position's slot in a store is no longer its rotary position: pos_offset
+ * [batch] gives the rotary position of slot 0 (slot i of request b continues at pos_offset[b] + i), so keys that have
+ * been rotated stay as they are and new positions go on where the sequence is.
+ *
+ * The operators take one layer of a store and need no model; fpd_draft_block_shared is the block pass built from them.
+ * Lengths live on the device.  Lengths outside their store are clamped and recorded (FPD_CHECK_BAD_CONTEXT).
+ * Calls that share a workspace must not overlap on the GPU.
+ *
+ * fpd_shared_attention: for every query row (b, j) and head i of kv head g = i / (n_q_heads / n_kv_heads), over the keys t of
+ *   [prefix 0..prefix_len) ; request b's context 0..ctx_len[b) ; its block 0..block_len)
+ *   lse = log sum_t exp(q . k_t / sqrt(h)),   out = sum_t exp(q . k_t / sqrt(h) - lse) v_t        (no mask)
+ * A row without any key (all lengths 0, no block keys) gives out 0 and lse -inf.  Sums are fp32, the softmax weights enter
+ * the second product as two bf16 terms (about 2^-17), out is rounded once.  Supported: head_dim 64 or 128,
+ * batch * block_len * n_q_heads <= 2^26, capacities <= 2^30.
+ *   q              device [batch * block_len, n_q_heads, h] bf16, normed and rotated
+ *   k_blk, v_blk   device [batch, n_kv_heads, block_len, h] bf16, or both NULL: no block keys
+ *   prefix_store   layer `layer` of it is read; NULL with prefix_cap 0 and prefix_len NULL: no prefix
+ *   prefix_len     device [1]
+ *   kv_store       layer `layer` of the batch's own store ([layer][batch][K|V][kv_head][t_cap][h]); NULL with t_cap 0 and
+ *                  ctx_len NULL: no own context
+ *   out            device [batch * block_len, n_q_heads, h] bf16
+ *   lse            device [batch * block_len, n_q_heads] fp32 (natural logarithm) or NULL
+ *   workspace      fpd_shared_attention_workspace_bytes bytes for the same sizes on the current device */
+fpd_status fpd_shared_attention(int batch, int block_len, int n_q_heads, int n_kv_heads, int head_dim, int layer,
+                                const void* q, const void* k_blk, const void* v_blk, const void* prefix_store,
+                                int prefix_cap, const int32_t* prefix_len, const void* kv_store, int t_cap,
+                                const int32_t* ctx_len, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream);
+/* Asks the current device for its SM count; 0 for sizes that the call refuses or without a device. */
+size_t fpd_shared_attention_workspace_bytes(int batch, int block_len, int n_q_heads, int n_kv_heads, int head_dim,
+                                            int prefix_cap, int t_cap);
+
+/* The attention weight that each context position collects from a block's rows, for one layer:
+ *   w[b][g][t] = sum over j and the heads i of kv head g of exp(q[b,j,i] . k_t / sqrt(h) - lse[b,j,i]),  t < ctx_len[b]
+ * written to (accumulate 0) or added to (otherwise) weights[layer][b][g][t]; entries from ctx_len[b] on stay as they are.
+ * With the lse of the attention over all keys a row hands out a total of 1.  Rows with lse -inf (no key) give nothing.  A
+ * shared prefix collects from all requests: batch 1, block_len = the batch's rows, the prefix store and its length.
+ *   lse       device [batch * block_len, n_q_heads] fp32
+ *   weights   device [n_layers > layer][batch][n_kv_heads][t_cap] fp32 */
+fpd_status fpd_context_weights(int batch, int block_len, int n_q_heads, int n_kv_heads, int head_dim, int layer,
+                               const void* q, const float* lse, const void* kv_store, int t_cap, const int32_t* ctx_len,
+                               float* weights, int accumulate, void* stream);
+
+/* Eviction to at most `budget` positions per request.  Where ctx_len[b] > budget, every layer and kv head keeps the last
+ * `recent` positions and, of the others, the budget - recent with the largest weight (ties: the lower position; NaN counts
+ * below every number), in the order of their positions; otherwise it keeps all.  With m = min(ctx_len[b], budget):
+ *   out_store[l][b][K|V][g][i] = kv_store[...][kept_i], out_weights[l][b][g][i] = weights[l][b][g][kept_i]   for i < m
+ *   out_weights[l][b][g][i] = 0 for m <= i < out_cap (positions still to come start from 0); K/V rows from m on stay
+ *   out_len[b] = m;  pos_offset[b] += ctx_len[b] - m
+ * Heads keep different positions but equally many.  Needs 0 <= recent <= budget <= out_cap.
+ *   out_store, out_weights, out_cap   another store, or all three those of kv_store: in place.  Other overlap is refused.
+ *   out_len      device [batch]; may be ctx_len
+ *   pos_offset   device [batch] (in/out) or NULL
+ *   kept         device [n_layers][batch][n_kv_heads][budget] int32 or NULL: the kept positions, -1 from m on
+ *   workspace    fpd_evict_workspace_bytes bytes */
+fpd_status fpd_evict_context(int n_layers, int batch, int n_kv_heads, int head_dim, int budget, int recent, const void* kv_store,
+                             int t_cap, const float* weights, const int32_t* ctx_len, void* out_store, int out_cap,
+                             float* out_weights, int32_t* out_len, int32_t* pos_offset, int32_t* kept, void* workspace,
+                             size_t workspace_bytes, void* stream);
+size_t fpd_evict_workspace_bytes(int n_layers, int batch, int n_kv_heads, int budget);
+
+/* fpd_prepare_context_rows with rotary positions of their own: row i of request b goes to slot pos_start[b] + i and is
+ * rotated for position pos_offset[b] + pos_start[b] + i, which must lie in [0, max_pos) (else the row is skipped and
+ * FPD_CHECK_BAD_POSITION recorded).  t_cap may then exceed max_pos.
+ *   pos_offset  device [batch] */
+fpd_status fpd_prepare_context_at(fpd_model* model, int batch, int total_rows, const int32_t* row_off,
+                                  const int32_t* row_cnt, const int32_t* pos_start, const int32_t* pos_offset,
+                                  const void* const* feats, void* kv_store, int t_cap, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* What a block attends to.  A capacity of 0 with its pointers NULL leaves that store out. */
+typedef struct fpd_shared_context {
+  const void* prefix_store;      /* [n_layers][1][K|V][kv_head][prefix_cap][h] */
+  int32_t prefix_cap;
+  const int32_t* prefix_len;     /* device [1] */
+  const void* kv_store;          /* [n_layers][batch][K|V][kv_head][t_cap][h] */
+  int32_t t_cap;
+  const int32_t* ctx_len;        /* device [batch] */
+  const int32_t* pos_offset;     /* device [batch] or NULL: prefix_len (0 without a prefix) */
+  float* weights;                /* device [n_layers][batch][kv_head][t_cap] or NULL: collected weight of the own context */
+  float* prefix_weights;         /* device [n_layers][1][kv_head][prefix_cap] or NULL */
+  int32_t accumulate;            /* 0: write the weights, else add to them */
+} fpd_shared_context;
+
+/* fpd_draft_block over a shared context: the same block pass, block position j of request b at rotary position
+ * pos_offset[b] + ctx_len[b] + j (clamped to the rotary table of max_pos positions, FPD_CHECK_BAD_CONTEXT recorded when it
+ * lies outside), attending to prefix, own context and block; optionally collects the context weights of every layer.
+ *   workspace  fpd_shared_workspace_bytes bytes (enough for any smaller batch and block length too) */
+fpd_status fpd_draft_block_shared(fpd_model* model, int batch, int block_len, const fpd_shared_context* ctx,
+                                  const int32_t* anchor, int32_t mask_id, void* hidden_out, void* layer_hidden,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+size_t fpd_shared_workspace_bytes(const fpd_model* model, int batch, int max_block_len, int prefix_cap, int t_cap);
+
 /* ---- diagnostics ---------------------------------------------------------------------------------------- */
 const char* fpd_last_error(void);          /* thread-local message of the last failing call */
 uint64_t fpd_kernel_launches(void);        /* kernels launched by this library since load (all threads) */

@@ -1,0 +1,115 @@
+"""CPU: what the operators on a context store refuse before they touch the device, their workspace sizes, and the
+reference's own selection rule."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import context_ops_ref as ref
+
+
+@pytest.fixture(scope="module")
+def fpd():
+    import __graft_entry__ as g
+    g._compile_all()
+    import block_diffusion_speculative_non_gb300 as pkg
+    return pkg
+
+
+A = 1 << 20   # an address that is never dereferenced
+
+
+def attn(fpd, **kw):
+    a = dict(batch=2, block=4, nq=8, nkv=2, h=64, layer=0, q=A, kb=A, vb=A, pre=A, p_cap=16, p_len=A, kv=A, t_cap=8, c_len=A,
+             out=A, lse=A, ws=A, n=1 << 30)
+    a.update(kw)
+    return fpd.lib().fpd_shared_attention(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=0), 2), (dict(block=0), 2), (dict(h=96), 4), (dict(nq=7), 2), (dict(nkv=0), 2), (dict(nq=1, nkv=2), 2),
+    (dict(layer=-1), 2), (dict(p_cap=-1), 2), (dict(t_cap=-1), 2), (dict(p_cap=(1 << 30) + 1), 2),
+    (dict(batch=1 << 20, block=1 << 12), 2), (dict(batch=1 << 14, block=1 << 10, nq=8), 2),
+    (dict(q=None), 1), (dict(out=None), 1), (dict(ws=None), 1), (dict(vb=None), 1), (dict(kb=None), 1),
+    (dict(pre=None), 1), (dict(p_len=None), 1), (dict(p_cap=0), 1), (dict(p_cap=0, pre=None), 1),
+    (dict(kv=None), 1), (dict(c_len=None), 1), (dict(t_cap=0), 1),
+    (dict(q=A + 8), 1), (dict(out=A + 2), 1), (dict(kv=A + 4), 1), (dict(ws=A + 8), 1), (dict(kb=A + 2), 1),
+])
+def test_shared_attention_refuses(fpd, kw, status):
+    assert attn(fpd, **kw) == status, fpd.fpd_last_error()
+    assert fpd.fpd_last_error()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=0), 2), (dict(h=32), 4), (dict(nq=3), 2), (dict(t_cap=0), 2), (dict(layer=-2), 2), (dict(q=None), 1),
+    (dict(lse=None), 1), (dict(kv=None), 1), (dict(c_len=None), 1), (dict(w=None), 1), (dict(q=A + 2), 1), (dict(w=A + 4), 1),
+    (dict(batch=1 << 10, block=1, t_cap=1 << 30), 2),
+])
+def test_context_weights_refuses(fpd, kw, status):
+    a = dict(batch=2, block=4, nq=8, nkv=2, h=64, layer=0, q=A, lse=A, kv=A, t_cap=8, c_len=A, w=A, acc=0)
+    a.update(kw)
+    assert fpd.lib().fpd_context_weights(*a.values(), None) == status, fpd.fpd_last_error()
+
+
+FAR = 1 << 40
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(layers=0), 2), (dict(batch=0), 2), (dict(nkv=0), 2), (dict(h=80), 4), (dict(budget=0), 2), (dict(recent=-1), 2),
+    (dict(recent=9), 2), (dict(budget=17, recent=0), 2), (dict(t_cap=0), 2), (dict(out_cap=0), 2),
+    (dict(kv=None), 1), (dict(w=None), 1), (dict(c_len=None), 1), (dict(out=None), 1), (dict(ow=None), 1),
+    (dict(on=None), 1), (dict(ws=None), 1), (dict(kv=A + 8), 1), (dict(kept=A + 4), 1),
+    (dict(n=16), 3), (dict(n=300, kept=A), 3),
+    (dict(out=A), 1),                                   # store in place, weights not
+    (dict(ow=A * 2), 1),                                # weights in place, store not
+    (dict(out=A, ow=A * 2), 1),                         # in place with another capacity
+    (dict(out=A + 4096), 1), (dict(ow=A * 2 + 16), 1),   # overlapping, not in place
+])
+def test_evict_refuses(fpd, kw, status):
+    a = dict(layers=2, batch=2, nkv=2, h=64, budget=8, recent=2, kv=A, t_cap=32, w=A * 2, c_len=A * 3, out=FAR, out_cap=16,
+             ow=2 * FAR, on=A * 3, off=None, kept=None, ws=3 * FAR, n=1 << 20)
+    a.update(kw)
+    assert fpd.lib().fpd_evict_context(*a.values(), None) == status, fpd.fpd_last_error()
+
+
+def test_model_calls_refuse(fpd):
+    l = fpd.lib()
+    feats = (ctypes.c_void_p * 1)(A)
+    assert l.fpd_prepare_context_at(None, 1, 1, A, None, None, A, feats, A, 8, A, 1, None) == 1
+    assert l.fpd_prepare_context_at(None, 1, 1, A, None, None, None, feats, A, 8, A, 1, None) == 1
+    assert l.fpd_draft_block_shared(None, 1, 16, ctypes.byref(fpd.shared_context()), A, 0, A, None, A, 1, None) == 1
+    assert l.fpd_draft_block_shared(None, 1, 16, None, A, 0, A, None, A, 1, None) == 1
+    assert l.fpd_shared_workspace_bytes(None, 1, 16, 8, 8) == 0
+
+
+def test_workspace_sizes_of_refused_calls_are_zero(fpd):
+    assert fpd.fpd_shared_attention_workspace_bytes(0, 1, 8, 2, 64, 8, 8) == 0
+    assert fpd.fpd_shared_attention_workspace_bytes(1, 1, 8, 2, 65, 8, 8) == 0
+    assert fpd.fpd_shared_attention_workspace_bytes(1, 1, 8, 2, 64, -1, 8) == 0
+    assert fpd.fpd_evict_workspace_bytes(0, 1, 2, 8) == 0
+    assert fpd.fpd_evict_workspace_bytes(5, 3, 8, 100) >= 5 * 3 * 8 * 100 * 4 + 12
+
+
+def test_binding_checks_tensors(fpd):
+    """Type, layout and size of a tensor are checked before its address is used."""
+    import torch
+    with pytest.raises(ValueError, match="must be torch.bfloat16"):
+        fpd._arg(torch.zeros(4), "bfloat16", 4, "q")
+    with pytest.raises(ValueError, match="contiguous"):
+        fpd._arg(torch.zeros(4, 4).t(), "float32", 4, "lse")
+    assert fpd._arg(None, "int32", 4, "ctx_len") is None and fpd._arg(64, "int32", 4, "ctx_len") == 64
+
+
+def test_selection_rule_of_the_reference():
+    nan, inf = float("nan"), float("inf")
+    assert ref.kept_positions([5, 1, 3, 2], 4, 4, 0) == [0, 1, 2, 3]
+    assert ref.kept_positions([5, 1, 3, 2], 4, 2, 0) == [0, 2]
+    assert ref.kept_positions([5, 1, 3, 2], 4, 2, 1) == [0, 3]
+    assert ref.kept_positions([1, 1, 1, 1], 4, 2, 0) == [0, 1]          # ties: the lower position
+    assert ref.kept_positions([nan, -inf, 0.0, -0.0, inf], 5, 3, 0) == [2, 3, 4]
+    assert ref.kept_positions([nan, -inf, nan], 3, 2, 0) == [0, 1]      # NaN below -inf
+    assert ref.kept_positions([9, 9, 9], 3, 2, 2) == [1, 2]
+    out, w, n, kept = ref.evict(np.arange(8, dtype=np.int16).reshape(1, 1, 2, 1, 4, 1), np.array([[[[3, 1, 2, 0]]]], np.float32),
+                                [4], 2, 0, np.zeros((1, 1, 2, 1, 2, 1), np.int16), 2)
+    assert out.reshape(2, 2).tolist() == [[0, 2], [4, 6]] and w.tolist() == [[[[3, 2]]]] and n.tolist() == [2]
+    assert kept.tolist() == [[[[0, 2]]]]
