@@ -620,7 +620,8 @@ static SharedWs carve_shared(const Model& m, Carver& c, int B, int L, int p_cap,
   const size_t n_out = (size_t)B * L * d.n_q_heads;
   w.base = c.take<int32_t>(B);
   w.lse = c.take<float>(n_out);
-  w.o_part = c.take<float>(n_out * w.plan.splits() * d.head_dim);
+  w.o_part = c.take<float>(n_out * w.plan.splits() * d.head_dim + 8);
+  w.o_part = (float*)align_up((uintptr_t)w.o_part, 32);   // the workspace itself is 16-byte aligned
   w.ml = c.take<float2>(n_out * w.plan.splits());
   return w;
 }

@@ -66,10 +66,11 @@ AttnWs carve(void* base, int batch, int L, int nq, int nkv, int h, int p_cap, in
   AttnWs w{};
   w.plan = shared_attn_plan(batch, L, L, nq, nkv, h, p_cap, t_cap, sms);
   const size_t n = (size_t)batch * L * nq * w.plan.splits();
+  const size_t lead = align_up((uintptr_t)base, 256) - (uintptr_t)base;   // the workspace itself is 16-byte aligned
   const size_t ml_at = align_up(n * h * sizeof(float), 256);
-  w.o_part = (float*)base;
-  w.ml = (float2*)((char*)base + ml_at);
-  w.bytes = ml_at + n * sizeof(float2);
+  w.o_part = (float*)((char*)base + lead);
+  w.ml = (float2*)((char*)base + lead + ml_at);
+  w.bytes = 256 + ml_at + n * sizeof(float2);
   return w;
 }
 

@@ -19,20 +19,24 @@ struct SharedAttn {
   const int32_t *prefix_len, *ctx_len;  // device [1], [batch]
   bf16* out;                            // [rows][nq][h]
   float* lse;                           // [rows][nq] or null
-  float* o_part;                        // [splits][rows][nq][h]
+  float* o_part;                        // [splits][rows][nq][h], 32-byte aligned
   float2* ml;                           // [splits][rows][nq]: running maximum (base 2) and sum
   int batch, L, lb, nq, nkv, h, p_cap, t_cap, rows;   // lb: keys of the block, L or 0; rows = batch * L
 };
 
-// How the (row tile, keys) work of a call is cut: a prefix unit is one tile of all requests' rows of a kv head over one
-// split of the prefix, an own unit one tile of a request's rows over one split of its context and block keys.
+// How the work of a call is cut.  The prefix part has the rows of all requests per kv head, the own part one request's;
+// each goes to tcgen05 (units of 256 rows, k_attention_shared_tc.cu) or to mma.sync (tiles of 64 rows).
 struct SharedPlan {
-  bool pre_tc, own_tc;                  // tensor-memory kernel for that part (else mma.sync)
-  int pre_tiles, pre_splits, own_tiles, own_splits;
+  bool pre_tc, own_tc;
+  int pre_tiles, pre_splits;            // row units of a kv head (0: no such part), partials of a row
+  int own_tiles, own_splits;            // the same per request
+  int pre_runs, tc_grid;                // CTAs that share the prefix's tiles, CTAs of the tcgen05 kernel
   int splits() const { return pre_splits + own_splits; }
 };
 SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms);
 cudaError_t shared_attn_init_attributes();
+cudaError_t shared_attn_tc_init_attributes();
+cudaError_t launch_shared_tc(const SharedAttn& a, const SharedPlan& pl, cudaStream_t st);
 cudaError_t launch_shared_attention(const SharedAttn& a, const SharedPlan& pl, cudaStream_t st);
 
 // weights[b][g][t] (+)= sum over the request's rows of kv head g of exp(q . k_t / sqrt(h) - lse)

@@ -6,6 +6,7 @@
 // each prefix key is read once per kv head and row tile instead of once per request.  The own context and the block
 // are the ordinary attention of one request.  Both parts leave unnormalised partials (o, m, l) per split of their keys;
 // the softmax of a row is put together from them in split order (deterministic, no atomics).
+#include <cstdlib>
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
 
@@ -161,60 +162,74 @@ __global__ void __launch_bounds__(NWARP * 32) shared_mma_kernel(const __grid_con
   }
 }
 
-// The softmax of one (row, head) from its partials, one warp: M = max m_s over the partials that hold a key
-// (l_s != 0; a NaN sum counts, so that it reaches the output), den = sum l_s 2^(m_s - M), out = sum o_s 2^(m_s - M) / den,
-// lse = (M + log2 den) ln 2.  Partials in split order: bit-reproducible.
-template <int H>
+// The softmax of one (row, head) from its partials: M = max m_s over the partials that hold a key (l_s != 0; a NaN sum
+// counts, so that it reaches the output), den = sum l_s 2^(m_s - M), out = sum o_s 2^(m_s - M) / den,
+// lse = (M + log2 den) ln 2.  W warps share an output and take every W-th partial, eight at a time, so that the reads of
+// many partials do not queue behind one another; the warps' sums are added in warp order: bit-reproducible.
+template <int H, int W>
 __global__ void __launch_bounds__(256) shared_merge_kernel(bf16* __restrict__ out, float* __restrict__ lse,
                                                            const float* __restrict__ o_part, const float2* __restrict__ ml,
                                                            int nsplit, int n_out) {
   pdl_wait();
   pdl_trigger();
   constexpr int DPL = H / 32;
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= n_out) return;
+  __shared__ float part[8][H];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
+  const int r = blockIdx.x * (8 / W) + warp / W;
+  const bool ok = r < n_out;
   float mx = -INFINITY;
-  for (int s0 = 0; s0 < nsplit; s0 += 32) {
-    const int s = s0 + lane;
-    const float2 v = s < nsplit ? __ldcg(ml + (size_t)s * n_out + r) : make_float2(-INFINITY, 0.f);
+  for (int s0 = 0; ok && s0 < nsplit; s0 += 32) {
+    const float2 v = s0 + lane < nsplit ? __ldcg(ml + (size_t)(s0 + lane) * n_out + r) : make_float2(-INFINITY, 0.f);
     mx = fmaxf(mx, warp_max(v.y == 0.f ? -INFINITY : v.x));
   }
   float den = 0.f, num[DPL];
 #pragma unroll
   for (int e = 0; e < DPL; e++) num[e] = 0.f;
-  for (int s0 = 0; s0 < nsplit; s0 += 8) {
-    float t[8][DPL], wgt[8];
+  for (int s0 = 0; ok && s0 < nsplit; s0 += 32) {
+    const float2 v = s0 + lane < nsplit ? __ldcg(ml + (size_t)(s0 + lane) * n_out + r) : make_float2(-INFINITY, 0.f);
+    const float wl = v.y == 0.f ? 0.f : exp2f(v.x - mx);   // lane s: weight of partial s0 + s
+    den += warp_sum(v.y == 0.f ? 0.f : v.y * wl);
+    const float* op = o_part + ((size_t)s0 * n_out + r) * H + lane * DPL;
+    for (int u0 = w; u0 < min(32, nsplit - s0); u0 += 8 * W) {
+      float t[8][DPL], wgt[8];
 #pragma unroll
-    for (int u = 0; u < 8; u++) {
-      const int s = s0 + u;
-      wgt[u] = 0.f;
+      for (int u = 0; u < 8; u++) {
+        const int s = u0 + u * W;
+        wgt[u] = __shfl_sync(0xffffffffu, wl, s & 31);
+        if (s >= 32 || s0 + s >= nsplit) wgt[u] = 0.f;
 #pragma unroll
-      for (int e = 0; e < DPL; e++) t[u][e] = 0.f;
-      if (s < nsplit) {
-        const float2 v = __ldcg(ml + (size_t)s * n_out + r);
-        if (v.y != 0.f) {
-          wgt[u] = exp2f(v.x - mx);
-          den += v.y * wgt[u];
-          const float* op = o_part + ((size_t)s * n_out + r) * H + lane * DPL;
+        for (int e = 0; e < DPL; e++) t[u][e] = 0.f;
+        if (wgt[u] != 0.f) {
           if constexpr (DPL == 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(op));
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(op + (size_t)s * n_out * H));
             t[u][0] = f.x;
             t[u][1] = f.y;
             t[u][2] = f.z;
             t[u][3] = f.w;
           } else {
-            const float2 f = __ldcg(reinterpret_cast<const float2*>(op));
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(op + (size_t)s * n_out * H));
             t[u][0] = f.x;
             t[u][1] = f.y;
           }
         }
       }
+#pragma unroll
+      for (int u = 0; u < 8; u++)
+#pragma unroll
+        for (int e = 0; e < DPL; e++) num[e] += wgt[u] != 0.f ? t[u][e] * wgt[u] : 0.f;
     }
-#pragma unroll
-    for (int u = 0; u < 8; u++)
-#pragma unroll
-      for (int e = 0; e < DPL; e++) num[e] += wgt[u] != 0.f ? t[u][e] * wgt[u] : 0.f;
   }
+  if (W > 1) {
+#pragma unroll
+    for (int e = 0; e < DPL; e++) part[warp][lane * DPL + e] = num[e];
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int k = 1; k < W; k++)
+#pragma unroll
+      for (int e = 0; e < DPL; e++) num[e] += part[warp + k][lane * DPL + e];
+  }
+  if (!ok) return;
   const bool none = den == 0.f;   // no key at all (or every score -inf): output 0, lse -inf
   bf16* dst = out + (size_t)r * H + lane * DPL;
 #pragma unroll
@@ -222,6 +237,18 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(bf16* __restrict__ ou
     *reinterpret_cast<__nv_bfloat162*>(dst + e) =
         __floats2bfloat162_rn(none ? 0.f : num[e] / den, none ? 0.f : num[e + 1] / den);
   if (lse && lane == 0) lse[r] = none ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
+}
+
+template <int H>
+cudaError_t launch_merge(const SharedAttn& a, int nsplit, cudaStream_t st) {
+  const int n_out = a.rows * a.nq;
+  auto go = [&](auto* k, int w) {
+    return launch_k(k, ceil_div(n_out, 8 / w), 256, 0, st, a.out, a.lse, (const float*)a.o_part, (const float2*)a.ml, nsplit, n_out);
+  };
+  // up to 8 partials are one round of loads for a warp; many outputs fill the GPU with one warp each
+  if (nsplit <= 8 || n_out >= 65536) return go(shared_merge_kernel<H, 1>, 1);
+  if (nsplit <= 16) return go(shared_merge_kernel<H, 2>, 2);
+  return nsplit <= 32 ? go(shared_merge_kernel<H, 4>, 4) : go(shared_merge_kernel<H, 8>, 8);
 }
 
 __global__ void rope_base_kernel(int32_t* base, const int32_t* ctx_len, const int32_t* prefix_len, const int32_t* pos_offset,
@@ -237,32 +264,69 @@ __global__ void rope_base_kernel(int32_t* base, const int32_t* ctx_len, const in
 
 }  // namespace
 
-// Splits: with `base` row tiles times heads and n key tiles each, a part has base * s CTAs of about n / s tiles.  The
-// total time of both parts is close to waves * (tiles per CTA + c) where c is what a CTA pays besides its tiles (Q,
-// the partial out, its share of the merge); the smallest such cost over tile counts per CTA wins, ties to fewer splits.
-SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms) {
-  SharedPlan pl{};
-  const int grp = nq / nkv, rows = batch * L;
-  const int pre_kt = ceil_div(p_cap, KT), own_kt = ceil_div(t_cap + lb, KT);
-  pl.pre_tiles = p_cap ? ceil_div(rows * grp, QT) : 0;
-  pl.own_tiles = t_cap + lb ? ceil_div(L * grp, QT) : 0;
-  const long pre_base = (long)pl.pre_tiles * nkv, own_base = (long)pl.own_tiles * nkv * batch;
-  const int slots = 2 * num_sms, most = std::max(pre_kt, own_kt);
+// Split count of a part on the 64-row kernel, `base` row tiles times heads and kt key tiles each, for `slots` resident CTAs:
+// the time is close to waves * (tiles per CTA + c), c what a CTA pays besides its tiles (Q, the partial out, its share
+// of the merge); the smallest cost wins, ties to fewer splits.
+static int mma_splits(long base, int kt, int slots) {
   double best = 0;
-  int best_w = std::max(most, 1);
-  for (int w = most; w >= 1; w = w > 16 ? w - std::max(1, w / 16) : w - 1) {
-    const long sp = ceil_div(pre_kt, w), so = ceil_div(own_kt, w);
-    if (sp > 128 || so > 128) break;
-    const long units = pre_base * sp + own_base * so;
-    const double waves = units <= slots ? 1.0 : (double)units / slots;
-    const double cost = waves * (w + 2);
-    if (w == most || cost < best) {
+  int best_s = 1;
+  for (int s = 1; s <= std::min(kt, 128); s = s < 16 ? s + 1 : s + s / 16) {
+    const long units = base * s;
+    const double cost = (units <= slots ? 1.0 : (double)units / slots) * (ceil_div(kt, s) + 2);
+    if (s == 1 || cost < best) {
       best = cost;
-      best_w = w;
+      best_s = s;
     }
   }
-  pl.pre_splits = pl.pre_tiles ? ceil_div(pre_kt, best_w) : 0;
-  pl.own_splits = pl.own_tiles ? ceil_div(own_kt, best_w) : 0;
+  return best_s;
+}
+
+SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms) {
+  SharedPlan pl{};
+  const int grp = nq / nkv, pre_rows = batch * L * grp, own_rows = L * grp, own_keys = t_cap + lb;
+  // rows of the tensor maps are 32-bit coordinates
+  const bool own_tma = (long long)batch * 2 * nkv * t_cap < INT32_MAX && (long long)batch * nkv * lb < INT32_MAX;
+  const bool pre_tma = (long long)2 * nkv * p_cap < INT32_MAX;
+  pl.pre_tc = p_cap && pre_tma && !getenv("FPD_MMA");
+  pl.own_tc = own_keys && own_tma && !getenv("FPD_MMA") && !getenv("FPD_MMA_OWN");
+  pl.pre_tiles = p_cap ? ceil_div(pre_rows, pl.pre_tc ? 256 : QT) : 0;
+  pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 256 : QT) : 0;
+  const long pre_units = (long)pl.pre_tiles * nkv, own_units = (long)pl.own_tiles * nkv * batch;
+  const int pre_kt = ceil_div(p_cap, 128), own_kt = ceil_div(t_cap, 128) + ceil_div(lb, 128);
+  if (pl.pre_tiles && !pl.pre_tc) pl.pre_splits = mma_splits(pre_units, ceil_div(p_cap, KT), 2 * num_sms);
+  if (pl.own_tiles && !pl.own_tc) pl.own_splits = mma_splits(own_units, ceil_div(own_keys, KT), 2 * num_sms);
+  if (pl.own_tc) {
+    pl.own_splits = 2;
+    if (!pl.pre_tc) pl.own_splits *= (int)std::max(1l, std::min<long>(own_kt / 2, num_sms / own_units));
+  }
+  const long own_segs = pl.own_tc ? own_units * (pl.own_splits / 2) : 0;
+  if (pl.pre_tc) {
+    // Either one even run per SM, which may span units, or s runs per unit.  A run costs about kSeg besides its tiles (Q, the
+    // first copies, the partial out); a partial is written and read once.  The time is the longest run's or, with the own
+    // part's runs, the average over the SMs, and the merge's reads.
+    const bool pair = pre_rows > 128;
+    const double kTile = (pair ? 2.2 : 1.1) * h / 128, kOwn = 1.1 * h / 128, kSeg = 5.0;   // us
+    const double part_us = (double)batch * L * nq * h * 8 / 3e6;                            // us per partial of every row
+    const double own_us = own_segs * (kSeg + kOwn * own_kt);
+    const long total = pre_units * pre_kt;
+    double best = 0;
+    auto consider = [&](long runs, double run_us, double pieces) {
+      const double cost = std::max(run_us, (runs * run_us + own_us) / num_sms) + pieces * part_us;
+      if (!pl.pre_runs || cost < best) {
+        best = cost;
+        pl.pre_runs = (int)runs;
+      }
+    };
+    for (long s = 1; s <= pre_kt && (s == 1 || pre_units * s <= num_sms); s++)
+      if (pre_units * s <= num_sms) consider(pre_units * s, kSeg + kTile * ceil_div(pre_kt, (int)s), s);
+    if (total >= num_sms) consider(num_sms, 2 * kSeg + kTile * total / num_sms, (double)num_sms / pre_units + 1);
+    // a unit's tiles span at most ceil(runs / units) + 1 of the even runs (one less when the runs divide evenly), and no
+    // more runs than it has tiles; a unit of at most 128 rows leaves two partials per run
+    const int pieces = (int)ceil_div(pl.pre_runs, (int)pre_units) + (pl.pre_runs % pre_units ? 1 : 0);
+    pl.pre_splits = std::min(pre_kt, pieces);
+    if ((pre_rows - 1) % 256 < 128) pl.pre_splits *= 2;
+  }
+  if (pl.pre_tc || pl.own_tc) pl.tc_grid = (int)std::min<long>(num_sms, pl.pre_runs + own_segs);
   return pl;
 }
 
@@ -271,22 +335,20 @@ cudaError_t shared_attn_init_attributes() {
                                        (int)sizeof(Smem<128>));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(shared_mma_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<64>));
+  if (e == cudaSuccess) e = shared_attn_tc_init_attributes();
   return e;
 }
 
 cudaError_t launch_shared_attention(const SharedAttn& a, const SharedPlan& pl, cudaStream_t st) {
-  const int pre_units = pl.pre_tiles * a.nkv * pl.pre_splits;
-  const int units = pre_units + pl.own_tiles * a.nkv * a.batch * pl.own_splits;
+  const int pre_units = pl.pre_tc ? 0 : pl.pre_tiles * a.nkv * pl.pre_splits;
+  const int units = pre_units + (pl.own_tc ? 0 : pl.own_tiles * a.nkv * a.batch * pl.own_splits);
   cudaError_t e = cudaSuccess;
   if (units > 0)
     e = a.h == 128 ? launch_k(shared_mma_kernel<128>, units, NWARP * 32, sizeof(Smem<128>), st, a, pl, pre_units)
                    : launch_k(shared_mma_kernel<64>, units, NWARP * 32, sizeof(Smem<64>), st, a, pl, pre_units);
+  if (e == cudaSuccess && pl.tc_grid) e = launch_shared_tc(a, pl, st);
   if (e != cudaSuccess) return e;
-  const int n_out = a.rows * a.nq, blocks = ceil_div(n_out, 8);
-  return a.h == 128 ? launch_k(shared_merge_kernel<128>, blocks, 256, 0, st, a.out, a.lse, (const float*)a.o_part,
-                               (const float2*)a.ml, pl.splits(), n_out)
-                    : launch_k(shared_merge_kernel<64>, blocks, 256, 0, st, a.out, a.lse, (const float*)a.o_part,
-                               (const float2*)a.ml, pl.splits(), n_out);
+  return a.h == 128 ? launch_merge<128>(a, pl.splits(), st) : launch_merge<64>(a, pl.splits(), st);
 }
 
 cudaError_t launch_rope_base(int32_t* base, const int32_t* ctx_len, const int32_t* prefix_len, const int32_t* pos_offset,
