@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           nq[t]++;
         }
         tc::tc_fence_after();
-        // Every wait but the one for P is done while the tensor core still has work, and the release of a slot follows the
-        // issue behind it: between a lane's P and its product stands nothing but that wait.
+        // Between a lane's P and its product stands nothing but the wait for P: a pair's other waits are done while the tensor
+        // core still has work.
         if (!sg.keys) {
           // a lane's next S follows its own product, so no lane waits for the other's softmax
           if (ok && (ok = wait_k(n0))) {
@@ -389,13 +389,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             issue_s(1, k0);
             commit_if(on, bar(B_KE + k0));
           }
-          if (ok) ok = wait_v(n0) && (nt < 2 || wait_k(n0 + 1));
+          if (ok) ok = wait_v(n0);
           for (int i = 0; i < nt && ok && !*abort_flag; i++) {
             const int n = n0 + i, vs = uni(n % VST), ks = uni((n + 1) % KST), acc = uni(i > 0);
             const bool more = i + 1 < nt;
             if (!(ok = pv(0, vs, acc))) break;
-            if (more && !(ok = wait_v(n + 1) && (i + 2 >= nt || wait_k(n + 2)))) break;
-            if (more) issue_s(0, ks);
+            if (more) {   // these copies started a whole tile ago
+              if (!(ok = wait_k(n + 1) && wait_v(n + 1))) break;
+              tc::tc_fence_after();
+              issue_s(0, ks);
+            }
             if (!(ok = pv(1, vs, acc))) break;
             commit_if(on, bar(B_VE + vs));
             if (more) {
@@ -411,14 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             issue_s(i, ks);
             commit_if(on, bar(B_KE + ks));
           }
-          if (ok) ok = wait_v(n0) && (nt < 3 || wait_k(n0 + 2));
           for (int i = 0; i < nt && ok && !*abort_flag; i++) {
-            const int n = n0 + i, t = i & 1, vs = uni(n % VST), ks = uni(n % KST), acc = uni(i > 1);
-            const bool more = i + 2 < nt;
-            if (!(ok = pv(t, vs, acc))) break;
+            const int n = n0 + i, t = i & 1, vs = uni(n % VST), ks = uni((n + 2) % KST), acc = uni(i > 1);
+            if (!(ok = wait_v(n) && pv(t, vs, acc))) break;
             commit_if(on, bar(B_VE + vs));
-            if (i + 1 < nt && !(ok = wait_v(n + 1) && (i + 3 >= nt || wait_k(n + 3)))) break;
-            if (more) {
+            if (i + 2 < nt) {
+              if (!(ok = wait_k(n + 2))) break;
+              tc::tc_fence_after();
               issue_s(t, ks);
               commit_if(on, bar(B_KE + ks));
             }
