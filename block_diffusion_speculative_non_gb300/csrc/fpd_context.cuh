@@ -49,6 +49,9 @@ struct CtxWeights {
   int batch, L, nq, nkv, h, t_cap, accumulate;
 };
 cudaError_t ctx_weights_init_attributes();
+bool ctx_weights_tc_supported(const CtxWeights& a);
+cudaError_t ctx_weights_tc_init_attributes();
+cudaError_t launch_ctx_weights_tc(const CtxWeights& a, int num_sms, cudaStream_t st);
 cudaError_t launch_ctx_weights(const CtxWeights& a, int num_sms, cudaStream_t st);
 
 struct Evict {

@@ -5,6 +5,7 @@
 // The sum runs over the query rows of one key, so keys take the product's row side: a warp holds 16 keys as A
 // fragments for the whole kernel and streams the query rows past them; the exponentials of a key stay in the quad of
 // lanes that owns it, and no intermediate leaves the registers.  One CTA owns its keys: no atomics, a fixed order.
+#include <cstdlib>
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
 
@@ -120,10 +121,12 @@ cudaError_t ctx_weights_init_attributes() {
                                        (int)sizeof(WeightSmem<128>));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(weights_mma_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(WeightSmem<64>));
+  if (e == cudaSuccess) e = ctx_weights_tc_init_attributes();
   return e;
 }
 
 cudaError_t launch_ctx_weights(const CtxWeights& a, int num_sms, cudaStream_t st) {
+  if (ctx_weights_tc_supported(a) && (getenv("FPD_WTC") || a.L * (a.nq / a.nkv) > 64)) return launch_ctx_weights_tc(a, num_sms, st);
   const int key_tiles = ceil_div(a.t_cap, KT);
   const int grid = a.batch * a.nkv * key_tiles;
   return a.h == 128 ? launch_k(weights_mma_kernel<128>, grid, NWARP * 32, sizeof(WeightSmem<128>), st, a, key_tiles)

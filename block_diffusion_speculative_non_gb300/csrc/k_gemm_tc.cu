@@ -716,9 +716,9 @@ static cudaError_t make_tmap_typed(CUtensorMap* tm, CUtensorMapDataType dt, cons
                                    const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
   auto enc = get_encode();
   if (!enc) return cudaErrorNotSupported;
-  if (((uintptr_t)ptr & 15) || rank < 2 || rank > 3) return cudaErrorInvalidValue;
-  cuuint64_t d[3], st[2];
-  cuuint32_t b[3], estr[3] = {1, 1, 1};
+  if (((uintptr_t)ptr & 15) || rank < 2 || rank > 4) return cudaErrorInvalidValue;
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; i++) {
     d[i] = dims[i];
     b[i] = box[i];

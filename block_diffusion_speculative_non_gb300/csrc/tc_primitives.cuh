@@ -97,6 +97,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm,
       "l"((uint64_t)tm), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// 4-D tiled load of the box at (x, y, z, w) into shared memory; completes bytes on bar.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"((uint64_t)tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 // Contiguous global -> shared copy of `bytes` (both addresses 16-byte aligned, bytes a multiple of 16).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -189,7 +197,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 // Row-major bf16 matrix [rows, cols] (row stride ld elements) as a TMA map with boxes of 64 columns x box_rows rows
 // and the 128-byte swizzle (k_gemm_tc.cu).
 cudaError_t make_tmap(CUtensorMap* tm, const void* ptr, int rows, int cols, int ld, int box_rows);
-// bf16 tensor of rank 2 or 3 (dims innermost first, byte strides of dims 1.., box in elements), 128-byte swizzle
+// bf16 tensor of rank 2 to 4 (dims innermost first, byte strides of dims 1.., box in elements), 128-byte swizzle
 cudaError_t make_tmap_nd(CUtensorMap* tm, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
                          const uint32_t* box);
 // byte matrix [rows, cols] (row stride ld bytes), box 128 bytes x box_rows, 128-byte swizzle (E4M3 weight atoms)
