@@ -24,7 +24,7 @@ using namespace attn_tc;
 
 constexpr int KT = 128, QT = 128;
 constexpr int kThreads = 12 * 32;
-constexpr int RST = 3, LST = 4;          // K and Q ring slots, lse slots
+constexpr int RST = 3, LST = 8;          // K and Q ring slots, lse slots
 constexpr int ATOM_BYTES = 128 * 64 * 2;
 enum {
   B_KF = 0,
@@ -179,25 +179,38 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     commit_if(on, bar(B_END));
     tc::mbar_wait(bar(B_END), 0);
   } else if (warp == 2) {
+    // four tiles' values are read together, so that a read's latency is paid once per group
+    int off[4], pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int r = i * 32 + lane;
+      pos[i] = r < p.rpt ? r / p.grp : INT32_MAX / 2;
+      off[i] = r / p.grp * p.a.nq + r % p.grp;
+    }
     int n = 0;
     while (!*abort_flag && next()) {
-      for (int q = 0; q < p.nqt && !*abort_flag; q++, n++) {
-        const int s = n % LST;
-        if (n >= LST && !wait_bar(bar(B_LE + s), ((n / LST) & 1) ^ 1)) { *abort_flag = 1; break; }
-        float v[4];
+      const float* src = p.a.lse + (size_t)b * p.a.L * p.a.nq + g * p.grp;
+      for (int q0 = 0; q0 < p.nqt && !*abort_flag; q0 += 4) {
+        float v[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int r = i * 32 + lane, row = q * p.rpt + r;
-          v[i] = -INFINITY;
-          if (r < p.rpt && row < nrows) {
-            const float l = p.a.lse[((size_t)b * p.a.L + row / p.grp) * p.a.nq + g * p.grp + row % p.grp];
-            v[i] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int n0 = (q0 + j) * p.npt;
+            v[j][i] = q0 + j < p.nqt && n0 + pos[i] < p.a.L ? src[(size_t)n0 * p.a.nq + off[i]] : -INFINITY;
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; i++) l2s[s * QT + i * 32 + lane] = v[i];
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B_LF + s));
+        for (int j = 0; j < 4; j++) {
+          if (q0 + j >= p.nqt) break;
+          const int s = n % LST;
+          if (n >= LST && !wait_bar(bar(B_LE + s), ((n / LST) & 1) ^ 1)) *abort_flag = 1;
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            l2s[s * QT + i * 32 + lane] = v[j][i] == -INFINITY ? -INFINITY : -v[j][i] * 1.4426950408889634f;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(B_LF + s));
+          n++;
+        }
       }
     }
   } else {
