@@ -264,102 +264,6 @@ def fpd_verify_prefix(batch, block_len, draft, margin, tau, layout, rule, pad_id
                                    _stream(stream)), "fpd_verify_prefix")
 
 
-# ---- operators on a context store (sizes and layouts: include/fpd.h) -------------------------------------------
-
-def _arg(t, dtype, n, what):
-    """Device address of a tensor that must be contiguous, of `dtype` ("bfloat16", "float32", "int32", "uint8"), on the
-    current device and hold at least n elements; an int address or None is passed on."""
-    if t is None or isinstance(t, int):
-        return t
-    import torch
-    if t.dtype is not getattr(torch, dtype):
-        raise ValueError(f"{what} must be torch.{dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous (row-major)")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if t.numel() < n:
-        raise ValueError(f"{what} holds {t.numel()} elements, the call needs {n}")
-    return t.data_ptr()
-
-
-def fpd_shared_attention_workspace_bytes(batch, block_len, n_q_heads, n_kv_heads, head_dim, prefix_cap, t_cap) -> int:
-    return int(lib().fpd_shared_attention_workspace_bytes(batch, block_len, n_q_heads, n_kv_heads, head_dim, prefix_cap,
-                                                          t_cap))
-
-
-def fpd_shared_attention(batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, q, k_blk, v_blk, prefix_store,
-                         prefix_cap, prefix_len, kv_store, t_cap, ctx_len, out, lse, workspace, workspace_bytes,
-                         stream=None):
-    """Attention of a batch over [shared prefix ; own context ; block] of one layer; out and lse are written."""
-    n, bf = batch * block_len * n_q_heads, "bfloat16"
-    blk, pos = batch * n_kv_heads * block_len * head_dim, 2 * n_kv_heads * head_dim
-    _check(lib().fpd_shared_attention(
-        batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, _arg(q, bf, n * head_dim, "q"),
-        _arg(k_blk, bf, blk, "k_blk"), _arg(v_blk, bf, blk, "v_blk"),
-        _arg(prefix_store, bf, (layer + 1) * prefix_cap * pos, "prefix_store"), prefix_cap,
-        _arg(prefix_len, "int32", 1, "prefix_len"),
-        _arg(kv_store, bf, (layer + 1) * batch * t_cap * pos, "kv_store"), t_cap, _arg(ctx_len, "int32", batch, "ctx_len"),
-        _arg(out, bf, n * head_dim, "out"), _arg(lse, "float32", n, "lse"),
-        _arg(workspace, "uint8", workspace_bytes, "workspace"), workspace_bytes, _stream(stream)), "fpd_shared_attention")
-
-
-def fpd_context_weights(batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, q, lse, kv_store, t_cap, ctx_len,
-                        weights, accumulate=False, stream=None):
-    """weights[layer] (+)= the attention weight every context position collects from the rows of q."""
-    n, at = batch * block_len * n_q_heads, (layer + 1) * batch * n_kv_heads * t_cap
-    _check(lib().fpd_context_weights(
-        batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, _arg(q, "bfloat16", n * head_dim, "q"),
-        _arg(lse, "float32", n, "lse"), _arg(kv_store, "bfloat16", at * 2 * head_dim, "kv_store"), t_cap,
-        _arg(ctx_len, "int32", batch, "ctx_len"), _arg(weights, "float32", at, "weights"), int(bool(accumulate)),
-        _stream(stream)), "fpd_context_weights")
-
-
-def fpd_evict_workspace_bytes(n_layers, batch, n_kv_heads, budget) -> int:
-    return int(lib().fpd_evict_workspace_bytes(n_layers, batch, n_kv_heads, budget))
-
-
-def fpd_evict_context(n_layers, batch, n_kv_heads, head_dim, budget, recent, kv_store, t_cap, weights, ctx_len, out_store,
-                      out_cap, out_weights, out_len, pos_offset, kept, workspace, workspace_bytes, stream=None):
-    """Keeps the last `recent` positions and those with the largest weights, `budget` in all, of every request."""
-    heads, bf = n_layers * batch * n_kv_heads, "bfloat16"
-    _check(lib().fpd_evict_context(
-        n_layers, batch, n_kv_heads, head_dim, budget, recent, _arg(kv_store, bf, heads * 2 * t_cap * head_dim, "kv_store"),
-        t_cap, _arg(weights, "float32", heads * t_cap, "weights"), _arg(ctx_len, "int32", batch, "ctx_len"),
-        _arg(out_store, bf, heads * 2 * out_cap * head_dim, "out_store"), out_cap,
-        _arg(out_weights, "float32", heads * out_cap, "out_weights"), _arg(out_len, "int32", batch, "out_len"),
-        _arg(pos_offset, "int32", batch, "pos_offset"), _arg(kept, "int32", heads * budget, "kept"),
-        _arg(workspace, "uint8", workspace_bytes, "workspace"), workspace_bytes, _stream(stream)), "fpd_evict_context")
-
-
-def fpd_prepare_context_at(model, batch, total_rows, row_off, row_cnt, pos_start, pos_offset, feats, kv_store, t_cap,
-                           workspace, workspace_bytes, stream=None):
-    arr = (ctypes.c_void_p * len(feats))(*[_ptr(f) for f in feats])
-    _check(lib().fpd_prepare_context_at(model, batch, total_rows, _ptr(row_off), _ptr(row_cnt), _ptr(pos_start),
-                                        _ptr(pos_offset), arr, _ptr(kv_store), t_cap, _ptr(workspace), workspace_bytes,
-                                        _stream(stream)), "fpd_prepare_context_at")
-
-
-def fpd_shared_workspace_bytes(model, batch, max_block_len, prefix_cap, t_cap) -> int:
-    return int(lib().fpd_shared_workspace_bytes(model, batch, max_block_len, prefix_cap, t_cap))
-
-
-def shared_context(prefix_store=None, prefix_cap=0, prefix_len=None, kv_store=None, t_cap=0, ctx_len=None, pos_offset=None,
-                   weights=None, prefix_weights=None, accumulate=False) -> SharedContext:
-    """Build an fpd_shared_context; it keeps its tensors alive."""
-    c = SharedContext(_ptr(prefix_store), prefix_cap, _ptr(prefix_len), _ptr(kv_store), t_cap, _ptr(ctx_len),
-                      _ptr(pos_offset), _ptr(weights), _ptr(prefix_weights), int(bool(accumulate)))
-    c._keep = (prefix_store, prefix_len, kv_store, ctx_len, pos_offset, weights, prefix_weights)
-    return c
-
-
-def fpd_draft_block_shared(model, batch, block_len, ctx: SharedContext, anchor, mask_id, hidden_out, layer_hidden,
-                           workspace, workspace_bytes, stream=None):
-    _check(lib().fpd_draft_block_shared(model, batch, block_len, ctypes.byref(ctx), _ptr(anchor), int(mask_id),
-                                        _ptr(hidden_out), _ptr(layer_hidden), _ptr(workspace), workspace_bytes,
-                                        _stream(stream)), "fpd_draft_block_shared")
-
-
 def grid_format(digit_ids, plus_id, minus_id, pad_id, n_axes=3, width=5, axis_sep=",", point_sep=";") -> GridFormat:
     f = GridFormat()
     for k, t in enumerate(digit_ids):
@@ -399,4 +303,7 @@ def fpd_device_status(stream=None) -> int:
     return int(code.value)
 
 
+from .context import (_arg, fpd_context_weights, fpd_draft_block_shared, fpd_evict_context,  # noqa: E402
+                      fpd_evict_workspace_bytes, fpd_prepare_context_at, fpd_shared_attention,
+                      fpd_shared_attention_workspace_bytes, fpd_shared_workspace_bytes, shared_context)
 from .drafter import Drafter, SharedDraft  # noqa: E402  (convenience wrapper over the calls above)

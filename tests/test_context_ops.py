@@ -94,10 +94,14 @@ def test_binding_checks_tensors(fpd):
     """Type, layout and size of a tensor are checked before its address is used."""
     import torch
     with pytest.raises(ValueError, match="must be torch.bfloat16"):
-        fpd._arg(torch.zeros(4), "bfloat16", 4, "q")
+        fpd._arg(torch.zeros(4), torch.bfloat16, 4, "q")
     with pytest.raises(ValueError, match="contiguous"):
-        fpd._arg(torch.zeros(4, 4).t(), "float32", 4, "lse")
-    assert fpd._arg(None, "int32", 4, "ctx_len") is None and fpd._arg(64, "int32", 4, "ctx_len") == 64
+        fpd._arg(torch.zeros(4, 4)[:, :2], torch.float32, 4, "lse")
+    with pytest.raises(ValueError, match="the call needs 5"):
+        fpd._arg(torch.zeros(4), torch.float32, 5, "lse")
+    with pytest.raises(ValueError, match="current device"):
+        fpd._arg(torch.zeros(4), torch.float32, 4, "lse", 0)
+    assert fpd._arg(None, torch.int32, 4, "ctx_len") is None and fpd._arg(64, torch.int32, 4, "ctx_len") == 64
 
 
 def test_selection_rule_of_the_reference():
