@@ -287,10 +287,11 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
   // rows of the tensor maps are 32-bit coordinates
   const bool own_tma = (long long)batch * 2 * nkv * t_cap < INT32_MAX && (long long)batch * nkv * lb < INT32_MAX;
   const bool pre_tma = (long long)2 * nkv * p_cap < INT32_MAX;
-  pl.pre_tc = p_cap && pre_tma && !getenv("FPD_MMA");
-  pl.own_tc = own_keys && own_tma && !getenv("FPD_MMA") && !getenv("FPD_MMA_OWN");
-  pl.pre_tiles = p_cap ? ceil_div(pre_rows, pl.pre_tc ? 256 : QT) : 0;
-  pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 256 : QT) : 0;
+  const int lane_rows = grp <= 128 ? 128 / grp * grp : 0;   // whole positions
+  pl.pre_tc = p_cap && pre_tma && lane_rows && !getenv("FPD_MMA");
+  pl.own_tc = own_keys && own_tma && lane_rows && !getenv("FPD_MMA") && !getenv("FPD_MMA_OWN");
+  pl.pre_tiles = p_cap ? ceil_div(pre_rows, pl.pre_tc ? 2 * lane_rows : QT) : 0;
+  pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 2 * lane_rows : QT) : 0;
   const long pre_units = (long)pl.pre_tiles * nkv, own_units = (long)pl.own_tiles * nkv * batch;
   const int pre_kt = ceil_div(p_cap, 128), own_kt = ceil_div(t_cap, 128) + ceil_div(lb, 128);
   if (pl.pre_tiles && !pl.pre_tc) pl.pre_splits = mma_splits(pre_units, ceil_div(p_cap, KT), 2 * num_sms);
@@ -304,7 +305,7 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
     // Either one even run per SM, which may span units, or s runs per unit.  A run costs about kSeg besides its tiles (Q, the
     // first copies, the partial out); a partial is written and read once.  The time is the longest run's or, with the own
     // part's runs, the average over the SMs, and the merge's reads.
-    const bool pair = pre_rows > 128;
+    const bool pair = pre_rows > lane_rows;
     const double kTile = (pair ? 2.2 : 1.1) * h / 128, kOwn = 1.1 * h / 128, kSeg = 5.0;   // us
     const double part_us = (double)batch * L * nq * h * 8 / 3e6;                            // us per partial of every row
     const double own_us = own_segs * (kSeg + kOwn * own_kt);
@@ -317,14 +318,15 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
         pl.pre_runs = (int)runs;
       }
     };
+    if (getenv("FPD_S")) { pl.pre_runs = pre_units * atoi(getenv("FPD_S")); } else
     for (long s = 1; s <= pre_kt && (s == 1 || pre_units * s <= num_sms); s++)
       if (pre_units * s <= num_sms) consider(pre_units * s, kSeg + kTile * ceil_div(pre_kt, (int)s), s);
-    if (total >= num_sms) consider(num_sms, 2 * kSeg + kTile * total / num_sms, (double)num_sms / pre_units + 1);
+    if (!getenv("FPD_S") && total >= num_sms) consider(num_sms, 2 * kSeg + kTile * total / num_sms, (double)num_sms / pre_units + 1);
     // a unit's tiles span at most ceil(runs / units) + 1 of the even runs (one less when the runs divide evenly), and no
-    // more runs than it has tiles; a unit of at most 128 rows leaves two partials per run
+    // more runs than it has tiles; a unit with one lane's rows leaves two partials per run
     const int pieces = (int)ceil_div(pl.pre_runs, (int)pre_units) + (pl.pre_runs % pre_units ? 1 : 0);
     pl.pre_splits = std::min(pre_kt, pieces);
-    if ((pre_rows - 1) % 256 < 128) pl.pre_splits *= 2;
+    if ((pre_rows - 1) % (2 * lane_rows) < lane_rows) pl.pre_splits *= 2;
   }
   if (pl.pre_tc || pl.own_tc) pl.tc_grid = (int)std::min<long>(num_sms, pl.pre_runs + own_segs);
   return pl;

@@ -6,13 +6,14 @@
 //   0, 3   TMA producers of K and of V: tiles of 128 keys (64-dim boxes, 128-byte swizzle), two K and three V deep;
 //   1      MMA issuer: S = Q K^T, then O += (P_hi + P_lo) V with P read from tensor memory; a lane's next S is issued right
 //          behind its product, so that it waits for its own softmax alone;
-//   2      clears the V rows past the last valid key of a partial tile (0 x a stale non-finite value would be NaN);
+//   2      loads Q, and clears the V rows past the last valid key of a partial tile (0 x a stale non-finite value would be NaN);
 //   4..7   softmax of lane 0, 8..11 of lane 1: one thread per query row, the 128 scores of a tile in registers (one read of
 //          tensor memory per tile), p = 2^(s log2e/sqrt(h) - m) written back over S as two bf16 terms; O is rescaled only
 //          when the maximum rises by more than 2^8 (p stays below 2^8: O / l is exact either way).
 //
-// A unit is a pair of 128-row tiles of a part's rows in one kv head: the lanes hold one tile each and share every K/V tile.
-// Where a unit has at most 128 rows (few blocks, the own part of a text block, the last rows of a long one), both lanes
+// A lane's rows are whole positions, the kv head's heads of each (128 rows, or less when the heads do not divide it): one
+// box of a [position][head][h] map of q.  A unit is a pair of such row tiles of a part's rows in one kv head: the lanes hold one tile each and share every K/V tile.
+// Where a unit has the rows of one lane only (few blocks, the own part of a text block, the last rows of a long one), both lanes
 // hold the same rows and take the even and the odd key tiles: such a unit is a read of the keys, and two key streams keep
 // the copies in flight.  The prefix's (unit, key tile) space is cut into one contiguous run of tiles per CTA, so that all
 // SMs finish together whatever the number of rows; a run that spans units leaves a partial in each.  The own part's units
@@ -27,7 +28,7 @@ namespace fpd {
 namespace {
 using namespace attn_tc;
 
-constexpr int QR = 128, KT = 128;      // rows of a lane, keys of a tile
+constexpr int QR = 128, KT = 128;      // most rows of a lane, keys of a tile
 constexpr int kThreads = 12 * 32;
 constexpr int KST = 2, VST = 3;        // K and V ring slots: a K tile is free once S is, a V tile only behind the softmax
 constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
@@ -41,10 +42,11 @@ struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64;
   static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, BAR = V + VST * TILE;
 };
-// barriers: q[lane], k_full, k_empty, v_full, v_empty, v_ready [slot], s_full, p_full, pv_done [lane], end
+// barriers: q_full, q_empty [lane], k_full, k_empty, v_full, v_empty, v_ready [slot], s_full, p_full, pv_done [lane], end
 enum {
   B_Q = 0,
-  B_KF = B_Q + 2,
+  B_QE = B_Q + 2,
+  B_KF = B_QE + 2,
   B_KE = B_KF + KST,
   B_VF = B_KE + KST,
   B_VE = B_VF + VST,
@@ -60,20 +62,41 @@ constexpr size_t smem_bytes() {
   return 1024 + (size_t)Lay<HD>::BAR + 8 * B_N + 16;
 }
 static_assert(smem_bytes<128>() <= 232448, "tile set exceeds the shared memory of one CTA");
+static_assert(2 * QR * (128 * 4 + 16) <= (KST + VST) * Lay<128>::TILE && 2 * QR * (64 * 4 + 16) <= (KST + VST) * Lay<64>::TILE,
+              "the staged partials must fit in the K and V slots");
+
+// Division by a number known on the host (Granlund and Montgomery's multiply, add and shift; exact for 32-bit operands).
+struct FastDiv {
+  uint32_t d, m, s1, s2;
+  void set(uint32_t n) {
+    d = n;
+    uint32_t l = 0;
+    while ((1ull << l) < n) l++;
+    m = (uint32_t)(((1ull << 32) * ((1ull << l) - n)) / n + 1);
+    s1 = l > 0 ? 1 : 0;
+    s2 = l > 0 ? l - 1 : 0;
+  }
+  __device__ __forceinline__ int div(int x) const {
+    const uint32_t t = __umulhi(m, (uint32_t)x);
+    return (int)((t + (((uint32_t)x - t) >> s1)) >> s2);
+  }
+};
 
 struct TcArgs {
+  CUtensorMap tm_q;                               // q as [rows][nq][h], boxes of npt positions x grp heads
   CUtensorMap tm_pre, tm_own, tm_kblk, tm_vblk;   // [rows][h] views of the prefix, the own store, the block keys and values
   SharedAttn a;
-  int grp;
+  int grp, npt, rpt;                     // heads per kv head, positions and rows of a lane
   int pre_tiles, pre_units, pre_slots;   // row pairs per kv head, units, partial slots of a prefix row (0 units: not here)
   int pre_runs;                          // CTAs that share the prefix's tiles
   int own_tiles, own_units, own_splits;  // the same for the own part, with the key splits of a unit
   int own_slot0;                         // first partial slot of the own part
+  FastDiv by_grp, by_pre_tiles, by_own_tiles, by_own_units, by_nkv;
 };
 
 // One run of key tiles of one unit.
 struct Seg {
-  bool prefix, keys;           // keys: at most 128 rows, the lanes take even and odd tiles
+  bool prefix, keys;           // keys: one lane's rows, the lanes take even and odd tiles
   int g, row0, nrows, n0;      // rows row0 .. of the part's nrows; the part's first row in [rows]
   int slot, pad_end;           // partial slot (of lane 0); slots up to pad_end that this run does not fill are marked empty
   int T, kb, ke, n_ctx, n_tiles;
@@ -92,7 +115,7 @@ struct Seg {
     valid = min(KT, (ctx ? min(ke, T) : ke) - first);
   }
   __device__ int lane_tiles(int t) const { return keys ? (n_tiles - t + 1) / 2 : n_tiles; }
-  __device__ int lane_row0(int t) const { return row0 + (keys ? 0 : t * QR); }
+  __device__ int lane_row0(int t, int rpt) const { return row0 + (keys ? 0 : t * rpt); }
 };
 
 // The runs of this CTA, in order.
@@ -107,26 +130,35 @@ struct Walk {
     P_tiles = (P + KT - 1) / KT;
     total = (long long)p.pre_units * P_tiles;
     G = (int)min((long long)p.pre_runs, max(total, 1ll));
-    x = c < G ? c * total / G : 0;
-    x_end = c < G ? (c + 1) * total / G : 0;
+    x = c < G ? run_start(c) : 0;
+    x_end = c < G ? run_start(c + 1) : 0;
     empty_u = total == 0 ? c : p.pre_units;
     own_i = (int)gridDim.x - 1 - c;
   }
+  // run c starts at tile c total / G; the run that holds tile t is the last one that starts at or before it
+  // (64-bit divisions cost a few hundred cycles: only where 32 bits do not hold the products)
+  __device__ long long run_start(int i) const {
+    return total < (1 << 20) ? (uint32_t)i * (uint32_t)total / (uint32_t)G : i * total / G;
+  }
+  __device__ int run_of(long long t) const {
+    return total < (1 << 20) ? (int)((((uint32_t)t + 1) * (uint32_t)G - 1) / (uint32_t)total) : (int)(((t + 1) * G - 1) / total);
+  }
   __device__ void rows(Seg& s, int qp, int nrows) const {
-    s.row0 = qp * 2 * QR;
+    s.row0 = qp * 2 * p.rpt;
     s.nrows = nrows;
-    s.keys = nrows - s.row0 <= QR;
+    s.keys = nrows - s.row0 <= p.rpt;
   }
   __device__ void prefix_unit(Seg& s, int u) const {
     s.prefix = true;
-    s.g = u / p.pre_tiles;
-    rows(s, u % p.pre_tiles, p.a.rows * p.grp);
+    s.g = p.by_pre_tiles.div(u);
+    rows(s, u - s.g * p.pre_tiles, p.a.rows * p.grp);
     s.n0 = 0;
     s.T = P;
     s.krow = s.g * p.a.p_cap;
     s.vrow = (p.a.nkv + s.g) * p.a.p_cap;
     s.brow = 0;
   }
+  __device__ bool more() const { return empty_u < p.pre_units || x < x_end || own_i < p.own_units * p.own_splits; }
   __device__ bool next(Seg& s) {
     if (empty_u < p.pre_units) {
       prefix_unit(s, empty_u);
@@ -137,29 +169,30 @@ struct Walk {
       return true;
     }
     if (x < x_end) {
-      const int u = (int)(x / P_tiles);
+      const int u = total < (1 << 20) ? (int)((uint32_t)x / (uint32_t)P_tiles) : (int)(x / P_tiles);
       const long long u0 = (long long)u * P_tiles, e = min(x_end, u0 + P_tiles);
       prefix_unit(s, u);
       s.range((int)(x - u0) * KT, (int)min((long long)P, (e - u0) * KT));
-      const int piece = c - (int)(((u0 + 1) * G - 1) / total);   // CTAs since the one that holds the unit's first tile
+      const int piece = c - run_of(u0);   // runs since the one that holds the unit's first tile
       s.slot = s.keys ? 2 * piece : piece;
       s.pad_end = e == u0 + P_tiles ? p.pre_slots : 0;
       x = e;
       return true;
     }
     if (own_i < p.own_units * p.own_splits) {
-      const int u = own_i % p.own_units, split = own_i / p.own_units;
-      const int bg = u / p.own_tiles, b = bg / p.a.nkv;
+      const int split = p.by_own_units.div(own_i), u = own_i - split * p.own_units;
+      const int bg = p.by_own_tiles.div(u), b = p.by_nkv.div(bg);
       s.prefix = false;
-      s.g = bg % p.a.nkv;
-      rows(s, u % p.own_tiles, p.a.L * p.grp);
+      s.g = bg - b * p.a.nkv;
+      rows(s, u - bg * p.own_tiles, p.a.L * p.grp);
       s.n0 = b * p.a.L;
       s.T = p.a.ck ? clamp_ctx(p.a.ctx_len[b], p.a.t_cap) : 0;
       s.krow = ((b * 2 + 0) * p.a.nkv + s.g) * p.a.t_cap;
       s.vrow = ((b * 2 + 1) * p.a.nkv + s.g) * p.a.t_cap;
       s.brow = (b * p.a.nkv + s.g) * p.a.lb;
-      const long long n = s.T + p.a.lb, nt = (n + KT - 1) / KT;
-      s.range((int)(split * nt / p.own_splits) * KT, (int)min(n, (split + 1) * nt / p.own_splits * KT));
+      const int n = s.T + p.a.lb, nt = (n + KT - 1) / KT;
+      if (p.own_splits == 1) s.range(0, n);
+      else s.range((int)((long long)split * nt / p.own_splits) * KT, (int)min((long long)n, (split + 1ll) * nt / p.own_splits * KT));
       s.slot = p.own_slot0 + 2 * split;
       s.pad_end = s.slot + 2;
       own_i += gridDim.x;
@@ -199,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; t++) {
-      tc::mbar_init(bar(B_Q + t), 4);
+      tc::mbar_init(bar(B_Q + t), 1);
+      tc::mbar_init(bar(B_QE + t), 1);
       tc::mbar_init(bar(B_SF + t), 1);
       tc::mbar_init(bar(B_PF + t), 4);
       tc::mbar_init(bar(B_PV + t), 1);
@@ -321,6 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             issue_s(1, k0);
             commit_if(on, bar(B_KE + k0));
           }
+          if (nt == 1) {
+            commit_if(on, bar(B_QE + 0));
+            commit_if(on, bar(B_QE + 1));
+          }
           if (ok) ok = wait_v(n0);
           for (int i = 0; i < nt && ok && !*abort_flag; i++) {
             const int n = n0 + i, vs = uni(n % VST), ks = uni((n + 1) % KST), acc = uni(i > 0);
@@ -330,12 +368,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               if (!(ok = wait_k(n + 1) && wait_v(n + 1))) break;
               tc::tc_fence_after();
               issue_s(0, ks);
+              if (i + 2 == nt) commit_if(on, bar(B_QE + 0));
             }
             if (!(ok = pv(1, vs, acc))) break;
             commit_if(on, bar(B_VE + vs));
             if (more) {
               issue_s(1, ks);
               commit_if(on, bar(B_KE + ks));
+              if (i + 2 == nt) commit_if(on, bar(B_QE + 1));
             }
           }
         } else {
@@ -345,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             const int ks = uni((n0 + i) % KST);
             issue_s(i, ks);
             commit_if(on, bar(B_KE + ks));
+            if (i + 2 >= nt) commit_if(on, bar(B_QE + i));
           }
           for (int i = 0; i < nt && ok && !*abort_flag; i++) {
             const int n = n0 + i, t = i & 1, vs = uni(n % VST), ks = uni((n + 2) % KST), acc = uni(i > 1);
@@ -355,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               tc::tc_fence_after();
               issue_s(t, ks);
               commit_if(on, bar(B_KE + ks));
+              if (i + 4 >= nt) commit_if(on, bar(B_QE + t));   // the lane's last S
             }
           }
         }
@@ -372,33 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     const uint32_t st = tmem + lane_off + t * KT, ot = tmem + lane_off + kTmemO + t * 128;
     // row r of the lane: index of its output row, or -1
     auto out_row = [&](const Seg& s) -> long long {
-      const int qi = s.lane_row0(t) + r;
-      return qi < s.nrows ? (long long)(s.n0 + qi / p.grp) * p.a.nq + s.g * p.grp + qi % p.grp : -1;
+      const int qi = s.lane_row0(t, p.rpt) + r;
+      const int pos = p.by_grp.div(qi);
+      return r < p.rpt && qi < s.nrows ? (long long)(s.n0 + pos) * p.a.nq + s.g * p.grp + qi - pos * p.grp : -1;
     };
-    // Q row r -> shared memory (K-major, 128-byte swizzle: chunk c of row r at c ^ (r & 7))
-    auto load_q = [&](const Seg& s) {
-      if (s.lane_tiles(t) == 0) return;
-      const long long o = out_row(s);
-      uint8_t* qs = smem + S::Q + t * S::TILE;
-      const uint4* src = reinterpret_cast<const uint4*>(p.a.q + (o < 0 ? 0 : o) * HD);
-#pragma unroll
-      for (int hf = 0; hf < S::ATOMS; hf++) {
-        uint4 u[8];
-#pragma unroll
-        for (int c = 0; c < 8; c++) u[c] = o >= 0 ? src[hf * 8 + c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < 8; c++) *reinterpret_cast<uint4*>(qs + hf * ATOM_BYTES + r * 128 + ((c ^ (r & 7)) << 4)) = u[c];
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(B_Q + t));
-    };
-    int cnt = 0;   // lane tiles so far: phases of S, P and PV
-    bool have = walk.next(sg);
-    if (have) load_q(sg);
-    while (have && !*abort_flag) {
+    int cnt = 0, other = 0;   // tiles of this lane and of the other so far: phases of S, P and PV
+    while (!*abort_flag && walk.next(sg)) {
       const long long orow = out_row(sg);
-      const bool warp_rows = sg.lane_row0(t) + quarter * 32 < sg.nrows;   // else this warp's rows are padding
+      const bool warp_rows = quarter * 32 < p.rpt && sg.lane_row0(t, p.rpt) + quarter * 32 < sg.nrows;   // else padding
       const int i0 = sg.keys ? t : 0, step = sg.keys ? 2 : 1;
       float m_ref = -INFINITY, l = 0.f;
       bool first_tile = true;
@@ -474,40 +497,68 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(B_PF + t));
       }
-      // the run's scores are done, so its Q is free: the next run's goes in before this one's epilogue
-      const Seg done = sg;
-      have = walk.next(sg);
-      if (have) load_q(sg);
+      other += sg.lane_tiles(1 - t);
       if (!first_tile && !wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
+      // behind the last run the K and V slots are free once the other lane's products are done too: rows go through them
+      // (16 bytes of padding each, so that a warp's writes spread over the banks) and out as one bulk copy per row.
+      // Written directly, 32 rows at a time, a CTA's partials took 4 us instead of 2.
+      const bool staged = !walk.more();
+      if (staged && other > 0 && !wait_bar(bar(B_PV + 1 - t), (other - 1) & 1)) *abort_flag = 1;
       tc::tc_fence_after();
       if (warp_rows) {
         const size_t n_out = (size_t)p.a.rows * p.a.nq;
-        const int slot = done.slot + (done.keys ? t : 0);
+        const int slot = sg.slot + (sg.keys ? t : 0);
         if (!first_tile) {
           float* dst = p.a.o_part + ((size_t)slot * n_out + (orow < 0 ? 0 : orow)) * HD;
-#pragma unroll 1
-          for (int c0 = 0; c0 < HD; c0 += 32) {
-            float o[32];
-            tmem_ld32_nowait(ot + c0, o);
-            wait_ld32(o);
-            if (orow >= 0) {
+          uint8_t* row = smem + S::K + (t * QR + r) * (HD * 4 + 16);
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) st8(dst + c0 + e, o + e);
+          for (int c0 = 0; c0 < HD; c0 += 64) {
+            float o[64];
+            tmem_ld32_nowait(ot + c0, o);
+            tmem_ld32_nowait(ot + c0 + 32, o + 32);
+            wait_ld32(o);
+            wait_ld32(o + 32);
+            if (staged) {
+#pragma unroll
+              for (int e = 0; e < 64; e += 4)
+                *reinterpret_cast<float4*>(row + (c0 + e) * 4) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else if (orow >= 0) {
+#pragma unroll
+              for (int e = 0; e < 64; e += 8) st8(dst + c0 + e, o + e);
             }
+          }
+          if (staged && orow >= 0 && !*abort_flag) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(tc::smem_u32(row)),
+                         "r"(HD * 4)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
           }
         }
         if (orow >= 0) {
           p.a.ml[(size_t)slot * n_out + orow] = make_float2(m_ref, l);
-          if (!done.keys || t == 1)
-            for (int s = slot + 1; s < done.pad_end; s++) p.a.ml[(size_t)s * n_out + orow] = make_float2(-INFINITY, 0.f);
+          if (!sg.keys || t == 1)
+            for (int s = slot + 1; s < sg.pad_end; s++) p.a.ml[(size_t)s * n_out + orow] = make_float2(-INFINITY, 0.f);
         }
       }
       tc::tc_fence_before();   // O has been read: the next run's first product follows this lane's next P
     }
   } else if (warp == 2) {
-    // ---------------- V rows past the last valid key -> 0 ----------------
-    int n = 0;
-    while (walk.next(sg) && !*abort_flag) {
+    // ---------------- Q; V rows past the last valid key -> 0 ----------------
+    int n = 0, nq[2] = {0, 0};
+    while (!*abort_flag && walk.next(sg)) {
+      for (int t = 0; t < 2; t++) {
+        if (sg.lane_tiles(t) == 0) continue;
+        if (nq[t] > 0 && !wait_bar(bar(B_QE + t), (nq[t] & 1) ^ 1)) { *abort_flag = 1; break; }
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar(B_Q + t), p.rpt * HD * 2);
+          for (int h = 0; h < S::ATOMS; h++)
+            tc::tma_load_3d(tc::smem_u32(smem + S::Q) + t * S::TILE + h * ATOM_BYTES, &p.tm_q, h * 64, sg.g * p.grp,
+                            sg.n0 + p.by_grp.div(sg.lane_row0(t, p.rpt)), bar(B_Q + t));
+        }
+        nq[t]++;
+        __syncwarp();
+      }
       for (int i = 0; i < sg.n_tiles && !*abort_flag; i++, n++) {
         const int s = n % VST;
         int first, valid;
@@ -527,6 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         if (lane == 0) tc::mbar_arrive(bar(B_VR + s));
       }
     }
+    if (*abort_flag)
+      for (int t = 0; t < 2; t++)
+        if (nq[t] > 0) tc::mbar_wait(bar(B_Q + t), (nq[t] & 1) ^ 1);
   }
 
   __syncwarp();
@@ -553,17 +607,24 @@ cudaError_t launch_shared_tc(const SharedAttn& a, const SharedPlan& pl, cudaStre
   memset(&p, 0, sizeof(p));
   p.a = a;
   p.grp = a.nq / a.nkv;
+  p.npt = QR / p.grp;
+  p.rpt = p.npt * p.grp;
   p.own_slot0 = pl.pre_splits;
+  p.by_grp.set(p.grp);
+  p.by_nkv.set(a.nkv);
   if (pl.pre_tc) {
     p.pre_tiles = pl.pre_tiles;
     p.pre_units = pl.pre_tiles * a.nkv;
     p.pre_slots = pl.pre_splits;
     p.pre_runs = pl.pre_runs;
+    p.by_pre_tiles.set(p.pre_tiles);
   }
   if (pl.own_tc) {
     p.own_tiles = pl.own_tiles;
     p.own_units = pl.own_tiles * a.nkv * a.batch;
     p.own_splits = pl.own_splits / 2;
+    p.by_own_tiles.set(p.own_tiles);
+    p.by_own_units.set(p.own_units);
   }
   const uint64_t str[1] = {(uint64_t)a.h * 2};
   const uint32_t box[2] = {64u, (uint32_t)KT};
@@ -571,8 +632,10 @@ cudaError_t launch_shared_tc(const SharedAttn& a, const SharedPlan& pl, cudaStre
     const uint64_t dims[2] = {(uint64_t)a.h, rows};
     return make_tmap_nd(tm, base, 2, dims, str, box);
   };
-  cudaError_t e = cudaSuccess;
-  if (p.pre_units) e = map(&p.tm_pre, a.pk, (uint64_t)2 * a.nkv * a.p_cap);
+  const uint64_t qd[3] = {(uint64_t)a.h, (uint64_t)a.nq, (uint64_t)a.rows}, qs[2] = {(uint64_t)a.h * 2, (uint64_t)a.h * 2 * a.nq};
+  const uint32_t qb[3] = {64u, (uint32_t)p.grp, (uint32_t)p.npt};
+  cudaError_t e = make_tmap_nd(&p.tm_q, a.q, 3, qd, qs, qb);
+  if (p.pre_units && e == cudaSuccess) e = map(&p.tm_pre, a.pk, (uint64_t)2 * a.nkv * a.p_cap);
   if (p.own_units && a.ck && e == cudaSuccess) e = map(&p.tm_own, a.ck, (uint64_t)a.batch * 2 * a.nkv * a.t_cap);
   if (p.own_units && a.lb) {
     if (e == cudaSuccess) e = map(&p.tm_kblk, a.kblk, (uint64_t)a.batch * a.nkv * a.lb);
