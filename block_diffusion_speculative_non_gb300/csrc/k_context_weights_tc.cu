@@ -2,16 +2,17 @@
 // cores, for many query rows.
 //
 // Keys are the product's rows here as well: S^T = K Q^T with 128 keys in the 128 lanes of tensor memory and the query rows
-// in its columns, so the sum over rows is a sum along one thread's registers.  A CTA takes units of 128 keys and runs all
-// query rows of their request and kv head past them, 128 rows at a time, even tiles on one lane and odd ones on the other;
-// each lane has two S buffers, so the next product runs while a tile is summed.  Per score: one product, one fma, one
-// 2^x, one add: the special-function unit (32 a cycle) and the tensor core (128 x 128 x h in 512 cycles at h = 128) are
-// about level.  Warps:
-//   0      TMA producer of K (three units deep), 3: of Q (three tiles deep; a 4-d map of [request][position][head][h] whose
+// in its columns, so the sum over rows is a sum along one thread's registers.  A CTA takes an even share of all the key
+// tiles that hold a key, two at a time where they belong to the same request and kv head: every query tile of 128 rows that
+// passes is multiplied with both, and a thread sums both keys of its tensor-memory lane, so that a query tile's copy and a
+// row's lse serve two keys (with one key tile per CTA the copies were 7.4 TB/s of L2 reads; with one key per thread the
+// shared-memory reads of lse, which compete with the product's operands, cost 20 %).  S is double buffered: the next
+// product runs while a tile is summed.  Per score: one product, one fma, one 2^x, one add.  Warps:
+//   0      TMA producer of K (three tiles deep), 3: of Q (three tiles deep; a 4-d map of [request][position][head][h] whose
 //          box is the kv head's heads, rows past the request's block come back as 0);
 //   1      MMA issuer;
 //   2      -lse log2(e) of a tile's rows into shared memory (-inf for rows without a key and past the last row: weight 0);
-//   4..7   lane 0, 8..11 lane 1: a thread is a key.  Lane 1 hands its sum to lane 0, which writes: a fixed order.
+//   4..19  sums: warp = [32 of the tile's columns][32 of the keys].  The four parts of a key's sum are added in a fixed order.
 #include <cstring>
 
 #include "attn_tc_prims.cuh"
@@ -23,7 +24,8 @@ namespace {
 using namespace attn_tc;
 
 constexpr int KT = 128, QT = 128;
-constexpr int kThreads = 12 * 32;
+constexpr int kConsumers = 16;           // warps that sum
+constexpr int kThreads = (4 + kConsumers) * 32;
 constexpr int RST = 3, LST = 8;          // K and Q ring slots, lse slots
 constexpr int ATOM_BYTES = 128 * 64 * 2;
 enum {
@@ -31,11 +33,11 @@ enum {
   B_KE = B_KF + RST,
   B_QF = B_KE + RST,
   B_QE = B_QF + RST,
-  B_SF = B_QE + RST,     // [lane][buffer]
-  B_SE = B_SF + 4,
-  B_LF = B_SE + 4,
+  B_SF = B_QE + RST,     // [buffer]
+  B_SE = B_SF + 2,
+  B_LF = B_SE + 2,
   B_LE = B_LF + LST,
-  B_CF = B_LE + LST,     // lane 1's sums of a unit, [unit parity]
+  B_CF = B_LE + LST,     // sums of a unit to be put together, [unit parity]
   B_CE = B_CF + 2,
   B_END = B_CE + 2,
   B_N = B_END + 1
@@ -43,7 +45,7 @@ enum {
 template <int HD>
 struct Lay {
   static constexpr int TILE = 128 * HD * 2, ATOMS = HD / 64;
-  static constexpr int K = 0, Q = RST * TILE, L2 = Q + RST * TILE, COMB = L2 + LST * QT * 4, BAR = COMB + 2 * KT * 4;
+  static constexpr int K = 0, Q = RST * TILE, L2 = Q + RST * TILE, COMB = L2 + LST * QT * 4, BAR = COMB + 2 * 2 * 3 * KT * 4;
   static constexpr size_t BYTES = 1024 + (size_t)BAR + 8 * B_N + 16;
   static_assert(BYTES <= 232448, "tile set exceeds the shared memory of one CTA");
 };
@@ -52,7 +54,62 @@ struct WtArgs {
   CUtensorMap tm_k, tm_q;
   CtxWeights a;
   int grp, npt, rpt, nqt;   // heads per kv head, positions and rows of a query tile, tiles of a request
-  int key_tiles, units;     // by capacity: units = batch * nkv * key_tiles
+};
+
+// The key tiles of CTA c: an even run of all (request, kv head, key tile) that hold a key, requests in order.
+struct Share {
+  const WtArgs& p;
+  int b, g, kt, tiles, T;   // request, kv head, next tile, the request's tiles and length
+  long long left;
+  // unit: nk key tiles of one request and kv head, the first at key k0
+  int nk, k0;
+  __device__ void load(int b_) {
+    b = b_;
+    T = b < p.a.batch ? clamp_ctx(p.a.ctx_len[b], p.a.t_cap) : 0;
+    tiles = (T + KT - 1) / KT;
+  }
+  __device__ Share(const WtArgs& p_) : p(p_) {   // by a whole warp
+    const int lane = threadIdx.x & 31;
+    auto count = [&](int i) { return i < p.a.batch ? (long long)p.a.nkv * ((clamp_ctx(p.a.ctx_len[i], p.a.t_cap) + KT - 1) / KT) : 0ll; };
+    auto sum = [&](long long v) {
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    };
+    long long total = 0;
+    for (int i0 = 0; i0 < p.a.batch; i0 += 32) total += sum(count(i0 + lane));
+    long long lo = blockIdx.x * total / gridDim.x;
+    left = (blockIdx.x + 1) * total / gridDim.x - lo;
+    int i0 = 0;
+    for (; left > 0; i0 += 32) {   // the 32 requests, then the request, that hold tile lo
+      const long long c = sum(count(i0 + lane));
+      if (lo < c) break;
+      lo -= c;
+    }
+    load(i0);
+    while (left > 0 && lo >= (long long)p.a.nkv * tiles) {
+      lo -= (long long)p.a.nkv * tiles;
+      load(b + 1);
+    }
+    g = left > 0 ? (int)(lo / tiles) : 0;
+    kt = left > 0 ? (int)(lo - (long long)g * tiles) : 0;
+    nk = 0;
+  }
+  __device__ bool next() {
+    kt += nk;
+    left -= nk;
+    nk = 0;
+    if (left <= 0) return false;
+    while (kt >= tiles) {
+      kt = 0;
+      if (++g == p.a.nkv || tiles == 0) {
+        g = 0;
+        load(b + 1);
+      }
+    }
+    k0 = kt * KT;
+    nk = (int)min(min(2ll, left), (long long)(tiles - kt));
+    return true;
+  }
 };
 
 template <int HD>
@@ -76,17 +133,15 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
       tc::mbar_init(bar(B_QF + s), 1);
       tc::mbar_init(bar(B_QE + s), 1);
     }
-    for (int s = 0; s < 4; s++) {
-      tc::mbar_init(bar(B_SF + s), 1);
-      tc::mbar_init(bar(B_SE + s), 4);
-    }
     for (int s = 0; s < LST; s++) {
       tc::mbar_init(bar(B_LF + s), 1);
-      tc::mbar_init(bar(B_LE + s), 4);
+      tc::mbar_init(bar(B_LE + s), kConsumers);
     }
     for (int s = 0; s < 2; s++) {
-      tc::mbar_init(bar(B_CF + s), 4);
-      tc::mbar_init(bar(B_CE + s), 4);
+      tc::mbar_init(bar(B_SF + s), 1);
+      tc::mbar_init(bar(B_SE + s), kConsumers);
+      tc::mbar_init(bar(B_CF + s), kConsumers);
+      tc::mbar_init(bar(B_CE + s), kConsumers);
     }
     tc::mbar_init(bar(B_END), 1);
     *abort_flag = 0;
@@ -108,19 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
   pdl_wait();
   pdl_trigger();
 
-  // this CTA's units that hold a key
-  int u = (int)blockIdx.x - (int)gridDim.x, b = 0, g = 0, k0 = 0, T = 0;
-  auto next = [&]() {
-    for (u += gridDim.x; u < p.units; u += gridDim.x) {
-      const int bg = u / p.key_tiles;
-      b = bg / p.a.nkv;
-      g = bg % p.a.nkv;
-      k0 = (u % p.key_tiles) * KT;
-      T = clamp_ctx(p.a.ctx_len[b], p.a.t_cap);
-      if (k0 < T) return true;
-    }
-    return false;
-  };
+  Share sh(p);
   const int nrows = p.a.L * p.grp;
 
   if (warp == 0 || warp == 3) {
@@ -129,15 +172,15 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
       const int full = is_q ? B_QF : B_KF, empty = is_q ? B_QE : B_KE;
       const uint32_t ring = tc::smem_u32(smem + (is_q ? S::Q : S::K));
       int n = 0;
-      while (!*abort_flag && next()) {
-        for (int q = 0; q < (is_q ? p.nqt : 1) && !*abort_flag; q++) {
+      while (!*abort_flag && sh.next()) {
+        for (int q = 0; q < (is_q ? p.nqt : sh.nk) && !*abort_flag; q++) {
           const int s = n % RST;
           if (n >= RST && !wait_bar(bar(empty + s), ((n / RST) & 1) ^ 1)) { *abort_flag = 1; break; }
           tc::mbar_arrive_expect_tx(bar(full + s), is_q ? p.rpt * HD * 2 : S::TILE);
           for (int h = 0; h < S::ATOMS; h++) {
             const uint32_t dst = ring + s * S::TILE + h * ATOM_BYTES;
-            if (is_q) tc::tma_load_4d(dst, &p.tm_q, h * 64, g * p.grp, q * p.npt, b, bar(full + s));
-            else tc::tma_load_2d(dst, &p.tm_k, h * 64, (b * 2 * p.a.nkv + g) * p.a.t_cap + k0, bar(full + s));
+            if (is_q) tc::tma_load_4d(dst, &p.tm_q, h * 64, sh.g * p.grp, q * p.npt, sh.b, bar(full + s));
+            else tc::tma_load_2d(dst, &p.tm_k, h * 64, (sh.b * 2 * p.a.nkv + sh.g) * p.a.t_cap + sh.k0 + q * KT, bar(full + s));
           }
           n++;
         }
@@ -148,31 +191,37 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
   } else if (warp == 1) {
     const uint32_t on = elect_one();
     const uint64_t dk = tc::sw128_kmajor_desc(tc::smem_u32(smem + S::K)), dq = tc::sw128_kmajor_desc(tc::smem_u32(smem + S::Q));
-    int nk = 0, nq = 0, nl[2] = {0, 0};
+    int nk = 0, nq = 0;
     auto uni = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     bool ok = true;
-    while (ok && !*abort_flag && next()) {
-      if (!(ok = wait_bar(bar(B_KF + nk % RST), (nk / RST) & 1))) break;
-      const int ks = uni(nk % RST);
-      for (int q = 0; q < p.nqt && !*abort_flag; q++, nq++) {
-        const int t = q & 1, buf = uni(nl[t] & 1), qs = uni(nq % RST);
-        if (!(ok = wait_bar(bar(B_QF + qs), (nq / RST) & 1))) break;
-        if (nl[t] >= 2 && !(ok = wait_bar(bar(B_SE + 2 * t + buf), ((nl[t] >> 1) & 1) ^ 1))) break;
-        tc::tc_fence_after();
+    while (ok && !*abort_flag && sh.next()) {
+      const int nt = uni(sh.nk), k0s = uni(nk % RST), k1s = uni((nk + 1) % RST);
+      ok = wait_bar(bar(B_KF + k0s), (nk / RST) & 1) && (nt < 2 || wait_bar(bar(B_KF + k1s), ((nk + 1) / RST) & 1));
+      for (int q = 0; q < p.nqt && ok && !*abort_flag; q++, nq++) {
+        const int qs = uni(nq % RST), buf = uni(nq & 1);
+        // whole 32-column chunks: the sums read no column that the product has not written
         const uint32_t id = idesc_bf16(KT, 32 * ceil_div(uni(min(p.rpt, nrows - q * p.rpt)), 32), 0);
-        const uint64_t da = dk + ks * (S::TILE >> 4), db = dq + qs * (S::TILE >> 4);
-        const uint32_t d = tmem + uni(t) * 256 + buf * 128;
+        if (!(ok = wait_bar(bar(B_QF + qs), (nq / RST) & 1) &&
+                   (nq < 2 || wait_bar(bar(B_SE + buf), ((nq >> 1) & 1) ^ 1)))) break;
+        tc::tc_fence_after();
+        const uint64_t db = dq + qs * (S::TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; kk++) {
-          const uint64_t step = ((kk >> 2) * ATOM_BYTES + (kk & 3) * 32) >> 4;
-          umma_ss_if(on, d, da + step, db + step, id, kk > 0 ? 1u : 0u);
+        for (int t = 0; t < 2; t++) {
+          if (t < nt) {
+            const uint64_t da = dk + (t ? k1s : k0s) * (S::TILE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; kk++) {
+              const uint64_t step = ((kk >> 2) * ATOM_BYTES + (kk & 3) * 32) >> 4;
+              umma_ss_if(on, tmem + t * 256 + buf * 128, da + step, db + step, id, kk > 0 ? 1u : 0u);
+            }
+          }
         }
-        commit_if(on, bar(B_SF + 2 * t + buf));
+        commit_if(on, bar(B_SF + buf));
         commit_if(on, bar(B_QE + qs));
-        nl[t]++;
       }
-      commit_if(on, bar(B_KE + ks));
-      nk++;
+      commit_if(on, bar(B_KE + k0s));
+      if (nt == 2) commit_if(on, bar(B_KE + k1s));
+      nk += nt;
     }
     if (!ok) *abort_flag = 1;
     // everything issued is done before tensor memory is freed (at once, unless a wait ran out)
@@ -188,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
       off[i] = r / p.grp * p.a.nq + r % p.grp;
     }
     int n = 0;
-    while (!*abort_flag && next()) {
-      const float* src = p.a.lse + (size_t)b * p.a.L * p.a.nq + g * p.grp;
+    while (!*abort_flag && sh.next()) {
+      const float* src = p.a.lse + (size_t)sh.b * p.a.L * p.a.nq + sh.g * p.grp;
       for (int q0 = 0; q0 < p.nqt && !*abort_flag; q0 += 4) {
         float v[4][4];
 #pragma unroll
@@ -214,67 +263,82 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
       }
     }
   } else {
-    const int t = (warp - 4) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
+    const int slice = (warp - 4) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
     const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;
     const uint64_t sl22 = pack2(sl2, sl2);
-    const uint32_t st = tmem + ((uint32_t)(quarter * 32) << 16) + t * 256;
-    int n0 = 0, cnt = 0, nu = 0;
-    while (!*abort_flag && next()) {
-      float w = 0.f;
-      for (int q = t; q < p.nqt && !*abort_flag; q += 2, cnt++) {
-        const int buf = cnt & 1, s = (n0 + q) % LST, nv = min(p.rpt, nrows - q * p.rpt);
-        if (!wait_bar(bar(B_SF + 2 * t + buf), (cnt >> 1) & 1)) *abort_flag = 1;
+    const uint32_t st = tmem + ((uint32_t)(quarter * 32) << 16) + slice * 32;
+    int n = 0, nu = 0;   // query tiles and units so far
+    while (!*abort_flag && sh.next()) {
+      const bool two = sh.nk == 2;
+      float w[2] = {0.f, 0.f};   // this lane's key of each tile
+      for (int q = 0; q < p.nqt && !*abort_flag; q++, n++) {
+        const int s = n % LST, buf = n & 1;
+        const bool live = slice * 32 < min(p.rpt, nrows - q * p.rpt);
+        if (!wait_bar(bar(B_LF + s), (n / LST) & 1)) *abort_flag = 1;
+        if (!wait_bar(bar(B_SF + buf), (n >> 1) & 1)) *abort_flag = 1;
         tc::tc_fence_after();
-        float sv[QT];
+        // this tile's share first: the long sum has one term per tile.  16 columns at a time: 32 of both keys would not
+        // fit the 96 registers of 20 warps (the spills doubled the time)
+        uint64_t a0[2] = {0ull, 0ull}, a1[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < QT; c += 32)
-          if (c < nv) tmem_ld32_nowait(st + buf * 128 + c, sv + c);
+        for (int c = 0; c < 32; c += 16) {
+          float s0[16], s1[16];
+          if (live) {
+            tmem_ld16_nowait(st + buf * 128 + c, s0);
+            if (two) tmem_ld16_nowait(st + 256 + buf * 128 + c, s1);
+            wait_ld16(s0);
+            if (two) wait_ld16(s1);
+          }
+          if (c == 16) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(B_SE + buf));
+          }
+          if (!live) continue;
 #pragma unroll
-        for (int c = 0; c < QT; c += 32)
-          if (c < nv) wait_ld32(sv + c);
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B_SE + 2 * t + buf));
-        if (!wait_bar(bar(B_LF + s), ((n0 + q) / LST) & 1)) *abort_flag = 1;
-        uint64_t acc[2] = {0ull, 0ull};   // this tile's share first: the long sum has one term per tile
-#pragma unroll
-        for (int c = 0; c < QT; c += 32) {
-          if (c >= nv) continue;
-#pragma unroll
-          for (int e = c; e < c + 32; e += 4) {
-            const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(l2s + s * QT + e);
+          for (int e = 0; e < 16; e += 4) {
+            const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(l2s + s * QT + slice * 32 + c + e);
             float x0, x1, x2, x3;
-            unpack2(fma2(pack2(sv[e], sv[e + 1]), sl22, nl.x), x0, x1);
-            unpack2(fma2(pack2(sv[e + 2], sv[e + 3]), sl22, nl.y), x2, x3);
-            acc[0] = add2(acc[0], pack2(ex2(x0), ex2(x1)));
-            acc[1] = add2(acc[1], pack2(ex2(x2), ex2(x3)));
+            unpack2(fma2(pack2(s0[e], s0[e + 1]), sl22, nl.x), x0, x1);
+            unpack2(fma2(pack2(s0[e + 2], s0[e + 3]), sl22, nl.y), x2, x3);
+            a0[0] = add2(a0[0], pack2(ex2(x0), ex2(x1)));
+            a0[1] = add2(a0[1], pack2(ex2(x2), ex2(x3)));
+            if (two) {
+              unpack2(fma2(pack2(s1[e], s1[e + 1]), sl22, nl.x), x0, x1);
+              unpack2(fma2(pack2(s1[e + 2], s1[e + 3]), sl22, nl.y), x2, x3);
+              a1[0] = add2(a1[0], pack2(ex2(x0), ex2(x1)));
+              a1[1] = add2(a1[1], pack2(ex2(x2), ex2(x3)));
+            }
           }
         }
+        float u, v;
+        unpack2(add2(a0[0], a0[1]), u, v);
+        w[0] += u + v;
+        unpack2(add2(a1[0], a1[1]), u, v);
+        w[1] += u + v;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(B_LE + s));
-        float a0, a1;
-        unpack2(add2(acc[0], acc[1]), a0, a1);
-        w += a0 + a1;
       }
-      n0 += p.nqt;
-      // lane 1's sums to lane 0, warp by warp
+      // the four column slices of a key's sum: the first one's warp adds and writes
       const int cs = nu & 1;
-      float* slot = comb + cs * KT + key;
-      if (t == 1) {
-        if (nu >= 2 && !wait_bar(bar(B_CE + cs), ((nu >> 1) & 1) ^ 1)) *abort_flag = 1;
-        *slot = w;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B_CF + cs));
-      } else {
-        if (!wait_bar(bar(B_CF + cs), (nu >> 1) & 1)) *abort_flag = 1;
-        w += *slot;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B_CE + cs));
-        if (k0 + key < T && !*abort_flag) {
-          float* dst = p.a.weights + ((size_t)b * p.a.nkv + g) * p.a.t_cap + k0 + key;
-          *dst = p.a.accumulate ? *dst + w : w;
-        }
+      float* slot = comb + cs * 6 * KT + key;
+      if (nu >= 2 && !wait_bar(bar(B_CE + cs), ((nu >> 1) & 1) ^ 1)) *abort_flag = 1;
+      if (slice > 0) {
+        slot[(slice - 1) * 2 * KT] = w[0];
+        slot[((slice - 1) * 2 + 1) * KT] = w[1];
       }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(B_CF + cs));
+      if (slice == 0) {
+        if (!wait_bar(bar(B_CF + cs), (nu >> 1) & 1)) *abort_flag = 1;
+        float* dst = p.a.weights + ((size_t)sh.b * p.a.nkv + sh.g) * p.a.t_cap + sh.k0 + key;
+        for (int t = 0; t < sh.nk; t++, dst += KT) {
+          const float sum = ((w[t] + slot[t * KT]) + slot[(2 + t) * KT]) + slot[(4 + t) * KT];
+          if (sh.k0 + t * KT + key < sh.T && !*abort_flag) *dst = p.a.accumulate ? *dst + sum : sum;
+        }
+        __syncwarp();
+      }
+      if (lane == 0) tc::mbar_arrive(bar(B_CE + cs));
       nu++;
     }
   }
@@ -310,8 +374,6 @@ cudaError_t launch_ctx_weights_tc(const CtxWeights& a, int num_sms, cudaStream_t
   p.npt = std::min(QT / p.grp, a.L);
   p.rpt = p.npt * p.grp;
   p.nqt = ceil_div(a.L, p.npt);
-  p.key_tiles = ceil_div(a.t_cap, KT);
-  p.units = a.batch * a.nkv * p.key_tiles;
   const uint64_t row = (uint64_t)a.h * 2;
   const uint64_t kd[2] = {(uint64_t)a.h, (uint64_t)a.batch * 2 * a.nkv * a.t_cap}, ks[1] = {row};
   const uint32_t kb[2] = {64u, (uint32_t)KT};
@@ -321,7 +383,7 @@ cudaError_t launch_ctx_weights_tc(const CtxWeights& a, int num_sms, cudaStream_t
   const uint32_t qb[4] = {64u, (uint32_t)p.grp, (uint32_t)p.npt, 1u};
   if (e == cudaSuccess) e = make_tmap_nd(&p.tm_q, a.q, 4, qd, qs, qb);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(p.units, num_sms);
+  const int grid = (int)std::min<long long>((long long)a.batch * a.nkv * ceil_div(a.t_cap, KT), num_sms);
   return a.h == 128 ? launch_k(weights_tc_kernel<128>, grid, kThreads, Lay<128>::BYTES, st, p)
                     : launch_k(weights_tc_kernel<64>, grid, kThreads, Lay<64>::BYTES, st, p);
 }
