@@ -269,7 +269,6 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     const uint32_t st = tmem + ((uint32_t)(quarter * 32) << 16) + slice * 32;
     int n = 0, nu = 0;   // query tiles and units so far
     while (!*abort_flag && sh.next()) {
-      const bool two = sh.nk == 2;
       float w[2] = {0.f, 0.f};   // this lane's key of each tile
       for (int q = 0; q < p.nqt && !*abort_flag; q++, n++) {
         const int s = n % LST, buf = n & 1;
@@ -285,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
           float s0[16], s1[16];
           if (live) {
             tmem_ld16_nowait(st + buf * 128 + c, s0);
-            if (two) tmem_ld16_nowait(st + 256 + buf * 128 + c, s1);
+            tmem_ld16_nowait(st + 256 + buf * 128 + c, s1);   // of a single tile: whatever is there, not used
             wait_ld16(s0);
-            if (two) wait_ld16(s1);
+            wait_ld16(s1);
           }
           if (c == 16) {
             tc::tc_fence_before();
@@ -303,12 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
             unpack2(fma2(pack2(s0[e + 2], s0[e + 3]), sl22, nl.y), x2, x3);
             a0[0] = add2(a0[0], pack2(ex2(x0), ex2(x1)));
             a0[1] = add2(a0[1], pack2(ex2(x2), ex2(x3)));
-            if (two) {
-              unpack2(fma2(pack2(s1[e], s1[e + 1]), sl22, nl.x), x0, x1);
-              unpack2(fma2(pack2(s1[e + 2], s1[e + 3]), sl22, nl.y), x2, x3);
-              a1[0] = add2(a1[0], pack2(ex2(x0), ex2(x1)));
-              a1[1] = add2(a1[1], pack2(ex2(x2), ex2(x3)));
-            }
+            unpack2(fma2(pack2(s1[e], s1[e + 1]), sl22, nl.x), x0, x1);
+            unpack2(fma2(pack2(s1[e + 2], s1[e + 3]), sl22, nl.y), x2, x3);
+            a1[0] = add2(a1[0], pack2(ex2(x0), ex2(x1)));
+            a1[1] = add2(a1[1], pack2(ex2(x2), ex2(x3)));
           }
         }
         float u, v;
