@@ -6,7 +6,6 @@
 // each prefix key is read once per kv head and row tile instead of once per request.  The own context and the block
 // are the ordinary attention of one request.  Both parts leave unnormalised partials (o, m, l) per split of their keys;
 // the softmax of a row is put together from them in split order (deterministic, no atomics).
-#include <cstdlib>
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
 
@@ -284,12 +283,24 @@ static int mma_splits(long base, int kt, int slots) {
 SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms) {
   SharedPlan pl{};
   const int grp = nq / nkv, pre_rows = batch * L * grp, own_rows = L * grp, own_keys = t_cap + lb;
-  // rows of the tensor maps are 32-bit coordinates
-  const bool own_tma = (long long)batch * 2 * nkv * t_cap < INT32_MAX && (long long)batch * nkv * lb < INT32_MAX;
-  const bool pre_tma = (long long)2 * nkv * p_cap < INT32_MAX;
-  const int lane_rows = grp <= 128 ? 128 / grp * grp : 0;   // whole positions
-  pl.pre_tc = p_cap && pre_tma && lane_rows && !getenv("FPD_MMA");
-  pl.own_tc = own_keys && own_tma && lane_rows && !getenv("FPD_MMA") && !getenv("FPD_MMA_OWN");
+  // tcgen05 needs whole positions in 128 rows and tensor maps whose rows are 32-bit coordinates
+  const int lane_rows = grp <= 128 ? 128 / grp * grp : 0;
+  const bool own_tma = lane_rows && (long long)batch * 2 * nkv * t_cap < INT32_MAX && (long long)batch * nkv * lb < INT32_MAX;
+  const bool pre_tma = lane_rows && (long long)2 * nkv * p_cap < INT32_MAX;
+  // Below two 64 x 64 tiles of h = 128 per resident CTA the whole call goes to mma.sync, which has no tensor memory, descriptors
+  // or rings to set up: 16 rows over 512 + 16 keys 8.6 against 11.4 us, 4 x 16 rows at h = 64 over 64 + 16 keys 5.9 against
+  // 9.4; above it tcgen05 wins (105 rows over 4999 keys 16.7 against 20.3, 512 rows over 2048 24.5 against 43).
+  const long long tiles64 = (long long)nkv * ceil_div(pre_rows, QT) * ceil_div(p_cap, KT) +
+                            (long long)nkv * batch * ceil_div(own_rows, QT) * ceil_div(own_keys, KT);
+  const bool small = tiles64 * h <= 128 * 4ll * num_sms;
+  pl.pre_tc = p_cap && pre_tma && !small;
+  // Own parts of at most one 64-row tile, several per SM: each costs its run on tcgen05 about 8 us besides 1.1 us a tile of
+  // 128 keys; on mma.sync 0.8 us a tile of 64 keys and a kernel more (64 text blocks with contexts up to 512: 332 against 309
+  // us; up to 2048: 137 against 168).  With fewer rows or runs the kernels are level or tcgen05 wins.
+  const double own_runs = (double)nkv * batch / num_sms;
+  const bool own_mma = own_rows > 32 && own_rows <= QT && own_runs > 1 &&
+                       own_runs * 0.8 * ceil_div(own_keys, KT) + 6 < own_runs * (8 + 1.1 * (ceil_div(t_cap, 128) + ceil_div(lb, 128)));
+  pl.own_tc = own_keys && own_tma && !small && !(own_mma && (pl.pre_tc || !p_cap));
   pl.pre_tiles = p_cap ? ceil_div(pre_rows, pl.pre_tc ? 2 * lane_rows : QT) : 0;
   pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 2 * lane_rows : QT) : 0;
   const long pre_units = (long)pl.pre_tiles * nkv, own_units = (long)pl.own_tiles * nkv * batch;
@@ -307,7 +318,8 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
     // part's runs, the average over the SMs, and the merge's reads.
     const bool pair = pre_rows > lane_rows;
     const double kTile = (pair ? 2.2 : 1.1) * h / 128, kOwn = 1.1 * h / 128, kSeg = 5.0;   // us
-    const double part_us = (double)batch * L * nq * h * 8 / 3e6;                            // us per partial of every row
+    // us per partial of every row: written and read at 3 TB/s, and the merge's own step
+    const double part_us = (double)batch * L * nq * h * 8 / 3e6 + (pair ? 0.2 : 0.4);
     const double own_us = own_segs * (kSeg + kOwn * own_kt);
     const long total = pre_units * pre_kt;
     double best = 0;
@@ -318,10 +330,9 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
         pl.pre_runs = (int)runs;
       }
     };
-    if (getenv("FPD_S")) { pl.pre_runs = pre_units * atoi(getenv("FPD_S")); } else
     for (long s = 1; s <= pre_kt && (s == 1 || pre_units * s <= num_sms); s++)
       if (pre_units * s <= num_sms) consider(pre_units * s, kSeg + kTile * ceil_div(pre_kt, (int)s), s);
-    if (!getenv("FPD_S") && total >= num_sms) consider(num_sms, 2 * kSeg + kTile * total / num_sms, (double)num_sms / pre_units + 1);
+    if (total >= num_sms) consider(num_sms, 2 * kSeg + kTile * total / num_sms, (double)num_sms / pre_units + 1);
     // a unit's tiles span at most ceil(runs / units) + 1 of the even runs (one less when the runs divide evenly), and no
     // more runs than it has tiles; a unit with one lane's rows leaves two partials per run
     const int pieces = (int)ceil_div(pl.pre_runs, (int)pre_units) + (pl.pre_runs % pre_units ? 1 : 0);

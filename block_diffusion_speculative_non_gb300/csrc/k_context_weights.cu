@@ -5,7 +5,6 @@
 // The sum runs over the query rows of one key, so keys take the product's row side: a warp holds 16 keys as A
 // fragments for the whole kernel and streams the query rows past them; the exponentials of a key stay in the quad of
 // lanes that owns it, and no intermediate leaves the registers.  One CTA owns its keys: no atomics, a fixed order.
-#include <cstdlib>
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
 
@@ -126,7 +125,12 @@ cudaError_t ctx_weights_init_attributes() {
 }
 
 cudaError_t launch_ctx_weights(const CtxWeights& a, int num_sms, cudaStream_t st) {
-  if (ctx_weights_tc_supported(a) && (getenv("FPD_WTC") || a.L * (a.nq / a.nkv) > 64)) return launch_ctx_weights_tc(a, num_sms, st);
+  // tcgen05 for more than 128 rows (256 rows over 512 keys 7.2 against 9.7 us), and for fewer from about 1536 64-key tiles of
+  // contexts that are not short (8 x 64 rows over 2048 keys 9.4 against 12.7, 64 rows over 16384 10.7 against 16.4); below
+  // that its setup costs more than the tiles (64 rows over 512 keys 4.1 against 5.9, 64 x 64 rows over 256 13.4 against 15.5)
+  const long long tiles = (long long)a.batch * a.nkv * ceil_div(a.t_cap, KT) * ceil_div(a.L * (a.nq / a.nkv), QT);
+  if (ctx_weights_tc_supported(a) && (a.L * (a.nq / a.nkv) > 128 || (tiles >= 1536 && a.t_cap >= 512)))
+    return launch_ctx_weights_tc(a, num_sms, st);
   const int key_tiles = ceil_div(a.t_cap, KT);
   const int grid = a.batch * a.nkv * key_tiles;
   return a.h == 128 ? launch_k(weights_mma_kernel<128>, grid, NWARP * 32, sizeof(WeightSmem<128>), st, a, key_tiles)

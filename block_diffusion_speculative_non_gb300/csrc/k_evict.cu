@@ -2,27 +2,27 @@
 // kv head) keep the last `recent` ones and, of the others, the `budget - recent` with the largest weight (ties: the
 // lower position), in the order of their positions.
 //
-// Two kernels.  evict_select_kernel: one CTA per (layer, request, kv head) finds the smallest kept weight by radix
-// selection on an order-preserving integer key (11 + 11 + 10 bits, shared-memory histograms) and turns it into the
-// list of kept positions with one ordered scan; it also moves the weights.  evict_move_kernel: copies the kept K and V
-// rows.  The result is a function of the inputs alone (integer counts, fixed order).
+// Two kernels.  evict_select_kernel: one CTA per (layer, request, kv head) finds the smallest kept weight and turns it into
+// the list of kept positions with one ordered scan; it also moves the weights.  The weight is found by radix selection on
+// an order-preserving integer key (11 + 11 + 10 bits, shared-memory histograms); up to 256 positions are ranked directly
+// instead, four threads a position.
+// evict_copy_kernel / evict_inplace_kernel: the kept K and V rows.  The result is a function of the inputs alone (integer
+// counts, fixed order).
 #include "fpd_context.cuh"
 
 namespace fpd {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kPerThread = 16;
-constexpr int kStage = kSelThreads * kPerThread;   // weights held in shared memory at a time
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kStage = 16 * kSelThreads;           // weights held in shared memory at a time: 16 rows of 32 per warp
 constexpr int kBins = 2048;
-// thread t reads positions 16 t ..: one word of padding per 32 keeps the warp's reads on distinct banks
-__device__ __forceinline__ int stage_at(int p) { return p + (p >> 5); }
+constexpr int kRank = 256;
 
 struct SelSmem {
-  float stage[kStage + kStage / 32];
+  float stage[kStage];
   uint32_t hist[kBins];
-  uint64_t warp_sum[32];
+  uint64_t warp_sum[kSelWarps];
   uint32_t bin, below;
 };
 
@@ -59,44 +59,73 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sum, u
   return inc - v + (warp ? warp_sum[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ Evict e) {
+// 32 registers a thread, so that two CTAs share an SM: this kernel is a chain of short steps between barriers.  Loops are
+// left rolled: unrolled, the one pass that a small context makes through the code was mostly instruction fetch.
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ Evict e) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(16) unsigned char smem_raw[];
   SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
-  const int tid = threadIdx.x, head = blockIdx.x, b = (head / e.nkv) % e.batch;
-  const int T = clamp_ctx(e.ctx_len[b], e.t_cap), m = min(T, e.budget);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.x, b = (head / e.nkv) % e.batch;
   const float* w = e.weights + (size_t)head * e.t_cap;
-  float* ow = e.out_weights + (size_t)head * e.out_cap;
-  int32_t* kept = e.kept + (size_t)head * e.budget;
+  for (int i = tid; i < kBins; i += kSelThreads) sm.hist[i] = 0;
+  const int T = clamp_ctx(e.ctx_len[b], e.t_cap), m = min(T, e.budget);
   if (tid == 0 && head < e.batch * e.nkv && head % e.nkv == 0) e.old_len[b] = T;   // layer 0, kv head 0 of each request
-
   const int old = T > e.budget ? T - e.recent : 0;   // positions that compete; below the budget all stay
   const int need = T > e.budget ? e.budget - e.recent : 0;
-  const bool staged = T <= kStage;
-  if (staged) {
-    for (int p = tid; p < T; p += kSelThreads) sm.stage[stage_at(p)] = w[p];
+  const bool staged = T <= kStage, ranked = T <= kRank;
+  __syncthreads();
+  if (staged) {   // the weights, and the histogram of their keys' upper bits on the way
+#pragma unroll 4
+    for (int p = tid; p < T; p += kSelThreads) {
+      const float v = w[p];
+      sm.stage[p] = v;
+      if (!ranked && p < old) atomicAdd(&sm.hist[weight_key(v) >> 21], 1u);
+    }
     __syncthreads();
   }
   // ---- the need-th largest key: `thr`, of which the first `ties` positions stay ----
   uint32_t thr = 0xFFFFFFFFu;
   int ties = 0;
-  if (need > 0) {
+  if (need > 0 && ranked) {
+    const int p = tid >> 2, part = tid & 3;
+    if (warp * 8 < old) {
+      const uint32_t k = p < old ? weight_key(sm.stage[p]) : 0u;
+      int greater = 0, before = 0;
+      for (int q = part; q < old; q += 4) {
+        const uint32_t o = weight_key(sm.stage[q]);
+        greater += o > k;
+        before += o == k && q < p;
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        greater += __shfl_xor_sync(0xffffffffu, greater, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+      }
+      if (part == 0 && p < old && greater + before == need - 1) {   // exactly one position has this rank
+        sm.bin = k;
+        sm.below = need - greater;
+      }
+    }
+    __syncthreads();
+    thr = sm.bin;
+    ties = (int)sm.below;
+  } else if (need > 0) {
     uint32_t prefix = 0;
     int rest = need;
 #pragma unroll 1
     for (int pass = 0; pass < 3; pass++) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kSelThreads) sm.hist[i] = 0;
-      __syncthreads();
-      for (int p = tid; p < old; p += kSelThreads) {
-        const uint32_t k = weight_key(staged ? sm.stage[stage_at(p)] : w[p]);
-        if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-      }
+      if (pass > 0 || !staged)
+        for (int p = tid; p < old; p += kSelThreads) {
+          const uint32_t k = weight_key(staged ? sm.stage[p] : w[p]);
+          if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+        }
       __syncthreads();
       // thread t owns bins kBins - 1 - 2 t and the one below: sums run from the largest key down
       const int hi = kBins - 1 - 2 * tid;
       const uint32_t c1 = sm.hist[hi], c0 = sm.hist[hi - 1];
+      sm.hist[hi] = sm.hist[hi - 1] = 0;   // for the next pass
       uint64_t total;
       const uint32_t above = (uint32_t)block_scan(c1 + c0, sm.warp_sum, total);
       if (above < (uint32_t)rest && above + c1 + c0 >= (uint32_t)rest) {
@@ -112,40 +141,46 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     ties = rest;
   }
   // ---- ordered list of the kept positions, the weights moved along ----
+  // A warp takes up to 16 rows of 32 consecutive positions; lane i keeps row i's masks of the positions that stay outright
+  // and of those equal to thr, whose turn the counts before them decide.
+  float* ow = e.out_weights + (size_t)head * e.out_cap;
+  int32_t* kept = e.kept + (size_t)head * e.budget;
   uint64_t base = 0;   // kept outright so far | equal to thr so far << 32
 #pragma unroll 1
   for (int c0 = 0; c0 < T; c0 += kStage) {
     const int n = min(kStage, T - c0);
     if (!staged) {
       __syncthreads();
-      for (int p = tid; p < n; p += kSelThreads) sm.stage[stage_at(p)] = w[c0 + p];
+#pragma unroll 4
+      for (int p = tid; p < n; p += kSelThreads) sm.stage[p] = w[c0 + p];
       __syncthreads();
     }
-    const int p0 = tid * kPerThread;
-    uint32_t sure = 0, tie = 0;
-#pragma unroll
-    for (int i = 0; i < kPerThread; i++) {
-      if (p0 + i >= n) break;
-      const int p = c0 + p0 + i;
-      const uint32_t k = weight_key(sm.stage[stage_at(p0 + i)]);
-      if (p >= old || k > thr) sure |= 1u << i;
-      else if (k == thr && need > 0) tie |= 1u << i;
+    const int rows = (n + kSelThreads - 1) / kSelThreads, r0 = warp * rows * 32;
+    uint32_t my_sure = 0, my_tie = 0;
+    for (int i = 0; i < rows && r0 + i * 32 < n; i++) {
+      const int at = r0 + i * 32 + lane, p = c0 + at;
+      const uint32_t k = at < n ? weight_key(sm.stage[at]) : 0u;
+      const uint32_t sure = __ballot_sync(0xffffffffu, at < n && (p >= old || k > thr));
+      const uint32_t tie = __ballot_sync(0xffffffffu, at < n && p < old && k == thr && need > 0);
+      if (lane == i) {
+        my_sure = sure;
+        my_tie = tie;
+      }
     }
     uint64_t total;
     const uint64_t before =
-        base + block_scan((uint64_t)__popc(sure) | ((uint64_t)__popc(tie) << 32), sm.warp_sum, total);
-    int at_sure = (int)(uint32_t)before, at_tie = (int)(before >> 32);
+        base + block_scan((uint64_t)__popc(my_sure) | ((uint64_t)__popc(my_tie) << 32), sm.warp_sum, total);
     // in place, slot i of this chunk is at or before its position: every weight it can overwrite has been staged
-#pragma unroll
-    for (int i = 0; i < kPerThread; i++) {
-      const bool s = (sure >> i) & 1, t = (tie >> i) & 1;
-      if (s || (t && at_tie < ties)) {
-        const int slot = at_sure + min(at_tie, ties);
-        kept[slot] = c0 + p0 + i;
-        ow[slot] = sm.stage[stage_at(p0 + i)];
+    for (int i = 0; i < rows && r0 + i * 32 < n; i++) {
+      const uint32_t sure = __shfl_sync(0xffffffffu, my_sure, i), tie = __shfl_sync(0xffffffffu, my_tie, i);
+      const uint64_t bf = __shfl_sync(0xffffffffu, before, i);
+      const uint32_t lt = (1u << lane) - 1;
+      const int at_tie = (int)(bf >> 32) + __popc(tie & lt);
+      if (((sure >> lane) & 1) || (((tie >> lane) & 1) && at_tie < ties)) {
+        const int slot = (int)(uint32_t)bf + __popc(sure & lt) + min(at_tie, ties);
+        kept[slot] = c0 + r0 + i * 32 + lane;
+        ow[slot] = sm.stage[r0 + i * 32 + lane];
       }
-      at_sure += s;
-      at_tie += t;
     }
     base += total;
   }
