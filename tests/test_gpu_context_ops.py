@@ -113,6 +113,16 @@ ATTN = {
     "many_rows": (24, 16, 8, 1, 128, 700, 704, [i * 5 for i in range(24)], 120, True),
     "wide_group": (9, 1, 128, 2, 128, 3000, 3000, [i for i in range(9)], 9, True),
     "long_prefix": (2, 1, 8, 2, 128, 70001, 70016, [500, 2], 512, True),
+    # sizes on each side of the rules between the kernels: own parts on mma.sync beside the prefix on tcgen05, runs that span
+    # units, one call without a prefix on tcgen05, heads per kv head that no 128 rows hold
+    "many_text_blocks": (40, 16, 32, 8, 128, 1000, 1001, [(37 * i) % 65 for i in range(40)], 64, True),
+    "many_text_blocks_h64": (40, 16, 16, 8, 64, 2100, 2100, [(37 * i) % 65 for i in range(40)], 64, False),
+    "spanning_runs": (4, 385, 32, 8, 128, 1500, 1600, [128, 0, 5, 77], 128, True),
+    "no_prefix_tc": (12, 40, 16, 4, 128, 0, 0, [(91 * i) % 700 for i in range(12)], 700, True),
+    "prefix_only_tc": (16, 16, 20, 4, 128, 3001, 3001, [0] * 16, 0, False),
+    "group_130": (3, 2, 130, 1, 128, 900, 900, [70, 0, 9], 70, True),
+    "group_7_h64": (30, 16, 14, 2, 64, 1700, 1700, [i for i in range(30)], 31, True),
+    "last_lane_only": (9, 15, 16, 4, 128, 2500, 2500, [i * 30 for i in range(9)], 256, True),
 }
 
 
@@ -229,6 +239,80 @@ def test_captured_call_follows_lengths_on_the_device(pkg, name):
         p.check()
 
 
+@pytest.mark.parametrize("name", ["prefix_only_tc", "no_prefix_tc"])
+def test_nothing_to_attend_to_on_large_calls(pkg, name):
+    """The same sizes with every length 0: no keys but the block's, or none at all."""
+    p = Problem(*ATTN[name], seed=14)
+    p.run(pkg)
+    p.P, p.lens = 0, [0] * p.shape[0]
+    for t in (p.p_len, p.c_len):
+        if t is not None:
+            t.zero_()
+    p.run(pkg)
+    p.check()
+    assert pkg.fpd_device_status() == 0
+
+
+def test_workspace_at_any_16_byte_offset(pkg):
+    for name in ("text_block", "many_text_blocks"):
+        p = Problem(*ATTN[name], seed=15)
+        n = pkg.fpd_shared_attention_workspace_bytes(*p.shape, p.p_cap, p.t_cap)
+        raw = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device=DEV)
+        for off in (16, 48, 112):
+            p.out.fill_(math.nan)
+            pkg.fpd_shared_attention(*p.shape, p.layer, p.q, p.kb, p.vb, p.prefix, p.p_cap, p.p_len, p.store, p.t_cap,
+                                     p.c_len, p.out, p.lse, raw.data_ptr() + off, n)
+            p.check()
+        assert (raw[n + 112:] == 0xFF).all()
+
+
+def test_stores_past_32_bit_offsets(pkg):
+    """The layer, request and positions in use start past 2^32 elements; everything below them is another layer."""
+    B, L, nq, nkv, h, cap = 2, 16, 8, 2, 128, 5_000_000
+    need = 2 * B * 2 * nkv * cap * h * 2
+    if torch.cuda.mem_get_info()[0] < need + (4 << 30):
+        pytest.skip("needs %d GB" % (need >> 30))
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    store = torch.empty(2, B, 2, nkv, cap, h, dtype=BF, device=DEV)
+    lens = [1500, 1333]
+    for b, n in enumerate(lens):
+        store[1, b, 0, :, :n] = unit(gen, nkv, n, h).to(BF)
+        store[1, b, 1, :, :n] = torch.randn(nkv, n, h, device=DEV, generator=gen).to(BF)
+    q = unit(gen, B * L, nq, h).to(BF)
+    small = store[1, :, :, :, :1600].contiguous()
+    want, lse_want, vmax = ref.attention(q, None, 0, small, lens, None, None, B, L, nkv)
+    out, lse = torch.empty(B * L, nq, h, dtype=BF, device=DEV), torch.empty(B * L, nq, device=DEV)
+    # as the requests' own store, and request by request as a prefix (the store of one request, layer 2 + b of its kind)
+    ws = torch.empty(max(pkg.fpd_shared_attention_workspace_bytes(B, L, nq, nkv, h, 0, cap),
+                         pkg.fpd_shared_attention_workspace_bytes(1, L, nq, nkv, h, cap, 0)), dtype=torch.uint8, device=DEV)
+    pkg.fpd_shared_attention(B, L, nq, nkv, h, 1, q, None, None, None, 0, None, store, cap, i32(lens), out, lse, ws, ws.numel())
+    bound = 2.0 ** -8 * want.abs() + 2 * 2.0 ** -14 * vmax[..., None]
+    assert ((out.double() - want).abs() <= bound).all() and (lse.double() - lse_want).abs().max() < 2.0 ** -14
+    for b in range(B):
+        o, l = torch.empty(L, nq, h, dtype=BF, device=DEV), torch.empty(L, nq, device=DEV)
+        pkg.fpd_shared_attention(1, L, nq, nkv, h, 2 + b, q[b * L:(b + 1) * L].contiguous(), None, None, store, cap, i32(lens[b:b + 1]),
+                                 None, 0, None, o, l, ws, ws.numel())
+        sl = slice(b * L, (b + 1) * L)
+        assert ((o.double() - want[sl]).abs() <= bound[sl]).all()
+    w = torch.full((2, B, nkv, cap), -1.0, device=DEV)
+    pkg.fpd_context_weights(B, L, nq, nkv, h, 1, q, lse, store, cap, i32(lens), w, False)
+    ww = ref.context_weights(q, lse, small, lens, B, L, nkv)
+    assert weights_close(w[1, :, :, :1600], ww) and (w[0] == -1).all() and (w[1, :, :, 1600:] == -1).all()
+    w.clamp_min_(0)
+    budget = 700
+    ews = torch.empty(pkg.fpd_evict_workspace_bytes(2, B, nkv, budget), dtype=torch.uint8, device=DEV)
+    n_d = i32(lens)
+    store[0, :, :, :, :1600] = 0
+    before = store[:, :, :, :, :1600].contiguous()
+    wb = w[..., :1600].cpu().numpy()
+    pkg.fpd_evict_context(2, B, nkv, h, budget, 100, store, cap, w, n_d, store, cap, w, n_d, None, None, ews, ews.numel())
+    bn = before.view(torch.int16).cpu().numpy()
+    o, ow, n, _ = ref.evict(bn, wb, lens, budget, 100, bn, 1600)
+    assert np.array_equal(store[:, :, :, :, :1600].contiguous().view(torch.int16).cpu().numpy(), o)
+    assert np.array_equal(w[..., :1600].cpu().numpy(), ow) and n_d.tolist() == [budget] * B
+    assert pkg.fpd_device_status() == 0
+
+
 def test_two_streams_two_workspaces(pkg):
     a, b = Problem(*ATTN["text_block"], seed=11), Problem(*ATTN["long_block"], seed=12)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
@@ -270,6 +354,16 @@ WEIGHTS = {
     "few_keys_many_rows": (1, 1024, 32, 2, 128, [17], 40),
     "single_token": (8, 1, 32, 8, 128, [2000, 1, 5, 64, 1999, 0, 3, 128], 2048),
     "wide_group": (2, 1, 128, 1, 128, [3000, 65], 3000),
+    # tcgen05: 5 and 3 heads per kv head leave rows of a tile unused, 128 fill it with one position; more requests than a
+    # warp counts at a time, some empty; few rows over long contexts
+    "group_5_tc": (3, 60, 20, 4, 128, [129, 0, 127], 200),
+    "group_3_h64_tc": (2, 100, 6, 2, 64, [257, 300], 300),
+    "wide_group_tc": (2, 3, 128, 1, 128, [700, 65], 700),
+    "many_requests_tc": (40, 40, 16, 4, 128, [(97 * i) % 300 if i % 7 else 0 for i in range(40)], 300),
+    "few_rows_tc": (13, 4, 32, 8, 128, [1100 - 90 * i for i in range(13)], 1111),
+    "few_rows_h64_tc": (26, 1, 16, 8, 64, [(211 * i) % 600 for i in range(26)], 600),
+    "group_130": (2, 2, 130, 1, 128, [100, 65], 130),
+    "nothing_tc": (2, 80, 8, 2, 128, [0, 0], 300),
 }
 
 
@@ -315,6 +409,19 @@ def test_weights_of_large_scores_and_of_rows_without_keys(pkg, name):
     w = torch.zeros(2, B, nkv, p.t_cap, device=DEV)
     run_weights(pkg, p, w)
     assert weights_close(w[1], ref.context_weights(p.q, p.lse, p.store[p.layer], p.lens, B, L, nkv), 20.0)
+
+
+@pytest.mark.parametrize("name", ["ragged", "many_requests_tc"])
+def test_a_nan_query_spoils_its_own_request_only(pkg, name):
+    p = weight_problem(name, seed=8)
+    B, L, nq, nkv, h = p.shape
+    w = torch.zeros(2, B, nkv, p.t_cap, device=DEV)
+    run_weights(pkg, p, w)
+    clean = w.clone()
+    p.q[L + 1] = math.nan       # request 1
+    run_weights(pkg, p, w)
+    keep = [b for b in range(B) if b != 1]
+    assert torch.equal(w[:, keep], clean[:, keep]) and w[1, 1, :, :p.lens[1]].isnan().all()
 
 
 def test_rows_hand_out_one_in_all(pkg):
