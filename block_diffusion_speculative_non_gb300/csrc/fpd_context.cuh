@@ -30,7 +30,9 @@ struct SharedPlan {
   bool pre_tc, own_tc;
   int pre_tiles, pre_splits;            // row units of a kv head (0: no such part), partials of a row
   int own_tiles, own_splits;            // the same per request
-  int pre_runs, tc_grid;                // CTAs that share the prefix's tiles, CTAs of the tcgen05 kernel
+  int pre_runs, pre_pieces;             // CTAs that share the prefix's tiles, most of them in one unit
+  int own_cost;                         // an own run in the prefix's key tiles, 0: not counted when the prefix is shared out
+  int tc_grid;                          // CTAs of the tcgen05 kernel
   int splits() const { return pre_splits + own_splits; }
 };
 SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms);

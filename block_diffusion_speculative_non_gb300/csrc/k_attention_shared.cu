@@ -335,8 +335,17 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
     if (total >= num_sms) consider(num_sms, 2 * kSeg + kTile * total / num_sms, (double)num_sms / pre_units + 1);
     // a unit's tiles span at most ceil(runs / units) + 1 of the even runs (one less when the runs divide evenly), and no
     // more runs than it has tiles; a unit with one lane's rows leaves two partials per run
-    const int pieces = (int)ceil_div(pl.pre_runs, (int)pre_units) + (pl.pre_runs % pre_units ? 1 : 0);
-    pl.pre_splits = std::min(pre_kt, pieces);
+    pl.pre_pieces = (int)ceil_div(pl.pre_runs, (int)pre_units) + (pl.pre_runs % pre_units ? 1 : 0);
+    if (own_segs && pl.pre_runs == num_sms && total >= 16l * num_sms) {
+      // own runs are counted at about 0.6 of the tiles they may have; the kernel gives that up where shorter contexts would
+      // leave more pieces than this
+      const long even = own_segs / num_sms;
+      const long w = std::min<long>((long)((kSeg + 0.6 * kOwn * own_kt) / kTile + 0.5), total / (2l * num_sms * (even + 1) - own_segs));
+      pl.own_cost = (int)w;
+      const long shortest = (total + w * own_segs) / num_sms - 1 - w * (even + 1);
+      pl.pre_pieces = std::max(pl.pre_pieces, (int)((pre_kt + shortest - 1) / shortest) + 1);
+    }
+    pl.pre_splits = pl.pre_pieces = std::min(pre_kt, pl.pre_pieces);
     if ((pre_rows - 1) % (2 * lane_rows) < lane_rows) pl.pre_splits *= 2;
   }
   if (pl.pre_tc || pl.own_tc) pl.tc_grid = (int)std::min<long>(num_sms, pl.pre_runs + own_segs);

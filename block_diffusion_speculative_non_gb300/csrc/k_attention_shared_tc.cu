@@ -17,7 +17,7 @@
 // hold the same rows and take the even and the odd key tiles: such a unit is a read of the keys, and two key streams keep
 // the copies in flight.  The prefix's (unit, key tile) space is cut into one contiguous run of tiles per CTA, so that all
 // SMs finish together whatever the number of rows; a run that spans units leaves a partial in each.  The own part's units
-// follow, dealt out from the other end.
+// follow, dealt out from the other end; where every CTA has a run, the prefix's runs are shorter by what a CTA has of them.
 #include <cstring>
 
 #include "attn_tc_prims.cuh"
@@ -89,6 +89,8 @@ struct TcArgs {
   int grp, npt, rpt;                     // heads per kv head, positions and rows of a lane
   int pre_tiles, pre_units, pre_slots;   // row pairs per kv head, units, partial slots of a prefix row (0 units: not here)
   int pre_runs;                          // CTAs that share the prefix's tiles
+  int pre_pieces;                        // most runs of a unit
+  int own_cost;                          // an own run in key tiles of the prefix, or 0: even runs
   int own_tiles, own_units, own_splits;  // the same for the own part, with the key splits of a unit
   int own_slot0;                         // first partial slot of the own part
   FastDiv by_grp, by_pre_tiles, by_own_tiles, by_own_units, by_nkv;
@@ -121,7 +123,7 @@ struct Seg {
 // The runs of this CTA, in order.
 struct Walk {
   const TcArgs& p;
-  int P, P_tiles, G, c, own_i;
+  int P, P_tiles, G, c, own_i, W, own_even, own_first;   // own runs: own_even each, one more from CTA own_first on
   long long x, x_end, total;
   int empty_u;      // an empty prefix still marks its partial slots
   __device__ Walk(const TcArgs& p_) : p(p_) {
@@ -130,17 +132,40 @@ struct Walk {
     P_tiles = (P + KT - 1) / KT;
     total = (long long)p.pre_units * P_tiles;
     G = (int)min((long long)p.pre_runs, max(total, 1ll));
+    W = 0;
+    if (p.own_cost && total >= 16ll * G && G == (int)gridDim.x) {
+      const int own_n = p.own_units * p.own_splits;
+      own_even = own_n / G;
+      own_first = G - own_n % G;
+      // no run shorter than half of the average, and no more runs in a unit than there are partial slots
+      W = (int)min((long long)p.own_cost, total / (2ll * G * (own_even + 1) - own_n));
+      const int shortest = (int)((total + (long long)W * own_n) / G) - 1 - W * (own_even + 1);
+      if ((P_tiles + shortest - 1) / shortest + 1 > p.pre_pieces) W = 0;
+    }
     x = c < G ? run_start(c) : 0;
     x_end = c < G ? run_start(c + 1) : 0;
     empty_u = total == 0 ? c : p.pre_units;
     own_i = (int)gridDim.x - 1 - c;
   }
-  // run c starts at tile c total / G; the run that holds tile t is the last one that starts at or before it
+  // run c starts at tile c total / G, or, with own runs that count as W tiles each, where the runs before it end; the run
+  // that holds tile t is the last one that starts at or before it
   // (64-bit divisions cost a few hundred cycles: only where 32 bits do not hold the products)
   __device__ long long run_start(int i) const {
+    if (W) {
+      const long long own_n = p.own_units * p.own_splits;
+      return i * (total + W * own_n) / G - (long long)W * (own_even * i + max(0, i - own_first));
+    }
     return total < (1 << 20) ? (uint32_t)i * (uint32_t)total / (uint32_t)G : i * total / G;
   }
   __device__ int run_of(long long t) const {
+    if (W) {
+      int lo = 0, hi = G;   // run_start(lo) <= t < run_start(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (run_start(mid) <= t) lo = mid; else hi = mid;
+      }
+      return lo;
+    }
     return total < (1 << 20) ? (int)((((uint32_t)t + 1) * (uint32_t)G - 1) / (uint32_t)total) : (int)(((t + 1) * G - 1) / total);
   }
   __device__ void rows(Seg& s, int qp, int nrows) const {
@@ -250,6 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     tc::mbar_init(bar(B_END), 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
+    tc::tma_prefetch(&p.tm_q);
+    if (p.pre_units) tc::tma_prefetch(&p.tm_pre);
+    if (p.own_units && p.a.ck) tc::tma_prefetch(&p.tm_own);
+    if (p.own_units && p.a.lb) {
+      tc::tma_prefetch(&p.tm_kblk);
+      tc::tma_prefetch(&p.tm_vblk);
+    }
   }
   if (warp == 1) {
     tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmemCols);
@@ -617,6 +649,8 @@ cudaError_t launch_shared_tc(const SharedAttn& a, const SharedPlan& pl, cudaStre
     p.pre_units = pl.pre_tiles * a.nkv;
     p.pre_slots = pl.pre_splits;
     p.pre_runs = pl.pre_runs;
+    p.pre_pieces = pl.pre_pieces;
+    p.own_cost = pl.own_cost;
     p.by_pre_tiles.set(p.pre_tiles);
   }
   if (pl.own_tc) {

@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
     tc::mbar_init(bar(B_END), 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
+    tc::tma_prefetch(&p.tm_k);
+    tc::tma_prefetch(&p.tm_q);
   }
   // a query tile of fewer than 128 rows (heads per kv head that do not divide it) leaves the slots' last rows as they are now
   for (int i = threadIdx.x; i < RST * S::TILE / 16; i += kThreads)
