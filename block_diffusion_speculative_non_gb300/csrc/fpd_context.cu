@@ -242,7 +242,7 @@ fpd_status fpd_evict_context(int n_layers, int batch, int n_kv_heads, int head_d
   v.budget = budget;
   v.recent = recent;
   v.in_place = in_place;
-  e = launch_evict(v, sms, (cudaStream_t)stream);
+  e = launch_evict(v, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_error(e, "fpd_evict_context");
   return scope.done(FPD_OK);
 }

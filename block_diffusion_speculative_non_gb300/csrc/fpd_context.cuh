@@ -67,7 +67,7 @@ struct Evict {
   bool in_place;                                    // out_store is store
 };
 cudaError_t evict_init_attributes();
-cudaError_t launch_evict(const Evict& e, int num_sms, cudaStream_t st);
+cudaError_t launch_evict(const Evict& e, cudaStream_t st);
 
 // base[b] = ctx_len[b] (clamped to [0, t_cap]; 0 without one) + pos_offset[b]: the rotary position of a block's first
 // slot.  Without pos_offset the prefix's length stands in for it.

@@ -1,5 +1,6 @@
 // fpd_testing.cu — diagnostic entry points declared in include/fpd_testing.h (single-kernel checks).
 #include "../../include/fpd_testing.h"
+#include "fpd_context.cuh"
 #include "fpd_kernels.cuh"
 
 using namespace fpd;
@@ -275,5 +276,17 @@ extern "C" int fpd_test_attn_plan(int impl, int batch, int L, int nq, int nkv, i
   attn_test_plan(impl, batch, L, nq, nkv, t_cap, num_sms, &s, &c);
   *splits = s;
   *chunk = c;
+  return FPD_OK;
+}
+
+extern "C" int fpd_test_shared_plan(int batch, int L, int block_keys, int nq, int nkv, int head_dim, int prefix_cap,
+                                    int t_cap, int num_sms, int32_t* out) {
+  if (!out || batch < 1 || L < 1 || nkv < 1 || nq % nkv || (head_dim != 64 && head_dim != 128) || prefix_cap < 0 ||
+      t_cap < 0 || num_sms < 1)
+    return FPD_ERR_SHAPE;
+  const SharedPlan pl = shared_attn_plan(batch, L, block_keys, nq, nkv, head_dim, prefix_cap, t_cap, num_sms);
+  const int v[10] = {pl.pre_tc, pl.own_tc, pl.pre_tiles, pl.pre_splits, pl.own_tiles,
+                     pl.own_splits, pl.pre_runs, pl.pre_pieces, pl.own_cost, pl.tc_grid};
+  for (int i = 0; i < 10; i++) out[i] = v[i];
   return FPD_OK;
 }

@@ -265,7 +265,7 @@ cudaError_t evict_init_attributes() {
   return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelSmem));
 }
 
-cudaError_t launch_evict(const Evict& e, int num_sms, cudaStream_t st) {
+cudaError_t launch_evict(const Evict& e, cudaStream_t st) {
   const int heads = e.layers * e.batch * e.nkv;
   cudaError_t err = launch_k(evict_select_kernel, heads, kSelThreads, sizeof(SelSmem), st, e);
   if (err != cudaSuccess) return err;

@@ -117,3 +117,99 @@ def test_selection_rule_of_the_reference():
                                 [4], 2, 0, np.zeros((1, 1, 2, 1, 2, 1), np.int16), 2)
     assert out.reshape(2, 2).tolist() == [[0, 2], [4, 6]] and w.tolist() == [[[[3, 2]]]] and n.tolist() == [2]
     assert kept.tolist() == [[[[0, 2]]]]
+
+
+# ---- how the shared attention cuts its work -------------------------------------------------------------------------
+
+def plan(fpd, batch, L, nq, nkv, h, p_cap, t_cap, blk=True, sms=152):
+    lib = fpd.lib()
+    lib.fpd_test_shared_plan.argtypes = [ctypes.c_int] * 9 + [ctypes.POINTER(ctypes.c_int32)]
+    out = (ctypes.c_int32 * 10)()
+    assert lib.fpd_test_shared_plan(batch, L, L if blk else 0, nq, nkv, h, p_cap, t_cap, sms, out) == 0
+    return dict(zip(("pre_tc", "own_tc", "pre_tiles", "pre_splits", "own_tiles", "own_splits", "pre_runs", "pre_pieces",
+                     "own_cost", "grid"), list(out)))
+
+
+def walk(pl, batch, L, nq, nkv, P, sms=152):
+    """The runs of every CTA of the tcgen05 kernel, as it takes them: (cta, unit, first tile, last tile, slots it writes)."""
+    grp = nq // nkv
+    rpt = 128 // grp * grp
+    units = pl["pre_tiles"] * nkv if pl["pre_tc"] else 0
+    own_n = pl["own_tiles"] * nkv * batch * (pl["own_splits"] // 2) if pl["own_tc"] else 0
+    tiles = -(-P // 128)
+    total, grid = units * tiles, pl["grid"]
+    G = min(pl["pre_runs"], max(total, 1))
+    W = 0
+    if pl["own_cost"] and total >= 16 * G and G == grid:
+        even, first = own_n // G, G - own_n % G
+        W = min(pl["own_cost"], total // (2 * G * (even + 1) - own_n))
+        shortest = (total + W * own_n) // G - 1 - W * (even + 1)
+        if -(-tiles // shortest) + 1 > pl["pre_pieces"]:
+            W = 0
+
+    def start(i):
+        return i * (total + W * own_n) // G - W * (even * i + max(0, i - first)) if W else i * total // G
+
+    def run_of(t):
+        return max(c for c in range(G) if start(c) <= t) if W else ((t + 1) * G - 1) // total
+
+    runs = []
+    for c in range(grid):
+        if total == 0:
+            runs += [(c, u, 0, 0, list(range(pl["pre_splits"]))) for u in range(c, units, grid)]
+        x, end = (start(c), start(c + 1)) if c < G else (0, 0)
+        while x < end:
+            u = x // tiles
+            e = min(end, (u + 1) * tiles)
+            keys = batch * L * grp - u % pl["pre_tiles"] * 2 * rpt <= rpt
+            piece = c - run_of(u * tiles)
+            slots = [2 * piece, 2 * piece + 1] if keys else [piece]
+            if e == (u + 1) * tiles:
+                slots += range(slots[-1] + 1, pl["pre_splits"])
+            runs.append((c, u, x - u * tiles, e - u * tiles, slots))
+            x = e
+    return runs, units, tiles
+
+
+SHAPES = [(1, 16, 32, 8, 128), (8, 16, 32, 8, 128), (64, 16, 32, 8, 128), (4, 385, 32, 8, 128), (16, 1, 32, 8, 128), (3, 7, 20, 4, 128),
+          (2, 200, 8, 1, 64), (30, 33, 14, 2, 64), (9, 15, 16, 4, 128), (200, 16, 8, 8, 128), (5, 61, 128, 1, 128), (1, 1, 130, 1, 64)]
+
+
+@pytest.mark.parametrize("B,L,nq,nkv,h", SHAPES)
+def test_shared_plan_covers_every_tile_and_slot_once(fpd, B, L, nq, nkv, h):
+    """For the planned capacities and every shorter prefix: each key tile of each unit falls in one run, and each partial
+    slot of a unit is written by exactly one run (or marked empty by its last)."""
+    for sms in (152, 148, 20):
+        for p_cap in (1, 100, 1000, 4096, 16384, 65536, 200001):
+            for t_cap in (0, 64, 1000):
+                pl = plan(fpd, B, L, nq, nkv, h, p_cap, t_cap, sms=sms)
+                assert pl["pre_splits"] >= 1 and pl["own_splits"] >= 1
+                if not pl["pre_tc"]:
+                    assert pl["pre_splits"] <= 128
+                    continue
+                assert 1 <= pl["pre_runs"] <= pl["grid"] <= sms
+                for P in sorted({0, 1, 129, p_cap // 7, p_cap // 2, p_cap - 1, p_cap}):
+                    if P > p_cap or P < 0:
+                        continue
+                    runs, units, tiles = walk(pl, B, L, nq, nkv, P, sms)
+                    seen, slots = {u: [] for u in range(units)}, {u: [] for u in range(units)}
+                    for c, u, lo, hi, sl in runs:
+                        seen[u] += range(lo, hi)
+                        slots[u] += sl
+                    for u in range(units):
+                        assert seen[u] == list(range(tiles)), (pl, P, u)
+                        assert sorted(slots[u]) == list(range(pl["pre_splits"])), (pl, P, u, slots[u])
+
+
+def test_shared_plan_rules(fpd):
+    """The calls whose choice the comments beside the rules quote."""
+    assert not plan(fpd, 1, 16, 32, 8, 128, 512, 0)["pre_tc"]                      # small: mma.sync
+    p = plan(fpd, 8, 16, 32, 8, 128, 2048, 256)
+    assert p["pre_tc"] and p["own_tc"] and p["pre_runs"] == 64                     # four runs per unit of 256 rows
+    p = plan(fpd, 64, 16, 32, 8, 128, 16384, 512)
+    assert p["pre_tc"] and not p["own_tc"] and p["pre_runs"] == 152                # own parts of 64 rows on mma.sync
+    assert plan(fpd, 64, 16, 32, 8, 128, 1024, 2048)["own_tc"]
+    p = plan(fpd, 4, 385, 32, 8, 128, 4096, 128)
+    assert p["pre_tc"] and p["own_tc"] and p["own_cost"] > 0                       # shorter prefix runs beside own runs
+    p = plan(fpd, 2, 2, 130, 1, 128, 20000, 0)
+    assert not p["pre_tc"] and not p["own_tc"]                                     # 130 heads do not fit 128 rows
