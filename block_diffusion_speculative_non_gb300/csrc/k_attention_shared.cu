@@ -238,16 +238,85 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(bf16* __restrict__ ou
   if (lse && lane == 0) lse[r] = none ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
 }
 
+// The same for up to 8 partials and many outputs: a warp puts together four consecutive ones, lane 8 i + s holding (m, l) of
+// output i's partial s, so that one round trip brings the weights of four outputs and each of the next two the partials of
+// two (one output per warp, three dependent round trips each, read the partials of 49280 outputs at 2 TB/s: 41 us).
+template <int H>
+__global__ void __launch_bounds__(256) shared_merge4_kernel(bf16* __restrict__ out, float* __restrict__ lse,
+                                                            const float* __restrict__ o_part, const float2* __restrict__ ml,
+                                                            int nsplit, int n_out) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int DPL = H / 32;
+  const int lane = threadIdx.x & 31, r0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
+  if (r0 >= n_out) return;
+  const int mine = r0 + (lane >> 3), s = lane & 7;
+  const float2 v = s < nsplit && mine < n_out ? __ldcg(ml + (size_t)s * n_out + mine) : make_float2(-INFINITY, 0.f);
+  float mx = v.y == 0.f ? -INFINITY : v.x;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float wl = v.y == 0.f ? 0.f : exp2f(v.x - mx);
+  float den = v.y == 0.f ? 0.f : v.y * wl;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (lse && s == 0 && mine < n_out) lse[mine] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 4; i0 += 2) {
+    float t[2][8][DPL], wgt[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        wgt[i][u] = __shfl_sync(0xffffffffu, wl, (i0 + i) * 8 + u);   // 0 past the last partial and the last output
+#pragma unroll
+        for (int e = 0; e < DPL; e++) t[i][u][e] = 0.f;
+        if (wgt[i][u] != 0.f) {
+          const float* op = o_part + ((size_t)u * n_out + r0 + i0 + i) * H + lane * DPL;
+          if constexpr (DPL == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(op));
+            t[i][u][0] = f.x;
+            t[i][u][1] = f.y;
+            t[i][u][2] = f.z;
+            t[i][u][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(op));
+            t[i][u][0] = f.x;
+            t[i][u][1] = f.y;
+          }
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      float num[DPL];
+#pragma unroll
+      for (int e = 0; e < DPL; e++) num[e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; u++)
+#pragma unroll
+        for (int e = 0; e < DPL; e++) num[e] += wgt[i][u] != 0.f ? t[i][u][e] * wgt[i][u] : 0.f;
+      const float d = __shfl_sync(0xffffffffu, den, (i0 + i) * 8);
+      if (r0 + i0 + i >= n_out) continue;
+      const bool none = d == 0.f;
+      bf16* dst = out + (size_t)(r0 + i0 + i) * H + lane * DPL;
+#pragma unroll
+      for (int e = 0; e < DPL; e += 2)
+        *reinterpret_cast<__nv_bfloat162*>(dst + e) =
+            __floats2bfloat162_rn(none ? 0.f : num[e] / d, none ? 0.f : num[e + 1] / d);
+    }
+  }
+}
+
 template <int H>
 cudaError_t launch_merge(const SharedAttn& a, int nsplit, cudaStream_t st) {
   const int n_out = a.rows * a.nq;
-  auto go = [&](auto* k, int w) {
-    return launch_k(k, ceil_div(n_out, 8 / w), 256, 0, st, a.out, a.lse, (const float*)a.o_part, (const float2*)a.ml, nsplit, n_out);
+  auto go = [&](auto* k, int per_cta) {
+    return launch_k(k, ceil_div(n_out, per_cta), 256, 0, st, a.out, a.lse, (const float*)a.o_part, (const float2*)a.ml, nsplit, n_out);
   };
-  // up to 8 partials are one round of loads for a warp; many outputs fill the GPU with one warp each
-  if (nsplit <= 8 || n_out >= 65536) return go(shared_merge_kernel<H, 1>, 1);
-  if (nsplit <= 16) return go(shared_merge_kernel<H, 2>, 2);
-  return nsplit <= 32 ? go(shared_merge_kernel<H, 4>, 4) : go(shared_merge_kernel<H, 8>, 8);
+  // many outputs fill the GPU with one warp for one or four of them; up to 8 partials are one round of loads for a warp
+  if (nsplit <= 8 && n_out >= 8192) return go(shared_merge4_kernel<H>, 32);
+  if (nsplit <= 8 || n_out >= 65536) return go(shared_merge_kernel<H, 1>, 8);
+  if (nsplit <= 16) return go(shared_merge_kernel<H, 2>, 4);
+  return nsplit <= 32 ? go(shared_merge_kernel<H, 4>, 2) : go(shared_merge_kernel<H, 8>, 1);
 }
 
 __global__ void rope_base_kernel(int32_t* base, const int32_t* ctx_len, const int32_t* prefix_len, const int32_t* pos_offset,
