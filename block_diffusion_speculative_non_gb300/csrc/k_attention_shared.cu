@@ -6,6 +6,11 @@
 // each prefix key is read once per kv head and row tile instead of once per request.  The own context and the block
 // are the ordinary attention of one request.  Both parts leave unnormalised partials (o, m, l) per split of their keys;
 // the softmax of a row is put together from them in split order (deterministic, no atomics).
+//
+// This file has the small form (mma.sync), the merge and the choice between the forms; k_attention_shared_tc.cu the large one.
+// Bounds: per row and key 4 h flops (6 h with the weights as two bf16 terms), per key 4 h bytes once for up to 256 rows.  So
+// few rows are a read of the keys, many rows tensor work, and small calls neither: launches and latency (4 tokens behind 512
+// positions: 5.9 us on the GPU, half of it the merge).
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
 
@@ -72,7 +77,9 @@ __device__ __forceinline__ Unit decode_unit(const SharedAttn& a, const SharedPla
   return w;
 }
 
-// One 64-row tile over one split on mma.sync (the tile math of attn_body.cuh).
+// One 64-row tile over one split on mma.sync (the tile math of attn_body.cuh).  Two CTAs of 80 KB per SM, two K/V buffers.
+// Bound by the legacy matrix path: 64 blocks of 16 positions behind 16384 keys took 1240 us here, 0.22 PFLOP/s of the
+// formula, and take 303 us on tcgen05; it stays for what is too small to notice.
 template <int H>
 __global__ void __launch_bounds__(NWARP * 32) shared_mma_kernel(const __grid_constant__ SharedAttn a, const __grid_constant__ SharedPlan pl,
                                                                 int pre_units) {

@@ -351,7 +351,7 @@ fpd_status fpd_grid_to_text(int batch, int block_len, const int32_t* committed, 
  *   [prefix 0..prefix_len) ; request b's context 0..ctx_len[b) ; its block 0..block_len)
  *   lse = log sum_t exp(q . k_t / sqrt(h)),   out = sum_t exp(q . k_t / sqrt(h) - lse) v_t        (no mask)
  * A row without any key (all lengths 0, no block keys) gives out 0 and lse -inf.  Sums are fp32, the softmax weights enter
- * the second product as two bf16 terms (about 2^-17), out is rounded once.  Supported: head_dim 64 or 128,
+ * the second product as two bf16 terms (2^-16 or better), out is rounded once.  Supported: head_dim 64 or 128,
  * batch * block_len * n_q_heads <= 2^26, capacities <= 2^30.
  *   q              device [batch * block_len, n_q_heads, h] bf16, normed and rotated
  *   k_blk, v_blk   device [batch, n_kv_heads, block_len, h] bf16, or both NULL: no block keys
