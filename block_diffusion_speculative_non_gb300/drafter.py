@@ -206,9 +206,10 @@ class SharedDraft:
     lengths, the rotary offset of each own store's slot 0, and a workspace for every call below.  collect=True keeps the
     attention weight that each position has collected over the draft calls, which evict() and evict_prefix() go by.
 
-    Everything runs on torch's current stream, without host synchronisation; the buffers stay where they are, so the
-    calls can be captured in a CUDA graph.  Objects share nothing but the drafter's weights.  Positions reach up to the
-    Drafter's max_pos."""
+    Everything runs on torch's current stream.  The buffers stay where they are: draft_block, append_rows, evict and
+    evict_prefix can be captured in a CUDA graph (prepare_prefix and append bring host offsets to the device first).  Objects
+    share nothing but the drafter's weights, so two of them may run on two streams; calls on one object must not overlap.
+    Positions reach up to the Drafter's max_pos; past it rows are skipped and recorded (fpd_device_status)."""
 
     def __init__(self, dr, batch, block_len, t_cap, prefix_cap=0, collect=False):
         s, dev = dr.shape, dr.device

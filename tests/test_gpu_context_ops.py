@@ -122,6 +122,8 @@ ATTN = {
     "prefix_only_tc": (16, 16, 20, 4, 128, 3001, 3001, [0] * 16, 0, False),
     "group_130": (3, 2, 130, 1, 128, 900, 900, [70, 0, 9], 70, True),
     "group_7_h64": (30, 16, 14, 2, 64, 1700, 1700, [i for i in range(30)], 31, True),
+    "block_of_5000": (1, 5000, 2, 1, 128, 100, 100, [50], 64, True),
+    "block_of_2900_h64": (2, 2900, 3, 3, 64, 0, 0, [50, 0], 64, True),
     "last_lane_only": (9, 15, 16, 4, 128, 2500, 2500, [i * 30 for i in range(9)], 256, True),
 }
 
