@@ -11,6 +11,8 @@
 // Bounds: per row and key 4 h flops (6 h with the weights as two bf16 terms), per key 4 h bytes once for up to 256 rows.  So
 // few rows are a read of the keys, many rows tensor work, and small calls neither: launches and latency (4 tokens behind 512
 // positions: 5.9 us on the GPU, half of it the merge).
+#include <cmath>
+
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
 
@@ -389,26 +391,43 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
   }
   const long own_segs = pl.own_tc ? own_units * (pl.own_splits / 2) : 0;
   if (pl.pre_tc) {
-    // Either one even run per SM, which may span units, or s runs per unit.  A run costs about kSeg besides its tiles (Q, the
-    // first copies, the partial out); a partial is written and read once.  The time is the longest run's or, with the own
-    // part's runs, the average over the SMs, and the merge's reads.
+    // Either even runs, which may span units, or s runs per unit.  A run costs about kSeg besides its tiles (Q, the first
+    // copies, the partial out); a partial is written and read once.  With many rows the time is the longest run's or, with
+    // the own part's runs, the average over the SMs.  A prefix under few rows is a read of its keys that does not need every
+    // SM: there the CTAs without a run of the prefix may take the own runs alone, so that the read goes on beside them.
     const bool pair = pre_rows > lane_rows;
-    const double kTile = (pair ? 2.2 : 1.1) * h / 128, kOwn = 1.1 * h / 128, kSeg = 5.0;   // us
+    const double kSeg = 5.0, kOwn = h == 128 ? 1.1 : 1.0, kTile = pair ? (h == 128 ? 2.2 : 1.7) : kOwn;   // us
     // us per partial of every row: written and read at 3 TB/s, and the merge's own step
     const double part_us = (double)batch * L * nq * h * 8 / 3e6 + (pair ? 0.2 : 0.4);
-    const double own_us = own_segs * (kSeg + kOwn * own_kt);
+    const double mem_us = pair ? 0.0 : 4.0 * h * nkv * p_cap / 6.7e6;
+    const double own_run = kSeg + 0.6 * kOwn * own_kt;   // contexts at 0.6 of what they may hold
     const long total = pre_units * pre_kt;
     double best = 0;
-    auto consider = [&](long runs, double run_us, double pieces) {
-      const double cost = std::max(run_us, (runs * run_us + own_us) / num_sms) + pieces * part_us;
-      if (!pl.pre_runs || cost < best) {
-        best = cost;
+    auto consider = [&](long runs, double tiles, int segs, double pieces) {
+      const double pre = segs * kSeg + std::max(kTile * tiles, mem_us);
+      const long left = num_sms - runs;
+      double t = pre;
+      int own_ctas = 0;
+      if (own_segs && pair) t = std::max(pre, (runs * pre + own_segs * (kSeg + kOwn * own_kt)) / num_sms);
+      if (own_segs && !pair) {
+        if (own_segs > left) t += std::ceil((double)(own_segs - left) / num_sms) * own_run;
+        const double apart = left > 0 ? std::max(pre, kSeg + std::ceil((double)own_segs / left) * own_run) : t;
+        if (apart < t) {
+          t = apart;
+          own_ctas = (int)left;
+        }
+      }
+      t += pieces * part_us;
+      if (!pl.pre_runs || t < best) {
+        best = t;
         pl.pre_runs = (int)runs;
+        pl.own_ctas = own_ctas;
       }
     };
     for (long s = 1; s <= pre_kt && (s == 1 || pre_units * s <= num_sms); s++)
-      if (pre_units * s <= num_sms) consider(pre_units * s, kSeg + kTile * ceil_div(pre_kt, (int)s), s);
-    if (total >= num_sms) consider(num_sms, 2 * kSeg + kTile * total / num_sms, (double)num_sms / pre_units + 1);
+      if (pre_units * s <= num_sms) consider(pre_units * s, ceil_div(pre_kt, (int)s), 1, s);
+    for (int r = own_segs && !pair ? num_sms / 2 : num_sms; r <= num_sms; r += 4)
+      if (total >= r) consider(r, (double)total / r, 2, (double)r / pre_units + 1);
     // a unit's tiles span at most ceil(runs / units) + 1 of the even runs (one less when the runs divide evenly), and no
     // more runs than it has tiles; a unit with one lane's rows leaves two partials per run
     pl.pre_pieces = (int)ceil_div(pl.pre_runs, (int)pre_units) + (pl.pre_runs % pre_units ? 1 : 0);
@@ -425,6 +444,7 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
     if ((pre_rows - 1) % (2 * lane_rows) < lane_rows) pl.pre_splits *= 2;
   }
   if (pl.pre_tc || pl.own_tc) pl.tc_grid = (int)std::min<long>(num_sms, pl.pre_runs + own_segs);
+  if (!pl.own_ctas) pl.own_ctas = pl.tc_grid;
   return pl;
 }
 

@@ -124,10 +124,10 @@ def test_selection_rule_of_the_reference():
 def plan(fpd, batch, L, nq, nkv, h, p_cap, t_cap, blk=True, sms=152):
     lib = fpd.lib()
     lib.fpd_test_shared_plan.argtypes = [ctypes.c_int] * 9 + [ctypes.POINTER(ctypes.c_int32)]
-    out = (ctypes.c_int32 * 10)()
+    out = (ctypes.c_int32 * 11)()
     assert lib.fpd_test_shared_plan(batch, L, L if blk else 0, nq, nkv, h, p_cap, t_cap, sms, out) == 0
     return dict(zip(("pre_tc", "own_tc", "pre_tiles", "pre_splits", "own_tiles", "own_splits", "pre_runs", "pre_pieces",
-                     "own_cost", "grid"), list(out)))
+                     "own_cost", "grid", "own_ctas"), list(out)))
 
 
 def walk(pl, batch, L, nq, nkv, P, sms=152):
@@ -153,6 +153,8 @@ def walk(pl, batch, L, nq, nkv, P, sms=152):
     def run_of(t):
         return max(c for c in range(G) if start(c) <= t) if W else ((t + 1) * G - 1) // total
 
+    own = [i for c in range(grid) if grid - 1 - c < pl["own_ctas"] for i in range(grid - 1 - c, own_n, pl["own_ctas"])]
+    assert sorted(own) == list(range(own_n))        # every own run once
     runs = []
     for c in range(grid):
         if total == 0:
@@ -211,5 +213,7 @@ def test_shared_plan_rules(fpd):
     assert plan(fpd, 64, 16, 32, 8, 128, 1024, 2048)["own_tc"]
     p = plan(fpd, 4, 385, 32, 8, 128, 4096, 128)
     assert p["pre_tc"] and p["own_tc"] and p["own_cost"] > 0                       # shorter prefix runs beside own runs
+    p = plan(fpd, 16, 1, 32, 8, 128, 65536, 512)
+    assert p["pre_tc"] and p["own_tc"] and p["pre_runs"] + p["own_ctas"] == 152      # own runs beside the prefix's read
     p = plan(fpd, 2, 2, 130, 1, 128, 20000, 0)
     assert not p["pre_tc"] and not p["own_tc"]                                     # 130 heads do not fit 128 rows
