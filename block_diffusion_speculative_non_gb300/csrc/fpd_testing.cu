@@ -285,8 +285,8 @@ extern "C" int fpd_test_shared_plan(int batch, int L, int block_keys, int nq, in
       t_cap < 0 || num_sms < 1)
     return FPD_ERR_SHAPE;
   const SharedPlan pl = shared_attn_plan(batch, L, block_keys, nq, nkv, head_dim, prefix_cap, t_cap, num_sms);
-  const int v[11] = {pl.pre_tc, pl.own_tc, pl.pre_tiles, pl.pre_splits, pl.own_tiles,
-                     pl.own_splits, pl.pre_runs, pl.pre_pieces, pl.own_cost, pl.tc_grid, pl.own_ctas};
-  for (int i = 0; i < 11; i++) out[i] = v[i];
+  const int v[12] = {pl.pre_tc, pl.own_tc, pl.pre_tiles, pl.pre_splits, pl.own_tiles,
+                     pl.own_splits, pl.pre_runs, pl.pre_pieces, pl.own_cost, pl.tc_grid, pl.own_ctas, pl.own_alone};
+  for (int i = 0; i < 12; i++) out[i] = v[i];
   return FPD_OK;
 }

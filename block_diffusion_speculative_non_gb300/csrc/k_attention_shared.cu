@@ -394,7 +394,7 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
     // Either even runs, which may span units, or s runs per unit.  A run costs about kSeg besides its tiles (Q, the first
     // copies, the partial out); a partial is written and read once.  With many rows the time is the longest run's or, with
     // the own part's runs, the average over the SMs.  A prefix under few rows is a read of its keys that does not need every
-    // SM: there the CTAs without a run of the prefix may take the own runs alone, so that the read goes on beside them.
+    // SM: the CTAs without a run of the prefix take own runs meanwhile.
     const bool pair = pre_rows > lane_rows;
     const double kSeg = 5.0, kOwn = h == 128 ? 1.1 : 1.0, kTile = pair ? (h == 128 ? 2.2 : 1.7) : kOwn;   // us
     // us per partial of every row: written and read at 3 TB/s, and the merge's own step
@@ -403,25 +403,32 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
     const double own_run = kSeg + 0.6 * kOwn * own_kt;   // contexts at 0.6 of what they may hold
     const long total = pre_units * pre_kt;
     double best = 0;
-    auto consider = [&](long runs, double tiles, int segs, double pieces) {
-      const double pre = segs * kSeg + std::max(kTile * tiles, mem_us);
+    // The time with the own runs, of which the CTAs without a run of the prefix take the first `alone` each before all CTAs
+    // take turns.
+    auto with_own = [&](long runs, double pre, long& alone) {
       const long left = num_sms - runs;
-      double t = pre;
-      int own_ctas = 0;
-      if (own_segs && pair) t = std::max(pre, (runs * pre + own_segs * (kSeg + kOwn * own_kt)) / num_sms);
-      if (own_segs && !pair) {
-        if (own_segs > left) t += std::ceil((double)(own_segs - left) / num_sms) * own_run;
-        const double apart = left > 0 ? std::max(pre, kSeg + std::ceil((double)own_segs / left) * own_run) : t;
-        if (apart < t) {
-          t = apart;
-          own_ctas = (int)left;
+      double best_t = 0;
+      for (long k = 0; k == 0 || (left > 0 && (k - 1) * own_run < pre && (k - 1) * left < own_segs); k++) {
+        const long turns = own_segs > k * left ? ceil_div(own_segs - k * left, (long)num_sms) : 0;
+        const double t = std::max(pre + turns * own_run, (k + turns) * own_run);
+        if (k == 0 || t < best_t) {
+          best_t = t;
+          alone = k;
         }
       }
+      return best_t;
+    };
+    auto consider = [&](long runs, double tiles, int segs, double pieces) {
+      const double pre = segs * kSeg + std::max(kTile * tiles, mem_us);
+      double t = pre;
+      long alone = 0;
+      if (own_segs > num_sms - runs || !pair) t = with_own(runs, pre, alone);
+      if (own_segs && pair) t = std::max(pre, (runs * pre + own_segs * (kSeg + kOwn * own_kt)) / num_sms);
       t += pieces * part_us;
       if (!pl.pre_runs || t < best) {
         best = t;
         pl.pre_runs = (int)runs;
-        pl.own_ctas = own_ctas;
+        pl.own_alone = (int)alone;
       }
     };
     for (long s = 1; s <= pre_kt && (s == 1 || pre_units * s <= num_sms); s++)
@@ -444,7 +451,7 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
     if ((pre_rows - 1) % (2 * lane_rows) < lane_rows) pl.pre_splits *= 2;
   }
   if (pl.pre_tc || pl.own_tc) pl.tc_grid = (int)std::min<long>(num_sms, pl.pre_runs + own_segs);
-  if (!pl.own_ctas) pl.own_ctas = pl.tc_grid;
+  pl.own_ctas = pl.tc_grid - pl.pre_runs;
   return pl;
 }
 

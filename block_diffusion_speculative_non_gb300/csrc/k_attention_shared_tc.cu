@@ -17,13 +17,15 @@
 // hold the same rows and take the even and the odd key tiles: such a unit is a read of the keys, and two key streams keep
 // the copies in flight.  The prefix's (unit, key tile) space is cut into one contiguous run of tiles per CTA, so that all
 // SMs finish together whatever the number of rows; a run that spans units leaves a partial in each.  The own part's units
-// follow, dealt out from the other end; where every CTA has a run, the prefix's runs are shorter by what a CTA has of them,
-// and beside a prefix that is bound by its read some CTAs take nothing else.
+// follow, dealt out from the other end: the CTAs without a run of the prefix take as many of them first as fit beside such a
+// run, then all CTAs take turns (64 tokens behind 4096 positions with contexts to 1024: 63 us, 89 when all take turns
+// from the start); where every CTA has a run, the prefix's runs are shorter by what a CTA has of them.
 //
 // What bounds it: with many rows the tensor core, 48 products of 64 cycles per pair of tiles and key tile, 71 % of the
 // cycles busy at 64 blocks of 16 positions behind 16384 keys (249 us, 1.10 PFLOP/s of the formula's 4 h, 1.66 of products;
 // the clock falls to 1.6-1.9 GHz under the power limit); with few rows the read of the keys, 6.7 TB/s while it lasts at 16
-// tokens behind 65536 positions (68 us in all, 42 the floor: start, own runs and merge do not overlap it).
+// tokens behind 65536 positions (62 us in all, 42 the floor: the start and the merge do not overlap it).  An own unit costs
+// about 5 us besides 1.1 us per tile: its first S waits for its Q and K, and its partial goes out before the next one's product.
 #include <cstring>
 
 #include "attn_tc_prims.cuh"
@@ -96,7 +98,7 @@ struct TcArgs {
   int pre_tiles, pre_units, pre_slots;   // row pairs per kv head, units, partial slots of a prefix row (0 units: not here)
   int pre_runs;                          // CTAs that share the prefix's tiles
   int pre_pieces;                        // most runs of a unit
-  int own_ctas;                          // CTAs, from the last, that take own runs
+  int own_ctas, own_alone;               // CTAs, from the last, that take own units up to own_alone by themselves
   int own_cost;                          // an own run in key tiles of the prefix, or 0: even runs
   int own_tiles, own_units, own_splits;  // the same for the own part, with the key splits of a unit
   int own_slot0;                         // first partial slot of the own part
@@ -153,7 +155,7 @@ struct Walk {
     x_end = c < G ? run_start(c + 1) : 0;
     empty_u = total == 0 ? c : p.pre_units;
     own_i = (int)gridDim.x - 1 - c;
-    if (own_i >= p.own_ctas) own_i = INT32_MAX;   // takes none
+    if (own_i >= p.own_ctas) own_i += p.own_alone;
   }
   // run c starts at tile c total / G, or, with own runs that count as W tiles each, where the runs before it end; the run
   // that holds tile t is the last one that starts at or before it
@@ -228,7 +230,7 @@ struct Walk {
       else s.range((int)((long long)split * nt / p.own_splits) * KT, (int)min((long long)n, (split + 1ll) * nt / p.own_splits * KT));
       s.slot = p.own_slot0 + 2 * split;
       s.pad_end = s.slot + 2;
-      own_i += p.own_ctas;
+      own_i += own_i < p.own_alone ? p.own_ctas : (int)gridDim.x;
       return true;
     }
     return false;
@@ -666,6 +668,7 @@ cudaError_t launch_shared_tc(const SharedAttn& a, const SharedPlan& pl, cudaStre
     p.own_units = pl.own_tiles * a.nkv * a.batch;
     p.own_splits = pl.own_splits / 2;
     p.own_ctas = pl.own_ctas;
+    p.own_alone = pl.own_ctas * pl.own_alone;
     p.by_own_tiles.set(p.own_tiles);
     p.by_own_units.set(p.own_units);
   }

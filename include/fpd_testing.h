@@ -76,10 +76,10 @@ int fpd_test_plan(int kind, int M, int N, int K, int num_sms, int32_t* out);
 /* Host only: the key splits and keys per split of the attention (impl 0: mma.sync tiles, 1: tensor-memory kernel). */
 int fpd_test_attn_plan(int impl, int batch, int L, int nq, int nkv, int t_cap, int num_sms, int32_t* splits,
                        int32_t* chunk);
-/* Host only: how fpd_shared_attention cuts its work (block_keys: L or 0).  out[11] = {prefix part on tcgen05, own part on
+/* Host only: how fpd_shared_attention cuts its work (block_keys: L or 0).  out[12] = {prefix part on tcgen05, own part on
  * tcgen05, row units of the prefix part per kv head, partials of a prefix row, the same two of the own part, CTAs that
- * share the prefix's key tiles, most of them in one unit, key tiles that an own run counts as, grid of the tcgen05 kernel, CTAs that take own
- * runs}. */
+ * share the prefix's key tiles, most of them in one unit, key tiles that an own run counts as, grid of the tcgen05 kernel,
+ * how many of its CTAs have no run of the prefix, how many own units each of those takes before all CTAs take turns}. */
 int fpd_test_shared_plan(int batch, int L, int block_keys, int nq, int nkv, int head_dim, int prefix_cap, int t_cap,
                          int num_sms, int32_t* out);
 

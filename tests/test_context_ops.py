@@ -124,10 +124,10 @@ def test_selection_rule_of_the_reference():
 def plan(fpd, batch, L, nq, nkv, h, p_cap, t_cap, blk=True, sms=152):
     lib = fpd.lib()
     lib.fpd_test_shared_plan.argtypes = [ctypes.c_int] * 9 + [ctypes.POINTER(ctypes.c_int32)]
-    out = (ctypes.c_int32 * 11)()
+    out = (ctypes.c_int32 * 12)()
     assert lib.fpd_test_shared_plan(batch, L, L if blk else 0, nq, nkv, h, p_cap, t_cap, sms, out) == 0
     return dict(zip(("pre_tc", "own_tc", "pre_tiles", "pre_splits", "own_tiles", "own_splits", "pre_runs", "pre_pieces",
-                     "own_cost", "grid", "own_ctas"), list(out)))
+                     "own_cost", "grid", "own_ctas", "own_alone"), list(out)))
 
 
 def walk(pl, batch, L, nq, nkv, P, sms=152):
@@ -153,7 +153,13 @@ def walk(pl, batch, L, nq, nkv, P, sms=152):
     def run_of(t):
         return max(c for c in range(G) if start(c) <= t) if W else ((t + 1) * G - 1) // total
 
-    own = [i for c in range(grid) if grid - 1 - c < pl["own_ctas"] for i in range(grid - 1 - c, own_n, pl["own_ctas"])]
+    own, alone = [], pl["own_ctas"] * pl["own_alone"]
+    for c in range(grid):
+        i = grid - 1 - c
+        i += alone if i >= pl["own_ctas"] else 0
+        while i < own_n:
+            own.append(i)
+            i += pl["own_ctas"] if i < alone else grid
     assert sorted(own) == list(range(own_n))        # every own run once
     runs = []
     for c in range(grid):
@@ -215,5 +221,8 @@ def test_shared_plan_rules(fpd):
     assert p["pre_tc"] and p["own_tc"] and p["own_cost"] > 0                       # shorter prefix runs beside own runs
     p = plan(fpd, 16, 1, 32, 8, 128, 65536, 512)
     assert p["pre_tc"] and p["own_tc"] and p["pre_runs"] + p["own_ctas"] == 152      # own runs beside the prefix's read
+    assert p["own_ctas"] * p["own_alone"] >= 16 * 8
+    p = plan(fpd, 200, 1, 32, 8, 128, 512, 512)
+    assert p["own_alone"] > 0 and p["own_ctas"] * p["own_alone"] < 200 * 8         # some of them, then all CTAs in turn
     p = plan(fpd, 2, 2, 130, 1, 128, 20000, 0)
     assert not p["pre_tc"] and not p["own_tc"]                                     # 130 heads do not fit 128 rows
