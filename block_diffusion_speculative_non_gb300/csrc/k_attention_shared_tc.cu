@@ -3,11 +3,10 @@
 //
 // A CTA works on two "lanes", each a 128-row S / P / O set in tensor memory with a softmax warpgroup of its own, so
 // that one lane's softmax runs while the tensor core works for the other.  Warps:
-//   0, 3   TMA producers of K and of V: tiles of 128 keys (64-dim boxes, 128-byte swizzle), two K and three V deep;
+//   0, 2   TMA producers of K and Q, and of V: tiles of 128 keys (64-dim boxes, 128-byte swizzle), two K and three V deep;
 //   1      MMA issuer: S = Q K^T, then O += (P_hi + P_lo) V with P read from tensor memory; a lane's next S is issued right
 //          behind its product, so that it waits for its own softmax alone;
-//   2      loads Q, and clears the V rows past the last valid key of a partial tile (0 x a stale non-finite value would be NaN);
-//   4..7   softmax of lane 0, 8..11 of lane 1: one thread per query row, the 128 scores of a tile in registers (one read of
+//   3..6   softmax of lane 0, 7..10 of lane 1: one thread per query row, the 128 scores of a tile in registers (one read of
 //          tensor memory per tile), p = 2^(s log2e/sqrt(h) - m) written back over S as two bf16 terms; O is rescaled only
 //          when the maximum rises by more than 2^8 (p stays below 2^8: O / l is exact either way).
 //
@@ -37,7 +36,7 @@ namespace {
 using namespace attn_tc;
 
 constexpr int QR = 128, KT = 128;      // most rows of a lane, keys of a tile
-constexpr int kThreads = 12 * 32;
+constexpr int kThreads = 11 * 32;
 constexpr int KST = 2, VST = 3;        // K and V ring slots: a K tile is free once S is, a V tile only behind the softmax
 constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
 constexpr uint32_t kTmemO = 256;
@@ -50,7 +49,7 @@ struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64;
   static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, BAR = V + VST * TILE;
 };
-// barriers: q_full, q_empty [lane], k_full, k_empty, v_full, v_empty, v_ready [slot], s_full, p_full, pv_done [lane], end
+// barriers: q_full, q_empty [lane], k_full, k_empty, v_full, v_empty [slot], s_full, p_full, pv_done [lane], end
 enum {
   B_Q = 0,
   B_QE = B_Q + 2,
@@ -58,8 +57,7 @@ enum {
   B_KE = B_KF + KST,
   B_VF = B_KE + KST,
   B_VE = B_VF + VST,
-  B_VR = B_VE + VST,
-  B_SF = B_VR + VST,
+  B_SF = B_VE + VST,
   B_PF = B_SF + 2,
   B_PV = B_PF + 2,
   B_END = B_PV + 2,
@@ -280,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     for (int s = 0; s < VST; s++) {
       tc::mbar_init(bar(B_VF + s), 1);
       tc::mbar_init(bar(B_VE + s), 1);
-      tc::mbar_init(bar(B_VR + s), 1);
     }
     tc::mbar_init(bar(B_END), 1);
     *abort_flag = 0;
@@ -308,15 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   Walk walk(p);
   Seg sg;
 
-  if (warp == 0 || warp == 3) {
-    // ---------------- TMA producers: K (warp 0), V (warp 3) ----------------
+  if (warp == 0 || warp == 2) {
+    // ---------------- TMA producers: K and Q (warp 0), V (warp 2) ----------------
     // one each: a K slot is free much earlier than a V slot, and its copy must not queue behind a V that waits
     if (lane == 0) {
-      const bool is_v = warp == 3;
+      const bool is_v = warp == 2;
       const int ST = is_v ? VST : KST, full = is_v ? B_VF : B_KF, empty = is_v ? B_VE : B_KE;
       const uint32_t ring = tc::smem_u32(smem + (is_v ? S::V : S::K));
       const CUtensorMap* blk = is_v ? &p.tm_vblk : &p.tm_kblk;
-      int n = 0;   // tiles since the start: ring slot and phase
+      int n = 0, nq[2] = {0, 0};   // tiles and Q loads since the start: ring slot and phase
       while (!*abort_flag && walk.next(sg)) {
         const CUtensorMap* ctx_map = sg.prefix ? &p.tm_pre : &p.tm_own;
         const int row0 = is_v ? sg.vrow : sg.krow;
@@ -331,10 +328,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           for (int h = 0; h < S::ATOMS; h++)
             tc::tma_load_2d(ring + s * S::TILE + h * ATOM_BYTES, ctx ? ctx_map : blk, h * 64, row, bar(full + s));
           n++;
+          if (is_v || i > 0) continue;
+          // Q behind the first K tile: its slots are free later, with the S before the last of the run before
+          for (int t = 0; t < 2; t++) {
+            if (sg.lane_tiles(t) == 0) continue;
+            if (nq[t] > 0 && !wait_bar(bar(B_QE + t), (nq[t] & 1) ^ 1)) { *abort_flag = 1; break; }
+            tc::mbar_arrive_expect_tx(bar(B_Q + t), p.rpt * HD * 2);
+            for (int h = 0; h < S::ATOMS; h++)
+              tc::tma_load_3d(tc::smem_u32(smem + S::Q) + t * S::TILE + h * ATOM_BYTES, &p.tm_q, h * 64, sg.g * p.grp,
+                              sg.n0 + p.by_grp.div(sg.lane_row0(t, p.rpt)), bar(B_Q + t));
+            nq[t]++;
+          }
         }
       }
-      if (*abort_flag)   // a wait ran out: let the copies in flight land before the CTA's memory goes
+      if (*abort_flag) {   // a wait ran out: let the copies in flight land before the CTA's memory goes
         for (int i = max(0, n - ST); i < n; i++) tc::mbar_wait(bar(full + i % ST), (i / ST) & 1);
+        for (int t = 0; t < 2; t++)
+          if (nq[t] > 0) tc::mbar_wait(bar(B_Q + t), (nq[t] & 1) ^ 1);
+      }
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
@@ -347,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       int n0 = 0, nq[2] = {0, 0}, nl[2] = {0, 0};        // ring tiles, Q loads, lane tiles so far
       auto fail = [&]() { *abort_flag = 1; return false; };
       auto wait_k = [&](int n) { return wait_bar(bar(B_KF + n % KST), (n / KST) & 1) || fail(); };
-      // the clearing warp has seen the tile arrive before it says the tile is ready
-      auto wait_v = [&](int n) { return wait_bar(bar(B_VR + n % VST), (n / VST) & 1) || fail(); };
+      auto wait_v = [&](int n) { return wait_bar(bar(B_VF + n % VST), (n / VST) & 1) || fail(); };
       auto issue_s = [&](int t, int slot) {   // S_t = Q_t K^T, K from the slot
         const uint64_t da = dq + t * (S::TILE >> 4), db = dk + slot * (S::TILE >> 4);
 #pragma unroll
@@ -448,9 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       commit_if(on, bar(B_END));
       tc::mbar_wait(bar(B_END), 0);
     }
-  } else if (warp >= 4) {
+  } else {
     // ---------------- softmax of lane t: thread = query row = TMEM lane ----------------
-    const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int t = (warp - 3) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lane_off + t * KT, ot = tmem + lane_off + kTmemO + t * 128;
@@ -460,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       const int pos = p.by_grp.div(qi);
       return r < p.rpt && qi < s.nrows ? (long long)(s.n0 + pos) * p.a.nq + s.g * p.grp + qi - pos * p.grp : -1;
     };
-    int cnt = 0, other = 0;   // tiles of this lane and of the other so far: phases of S, P and PV
+    int cnt = 0, other = 0, base = 0;   // tiles of this lane and of the other so far: phases of S, P and PV; of both: V slots
     while (!*abort_flag && walk.next(sg)) {
       const long long orow = out_row(sg);
       const bool warp_rows = quarter * 32 < p.rpt && sg.lane_row0(t, p.rpt) + quarter * 32 < sg.nrows;   // else padding
@@ -535,11 +545,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           tmem_wait_st();
         }
         first_tile = false;
+        if (valid < KT && (sg.keys || t == 0)) {
+          // V rows past the last key -> 0 before the product: 0 x a stale non-finite value would be NaN.  A pair's lane 1 comes
+          // after lane 0's product.  Row k: 128 bytes at k * 128 in each 64-dim atom (the swizzle permutes within a row).
+          const int n = base + i, s = n % VST;
+          if (!wait_bar(bar(B_VF + s), (n / VST) & 1)) *abort_flag = 1;
+          uint8_t* tile = smem + S::V + s * S::TILE;
+          for (int c = r; c < (KT - valid) * 8 * S::ATOMS; c += QR) {
+            const int k = valid + c / (8 * S::ATOMS), h = (c >> 3) & (S::ATOMS - 1), q = c & 7;
+            *reinterpret_cast<uint4*>(tile + h * ATOM_BYTES + k * 128 + q * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(B_PF + t));
       }
       other += sg.lane_tiles(1 - t);
+      base += sg.n_tiles;
       if (!first_tile && !wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
       // behind the last run the K and V slots are free once the other lane's products are done too: rows go through them
       // (16 bytes of padding each, so that a warp's writes spread over the banks) and out as one bulk copy per row.
@@ -585,44 +608,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       }
       tc::tc_fence_before();   // O has been read: the next run's first product follows this lane's next P
     }
-  } else if (warp == 2) {
-    // ---------------- Q; V rows past the last valid key -> 0 ----------------
-    int n = 0, nq[2] = {0, 0};
-    while (!*abort_flag && walk.next(sg)) {
-      for (int t = 0; t < 2; t++) {
-        if (sg.lane_tiles(t) == 0) continue;
-        if (nq[t] > 0 && !wait_bar(bar(B_QE + t), (nq[t] & 1) ^ 1)) { *abort_flag = 1; break; }
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(bar(B_Q + t), p.rpt * HD * 2);
-          for (int h = 0; h < S::ATOMS; h++)
-            tc::tma_load_3d(tc::smem_u32(smem + S::Q) + t * S::TILE + h * ATOM_BYTES, &p.tm_q, h * 64, sg.g * p.grp,
-                            sg.n0 + p.by_grp.div(sg.lane_row0(t, p.rpt)), bar(B_Q + t));
-        }
-        nq[t]++;
-        __syncwarp();
-      }
-      for (int i = 0; i < sg.n_tiles && !*abort_flag; i++, n++) {
-        const int s = n % VST;
-        int first, valid;
-        bool ctx;
-        sg.tile(i, first, valid, ctx);
-        if (!wait_bar(bar(B_VF + s), (n / VST) & 1)) *abort_flag = 1;
-        if (valid < KT) {
-          // row k of the tile: 128 bytes at k * 128 in each 64-dim atom (the swizzle permutes within a row)
-          uint8_t* tile = smem + S::V + s * S::TILE;
-          for (int c = lane; c < (KT - valid) * 8 * S::ATOMS; c += 32) {
-            const int k = valid + c / (8 * S::ATOMS), h = (c >> 3) & (S::ATOMS - 1), q = c & 7;
-            *reinterpret_cast<uint4*>(tile + h * ATOM_BYTES + k * 128 + q * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B_VR + s));
-      }
-    }
-    if (*abort_flag)
-      for (int t = 0; t < 2; t++)
-        if (nq[t] > 0) tc::mbar_wait(bar(B_Q + t), (nq[t] & 1) ^ 1);
   }
 
   __syncwarp();
