@@ -472,7 +472,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     };
     int cnt = 0, other = 0, base = 0;   // tiles of this lane and of the other so far: phases of S, P and PV; of both: V slots
     while (!*abort_flag && walk.next(sg)) {
-      const long long orow = out_row(sg);
       const bool warp_rows = quarter * 32 < p.rpt && sg.lane_row0(t, p.rpt) + quarter * 32 < sg.nrows;   // else padding
       const int i0 = sg.keys ? t : 0, step = sg.keys ? 2 : 1;
       float m_ref = -INFINITY, l = 0.f;
@@ -526,18 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           const uint64_t sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
           uint64_t lq[2] = {0ull, 0ull};
 #pragma unroll
-          for (int c0 = 0; c0 < KT; c0 += 32) {
-            uint32_t hi[16], lo[16];
+          for (int c0 = 0; c0 < KT; c0 += 16) {
+            uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+            for (int e = 0; e < 16; e += 2) {
               float x0, x1;
               unpack2(fma2(pack2(sv[c0 + e], sv[c0 + e + 1]), sl22, nm2), x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
               split_trunc(p0, p1, hi[e / 2], lo[e / 2]);
             }
-            tmem_st16(st + c0, hi);
-            tmem_st16(st + c0 + 16, lo);
+            const uint32_t pt = st + (c0 & ~31) + (c0 & 16) / 2;   // 32 keys: 16 columns of hi, 16 of lo
+            tmem_st8(pt, hi);
+            tmem_st8(pt + 16, lo);
           }
           float la, lb;
           unpack2(add2(lq[0], lq[1]), la, lb);
@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       if (staged && other > 0 && !wait_bar(bar(B_PV + 1 - t), (other - 1) & 1)) *abort_flag = 1;
       tc::tc_fence_after();
       if (warp_rows) {
+        const long long orow = out_row(sg);
         const size_t n_out = (size_t)p.a.rows * p.a.nq;
         const int slot = sg.slot + (sg.keys ? t : 0);
         if (!first_tile) {
