@@ -1,40 +1,48 @@
 """Binding of the operators on a context store: attention over a shared prefix, collected attention weight, eviction.
 Sizes and layouts are those of include/fpd.h.
 
-The operators are short calls (a few microseconds on the GPU), so the checks here are one comparison chain per tensor and
-the current stream is asked for once.
+The operators are short calls (a few microseconds on the GPU), so their arguments are checked and handed over by the
+compiled module `_calls` (csrc/py_calls.cpp); the rest goes through ctypes.
 """
 from __future__ import annotations
 
 import ctypes
+import os
 
 import torch
 
 from . import SharedContext, _check, _ptr, _stream, lib
 
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_module = None
 
 
-def _arg(t, dtype, n, what, dev=None):
+def _compiled():
+    """The compiled calls, bound to the loaded library (raises when they have not been built for this PyTorch)."""
+    global _module
+    if _module is None:
+        here = os.path.dirname(os.path.abspath(__file__))
+        if not os.path.exists(os.path.join(here, "_calls.so")):
+            raise RuntimeError(f"_calls.so not built in {here}; run __graft_entry__.build()")
+        from . import _calls as m
+        if m.torch_version != torch.__version__:
+            raise RuntimeError(f"_calls.so was built for PyTorch {m.torch_version}, this is {torch.__version__}; "
+                               "run __graft_entry__.build()")
+        m.bind(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value
+                 for f in ("fpd_shared_attention", "fpd_context_weights", "fpd_evict_context")))
+        _module = m
+    return _module
+
+
+def _arg(t, dtype, n, what, dev=-1):
     """Device address of a tensor that must be contiguous, of `dtype`, on the current device `dev` and hold at least n
     elements; an int address or None is passed on."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous (row-major)")
-    if t.numel() < n:
-        raise ValueError(f"{what} holds {t.numel()} elements, the call needs {n}")
-    raise ValueError(f"{what} is on {t.device}, the current device is cuda:{dev}")
+    return _compiled().arg(t, dtype, n, what, dev)
 
 
 def _here(stream):
-    """(current device, address of the stream)"""
-    dev = torch.cuda.current_device()
-    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    """(address of the stream, current device)"""
+    dev = torch._C._cuda_getDevice()
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream), dev
 
 
 def fpd_shared_attention_workspace_bytes(batch, block_len, n_q_heads, n_kv_heads, head_dim, prefix_cap, t_cap) -> int:
@@ -46,30 +54,16 @@ def fpd_shared_attention(batch, block_len, n_q_heads, n_kv_heads, head_dim, laye
                          prefix_cap, prefix_len, kv_store, t_cap, ctx_len, out, lse, workspace, workspace_bytes,
                          stream=None):
     """Attention of a batch over [shared prefix ; own context ; block] of one layer; out and lse are written."""
-    n, pos = batch * block_len * n_q_heads, 2 * n_kv_heads * head_dim
-    blk = batch * n_kv_heads * block_len * head_dim
-    dev, st = _here(stream)
-    _check(lib().fpd_shared_attention(
-        batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, _arg(q, _BF16, n * head_dim, "q", dev),
-        _arg(k_blk, _BF16, blk, "k_blk", dev), _arg(v_blk, _BF16, blk, "v_blk", dev),
-        _arg(prefix_store, _BF16, (layer + 1) * prefix_cap * pos, "prefix_store", dev), prefix_cap,
-        _arg(prefix_len, _I32, 1, "prefix_len", dev),
-        _arg(kv_store, _BF16, (layer + 1) * batch * t_cap * pos, "kv_store", dev), t_cap,
-        _arg(ctx_len, _I32, batch, "ctx_len", dev), _arg(out, _BF16, n * head_dim, "out", dev),
-        _arg(lse, _F32, n, "lse", dev), _arg(workspace, _U8, workspace_bytes, "workspace", dev), workspace_bytes, st),
-           "fpd_shared_attention")
+    _check(_compiled().shared_attention(batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, q, k_blk, v_blk,
+                                        prefix_store, prefix_cap, prefix_len, kv_store, t_cap, ctx_len, out, lse,
+                                        workspace, workspace_bytes, *_here(stream)), "fpd_shared_attention")
 
 
 def fpd_context_weights(batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, q, lse, kv_store, t_cap, ctx_len,
                         weights, accumulate=False, stream=None):
     """weights[layer] (+)= the attention weight every context position collects from the rows of q."""
-    n, at = batch * block_len * n_q_heads, (layer + 1) * batch * n_kv_heads * t_cap
-    dev, st = _here(stream)
-    _check(lib().fpd_context_weights(
-        batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, _arg(q, _BF16, n * head_dim, "q", dev),
-        _arg(lse, _F32, n, "lse", dev), _arg(kv_store, _BF16, at * 2 * head_dim, "kv_store", dev), t_cap,
-        _arg(ctx_len, _I32, batch, "ctx_len", dev), _arg(weights, _F32, at, "weights", dev), 1 if accumulate else 0, st),
-           "fpd_context_weights")
+    _check(_compiled().context_weights(batch, block_len, n_q_heads, n_kv_heads, head_dim, layer, q, lse, kv_store, t_cap,
+                                       ctx_len, weights, 1 if accumulate else 0, *_here(stream)), "fpd_context_weights")
 
 
 def fpd_evict_workspace_bytes(n_layers, batch, n_kv_heads, budget) -> int:
@@ -79,16 +73,9 @@ def fpd_evict_workspace_bytes(n_layers, batch, n_kv_heads, budget) -> int:
 def fpd_evict_context(n_layers, batch, n_kv_heads, head_dim, budget, recent, kv_store, t_cap, weights, ctx_len, out_store,
                       out_cap, out_weights, out_len, pos_offset, kept, workspace, workspace_bytes, stream=None):
     """Keeps the last `recent` positions and those with the largest weights, `budget` in all, of every request."""
-    heads = n_layers * batch * n_kv_heads
-    dev, st = _here(stream)
-    _check(lib().fpd_evict_context(
-        n_layers, batch, n_kv_heads, head_dim, budget, recent,
-        _arg(kv_store, _BF16, heads * 2 * t_cap * head_dim, "kv_store", dev), t_cap,
-        _arg(weights, _F32, heads * t_cap, "weights", dev), _arg(ctx_len, _I32, batch, "ctx_len", dev),
-        _arg(out_store, _BF16, heads * 2 * out_cap * head_dim, "out_store", dev), out_cap,
-        _arg(out_weights, _F32, heads * out_cap, "out_weights", dev), _arg(out_len, _I32, batch, "out_len", dev),
-        _arg(pos_offset, _I32, batch, "pos_offset", dev), _arg(kept, _I32, heads * budget, "kept", dev),
-        _arg(workspace, _U8, workspace_bytes, "workspace", dev), workspace_bytes, st), "fpd_evict_context")
+    _check(_compiled().evict_context(n_layers, batch, n_kv_heads, head_dim, budget, recent, kv_store, t_cap, weights, ctx_len,
+                                     out_store, out_cap, out_weights, out_len, pos_offset, kept, workspace,
+                                     workspace_bytes, *_here(stream)), "fpd_evict_context")
 
 
 def fpd_prepare_context_at(model, batch, total_rows, row_off, row_cnt, pos_start, pos_offset, feats, kv_store, t_cap,

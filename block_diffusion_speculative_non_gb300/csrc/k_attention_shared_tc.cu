@@ -11,19 +11,19 @@
 //          when the maximum rises by more than 2^8 (p stays below 2^8: O / l is exact either way).
 //
 // A lane's rows are whole positions, the kv head's heads of each (128 rows, or less when the heads do not divide it): one
-// box of a [position][head][h] map of q.  A unit is a pair of such row tiles of a part's rows in one kv head: the lanes hold one tile each and share every K/V tile.
-// Where a unit has the rows of one lane only (few blocks, the own part of a text block, the last rows of a long one), both lanes
-// hold the same rows and take the even and the odd key tiles: such a unit is a read of the keys, and two key streams keep
-// the copies in flight.  The prefix's (unit, key tile) space is cut into one contiguous run of tiles per CTA, so that all
+// box of a [position][head][h] map of q.  A unit is a pair of such row tiles of a part's rows in one kv head: the lanes hold
+// one tile each and share every K/V tile.  Where a unit has the rows of one lane only (few blocks, the own part
+// of a text block, the last rows of a long one), both lanes hold the same rows and take the even and the odd key tiles: such a
+// unit is a read of the keys, and two key streams keep the copies in flight.  The prefix's (unit, key tile) space is cut into one contiguous run of tiles per CTA, so that all
 // SMs finish together whatever the number of rows; a run that spans units leaves a partial in each.  The own part's units
 // follow, dealt out from the other end: the CTAs without a run of the prefix take as many of them first as fit beside such a
 // run, then all CTAs take turns (64 tokens behind 4096 positions with contexts to 1024: 63 us, 89 when all take turns
 // from the start); where every CTA has a run, the prefix's runs are shorter by what a CTA has of them.
 //
-// What bounds it: with many rows the tensor core, 48 products of 64 cycles per pair of tiles and key tile, 71 % of the
-// cycles busy at 64 blocks of 16 positions behind 16384 keys (249 us, 1.10 PFLOP/s of the formula's 4 h, 1.66 of products;
+// What bounds it: with many rows the tensor core, 48 products of 64 cycles per pair of tiles and key tile, 72 % of the
+// cycles busy at 64 blocks of 16 positions behind 16384 keys (244 us, 1.13 PFLOP/s of the formula's 4 h, 1.69 of products;
 // the clock falls to 1.6-1.9 GHz under the power limit); with few rows the read of the keys, 6.7 TB/s while it lasts at 16
-// tokens behind 65536 positions (62 us in all, 42 the floor: the start and the merge do not overlap it).  An own unit costs
+// tokens behind 65536 positions (59 us in all, 42 the floor: the start and the merge do not overlap it).  An own unit costs
 // about 5 us besides 1.1 us per tile: its first S waits for its Q and K, and its partial goes out before the next one's product.
 #include <cstring>
 

@@ -104,6 +104,32 @@ def test_binding_checks_tensors(fpd):
     assert fpd._arg(None, torch.int32, 4, "ctx_len") is None and fpd._arg(64, torch.int32, 4, "ctx_len") == 64
 
 
+def test_compiled_calls_refuse_what_is_no_argument(fpd):
+    """Counts, integers and objects of the compiled calls: a Python error, and nothing reaches the library."""
+    import torch
+    calls = fpd.context._compiled()
+    att = [1, 1, 8, 2, 64, 0] + [64] * 4 + [8, 64, 64, 8, 64, 64, 64, 64, 1, None, 0]
+    with pytest.raises(TypeError, match="20 arguments, the call takes 21"):
+        calls.shared_attention(*att[:-1])
+    with pytest.raises(OverflowError):
+        calls.shared_attention(2 ** 40, *att[1:])
+    with pytest.raises(OverflowError):
+        calls.shared_attention(*att[:18], -1, *att[19:])                       # a negative workspace size
+    with pytest.raises(TypeError):
+        calls.shared_attention(1.5, *att[1:])
+    with pytest.raises(TypeError, match="prefix_store must be a tensor"):
+        calls.shared_attention(*att[:9], [1.0], *att[10:])
+    with pytest.raises(ValueError, match="lse must be torch.float32, got torch.int32"):
+        calls.shared_attention(*att[:16], torch.zeros(8, dtype=torch.int32), *att[17:])
+    with pytest.raises(ValueError, match="current device"):
+        calls.context_weights(1, 1, 8, 2, 64, 0, torch.zeros(512, dtype=torch.bfloat16), 64, 64, 8, 64, 64, 0, None, 0)
+    with pytest.raises(ValueError, match="kv_store holds 4 elements, the call needs 9223372036854775807"):
+        big = 2 ** 31 - 1                                                      # sizes whose product passes 64 bits
+        calls.evict_context(big, big, big, 128, 8, 0, torch.zeros(4, dtype=torch.bfloat16), big, *[64] * 3, 8, *[64] * 6, None, 0)
+    assert calls.shared_attention(0, *att[1:]) != 0                            # the library's own refusal
+    assert calls.evict_context(0, 1, 2, 64, 8, 0, 64, 8, 64, 64, 64, 8, 64, 64, None, None, 64, 8, None, 0) != 0
+
+
 def test_selection_rule_of_the_reference():
     nan, inf = float("nan"), float("inf")
     assert ref.kept_positions([5, 1, 3, 2], 4, 4, 0) == [0, 1, 2, 3]
