@@ -85,7 +85,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     for (int p = tid; p < T; p += kSelThreads) {
       const float v = w[p];
       sm.stage[p] = v;
-      if (!ranked && p < old) atomicAdd(&sm.hist[weight_key(v) >> 21], 1u);
+      if (p < old) {
+        if (ranked) sm.hist[p] = weight_key(v);   // up to 256 keys, 0 behind them
+        else atomicAdd(&sm.hist[weight_key(v) >> 21], 1u);
+      }
     }
     __syncthreads();
   }
@@ -95,12 +98,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   if (need > 0 && ranked) {
     const int p = tid >> 2, part = tid & 3;
     if (warp * 8 < old) {
-      const uint32_t k = p < old ? weight_key(sm.stage[p]) : 0u;
+      const uint32_t k = sm.hist[p];
       int greater = 0, before = 0;
-      for (int q = part; q < old; q += 4) {
-        const uint32_t o = weight_key(sm.stage[q]);
-        greater += o > k;
-        before += o == k && q < p;
+      for (int q = part * 4; q < old; q += 16) {
+        const uint4 o = *reinterpret_cast<const uint4*>(sm.hist + q);
+        greater += (o.x > k) + (o.y > k) + (o.z > k) + (o.w > k);
+        before += (o.x == k && q < p) + (o.y == k && q + 1 < p) + (o.z == k && q + 2 < p) + (o.w == k && q + 3 < p);
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
