@@ -372,13 +372,16 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
                             (long long)nkv * batch * ceil_div(own_rows, QT) * ceil_div(own_keys, KT);
   const bool small = tiles64 * h <= 128 * 4ll * num_sms;
   pl.pre_tc = p_cap && pre_tma && !small;
-  // Own parts of at most one 64-row tile, several per SM: each costs its run on tcgen05 about 8 us besides 1.1 us a tile of
-  // 128 keys; on mma.sync 0.8 us a tile of 64 keys and a kernel more (64 text blocks with contexts up to 512: 332 against 309
-  // us; up to 2048: 137 against 168).  With fewer rows or runs the kernels are level or tcgen05 wins.
+  // Own parts of 33 to 64 rows, several per SM: on tcgen05 each costs its run about 7 us besides 0.9 us a tile of 128 keys, on
+  // mma.sync 0.9 us a tile of 64 keys, and beside a prefix a kernel more (h / 16 us).  64 text blocks behind 16384
+  // positions: 287 against 321 us with contexts up to 256, behind 8192 203 against 197 up to 768, 238 against 214 up to 1500; 24
+  // behind 1024: 34 against 35 us without contexts, 57 against 41 up to 768.  Of 190 such calls the rule is on average
+  // 0.8 % from the better kernel.  With fewer rows or runs the kernels are level or tcgen05 wins.
   const double own_runs = (double)nkv * batch / num_sms;
-  const bool own_mma = own_rows > 32 && own_rows <= QT && own_runs > 1 &&
-                       own_runs * 0.8 * ceil_div(own_keys, KT) + 6 < own_runs * (8 + 1.1 * (ceil_div(t_cap, 128) + ceil_div(lb, 128)));
-  pl.own_tc = own_keys && own_tma && !small && !(own_mma && (pl.pre_tc || !p_cap));
+  const bool own_mma = own_rows > 32 && own_rows <= QT && own_runs > 1 && (pl.pre_tc || !p_cap) &&
+                       own_runs * 0.9 * ceil_div(own_keys, KT) + (p_cap ? h / 16 : 0) <
+                           own_runs * (7 + 0.9 * (ceil_div(t_cap, 128) + ceil_div(lb, 128)));
+  pl.own_tc = own_keys && own_tma && !small && !own_mma;
   pl.pre_tiles = p_cap ? ceil_div(pre_rows, pl.pre_tc ? 2 * lane_rows : QT) : 0;
   pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 2 * lane_rows : QT) : 0;
   const long pre_units = (long)pl.pre_tiles * nkv, own_units = (long)pl.own_tiles * nkv * batch;
