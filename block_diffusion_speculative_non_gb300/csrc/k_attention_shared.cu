@@ -358,6 +358,54 @@ static int mma_splits(long base, int kt, int slots) {
   return best_s;
 }
 
+// How the tcgen05 kernel's CTAs share the prefix's key tiles (kt of each of `units` units) beside the own part's runs (segs of
+// own_kt key tiles).  Either even runs, which may span units, or s runs per unit.  A run costs about kSeg us besides its
+// tiles (Q, the first copies, the partial out); a partial is written and read once.  With many rows (pair) the time is the
+// longest run's or, with the own part's runs, the average over the SMs.  A prefix under few rows is a read of its keys that
+// does not need every SM: the CTAs without a run of the prefix take own runs meanwhile.
+struct PrefixRuns {
+  double us = 0;
+  int runs = 0;      // CTAs that share the prefix
+  int alone = 0;     // own runs that each of the others takes before all take turns
+  double kSeg = 5.0, kOwn, kTile;
+  PrefixRuns(bool pair, int h, long units, int kt, long segs, int own_kt, double part_us, double mem_us, int num_sms) {
+    kOwn = h == 128 ? 1.1 : 1.0;
+    kTile = pair ? (h == 128 ? 2.2 : 1.7) : kOwn;
+    const double own_run = kSeg + 0.6 * kOwn * own_kt;   // contexts at 0.6 of what they may hold
+    const long total = units * kt;
+    auto with_own = [&](long r, double pre, long& first) {
+      const long left = num_sms - r;
+      double best = 0;
+      for (long k = 0; k == 0 || (left > 0 && (k - 1) * own_run < pre && (k - 1) * left < segs); k++) {
+        const long turns = segs > k * left ? ceil_div(segs - k * left, (long)num_sms) : 0;
+        const double t = std::max(pre + turns * own_run, (k + turns) * own_run);
+        if (k == 0 || t < best) {
+          best = t;
+          first = k;
+        }
+      }
+      return best;
+    };
+    auto consider = [&](long r, double tiles, int n, double pieces) {
+      const double pre = n * kSeg + std::max(kTile * tiles, mem_us);
+      double t = pre;
+      long first = 0;
+      if (segs > num_sms - r || !pair) t = with_own(r, pre, first);
+      if (segs && pair) t = std::max(pre, (r * pre + segs * (kSeg + kOwn * own_kt)) / num_sms);
+      t += pieces * part_us;
+      if (!runs || t < us) {
+        us = t;
+        runs = (int)r;
+        alone = (int)first;
+      }
+    };
+    for (long s = 1; s <= kt && (s == 1 || units * s <= num_sms); s++)
+      if (units * s <= num_sms) consider(units * s, ceil_div(kt, (int)s), 1, s);
+    for (int r = segs && !pair ? num_sms / 2 : num_sms; r <= num_sms; r += 4)
+      if (total >= r) consider(r, (double)total / r, 2, (double)r / units + 1);
+  }
+};
+
 SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms) {
   SharedPlan pl{};
   const int grp = nq / nkv, pre_rows = batch * L * grp, own_rows = L * grp, own_keys = t_cap + lb;
@@ -372,20 +420,35 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
                             (long long)nkv * batch * ceil_div(own_rows, QT) * ceil_div(own_keys, KT);
   const bool small = tiles64 * h <= 128 * 4ll * num_sms;
   pl.pre_tc = p_cap && pre_tma && !small;
-  // Own parts of 33 to 64 rows, several per SM: on tcgen05 each costs its run about 7 us besides 0.9 us a tile of 128 keys, on
-  // mma.sync 0.9 us a tile of 64 keys, and beside a prefix a kernel more (h / 16 us).  64 text blocks behind 16384
-  // positions: 287 against 321 us with contexts up to 256, behind 8192 203 against 197 up to 768, 238 against 214 up to 1500; 24
-  // behind 1024: 34 against 35 us without contexts, 57 against 41 up to 768.  Of 190 such calls the rule is on average
-  // 0.8 % from the better kernel.  With fewer rows or runs the kernels are level or tcgen05 wins.
-  const double own_runs = (double)nkv * batch / num_sms;
-  const bool own_mma = own_rows > 32 && own_rows <= QT && own_runs > 1 && (pl.pre_tc || !p_cap) &&
-                       own_runs * 0.9 * ceil_div(own_keys, KT) + (p_cap ? h / 16 : 0) <
-                           own_runs * (7 + 0.9 * (ceil_div(t_cap, 128) + ceil_div(lb, 128)));
-  pl.own_tc = own_keys && own_tma && !small && !own_mma;
+  pl.own_tc = own_keys && own_tma && !small;
   pl.pre_tiles = p_cap ? ceil_div(pre_rows, pl.pre_tc ? 2 * lane_rows : QT) : 0;
-  pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 2 * lane_rows : QT) : 0;
-  const long pre_units = (long)pl.pre_tiles * nkv, own_units = (long)pl.own_tiles * nkv * batch;
+  const long pre_units = (long)pl.pre_tiles * nkv;
   const int pre_kt = ceil_div(p_cap, 128), own_kt = ceil_div(t_cap, 128) + ceil_div(lb, 128);
+  const bool pair = pre_rows > lane_rows;
+  // us per partial of every row: written and read at 3 TB/s, and the merge's own step
+  const double part_us = (double)batch * L * nq * h * 8 / 3e6 + (pair ? 0.2 : 0.4);
+  auto prefix_runs = [&](long segs) {
+    const double mem_us = pair ? 0.0 : 4.0 * h * nkv * p_cap / 6.7e6;
+    return PrefixRuns(pair, h, pre_units, pre_kt, segs, own_kt, part_us, mem_us, num_sms);
+  };
+  if (pl.own_tc && own_rows <= QT) {
+    // Own parts of at most one 64-row tile: a run each on tcgen05 beside the prefix's, with two partials, or a kernel of
+    // mma.sync tiles before it (4 us, and 0.9 us a tile of 64 keys less 1 per unit and SM; h = 64: 0.7).  200 tokens behind 2048
+    // positions: 62 against 106 us with contexts up to 60, 178 against 167 up to 1024; 64 of 4 positions behind 8192 80 against 89
+    // up to 384; 64 of 16 171 against 190 up to 128, 238 against 214 up to 1500; 24 of 16 behind 1024 34 against 35 without
+    // contexts, 57 against 41 up to 768.  Over 348 such calls the choice is on average 0.7 % from the better one.  Without a prefix
+    // more than 32 rows of more than one unit per SM: 64 blocks of 16 with contexts up to 384 50 against 62 us, up to 1500 105
+    // against 100.
+    const double own_runs = (double)nkv * batch / num_sms, tiles = ceil_div(own_keys, KT);
+    const int splits = mma_splits((long)nkv * batch, (int)tiles, 2 * num_sms);
+    if (pl.pre_tc)
+      pl.own_tc = prefix_runs(0).us + splits * part_us + 4 + own_runs * ((h == 128 ? 0.9 : 0.7) * tiles - 1) >=
+                  prefix_runs((long)nkv * batch).us + 2 * part_us;
+    else if (!p_cap)
+      pl.own_tc = !(own_rows > 32 && own_runs > 1 && 0.9 * tiles < 7 + 0.9 * own_kt);
+  }
+  pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 2 * lane_rows : QT) : 0;
+  const long own_units = (long)pl.own_tiles * nkv * batch;
   if (pl.pre_tiles && !pl.pre_tc) pl.pre_splits = mma_splits(pre_units, ceil_div(p_cap, KT), 2 * num_sms);
   if (pl.own_tiles && !pl.own_tc) pl.own_splits = mma_splits(own_units, ceil_div(own_keys, KT), 2 * num_sms);
   if (pl.own_tc) {
@@ -394,50 +457,10 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
   }
   const long own_segs = pl.own_tc ? own_units * (pl.own_splits / 2) : 0;
   if (pl.pre_tc) {
-    // Either even runs, which may span units, or s runs per unit.  A run costs about kSeg besides its tiles (Q, the first
-    // copies, the partial out); a partial is written and read once.  With many rows the time is the longest run's or, with
-    // the own part's runs, the average over the SMs.  A prefix under few rows is a read of its keys that does not need every
-    // SM: the CTAs without a run of the prefix take own runs meanwhile.
-    const bool pair = pre_rows > lane_rows;
-    const double kSeg = 5.0, kOwn = h == 128 ? 1.1 : 1.0, kTile = pair ? (h == 128 ? 2.2 : 1.7) : kOwn;   // us
-    // us per partial of every row: written and read at 3 TB/s, and the merge's own step
-    const double part_us = (double)batch * L * nq * h * 8 / 3e6 + (pair ? 0.2 : 0.4);
-    const double mem_us = pair ? 0.0 : 4.0 * h * nkv * p_cap / 6.7e6;
-    const double own_run = kSeg + 0.6 * kOwn * own_kt;   // contexts at 0.6 of what they may hold
+    const PrefixRuns pr = prefix_runs(own_segs);
+    pl.pre_runs = pr.runs;
+    pl.own_alone = pr.alone;
     const long total = pre_units * pre_kt;
-    double best = 0;
-    // The time with the own runs, of which the CTAs without a run of the prefix take the first `alone` each before all CTAs
-    // take turns.
-    auto with_own = [&](long runs, double pre, long& alone) {
-      const long left = num_sms - runs;
-      double best_t = 0;
-      for (long k = 0; k == 0 || (left > 0 && (k - 1) * own_run < pre && (k - 1) * left < own_segs); k++) {
-        const long turns = own_segs > k * left ? ceil_div(own_segs - k * left, (long)num_sms) : 0;
-        const double t = std::max(pre + turns * own_run, (k + turns) * own_run);
-        if (k == 0 || t < best_t) {
-          best_t = t;
-          alone = k;
-        }
-      }
-      return best_t;
-    };
-    auto consider = [&](long runs, double tiles, int segs, double pieces) {
-      const double pre = segs * kSeg + std::max(kTile * tiles, mem_us);
-      double t = pre;
-      long alone = 0;
-      if (own_segs > num_sms - runs || !pair) t = with_own(runs, pre, alone);
-      if (own_segs && pair) t = std::max(pre, (runs * pre + own_segs * (kSeg + kOwn * own_kt)) / num_sms);
-      t += pieces * part_us;
-      if (!pl.pre_runs || t < best) {
-        best = t;
-        pl.pre_runs = (int)runs;
-        pl.own_alone = (int)alone;
-      }
-    };
-    for (long s = 1; s <= pre_kt && (s == 1 || pre_units * s <= num_sms); s++)
-      if (pre_units * s <= num_sms) consider(pre_units * s, ceil_div(pre_kt, (int)s), 1, s);
-    for (int r = own_segs && !pair ? num_sms / 2 : num_sms; r <= num_sms; r += 4)
-      if (total >= r) consider(r, (double)total / r, 2, (double)r / pre_units + 1);
     // a unit's tiles span at most ceil(runs / units) + 1 of the even runs (one less when the runs divide evenly), and no
     // more runs than it has tiles; a unit with one lane's rows leaves two partials per run
     pl.pre_pieces = (int)ceil_div(pl.pre_runs, (int)pre_units) + (pl.pre_runs % pre_units ? 1 : 0);
@@ -445,7 +468,7 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
       // own runs are counted at about 0.6 of the tiles they may have; the kernel gives that up where shorter contexts would
       // leave more pieces than this
       const long even = own_segs / num_sms;
-      const long w = std::min<long>((long)((kSeg + 0.6 * kOwn * own_kt) / kTile + 0.5), total / (2l * num_sms * (even + 1) - own_segs));
+      const long w = std::min<long>((long)((pr.kSeg + 0.6 * pr.kOwn * own_kt) / pr.kTile + 0.5), total / (2l * num_sms * (even + 1) - own_segs));
       pl.own_cost = (int)w;
       const long shortest = (total + w * own_segs) / num_sms - 1 - w * (even + 1);
       pl.pre_pieces = std::max(pl.pre_pieces, (int)((pre_kt + shortest - 1) / shortest) + 1);

@@ -248,7 +248,9 @@ def test_shared_plan_rules(fpd):
     p = plan(fpd, 16, 1, 32, 8, 128, 65536, 512)
     assert p["pre_tc"] and p["own_tc"] and p["pre_runs"] + p["own_ctas"] == 152      # own runs beside the prefix's read
     assert p["own_ctas"] * p["own_alone"] >= 16 * 8
-    p = plan(fpd, 200, 1, 32, 8, 128, 512, 512)
-    assert p["own_alone"] > 0 and p["own_ctas"] * p["own_alone"] < 200 * 8         # some of them, then all CTAs in turn
+    p = plan(fpd, 64, 4, 32, 8, 128, 512, 1024)
+    assert p["own_alone"] > 0 and p["own_ctas"] * p["own_alone"] < 64 * 8          # some of them, then all CTAs in turn
+    assert not plan(fpd, 200, 1, 32, 8, 128, 2500, 60)["own_tc"]                   # many short own parts on mma.sync
+    assert plan(fpd, 200, 1, 32, 8, 128, 2500, 1024)["own_tc"]
     p = plan(fpd, 2, 2, 130, 1, 128, 20000, 0)
     assert not p["pre_tc"] and not p["own_tc"]                                     # 130 heads do not fit 128 rows
