@@ -33,7 +33,7 @@ struct SharedPlan {
   int pre_runs, pre_pieces;             // CTAs that share the prefix's tiles, most of them in one unit
   int own_cost;                         // an own run in the prefix's key tiles, 0: not counted when the prefix is shared out
   int tc_grid;                          // CTAs of the tcgen05 kernel
-  int own_ctas, own_alone;              // of them, from the last, without a run of the prefix; own runs that they take before the rest
+  int own_ctas, own_alone;              // of them, from the last, without a run of the prefix; own runs that each takes first
   int splits() const { return pre_splits + own_splits; }
 };
 SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, int p_cap, int t_cap, int num_sms);

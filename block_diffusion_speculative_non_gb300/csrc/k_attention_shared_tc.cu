@@ -12,13 +12,14 @@
 //
 // A lane's rows are whole positions, the kv head's heads of each (128 rows, or less when the heads do not divide it): one
 // box of a [position][head][h] map of q.  A unit is a pair of such row tiles of a part's rows in one kv head: the lanes hold
-// one tile each and share every K/V tile.  Where a unit has the rows of one lane only (few blocks, the own part
-// of a text block, the last rows of a long one), both lanes hold the same rows and take the even and the odd key tiles: such a
-// unit is a read of the keys, and two key streams keep the copies in flight.  The prefix's (unit, key tile) space is cut into one contiguous run of tiles per CTA, so that all
-// SMs finish together whatever the number of rows; a run that spans units leaves a partial in each.  The own part's units
-// follow, dealt out from the other end: the CTAs without a run of the prefix take as many of them first as fit beside such a
-// run, then all CTAs take turns (64 tokens behind 4096 positions with contexts to 1024: 63 us, 89 when all take turns
-// from the start); where every CTA has a run, the prefix's runs are shorter by what a CTA has of them.
+// one tile each and share every K/V tile.  Where a unit has the rows of one lane only (few blocks, the own part of a text
+// block, the last rows of a long one), both lanes hold the same rows and take the even and the odd key tiles: such a unit is
+// a read of the keys, and two key streams keep the copies in flight.  The prefix's (unit, key tile) space is cut into one
+// contiguous run of tiles per CTA, so that all SMs finish together whatever the number of rows; a run that spans units
+// leaves a partial in each.  The own part's units follow, dealt out from the other end: the CTAs without a run of the prefix
+// take as many of them first as fit beside such a run, then all CTAs take turns (64 tokens behind 4096 positions with
+// contexts to 1024: 60 us, 89 when all took turns from the start); where every CTA has a run, the prefix's runs are shorter
+// by what a CTA has of them.
 //
 // What bounds it: with many rows the tensor core, 48 products of 64 cycles per pair of tiles and key tile, 72 % of the
 // cycles busy at 64 blocks of 16 positions behind 16384 keys (244 us, 1.13 PFLOP/s of the formula's 4 h, 1.69 of products;
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             tc::tma_load_2d(ring + s * S::TILE + h * ATOM_BYTES, ctx ? ctx_map : blk, h * 64, row, bar(full + s));
           n++;
           if (is_v || i > 0) continue;
-          // Q behind the first K tile: its slots are free later, with the S before the last of the run before
+          // Q behind the first K tile, whose slot is free one S before Q's (with the last S of the run before)
           for (int t = 0; t < 2; t++) {
             if (sg.lane_tiles(t) == 0) continue;
             if (nq[t] > 0 && !wait_bar(bar(B_QE + t), (nq[t] & 1) ^ 1)) { *abort_flag = 1; break; }
