@@ -125,6 +125,12 @@ ATTN = {
     "block_of_5000": (1, 5000, 2, 1, 128, 100, 100, [50], 64, True),
     "block_of_2900_h64": (2, 2900, 3, 3, 64, 0, 0, [50, 0], 64, True),
     "last_lane_only": (9, 15, 16, 4, 128, 2500, 2500, [i * 30 for i in range(9)], 256, True),
+    # own units of which some CTAs take several before all take turns, or all of them; few rows of many requests on mma.sync
+    "own_first_then_turns": (60, 4, 16, 8, 128, 500, 500, [(113 * i) % 901 for i in range(60)], 900, True),
+    "own_apart": (20, 1, 32, 8, 128, 9000, 9000, [(113 * i) % 701 for i in range(20)], 700, False),
+    "own_apart_h64": (40, 2, 16, 8, 64, 2999, 3000, [(113 * i) % 601 for i in range(40)], 600, True),
+    "many_decodes": (150, 1, 16, 8, 128, 1500, 1500, [(7 * i) % 51 for i in range(150)], 50, True),
+    "many_decodes_h64": (150, 1, 16, 8, 64, 1500, 1501, [(7 * i) % 51 for i in range(150)], 50, False),
 }
 
 
@@ -185,7 +191,8 @@ def test_nan_reaches_its_own_rows_only(pkg, name):
     assert torch.equal(p.out[keep], clean[0][keep]) and torch.equal(p.lse[keep], clean[1][keep])
 
 
-@pytest.mark.parametrize("name", ["decode_small", "text_block", "group_5", "tile_edges_128", "long_block", "many_rows"])
+@pytest.mark.parametrize("name", ["decode_small", "text_block", "group_5", "tile_edges_128", "long_block", "many_rows",
+                                  "own_first_then_turns", "own_apart_h64", "many_decodes"])
 def test_every_key_counts_once(pkg, name):
     """Keys of 0 make every weight equal; value t is 1 in dimension t % h, so output dimension d counts keys."""
     p = Problem(*ATTN[name], seed=8, stale=0.0)
@@ -219,7 +226,7 @@ def test_repeats_are_bit_identical_and_lse_is_optional(pkg):
         assert torch.equal(p.lse, l)
 
 
-@pytest.mark.parametrize("name", ["decode_h128", "text_block", "many_rows"])
+@pytest.mark.parametrize("name", ["decode_h128", "text_block", "many_rows", "own_first_then_turns", "own_apart"])
 def test_captured_call_follows_lengths_on_the_device(pkg, name):
     """One graph, replayed after the lengths on the device have changed; captured on a stream of its own."""
     p = Problem(*ATTN[name], seed=10, stale=0.5)
