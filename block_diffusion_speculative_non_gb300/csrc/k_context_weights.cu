@@ -9,6 +9,8 @@
 // Bounds: 2 h flops and one 2^x per row and key, 2 h bytes per key.  This small form is latency (16 rows over 128 keys:
 // 2.6 us); with many rows it is held back by the legacy matrix path and by reading the queries once per 64 keys (4096 rows
 // over 16384 keys 855 us against 125 on tcgen05).
+#include <algorithm>
+
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
 
@@ -129,12 +131,20 @@ cudaError_t ctx_weights_init_attributes() {
 }
 
 cudaError_t launch_ctx_weights(const CtxWeights& a, int num_sms, cudaStream_t st) {
-  // tcgen05 for more than 128 rows (256 rows over 512 keys 7.2 against 9.7 us), and for fewer from about 1536 64-key tiles of
-  // contexts that are not short (8 x 64 rows over 2048 keys 9.4 against 12.7, 64 rows over 16384 10.7 against 16.4); below
-  // that its setup costs more than the tiles (64 rows over 512 keys 4.1 against 5.9, 64 x 64 rows over 256 13.4 against 15.5)
-  const long long tiles = (long long)a.batch * a.nkv * ceil_div(a.t_cap, KT) * ceil_div(a.L * (a.nq / a.nkv), QT);
-  if (ctx_weights_tc_supported(a) && (a.L * (a.nq / a.nkv) > 128 || (tiles >= 1536 && a.t_cap >= 512)))
-    return launch_ctx_weights_tc(a, num_sms, st);
+  // The kernel whose time (us, fitted to 276 calls) is the smaller: on average 0.5 % from the better one over 476.  mma.sync: a
+  // CTA's row tiles in turn, and the SM's share of all tiles.  tcgen05: tensor memory to set up, the query tiles in turn, the
+  // SM's share of the key tiles, and a step from one head's keys to the next.  (16 positions, 8 kv heads: 8192 keys 8.2 on
+  // tcgen05 against 12.5, 2048 keys 5.4 on mma.sync against 6.3; 64 requests of 512 keys at h = 64 13.9 on mma.sync against
+  // 18.4.)
+  const int grp = a.nq / a.nkv, rt = ceil_div(a.L * grp, QT);
+  if (ctx_weights_tc_supported(a)) {
+    const bool wide = a.h == 128;
+    const int nqt = ceil_div(a.L, std::min(128 / grp, a.L));
+    const double heads = (double)a.batch * a.nkv / num_sms;
+    const double mma_us = 2 + (wide ? 1.7 : 1.15) * rt + heads * ceil_div(a.t_cap, KT) * (0.12 + (wide ? 0.5 : 0.25) * rt);
+    const double tc_us = 5 + 0.8 * nqt + heads * (ceil_div(a.t_cap, 128) * ((wide ? 0.28 : 0.15) + 0.27 * nqt) + 2.1);
+    if (tc_us < mma_us) return launch_ctx_weights_tc(a, num_sms, st);
+  }
   const int key_tiles = ceil_div(a.t_cap, KT);
   const int grid = a.batch * a.nkv * key_tiles;
   return a.h == 128 ? launch_k(weights_mma_kernel<128>, grid, NWARP * 32, sizeof(WeightSmem<128>), st, a, key_tiles)

@@ -371,6 +371,7 @@ WEIGHTS = {
     "many_requests_tc": (40, 40, 16, 4, 128, [(97 * i) % 300 if i % 7 else 0 for i in range(40)], 300),
     "few_rows_tc": (13, 4, 32, 8, 128, [1100 - 90 * i for i in range(13)], 1111),
     "few_rows_h64_tc": (26, 1, 16, 8, 64, [(211 * i) % 600 for i in range(26)], 600),
+    "few_rows_long_h64_tc": (6, 1, 32, 8, 64, [9000, 1, 0, 4097, 513, 8192], 9000),
     "group_130": (2, 2, 130, 1, 128, [100, 65], 130),
     "nothing_tc": (2, 80, 8, 2, 128, [0, 0], 300),
 }
