@@ -413,12 +413,13 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
   const int lane_rows = grp <= 128 ? 128 / grp * grp : 0;
   const bool own_tma = lane_rows && (long long)batch * 2 * nkv * t_cap < INT32_MAX && (long long)batch * nkv * lb < INT32_MAX;
   const bool pre_tma = lane_rows && (long long)2 * nkv * p_cap < INT32_MAX;
-  // Below two 64 x 64 tiles of h = 128 per resident CTA the whole call goes to mma.sync, which has no tensor memory, descriptors
-  // or rings to set up: 16 rows over 512 + 16 keys 8.6 against 11.4 us, 4 x 16 rows at h = 64 over 64 + 16 keys 5.9 against
-  // 9.4; above it tcgen05 wins (105 rows over 4999 keys 16.7 against 20.3, 512 rows over 2048 24.5 against 43).
+  // Up to 3.5 64 x 64 tiles of h = 128 per SM, or 13 of h = 64, the whole call goes to mma.sync, which has no tensor memory,
+  // descriptors or rings to set up: 16 rows over 512 + 16 keys 8.6 against 11.4 us, 4 x 16 rows at h = 64 over 64 + 16 keys 5.9
+  // against 9.4, 16 x 4 rows at h = 64 over 400 and 600 keys 13.1 against 15.6; above it tcgen05 wins (4 x 64 rows over 400 and 600
+  // keys 17.9 against 23.6, 512 rows over 2048 24.5 against 43).  Over 554 calls 0.5 % from the better kernel on average.
   const long long tiles64 = (long long)nkv * ceil_div(pre_rows, QT) * ceil_div(p_cap, KT) +
                             (long long)nkv * batch * ceil_div(own_rows, QT) * ceil_div(own_keys, KT);
-  const bool small = tiles64 * h <= 128 * 4ll * num_sms;
+  const bool small = 2 * tiles64 <= (h == 128 ? 7ll : 26ll) * num_sms;
   pl.pre_tc = p_cap && pre_tma && !small;
   pl.own_tc = own_keys && own_tma && !small;
   pl.pre_tiles = p_cap ? ceil_div(pre_rows, pl.pre_tc ? 2 * lane_rows : QT) : 0;

@@ -110,6 +110,7 @@ ATTN = {
     "tile_edges_128": (3, 40, 8, 2, 128, 128, 129, [127, 128, 129], 130, True),
     "long_block": (2, 385, 8, 2, 128, 300, 300, [77, 0], 128, True),
     "long_block_h64": (2, 200, 8, 2, 64, 1000, 1024, [0, 513], 600, True),
+    "long_block_h64_tc": (2, 300, 8, 2, 64, 2500, 2511, [0, 513], 600, True),
     "many_rows": (24, 16, 8, 1, 128, 700, 704, [i * 5 for i in range(24)], 120, True),
     "wide_group": (9, 1, 128, 2, 128, 3000, 3000, [i for i in range(9)], 9, True),
     "long_prefix": (2, 1, 8, 2, 128, 70001, 70016, [500, 2], 512, True),
@@ -157,7 +158,7 @@ def test_rows_without_a_key(pkg, h, L):
 
 
 @pytest.mark.parametrize("scale", [8.0, 40.0])
-@pytest.mark.parametrize("name", ["decode_h128", "text_block", "many_rows", "long_block_h64"])
+@pytest.mark.parametrize("name", ["decode_h128", "text_block", "many_rows", "long_block_h64", "long_block_h64_tc"])
 def test_large_scores(pkg, name, scale):
     """Scores up to hundreds: one key takes nearly all of a row, the running maximum jumps."""
     p = Problem(*ATTN[name], seed=5, scale=scale)
