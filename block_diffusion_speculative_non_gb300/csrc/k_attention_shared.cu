@@ -358,6 +358,45 @@ static int mma_splits(long base, int kt, int slots) {
   return best_s;
 }
 
+// Splits of both parts where the whole call is on the 64-row kernel, chosen together (units and kt as above; kt 0: no such
+// part).  In key tiles, a split pays 3 besides its own; the call takes its longest split or 0.6 of the work over the resident
+// CTAs, and 0.1 and one per 10^6 outputs for every partial that the merge reads.  Over 65 calls 4 % from the best of their
+// combinations, 10 % with each part by itself (16 x 8 positions at h = 64 over 1500 and 300 keys 11.8 against 14.9 us).
+struct MmaSplits {
+  int pre = 0, own = 0;
+  MmaSplits(long pre_units, int pre_kt, long own_units, int own_kt, double outputs, int slots) {
+    struct Cut {
+      int n;
+      double tiles, work;
+    } cut[2][16];
+    int cuts[2] = {0, 0};
+    auto list = [&](int part, long units, int kt) {
+      if (!kt) {
+        cut[part][cuts[part]++] = {0, 0, 0};
+        return;
+      }
+      for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, kt}) {
+        if (s > std::min(kt, 128) || (cuts[part] && cut[part][cuts[part] - 1].n == s)) continue;
+        const double t = ceil_div(kt, s) + 3;
+        cut[part][cuts[part]++] = {s, t, (double)units * s * t};
+      }
+    };
+    list(0, pre_units, pre_kt);
+    list(1, own_units, own_kt);
+    const double per_partial = 0.1 + 1e-6 * outputs;
+    double best = 0;
+    for (int i = 0; i < cuts[0]; i++)
+      for (int j = 0; j < cuts[1]; j++) {
+        const Cut &p = cut[0][i], &o = cut[1][j];
+        const double t = std::max(std::max(p.tiles, o.tiles), 0.6 * (p.work + o.work) / slots) + (p.n + o.n) * per_partial;
+        if ((i || j) && t >= best) continue;
+        best = t;
+        pre = p.n;
+        own = o.n;
+      }
+  }
+};
+
 // How the tcgen05 kernel's CTAs share the prefix's key tiles (kt of each of `units` units) beside the own part's runs (segs of
 // own_kt key tiles).  Either even runs, which may span units, or s runs per unit.  A run costs about kSeg us besides its
 // tiles (Q, the first copies, the partial out); a partial is written and read once.  With many rows (pair) the time is the
@@ -450,8 +489,13 @@ SharedPlan shared_attn_plan(int batch, int L, int lb, int nq, int nkv, int h, in
   }
   pl.own_tiles = own_keys ? ceil_div(own_rows, pl.own_tc ? 2 * lane_rows : QT) : 0;
   const long own_units = (long)pl.own_tiles * nkv * batch;
-  if (pl.pre_tiles && !pl.pre_tc) pl.pre_splits = mma_splits(pre_units, ceil_div(p_cap, KT), 2 * num_sms);
   if (pl.own_tiles && !pl.own_tc) pl.own_splits = mma_splits(own_units, ceil_div(own_keys, KT), 2 * num_sms);
+  if (pl.pre_tiles && !pl.pre_tc) {
+    const MmaSplits m(pre_units, ceil_div(p_cap, KT), own_units, pl.own_tc ? 0 : ceil_div(own_keys, KT), (double)batch * L * nq * h,
+                      2 * num_sms);
+    pl.pre_splits = m.pre;
+    pl.own_splits = m.own;
+  }
   if (pl.own_tc) {
     pl.own_splits = 2;
     if (!pl.pre_tc) pl.own_splits *= (int)std::max(1l, std::min<long>(own_kt / 2, num_sms / own_units));
