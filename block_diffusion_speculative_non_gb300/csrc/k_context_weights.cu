@@ -23,7 +23,7 @@ template <int H>
 struct WeightSmem {
   bf16 k[KT * H];
   bf16 q[2][QT * H];
-  float l2[2][QT];   // lse log2(e) of the rows, +inf for rows that hold no key and past the last row: weight 0
+  float l2[2][QT];   // lse log2(e) of the rows; -inf (rows that hold no key and past the last row): weight 0, whatever their score
 };
 
 template <int H>
@@ -55,12 +55,7 @@ __global__ void __launch_bounds__(NWARP * 32) weights_mma_kernel(const __grid_co
     }
     if (tid < QT) {
       const int qi = r0 + tid;
-      float v = INFINITY;
-      if (qi < nrows) {
-        v = a.lse[((size_t)b * a.L + qi / grp) * a.nq + g * grp + qi % grp];
-        v = v == -INFINITY ? INFINITY : v * log2e;
-      }
-      sm.l2[buf][tid] = v;
+      sm.l2[buf][tid] = qi < nrows ? a.lse[((size_t)b * a.L + qi / grp) * a.nq + g * grp + qi % grp] * log2e : -INFINITY;
     }
     cp_async_commit();
   };
@@ -98,8 +93,9 @@ __global__ void __launch_bounds__(NWARP * 32) weights_mma_kernel(const __grid_co
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         const float2 l = *reinterpret_cast<const float2*>(&sm.l2[buf][np * 16 + e * 8 + (lane & 3) * 2]);
-        t0 += ex2_approx(fmaf(s[e][0], sl2, -l.x)) + ex2_approx(fmaf(s[e][1], sl2, -l.y));
-        t1 += ex2_approx(fmaf(s[e][2], sl2, -l.x)) + ex2_approx(fmaf(s[e][3], sl2, -l.y));
+        const bool x = l.x != -INFINITY, y = l.y != -INFINITY;
+        t0 += (x ? ex2_approx(fmaf(s[e][0], sl2, -l.x)) : 0.f) + (y ? ex2_approx(fmaf(s[e][1], sl2, -l.y)) : 0.f);
+        t1 += (x ? ex2_approx(fmaf(s[e][2], sl2, -l.x)) : 0.f) + (y ? ex2_approx(fmaf(s[e][3], sl2, -l.y)) : 0.f);
       }
     }
     w0 += t0;

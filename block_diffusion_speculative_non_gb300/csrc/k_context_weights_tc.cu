@@ -10,8 +10,9 @@
 // product runs while a tile is summed.  Per score: one product, one fma, one 2^x, one add.  Warps:
 //   0      TMA producer of K (three tiles deep), 3: of Q (three tiles deep; a 4-d map of [request][position][head][h] whose
 //          box is the kv head's heads, rows past the request's block come back as 0);
-//   1      MMA issuer;
-//   2      -lse log2(e) of a tile's rows into shared memory (-inf for rows without a key and past the last row: weight 0);
+//   1      MMA issuer; it zeroes the query rows that warp 2 names before the tile's first product;
+//   2      -lse log2(e) of a tile's rows into shared memory (-inf for rows without a key and past the last row: weight 0), and
+//          which rows have no key: what such a row holds must not count, and NaN would pass through the -inf;
 //   4..19  sums: warp = [32 of the tile's columns][32 of the keys].  The four parts of a key's sum are added in a fixed order.
 //
 // Measured: 4096 rows per kv head over 16384 keys, 8 kv heads: 125 us, 1.10 PFLOP/s (the floor is 72).  The sums bound it
@@ -48,7 +49,7 @@ enum {
 template <int HD>
 struct Lay {
   static constexpr int TILE = 128 * HD * 2, ATOMS = HD / 64;
-  static constexpr int K = 0, Q = RST * TILE, L2 = Q + RST * TILE, COMB = L2 + LST * QT * 4, BAR = COMB + 2 * 2 * 3 * KT * 4;
+  static constexpr int K = 0, Q = RST * TILE, L2 = Q + RST * TILE, DEAD = L2 + LST * QT * 4, COMB = DEAD + LST * 4 * 4, BAR = COMB + 2 * 2 * 3 * KT * 4;
   static constexpr size_t BYTES = 1024 + (size_t)BAR + 8 * B_N + 16;
   static_assert(BYTES <= 232448, "tile set exceeds the shared memory of one CTA");
 };
@@ -115,12 +116,26 @@ struct Share {
   }
 };
 
+// Zeroes the rows of a query tile whose bits are set, for the products that follow; by a whole warp.
+template <int HD>
+__device__ __noinline__ void zero_rows(uint8_t* tile, uint4 rows) {
+  const int lane = threadIdx.x & 31, atom = lane >> 3, chunk = lane & 7;   // a row: 128 bytes in each 64-dim atom
+  for (int r = 0; r < QT; r++) {
+    const uint32_t word = r < 32 ? rows.x : r < 64 ? rows.y : r < 96 ? rows.z : rows.w;
+    if (((word >> (r & 31)) & 1) && atom < HD / 64)
+      *reinterpret_cast<uint4*>(tile + atom * ATOM_BYTES + r * 128 + chunk * 16) = make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_constant__ WtArgs p) {
   using S = Lay<HD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* l2s = reinterpret_cast<float*>(smem + S::L2);
+  uint32_t* dead = reinterpret_cast<uint32_t*>(smem + S::DEAD);
   float* comb = reinterpret_cast<float*>(smem + S::COMB);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_N);
@@ -206,8 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
         const int qs = uni(nq % RST), buf = uni(nq & 1);
         // whole 32-column chunks: the sums read no column that the product has not written
         const uint32_t id = idesc_bf16(KT, 32 * ceil_div(uni(min(p.rpt, nrows - q * p.rpt)), 32), 0);
-        if (!(ok = wait_bar(bar(B_QF + qs), (nq / RST) & 1) &&
-                   (nq < 2 || wait_bar(bar(B_SE + buf), ((nq >> 1) & 1) ^ 1)))) break;
+        if (!(ok = wait_bar(bar(B_QF + qs), (nq / RST) & 1) && wait_bar(bar(B_LF + nq % LST), (nq / LST) & 1))) break;
+        const uint4 none = *reinterpret_cast<const uint4*>(dead + nq % LST * 4);
+        if (none.x | none.y | none.z | none.w) zero_rows<HD>(smem + S::Q + qs * S::TILE, none);
+        if (nq >= 2 && !(ok = wait_bar(bar(B_SE + buf), ((nq >> 1) & 1) ^ 1))) break;
         tc::tc_fence_after();
         const uint64_t db = dq + qs * (S::TILE >> 4);
 #pragma unroll
@@ -259,8 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
           const int s = n % LST;
           if (n >= LST && !wait_bar(bar(B_LE + s), ((n / LST) & 1) ^ 1)) *abort_flag = 1;
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            l2s[s * QT + i * 32 + lane] = v[j][i] == -INFINITY ? -INFINITY : -v[j][i] * 1.4426950408889634f;
+          for (int i = 0; i < 4; i++) {
+            const bool none = v[j][i] == -INFINITY;
+            l2s[s * QT + i * 32 + lane] = none ? -INFINITY : -v[j][i] * 1.4426950408889634f;
+            const uint32_t rows = __ballot_sync(0xffffffffu, none && (q0 + j) * p.npt + pos[i] < p.a.L);
+            if (lane == 0) dead[s * 4 + i] = rows;
+          }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar(B_LF + s));
           n++;

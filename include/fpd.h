@@ -374,8 +374,9 @@ size_t fpd_shared_attention_workspace_bytes(int batch, int block_len, int n_q_he
 /* The attention weight that each context position collects from a block's rows, for one layer:
  *   w[b][g][t] = sum over j and the heads i of kv head g of exp(q[b,j,i] . k_t / sqrt(h) - lse[b,j,i]),  t < ctx_len[b]
  * written to (accumulate 0) or added to (otherwise) weights[layer][b][g][t]; entries from ctx_len[b] on stay as they are.
- * With the lse of the attention over all keys a row hands out a total of 1.  Rows with lse -inf (no key) give nothing.  A
- * shared prefix collects from all requests: batch 1, block_len = the batch's rows, the prefix store and its length.
+ * With the lse of the attention over all keys a row hands out a total of 1.  Rows with lse -inf (no key) give nothing, whatever
+ * their q holds.  Stored keys below the length must be finite (an infinite one may get NaN where its weight is 0).  A shared
+ * prefix collects from all requests: batch 1, block_len = the batch's rows, the prefix store and its length.
  *   lse       device [batch * block_len, n_q_heads] fp32
  *   weights   device [n_layers > layer][batch][n_kv_heads][t_cap] fp32 */
 fpd_status fpd_context_weights(int batch, int block_len, int n_q_heads, int n_kv_heads, int head_dim, int layer,

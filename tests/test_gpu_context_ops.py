@@ -435,6 +435,33 @@ def test_a_nan_query_spoils_its_own_request_only(pkg, name):
     assert torch.equal(w[:, keep], clean[:, keep]) and w[1, 1, :, :p.lens[1]].isnan().all()
 
 
+@pytest.mark.parametrize("name", ["small", "ragged", "group_5", "group_3_h64", "many_rows", "many_rows_h64", "group_5_tc", "group_3_h64_tc",
+                                  "wide_group_tc", "few_rows_tc"])
+def test_rows_without_a_key_give_nothing_whatever_they_hold(pkg, name):
+    """A row with lse -inf is left out even where its query holds NaN or infinities (a padded position of a batch).  A key whose
+    scores overflow to -inf has weight 0."""
+    p = weight_problem(name, seed=17)
+    B, L, nq, nkv, h = p.shape
+    gen = torch.Generator(device=DEV).manual_seed(18)
+    out = torch.rand(B * L, nq, device=DEV, generator=gen) < 0.3
+    p.lse[out] = -math.inf
+    p.q[out] = 0
+    w = torch.zeros(2, B, nkv, p.t_cap, device=DEV)
+    run_weights(pkg, p, w)
+    clean = w.clone()
+    assert weights_close(w[1], ref.context_weights(p.q, p.lse, p.store[p.layer], p.lens, B, L, nkv))
+    for bad in (math.nan, math.inf, -math.inf):
+        p.q[out] = bad
+        run_weights(pkg, p, w)
+        assert torch.equal(w, clean), bad
+    p.q[out] = math.nan
+    p.q[..., 0][~out] = 8
+    p.store[p.layer, :, 0, :, :1, 0] = -3.0e38
+    run_weights(pkg, p, w)
+    assert (w[1, [b for b in range(B) if p.lens[b]], :, 0] == 0).all()
+    assert weights_close(w[1], ref.context_weights(p.q, p.lse, p.store[p.layer], p.lens, B, L, nkv))
+
+
 def test_rows_hand_out_one_in_all(pkg):
     """Without block keys, the weights of a request's positions and its share of the prefix's add up to its rows."""
     p = Problem(3, 16, 32, 8, 128, 500, 512, [100, 0, 33], 128, False, seed=21)
