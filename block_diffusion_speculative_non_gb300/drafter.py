@@ -36,12 +36,12 @@ class Drafter:
         self.shape = shape
         self.device = torch.device(device)
         self.max_batch, self.max_block_len, self.t_cap = max_batch, max_block_len, t_cap
+        self.max_pos, self.max_pos_given = max(max_pos or 0, t_cap + max_block_len), max_pos is not None
         self.w = {k: to_device_bf16(weights[k], self.device) for k in ("embed", "w_fc", "hidden_norm", "final_norm",
                                                                        "lm_head")}
         self.layers = [{k: to_device_bf16(lw[k], self.device) for k in _LAYER_KEYS} for lw in weights["layers"]]
         desc = ModelDesc(shape.n_layers, shape.d_model, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, shape.d_ff,
-                         shape.vocab, shape.n_feat, max(max_pos or 0, t_cap + max_block_len), shape.rms_eps,
-                         shape.rope_theta)
+                         shape.vocab, shape.n_feat, self.max_pos, shape.rms_eps, shape.rope_theta)
         W = Weights()
         for k, t in self.w.items():
             setattr(W, k, t.data_ptr())
@@ -209,9 +209,14 @@ class SharedDraft:
     Everything runs on torch's current stream.  The buffers stay where they are: draft_block, append_rows, evict and
     evict_prefix can be captured in a CUDA graph (prepare_prefix and append bring host offsets to the device first).  Objects
     share nothing but the drafter's weights, so two of them may run on two streams; calls on one object must not overlap.
-    Positions reach up to the Drafter's max_pos; past it rows are skipped and recorded (fpd_device_status)."""
+    Positions reach up to the Drafter's max_pos, which must be given where prefix_cap + t_cap + block_len passes the table a Drafter
+    has by itself.  Rows past it, or past a store's capacity, are skipped and recorded (fpd_device_status); prepare_prefix and
+    append leave them out of the lengths."""
 
     def __init__(self, dr, batch, block_len, t_cap, prefix_cap=0, collect=False):
+        if prefix_cap + t_cap + block_len > dr.max_pos and not dr.max_pos_given:
+            raise ValueError(f"prefix_cap {prefix_cap} + t_cap {t_cap} + block_len {block_len} passes the Drafter's {dr.max_pos} rotary "
+                             "positions; give the Drafter max_pos")
         s, dev = dr.shape, dr.device
         self.dr, self.batch, self.block_len, self.t_cap, self.prefix_cap = dr, batch, block_len, t_cap, prefix_cap
         i32 = dict(dtype=torch.int32, device=dev)
@@ -236,25 +241,45 @@ class SharedDraft:
             self.prefix_kv, prefix_cap, self.prefix_len if prefix_cap else None, self.kv, t_cap,
             self.ctx_len if t_cap else None, self.pos_offset, self.weights, self.prefix_weights, accumulate=True)
 
+    def _features(self, feats, rows=None):
+        """Device copies of the feature tensors [rows, d], and the rows."""
+        s = self.dr.shape
+        if len(feats) != s.n_feat:
+            raise ValueError(f"{len(feats)} feature tensors, the model takes {s.n_feat}")
+        rows = int(feats[0].shape[0]) if rows is None else rows
+        for f in feats:
+            if int(np.prod(f.shape)) < rows * s.d_model:
+                raise ValueError(f"a feature tensor of shape {tuple(f.shape)}, the call needs [{rows}, {s.d_model}]")
+        return [to_device_bf16(f, self.dr.device) for f in feats], rows
+
+    def _grown(self, lens, offset, rows, cap):
+        """Lengths after `rows` more rows each: as many as the store and the rotary table hold."""
+        end = torch.minimum(lens + rows, (self.dr.max_pos - offset).clamp_(max=cap))
+        return torch.maximum(lens, end)
+
     def prepare_prefix(self, feats):
         """Appends target features [rows, d] to the prefix; the requests' positions move behind it.  Call it before the
         requests have context of their own."""
-        fd = [to_device_bf16(f, self.dr.device) for f in feats]
-        rows = int(fd[0].shape[0])
+        fd, rows = self._features(feats)
         off = torch.tensor([0, rows], dtype=torch.int32, device=self.dr.device)
         fpd_prepare_context_at(self.dr.handle, 1, rows, off, None, self.prefix_len, self.prefix_offset, fd, self.prefix_kv,
                                self.prefix_cap, self.workspace, self.workspace.numel())
-        self.prefix_len.add_(rows)
-        self.pos_offset.add_(rows)
+        end = self._grown(self.prefix_len, self.prefix_offset, rows, self.prefix_cap)
+        self.pos_offset.add_(end - self.prefix_len)
+        self.prefix_len.copy_(end)
 
     def append(self, row_off, feats):
         """Appends packed target features to the requests' own contexts: request b's rows are [row_off[b], row_off[b + 1])
         of every feature tensor (row_off: host sequence)."""
-        fd = [to_device_bf16(f, self.dr.device) for f in feats]
-        off = np.asarray(row_off, np.int32)
-        off_d = torch.from_numpy(off.copy()).to(self.dr.device)
-        self.append_rows(int(off[-1]), off_d, None, self.ctx_len, fd)
-        self.ctx_len.add_(off_d[1:] - off_d[:-1])
+        off = np.array(row_off, np.int32)
+        if off.shape != (self.batch + 1,) or off[0] != 0 or (np.diff(off) < 0).any():
+            raise ValueError(f"row_off must be {self.batch + 1} row numbers from 0 on, in order")
+        if (np.diff(off) > self.t_cap).any():
+            raise ValueError(f"more rows of a request than its store's {self.t_cap}")
+        fd, rows = self._features(feats, int(off[-1]))
+        off_d = torch.from_numpy(off).to(self.dr.device)
+        self.append_rows(rows, off_d, None, self.ctx_len, fd)
+        self.ctx_len.copy_(self._grown(self.ctx_len, self.pos_offset, off_d[1:] - off_d[:-1], self.t_cap))
 
     def append_rows(self, total_rows, row_off_d, row_cnt_d, pos_start_d, feats_d):
         """fpd_prepare_context_at on device arrays, into the own stores at slots pos_start_d (lengths are the caller's to

@@ -130,6 +130,18 @@ def test_compiled_calls_refuse_what_is_no_argument(fpd):
     assert calls.evict_context(0, 1, 2, 64, 8, 0, 64, 8, 64, 64, 64, 8, 64, 64, None, None, 64, 8, None, 0) != 0
 
 
+def test_shared_draft_refuses_more_positions_than_the_drafter_has(fpd):
+    """A Drafter that was not told max_pos has its own t_cap + max_block_len rotary positions: no room behind a long prefix."""
+    import types
+    dr = types.SimpleNamespace(max_pos=528, max_pos_given=False)
+    with pytest.raises(ValueError, match="max_pos"):
+        fpd.SharedDraft(dr, 8, 16, 512, 4096)
+    with pytest.raises(ValueError, match="max_pos"):
+        fpd.SharedDraft(dr, 8, 17, 512)
+    with pytest.raises(AttributeError):      # past the check
+        fpd.SharedDraft(dr, 8, 16, 500, 12)
+
+
 def test_selection_rule_of_the_reference():
     nan, inf = float("nan"), float("inf")
     assert ref.kept_positions([5, 1, 3, 2], 4, 4, 0) == [0, 1, 2, 3]

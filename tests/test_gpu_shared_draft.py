@@ -316,3 +316,42 @@ def test_speculative_steps_behind_a_prefix_in_a_graph(pkg):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
     assert torch.equal(sd.kv, kv) and torch.equal(sd.weights, wts) and pkg.fpd_device_status() == 0
+
+
+def test_rows_without_a_slot_or_a_position_are_not_counted(pkg):
+    """Rows past the rotary table or the store are recorded and left out of the lengths: what is drafted is what the rows
+    that are there give."""
+    P, n = 30, 12
+    w, dr, sd = build(pkg, TINY, 1, 8, 40, 30, seed=16, max_pos=50)
+    pf, of = synth.make_features(TINY, P + 5, 96), synth.make_features(TINY, 40, 97)
+    sd.prepare_prefix(rows_of(pf, 0, 25))
+    sd.prepare_prefix(rows_of(pf, 25, P + 5))            # 5 rows past prefix_cap
+    assert pkg.fpd_device_status() == 6
+    assert sd.prefix_len.item() == P and sd.pos_offset.tolist() == [P]
+    sd.append([0, n], rows_of(of, 0, n))
+    assert pkg.fpd_device_status() == 0 and sd.ctx_len.tolist() == [n]
+    hid = sd.draft_block(dev_i32([3]), 5)                # positions 42..49: the last that fit
+    torch.cuda.synchronize()
+    assert pkg.fpd_device_status() == 0
+    sd.ctx_len.zero_()
+    sd.append([0, 40], of)                               # 20 of 40 rows have a position
+    assert pkg.fpd_device_status() == 6 and sd.ctx_len.tolist() == [20]
+    w2, dr2, alone = build(pkg, TINY, 1, 8, 40, 30, seed=16, max_pos=50)
+    alone.prepare_prefix(rows_of(pf, 0, 25))
+    alone.prepare_prefix(rows_of(pf, 25, P))
+    alone.append([0, n], rows_of(of, 0, n))
+    assert torch.equal(alone.draft_block(dev_i32([3]), 5), hid) and pkg.fpd_device_status() == 0
+
+
+def test_appends_refuse_what_they_cannot_hold(pkg):
+    w, dr, sd = build(pkg, TINY, 2, 8, 16, 16, seed=17)
+    f = synth.make_features(TINY, 20, 98)
+    for off, feats, what in (([0, 17, 20], f, "more rows"), ([0, 20], f, "row_off"), ([1, 5, 9], f, "row_off"), ([0, 9, 5], f, "row_off"),
+                             ([0, 5, 9], rows_of(f, 0, 8), "the call needs"), ([0, 5, 9], f[:-1], "feature tensors")):
+        with pytest.raises(ValueError, match=what):
+            sd.append(off, feats)
+    with pytest.raises(ValueError, match="the call needs"):
+        sd.prepare_prefix([f[0]] + rows_of(f[1:], 0, 8))
+    with pytest.raises(pkg.FpdError):
+        sd.prepare_prefix(f)                             # 20 rows, 16 slots
+    assert sd.ctx_len.tolist() == [0, 0] and sd.prefix_len.item() == 0 and sd.pos_offset.tolist() == [0, 0]
