@@ -440,8 +440,10 @@ struct PrefixRuns {
     };
     for (long s = 1; s <= kt && (s == 1 || units * s <= num_sms); s++)
       if (units * s <= num_sms) consider(units * s, ceil_div(kt, (int)s), 1, s);
-    for (int r = segs && !pair ? num_sms / 2 : num_sms; r <= num_sms; r += 4)
+    for (int r = segs && !pair ? std::max(1, num_sms / 2) : num_sms;; r = std::min(r + 4, num_sms)) {
       if (total >= r) consider(r, (double)total / r, 2, (double)r / units + 1);
+      if (r == num_sms) break;
+    }
   }
 };
 

@@ -247,6 +247,31 @@ def test_shared_plan_covers_every_tile_and_slot_once(fpd, B, L, nq, nkv, h):
                         assert sorted(slots[u]) == list(range(pl["pre_splits"])), (pl, P, u, slots[u])
 
 
+def check_cover(fpd, B, L, nq, nkv, h, p_cap, t_cap, sms):
+    pl = plan(fpd, B, L, nq, nkv, h, p_cap, t_cap, sms=sms)
+    assert pl["pre_splits"] >= 1 and pl["own_splits"] >= 1, pl
+    if not pl["pre_tc"]:
+        return
+    assert 1 <= pl["pre_runs"] <= pl["grid"] <= sms, pl
+    for P in sorted({0, 1, min(129, p_cap), p_cap // 2, p_cap}):
+        runs, units, tiles = walk(pl, B, L, nq, nkv, P, sms)
+        seen, slots = {u: [] for u in range(units)}, {u: [] for u in range(units)}
+        for c, u, lo, hi, sl in runs:
+            seen[u] += range(lo, hi)
+            slots[u] += sl
+        for u in range(units):
+            assert seen[u] == list(range(tiles)) and sorted(slots[u]) == list(range(pl["pre_splits"])), (pl, P, u)
+
+
+@pytest.mark.parametrize("sms", [1, 2, 3, 7])
+def test_shared_plan_covers_on_few_sms(fpd, sms):
+    check_cover(fpd, 1, 2, 128, 2, 128, 18305, 1000, sms)
+    for B, L, nq, nkv, h in SHAPES[:8]:
+        for p_cap in (100, 4096, 20000):
+            for t_cap in (0, 1000):
+                check_cover(fpd, B, L, nq, nkv, h, p_cap, t_cap, sms)
+
+
 def test_shared_plan_rules(fpd):
     """The calls whose choice the comments beside the rules quote."""
     assert not plan(fpd, 1, 16, 32, 8, 128, 512, 0)["pre_tc"]                      # small: mma.sync
