@@ -2,6 +2,7 @@
 #include "../../include/fpd_testing.h"
 #include "fpd_context.cuh"
 #include "fpd_kernels.cuh"
+#include "weights_share.cuh"
 
 using namespace fpd;
 
@@ -288,5 +289,24 @@ extern "C" int fpd_test_shared_plan(int batch, int L, int block_keys, int nq, in
   const int v[12] = {pl.pre_tc, pl.own_tc, pl.pre_tiles, pl.pre_splits, pl.own_tiles,
                      pl.own_splits, pl.pre_runs, pl.pre_pieces, pl.own_cost, pl.tc_grid, pl.own_ctas, pl.own_alone};
   for (int i = 0; i < 12; i++) out[i] = v[i];
+  return FPD_OK;
+}
+
+extern "C" int fpd_test_weight_shares(int batch, int nkv, const int32_t* counted, const int32_t* walked, int cta, int ctas, int max_units,
+                                      int32_t* units, int32_t* n_units) {
+  if (batch < 1 || nkv < 1 || !counted || !walked || cta < 0 || cta >= ctas || !units || !n_units) return FPD_ERR_SHAPE;
+  struct Len {
+    const int32_t *counted, *walked;
+    int reads;   // the first pass over the requests counts the tiles
+    int operator()(int b) { return reads > 0 ? (reads--, counted[b]) : walked[b]; }
+  };
+  Share<Len> sh(Len{counted, walked, batch}, batch, nkv, cta, ctas);
+  int n = 0;
+  for (; sh.next(); n++) {
+    if (n == max_units) return FPD_ERR_CAPACITY;
+    const int32_t u[4] = {sh.b, sh.g, sh.k0, sh.nk};
+    for (int i = 0; i < 4; i++) units[4 * n + i] = u[i];
+  }
+  *n_units = n;
   return FPD_OK;
 }

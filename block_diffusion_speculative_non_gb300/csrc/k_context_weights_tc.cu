@@ -21,13 +21,14 @@
 
 #include "attn_tc_prims.cuh"
 #include "fpd_context.cuh"
+#include "weights_share.cuh"
 
 namespace fpd {
 
 namespace {
 using namespace attn_tc;
 
-constexpr int KT = 128, QT = 128;
+constexpr int KT = kShareTile, QT = 128;
 constexpr int kConsumers = 16;           // warps that sum
 constexpr int kThreads = (4 + kConsumers) * 32;
 constexpr int RST = 3, LST = 8;          // K and Q ring slots, lse slots
@@ -60,59 +61,15 @@ struct WtArgs {
   int grp, npt, rpt, nqt;   // heads per kv head, positions and rows of a query tile, tiles of a request
 };
 
-// The key tiles of CTA c: an even run of all (request, kv head, key tile) that hold a key, requests in order.
-struct Share {
-  const WtArgs& p;
-  int b, g, kt, tiles, T;   // request, kv head, next tile, the request's tiles and length
-  long long left;
-  // unit: nk key tiles of one request and kv head, the first at key k0
-  int nk, k0;
-  __device__ void load(int b_) {
-    b = b_;
-    T = b < p.a.batch ? clamp_ctx(p.a.ctx_len[b], p.a.t_cap) : 0;
-    tiles = (T + KT - 1) / KT;
-  }
-  __device__ Share(const WtArgs& p_) : p(p_) {   // by a whole warp
-    const int lane = threadIdx.x & 31;
-    auto count = [&](int i) { return i < p.a.batch ? (long long)p.a.nkv * ((clamp_ctx(p.a.ctx_len[i], p.a.t_cap) + KT - 1) / KT) : 0ll; };
-    auto sum = [&](long long v) {
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      return v;
-    };
-    long long total = 0;
-    for (int i0 = 0; i0 < p.a.batch; i0 += 32) total += sum(count(i0 + lane));
-    long long lo = blockIdx.x * total / gridDim.x;
-    left = (blockIdx.x + 1) * total / gridDim.x - lo;
-    int i0 = 0;
-    for (; left > 0; i0 += 32) {   // the 32 requests, then the request, that hold tile lo
-      const long long c = sum(count(i0 + lane));
-      if (lo < c) break;
-      lo -= c;
-    }
-    load(i0);
-    while (left > 0 && lo >= (long long)p.a.nkv * tiles) {
-      lo -= (long long)p.a.nkv * tiles;
-      load(b + 1);
-    }
-    g = left > 0 ? (int)(lo / tiles) : 0;
-    kt = left > 0 ? (int)(lo - (long long)g * tiles) : 0;
-    nk = 0;
-  }
-  __device__ bool next() {
-    kt += nk;
-    left -= nk;
-    nk = 0;
-    if (left <= 0) return false;
-    while (kt >= tiles) {
-      kt = 0;
-      if (++g == p.a.nkv || tiles == 0) {
-        g = 0;
-        load(b + 1);
-      }
-    }
-    k0 = kt * KT;
-    nk = (int)min(min(2ll, left), (long long)(tiles - kt));
-    return true;
+struct CtxLen {
+  const int32_t* ctx_len;
+  int t_cap;
+  __host__ __device__ int operator()(int b) const {
+#ifdef __CUDA_ARCH__
+    return clamp_ctx(ctx_len[b], t_cap);
+#else
+    return 0;   // device lengths
+#endif
   }
 };
 
@@ -183,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const __grid_co
   pdl_wait();
   pdl_trigger();
 
-  Share sh(p);
+  Share<CtxLen> sh(CtxLen{p.a.ctx_len, p.a.t_cap}, p.a.batch, p.a.nkv, blockIdx.x, gridDim.x);
   const int nrows = p.a.L * p.grp;
 
   if (warp == 0 || warp == 3) {

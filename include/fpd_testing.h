@@ -82,6 +82,11 @@ int fpd_test_attn_plan(int impl, int batch, int L, int nq, int nkv, int t_cap, i
  * how many of its CTAs have no run of the prefix, how many own units each of those takes before all CTAs take turns}. */
 int fpd_test_shared_plan(int batch, int L, int block_keys, int nq, int nkv, int head_dim, int prefix_cap, int t_cap,
                          int num_sms, int32_t* out);
+/* Host only: the units of CTA `cta` of `ctas` of the collected weights' tcgen05 kernel, {request, kv head, first key, key
+ * tiles (1 or 2)} each.  counted, walked: the lengths as the kernel first counts them and as it reads them later (the same,
+ * unless another stream writes them meanwhile). */
+int fpd_test_weight_shares(int batch, int nkv, const int32_t* counted, const int32_t* walked, int cta, int ctas, int max_units,
+                           int32_t* units, int32_t* n_units);
 
 #ifdef __cplusplus
 }

@@ -291,3 +291,42 @@ def test_shared_plan_rules(fpd):
     assert plan(fpd, 200, 1, 32, 8, 128, 2500, 1024)["own_tc"]
     p = plan(fpd, 2, 2, 130, 1, 128, 20000, 0)
     assert not p["pre_tc"] and not p["own_tc"]                                     # 130 heads do not fit 128 rows
+
+
+# ---- how the collected weights' key tiles are dealt -----------------------------------------------------------------
+
+def shares(fpd, lens, nkv, ctas, walked=None, max_units=100000):
+    lib, I = fpd.lib(), ctypes.c_int
+    P = ctypes.POINTER(ctypes.c_int32)
+    lib.fpd_test_weight_shares.argtypes = [I, I, P, P, I, I, I, P, P]
+    a, b = ((ctypes.c_int32 * len(lens))(*v) for v in (lens, walked or lens))
+    out, n = (ctypes.c_int32 * (4 * max_units))(), ctypes.c_int32()
+    got = []
+    for c in range(ctas):
+        assert lib.fpd_test_weight_shares(len(lens), nkv, a, b, c, ctas, max_units, out, ctypes.byref(n)) == 0
+        got.append([tuple(out[4 * i:4 * i + 4]) for i in range(n.value)])
+    return got
+
+
+@pytest.mark.parametrize("lens", [[1], [0, 0], [128, 129, 0, 1], [2000, 1, 5, 64, 1999, 0, 3, 128], [0] * 40 + [300] + [0] * 50,
+                                  [(97 * i) % 700 for i in range(75)]])
+def test_weight_shares_cover_every_key_tile_once(fpd, lens):
+    for nkv in (1, 8):
+        for ctas in (1, 2, 7, 152):
+            got = shares(fpd, lens, nkv, ctas)
+            tiles = [(b, g, t) for b, n in enumerate(lens) for g in range(nkv) for t in range(-(-n // 128))]
+            seen = [(b, g, k // 128 + i) for c in got for b, g, k, nk in c for i in range(nk)]
+            assert seen == tiles
+            per = [sum(u[3] for u in c) for c in got]
+            assert max(per) - min(per) <= 1
+
+
+def test_weight_shares_end_under_lengths_that_change(fpd):
+    """Shorter or longer lengths after the count: a walk that ends, within the requests and kv heads."""
+    rng = np.random.default_rng(3)
+    for k in range(60):
+        n = int(rng.integers(1, 70))
+        lens = rng.integers(0, 2000, n).tolist()
+        walked = [0] * n if k % 3 == 0 else rng.integers(0, 2000, n).tolist()
+        for c in shares(fpd, lens, 2, 9, walked):
+            assert all(0 <= b < n and 0 <= g < 2 and k0 < walked[b] and nk in (1, 2) for b, g, k0, nk in c)
