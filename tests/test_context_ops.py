@@ -142,6 +142,19 @@ def test_shared_draft_refuses_more_positions_than_the_drafter_has(fpd):
         fpd.SharedDraft(dr, 8, 16, 500, 12)
 
 
+def test_compiling_the_library_compiles_the_python_calls(fpd, monkeypatch, tmp_path):
+    """What this file's fixture builds is enough for the compiled calls, and they are made again when their source is newer."""
+    import os
+
+    import __graft_entry__ as g
+    made = tmp_path / "_calls.so"
+    made.write_bytes(b"")
+    os.utime(made, (1, 1))
+    monkeypatch.setattr(g, "PKG", str(tmp_path))
+    g._compile_all()
+    assert made.stat().st_size > 0
+
+
 def test_selection_rule_of_the_reference():
     nan, inf = float("nan"), float("inf")
     assert ref.kept_positions([5, 1, 3, 2], 4, 4, 0) == [0, 1, 2, 3]
