@@ -11,7 +11,7 @@ import os
 
 import torch
 
-from . import SharedContext, _check, _ptr, _stream, lib
+from . import SharedContext, _check, _stream, lib
 
 _module = None
 
@@ -78,11 +78,22 @@ def fpd_evict_context(n_layers, batch, n_kv_heads, head_dim, budget, recent, kv_
                                      workspace_bytes, *_here(stream)), "fpd_evict_context")
 
 
+def _on_device(t, dtype, n, what):
+    """_arg on the current device."""
+    if t is None or isinstance(t, int):
+        return t
+    return _arg(t, dtype, n, what, torch._C._cuda_getDevice() if getattr(t, "is_cuda", False) else 0)
+
+
 def fpd_prepare_context_at(model, batch, total_rows, row_off, row_cnt, pos_start, pos_offset, feats, kv_store, t_cap,
                            workspace, workspace_bytes, stream=None):
-    arr = (ctypes.c_void_p * len(feats))(*[_ptr(f) for f in feats])
-    _check(lib().fpd_prepare_context_at(model, batch, total_rows, _ptr(row_off), _ptr(row_cnt), _ptr(pos_start),
-                                        _ptr(pos_offset), arr, _ptr(kv_store), t_cap, _ptr(workspace), workspace_bytes,
+    bf, i32 = torch.bfloat16, torch.int32
+    arr = (ctypes.c_void_p * len(feats))(*[_on_device(f, bf, total_rows, "feats") for f in feats])
+    _check(lib().fpd_prepare_context_at(model, batch, total_rows, _on_device(row_off, i32, batch + 1, "row_off"),
+                                        _on_device(row_cnt, i32, batch, "row_cnt"), _on_device(pos_start, i32, batch, "pos_start"),
+                                        _on_device(pos_offset, i32, batch, "pos_offset"), arr,
+                                        _on_device(kv_store, bf, batch * t_cap, "kv_store"), t_cap,
+                                        _on_device(workspace, torch.uint8, workspace_bytes, "workspace"), workspace_bytes,
                                         _stream(stream)), "fpd_prepare_context_at")
 
 
@@ -93,14 +104,24 @@ def fpd_shared_workspace_bytes(model, batch, max_block_len, prefix_cap, t_cap) -
 def shared_context(prefix_store=None, prefix_cap=0, prefix_len=None, kv_store=None, t_cap=0, ctx_len=None, pos_offset=None,
                    weights=None, prefix_weights=None, accumulate=False) -> SharedContext:
     """Build an fpd_shared_context; it keeps its tensors alive."""
-    c = SharedContext(_ptr(prefix_store), prefix_cap, _ptr(prefix_len), _ptr(kv_store), t_cap, _ptr(ctx_len),
-                      _ptr(pos_offset), _ptr(weights), _ptr(prefix_weights), int(bool(accumulate)))
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    c = SharedContext(_on_device(prefix_store, bf, prefix_cap, "prefix_store"), prefix_cap, _on_device(prefix_len, i32, 1, "prefix_len"),
+                      _on_device(kv_store, bf, t_cap, "kv_store"), t_cap, _on_device(ctx_len, i32, 1, "ctx_len"),
+                      _on_device(pos_offset, i32, 1, "pos_offset"), _on_device(weights, f32, t_cap, "weights"),
+                      _on_device(prefix_weights, f32, prefix_cap, "prefix_weights"), int(bool(accumulate)))
     c._keep = (prefix_store, prefix_len, kv_store, ctx_len, pos_offset, weights, prefix_weights)
+    c._per_request = ((ctx_len, "ctx_len"), (pos_offset, "pos_offset"))
     return c
 
 
 def fpd_draft_block_shared(model, batch, block_len, ctx: SharedContext, anchor, mask_id, hidden_out, layer_hidden,
                            workspace, workspace_bytes, stream=None):
-    _check(lib().fpd_draft_block_shared(model, batch, block_len, ctypes.byref(ctx), _ptr(anchor), int(mask_id),
-                                        _ptr(hidden_out), _ptr(layer_hidden), _ptr(workspace), workspace_bytes,
+    for t, what in getattr(ctx, "_per_request", ()):   # its builder did not know the batch
+        if isinstance(t, torch.Tensor) and t.numel() < batch:
+            raise ValueError(f"{what} holds {t.numel()} elements, the call needs {batch}")
+    rows = batch * block_len
+    _check(lib().fpd_draft_block_shared(model, batch, block_len, ctypes.byref(ctx), _on_device(anchor, torch.int32, batch, "anchor"),
+                                        int(mask_id), _on_device(hidden_out, torch.bfloat16, rows, "hidden_out"),
+                                        _on_device(layer_hidden, torch.bfloat16, rows, "layer_hidden"),
+                                        _on_device(workspace, torch.uint8, workspace_bytes, "workspace"), workspace_bytes,
                                         _stream(stream)), "fpd_draft_block_shared")

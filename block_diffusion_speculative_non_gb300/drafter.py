@@ -289,9 +289,13 @@ class SharedDraft:
 
     def draft_block(self, anchor, mask_id, hidden_out=None, layer_hidden=None):
         """One block pass of every request over [prefix ; own context ; block] -> hidden_out [batch * block_len, d]."""
+        n = self.batch * self.block_len * self.dr.shape.d_model
         if hidden_out is None:
             hidden_out = torch.empty(self.batch * self.block_len, self.dr.shape.d_model, dtype=torch.bfloat16,
                                      device=self.dr.device)
+        for t, need, what in ((hidden_out, n, "hidden_out"), (layer_hidden, n * self.dr.shape.n_layers, "layer_hidden")):
+            if isinstance(t, torch.Tensor) and t.numel() < need:
+                raise ValueError(f"{what} holds {t.numel()} elements, the call needs {need}")
         fpd_draft_block_shared(self.dr.handle, self.batch, self.block_len, self.context, anchor, mask_id, hidden_out,
                                layer_hidden, self.workspace, self.workspace.numel())
         return hidden_out

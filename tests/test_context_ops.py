@@ -130,6 +130,26 @@ def test_compiled_calls_refuse_what_is_no_argument(fpd):
     assert calls.evict_context(0, 1, 2, 64, 8, 0, 64, 8, 64, 64, 64, 8, 64, 64, None, None, 64, 8, None, 0) != 0
 
 
+def test_model_calls_check_tensors(fpd):
+    """A tensor on the host, of another type or too small is refused before the library sees its address."""
+    import torch
+    i32, bf = torch.zeros(4, dtype=torch.int32), torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="anchor is on cpu"):
+        fpd.fpd_draft_block_shared(64, 2, 8, fpd.shared_context(), i32, 0, 64, None, 64, 64)
+    with pytest.raises(ValueError, match="anchor must be torch.int32, got torch.int64"):
+        fpd.fpd_draft_block_shared(64, 2, 8, fpd.shared_context(), i32.long(), 0, 64, None, 64, 64)
+    with pytest.raises(ValueError, match="hidden_out holds 4 elements, the call needs 16"):
+        fpd.fpd_draft_block_shared(64, 2, 8, fpd.shared_context(), 64, 0, bf[:4], None, 64, 64)
+    with pytest.raises(ValueError, match="ctx_len is on cpu"):
+        fpd.shared_context(kv_store=64, t_cap=8, ctx_len=i32)
+    with pytest.raises(ValueError, match="weights must be torch.float32"):
+        fpd.shared_context(weights=bf)
+    with pytest.raises(ValueError, match="row_off holds 4 elements, the call needs 5"):
+        fpd.fpd_prepare_context_at(64, 4, 4, i32, None, None, 64, [64], 64, 8, 64, 64)
+    with pytest.raises(ValueError, match="pos_offset must be torch.int32"):
+        fpd.fpd_prepare_context_at(64, 4, 4, 64, None, None, i32.long(), [64], 64, 8, 64, 64)
+
+
 def test_shared_draft_refuses_more_positions_than_the_drafter_has(fpd):
     """A Drafter that was not told max_pos has its own t_cap + max_block_len rotary positions: no room behind a long prefix."""
     import types

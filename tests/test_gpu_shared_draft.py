@@ -355,3 +355,18 @@ def test_appends_refuse_what_they_cannot_hold(pkg):
     with pytest.raises(pkg.FpdError):
         sd.prepare_prefix(f)                             # 20 rows, 16 slots
     assert sd.ctx_len.tolist() == [0, 0] and sd.prefix_len.item() == 0 and sd.pos_offset.tolist() == [0, 0]
+
+
+def test_draft_calls_refuse_tensors_of_another_type_or_size(pkg):
+    w, dr, sd = build(pkg, TINY, 2, 8, 16, 16, seed=18)
+    for bad in (torch.tensor([1, 2], device=DEV), torch.tensor([1, 2], dtype=torch.int32), dev_i32([1])):
+        with pytest.raises(ValueError, match="anchor"):
+            sd.draft_block(bad, 5)
+    h = torch.empty(16, TINY.d_model, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="hidden_out"):
+        sd.draft_block(dev_i32([1, 2]), 5, hidden_out=h[1:])
+    with pytest.raises(ValueError, match="layer_hidden"):
+        sd.draft_block(dev_i32([1, 2]), 5, hidden_out=h, layer_hidden=h)
+    one = pkg.shared_context(sd.prefix_kv, 16, sd.prefix_len, sd.kv, 16, sd.ctx_len[:1], sd.pos_offset)
+    with pytest.raises(ValueError, match="ctx_len holds 1 elements"):
+        pkg.fpd_draft_block_shared(dr.handle, 2, 8, one, dev_i32([1, 2]), 5, h, None, sd.workspace, sd.workspace.numel())
