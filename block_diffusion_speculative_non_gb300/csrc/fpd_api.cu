@@ -628,6 +628,9 @@ static SharedWs carve_shared(const Model& m, Carver& c, int B, int L, int p_cap,
 
 size_t fpd_shared_workspace_bytes(const fpd_model* m, int batch, int max_block_len, int prefix_cap, int t_cap) {
   if (!m || batch < 1 || max_block_len < 2 || prefix_cap < 0 || t_cap < 0) return 0;
+  if (prefix_cap > kMaxStoreCap || t_cap > kMaxStoreCap ||
+      (long long)batch * max_block_len > kMaxAttnRows / m->d.n_q_heads)
+    return 0;
   size_t best = 0;   // calls may use any smaller batch and block length: the maximum over all of them
   for (int b = 1; b <= batch; b++)
     for (int l = 2; l <= max_block_len; l++) {

@@ -431,6 +431,7 @@ typedef struct fpd_shared_context {
 fpd_status fpd_draft_block_shared(fpd_model* model, int batch, int block_len, const fpd_shared_context* ctx,
                                   const int32_t* anchor, int32_t mask_id, void* hidden_out, void* layer_hidden,
                                   void* workspace, size_t workspace_bytes, void* stream);
+/* 0 for sizes that the call refuses. */
 size_t fpd_shared_workspace_bytes(const fpd_model* model, int batch, int max_block_len, int prefix_cap, int t_cap);
 
 /* ---- diagnostics ---------------------------------------------------------------------------------------- */

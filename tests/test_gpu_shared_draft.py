@@ -370,3 +370,12 @@ def test_draft_calls_refuse_tensors_of_another_type_or_size(pkg):
     one = pkg.shared_context(sd.prefix_kv, 16, sd.prefix_len, sd.kv, 16, sd.ctx_len[:1], sd.pos_offset)
     with pytest.raises(ValueError, match="ctx_len holds 1 elements"):
         pkg.fpd_draft_block_shared(dr.handle, 2, 8, one, dev_i32([1, 2]), 5, h, None, sd.workspace, sd.workspace.numel())
+
+
+def test_workspace_of_sizes_that_the_block_pass_refuses_is_zero(pkg):
+    w, dr, sd = build(pkg, TINY, 2, 8, 16, 16, seed=19)
+    size = lambda *a: pkg.fpd_shared_workspace_bytes(dr.handle, *a)
+    big = (1 << 26) // TINY.n_q_heads // 8
+    assert size(2, 8, 16, 16) > 0 and size(1, 2, 1 << 30, 1 << 30) > 0
+    for bad in ((big + 1, 8, 16, 16), (1 << 30, 8, 16, 16), (9, 1 << 20, 16, 16), (2, 8, (1 << 30) + 1, 16), (2, 8, 16, (1 << 30) + 1), (2, 1, 16, 16)):
+        assert size(*bad) == 0, bad
