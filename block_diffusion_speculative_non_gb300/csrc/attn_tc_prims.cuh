@@ -113,8 +113,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok || tc::mbar_wait(bar, parity);
 }
-// The issuing warp runs converged, so that descriptors stay in uniform registers, and one elected lane issues: the same
-// products from inside a single-lane branch took 96 to 117 cycles each instead of 64, most of it moves to uniform registers.
+// The issuing warp runs converged and one elected lane issues: the same products from inside a single-lane branch took 96 to
+// 117 cycles each instead of 64.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));

@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(NWARP * 32) shared_mma_kernel(const __grid_con
 // The softmax of one (row, head) from its partials: M = max m_s over the partials that hold a key (l_s != 0; a NaN sum
 // counts, so that it reaches the output), den = sum l_s 2^(m_s - M), out = sum o_s 2^(m_s - M) / den,
 // lse = (M + log2 den) ln 2.  W warps share an output and take every W-th partial, eight at a time, so that the reads of
-// many partials do not queue behind one another; the warps' sums are added in warp order: bit-reproducible.
+// many partials do not queue behind one another; the warps' sums are added in warp order, so repeats
+// of a call are bit-identical (other sizes, capacities or SM counts may cut the keys, and with them the sums, elsewhere).
 template <int H, int W>
 __global__ void __launch_bounds__(256) shared_merge_kernel(bf16* __restrict__ out, float* __restrict__ lse,
                                                            const float* __restrict__ o_part, const float2* __restrict__ ml,

@@ -237,7 +237,7 @@ struct Walk {
 };
 
 // (a, b) >= 0 -> two packed bf16 pairs, a = hi_a + lo_a to 2^-16: hi keeps the upper half of the word (no rounding, so the
-// rest is exact in fp32), lo is the rest rounded.  Three instructions fewer per pair than rounding hi to nearest.
+// rest is exact in fp32), lo is the rest rounded.  Fewer steps per pair than rounding hi to nearest.
 __device__ __forceinline__ void split_trunc(float a, float b, uint32_t& hi, uint32_t& lo) {
   const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
   hi = __byte_perm(ua, ub, 0x7632);

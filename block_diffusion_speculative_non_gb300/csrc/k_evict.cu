@@ -65,7 +65,7 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* warp_sum, u
 }
 
 // 32 registers a thread, so that two CTAs share an SM: this kernel is a chain of short steps between barriers.  Loops are
-// left rolled: unrolled, the one pass that a small context makes through the code was mostly instruction fetch.
+// left rolled: a small context makes one short pass through the code, and unrolled loops made that pass slower.
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ Evict e) {
   pdl_wait();
   pdl_trigger();

@@ -379,3 +379,39 @@ def test_workspace_of_sizes_that_the_block_pass_refuses_is_zero(pkg):
     assert size(2, 8, 16, 16) > 0 and size(1, 2, 1 << 30, 1 << 30) > 0
     for bad in ((big + 1, 8, 16, 16), (1 << 30, 8, 16, 16), (9, 1 << 20, 16, 16), (2, 8, (1 << 30) + 1, 16), (2, 8, 16, (1 << 30) + 1), (2, 1, 16, 16)):
         assert size(*bad) == 0, bad
+
+
+def test_two_objects_on_two_streams(pkg):
+    """Objects share the drafter's weights alone: passes and evictions of both at once give what each gives by itself."""
+    w, dr, a = build(pkg, TINY, 3, 16, 64, 48, seed=20)
+    b = dr.shared(2, 8, 40, 48, collect=True)
+    anchor = dev_i32([4, 9, 2])
+
+    def steps(sd, n):
+        out = []
+        for _ in range(3):
+            out.append(sd.draft_block(anchor[:n], 5))
+            sd.evict(16, 4)
+            sd.evict_prefix(20, 0)
+        return out + [sd.kv.clone(), sd.weights.clone(), sd.prefix_weights.clone()]
+
+    def reset(sd, P, lens, seed):
+        for t in (sd.kv, sd.prefix_kv, sd.weights, sd.prefix_weights, sd.ctx_len, sd.prefix_len, sd.pos_offset, sd.prefix_offset):
+            t.zero_()
+        fill(sd, TINY, P, lens, seed)
+
+    sets = ((a, 3, 40, [50, 0, 33], 60), (b, 2, 45, [7, 40], 70))
+    want = []
+    for sd, n, P, lens, seed in sets:
+        reset(sd, P, lens, seed)
+        want.append(steps(sd, n))
+    for sd, n, P, lens, seed in sets:
+        reset(sd, P, lens, seed)
+    torch.cuda.synchronize()
+    got = []
+    for sd, n, *_ in sets:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got.append(steps(sd, n))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for g, v in zip(got, want) for x, y in zip(g, v)) and pkg.fpd_device_status() == 0
