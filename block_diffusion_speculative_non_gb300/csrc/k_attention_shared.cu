@@ -81,7 +81,7 @@ __device__ __forceinline__ Unit decode_unit(const SharedAttn& a, const SharedPla
 
 // One 64-row tile over one split on mma.sync (the tile math of attn_body.cuh).  Two CTAs of 80 KB per SM, two K/V buffers.
 // Bound by the legacy matrix path: 64 blocks of 16 positions behind 16384 keys took 1240 us here, 0.22 PFLOP/s of the
-// formula, and take 303 us on tcgen05; it stays for what is too small to notice.
+// formula, and take 310 us on tcgen05; it stays for what is too small to notice.
 template <int H>
 __global__ void __launch_bounds__(NWARP * 32) shared_mma_kernel(const __grid_constant__ SharedAttn a, const __grid_constant__ SharedPlan pl,
                                                                 int pre_units) {

@@ -22,7 +22,7 @@
 // by what a CTA has of them.
 //
 // What bounds it: with many rows the tensor core, 48 products of 64 cycles per pair of tiles and key tile, 72 % of the
-// cycles busy at 64 blocks of 16 positions behind 16384 keys (244 us, 1.13 PFLOP/s of the formula's 4 h, 1.69 of products;
+// cycles busy at 64 blocks of 16 positions behind 16384 keys (237 us, 1.16 PFLOP/s of the formula's 4 h, 1.74 of products;
 // the clock falls to 1.6-1.9 GHz under the power limit); with few rows the read of the keys, 6.7 TB/s while it lasts at 16
 // tokens behind 65536 positions (59 us in all, 42 the floor: the start and the merge do not overlap it).  An own unit costs
 // about 5 us besides 1.1 us per tile: its first S waits for its Q and K, and its partial goes out before the next one's product.

@@ -8,7 +8,7 @@
 //
 // Bounds: 2 h flops and one 2^x per row and key, 2 h bytes per key.  This small form is latency (16 rows over 128 keys:
 // 2.6 us); with many rows it is held back by the legacy matrix path and by reading the queries once per 64 keys (4096 rows
-// over 16384 keys 855 us against 125 on tcgen05).
+// over 16384 keys 855 us against 129 on tcgen05).
 #include <algorithm>
 
 #include "attn_body.cuh"

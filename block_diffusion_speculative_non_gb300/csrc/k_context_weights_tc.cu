@@ -15,7 +15,7 @@
 //          which rows have no key: what such a row holds must not count, and NaN would pass through the -inf;
 //   4..19  sums: warp = [32 of the tile's columns][32 of the keys].  The four parts of a key's sum are added in a fixed order.
 //
-// Measured: 4096 rows per kv head over 16384 keys, 8 kv heads: 125 us, 1.10 PFLOP/s (the floor is 72).  The sums bound it
+// Measured: 4096 rows per kv head over 16384 keys, 8 kv heads: 129 us, 1.07 PFLOP/s (the floor is 72).  The sums bound it
 // (issue slots 57 % busy, special-function unit 54 %); the products alone take 93.
 #include <cstring>
 

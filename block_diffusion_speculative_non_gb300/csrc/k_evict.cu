@@ -10,8 +10,8 @@
 // counts, fixed order).
 //
 // Bound by HBM: every kept row once in and once out, every weight once in.  8 ragged contexts of up to 16384 positions in
-// five layers to 4096: 204 us where 182 is the floor, the copy at 5.9 TB/s and 20 to 30 us of selection before it (issue
-// slots: about ten instructions per weight and pass, five passes); 2048 positions to 1024: 18 us, half of it the selection's
+// five layers to 4096: 208 us where 182 is the floor, the copy at 5.9 TB/s and 20 to 30 us of selection before it (issue
+// slots: about ten instructions per weight and pass, five passes); 2048 positions to 1024: 19 us, half of it the selection's
 // chain of barriers.
 #include "fpd_context.cuh"
 
