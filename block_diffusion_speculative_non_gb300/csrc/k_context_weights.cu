@@ -10,6 +10,7 @@
 // 2.6 us); with many rows it is held back by the legacy matrix path and by reading the queries once per 64 keys (4096 rows
 // over 16384 keys 855 us against 129 on tcgen05).
 #include <algorithm>
+#include <cfloat>
 
 #include "attn_body.cuh"
 #include "fpd_context.cuh"
@@ -55,7 +56,13 @@ __global__ void __launch_bounds__(NWARP * 32) weights_mma_kernel(const __grid_co
     }
     if (tid < QT) {
       const int qi = r0 + tid;
-      sm.l2[buf][tid] = qi < nrows ? a.lse[((size_t)b * a.L + qi / grp) * a.nq + g * grp + qi % grp] * log2e : -INFINITY;
+      float v = -INFINITY;
+      if (qi < nrows) {
+        const float lse = a.lse[((size_t)b * a.L + qi / grp) * a.nq + g * grp + qi % grp];
+        v = lse * log2e;
+        if (v == -INFINITY && lse != v) v = -FLT_MAX;   // a finite lse that overflows here is a row that has keys
+      }
+      sm.l2[buf][tid] = v;
     }
     cp_async_commit();
   };

@@ -462,6 +462,26 @@ def test_rows_without_a_key_give_nothing_whatever_they_hold(pkg, name):
     assert weights_close(w[1], ref.context_weights(p.q, p.lse, p.store[p.layer], p.lens, B, L, nkv))
 
 
+@pytest.mark.parametrize("name", ["small", "group_5", "many_rows", "group_3_h64_tc"])
+def test_only_minus_infinity_means_no_key(pkg, name):
+    """The lowest finite lse is a number: exp(s - lse) overflows to inf.  An lse of inf gives 0, NaN gives NaN."""
+    B, _, _, nkv, _ = WEIGHTS[name][:5]
+    for value, want in ((torch.finfo(torch.float32).min, math.inf), (math.inf, None), (math.nan, math.nan)):
+        q = weight_problem(name, seed=19)
+        q.lse[0, 0] = value                        # kv head 0 of request 0
+        w, clean = torch.zeros(2, B, nkv, q.t_cap, device=DEV), torch.zeros(2, B, nkv, q.t_cap, device=DEV)
+        run_weights(pkg, q, w)
+        q.lse[0, 0] = -math.inf                    # the same without the row
+        run_weights(pkg, q, clean)
+        got, rest = w[1, 0, 0, :q.lens[0]], clean[1, 0, 0, :q.lens[0]]
+        if want is None:
+            assert torch.equal(got, rest)
+        else:
+            assert torch.equal(got, torch.full_like(got, want)) or (math.isnan(want) and got.isnan().all())
+        w[1, 0, 0], clean[1, 0, 0] = 0, 0
+        assert torch.equal(w, clean)
+
+
 def test_rows_hand_out_one_in_all(pkg):
     """Without block keys, the weights of a request's positions and its share of the prefix's add up to its rows."""
     p = Problem(3, 16, 32, 8, 128, 500, 512, [100, 0, 33], 128, False, seed=21)
