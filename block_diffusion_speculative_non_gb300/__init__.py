@@ -24,6 +24,8 @@ STATUS = {0: "FPD_OK", 1: "FPD_ERR_INVALID_ARG", 2: "FPD_ERR_SHAPE", 3: "FPD_ERR
 FPD_VERIFY_TEXT, FPD_VERIFY_SCHEMA = 0, 1
 FPD_RULE_NONE, FPD_RULE_MEMBER, FPD_RULE_DIGIT, FPD_RULE_DIGIT_LAST, FPD_RULE_CONFIDENT = 0, 1, 2, 3, 4
 
+FPD_PAGE_BF16, FPD_PAGE_INT4 = 0, 1
+
 
 class GridFormat(ctypes.Structure):
     _fields_ = [("digit_id", ctypes.c_int32 * 10), ("plus_id", ctypes.c_int32), ("minus_id", ctypes.c_int32),
@@ -64,6 +66,12 @@ class SharedContext(ctypes.Structure):
                 ("accumulate", ctypes.c_int32)]
 
 
+class PagedStore(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("table", ctypes.c_void_p), ("format", ctypes.c_int32), ("n_layers", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("table_width", ctypes.c_int32)]
+
+
 _lib = None
 _EXPORTS = ["fpd_model_create", "fpd_model_destroy", "fpd_kv_store_bytes", "fpd_workspace_bytes",
             "fpd_prepare_context", "fpd_prepare_context_rows", "fpd_draft_block", "fpd_constrain_argmax",
@@ -71,7 +79,8 @@ _EXPORTS = ["fpd_model_create", "fpd_model_destroy", "fpd_kv_store_bytes", "fpd_
             "fpd_model_enable_fp8", "fpd_model_fp8_enabled", "fpd_quantize_fp8", "fpd_last_error",
             "fpd_kernel_launches", "fpd_device_status", "fpd_shared_attention", "fpd_shared_attention_workspace_bytes",
             "fpd_context_weights", "fpd_evict_context", "fpd_evict_workspace_bytes", "fpd_prepare_context_at",
-            "fpd_draft_block_shared", "fpd_shared_workspace_bytes"]
+            "fpd_draft_block_shared", "fpd_shared_workspace_bytes", "fpd_page_bytes", "fpd_paged_append", "fpd_paged_read",
+            "fpd_paged_attention", "fpd_paged_attention_workspace_bytes", "fpd_verify_sampled"]
 
 
 def lib():
@@ -122,13 +131,21 @@ def lib():
         l.fpd_prepare_context_at.argtypes = [vp, ci, ci, vp, vp, vp, vp, ctypes.POINTER(vp), vp, ci, vp, sz, vp]
         l.fpd_draft_block_shared.argtypes = [vp, ci, ci, ctypes.POINTER(SharedContext), vp, i32, vp, vp, vp, sz, vp]
         l.fpd_shared_workspace_bytes.argtypes = [vp] + [ci] * 4
-        for f in ("fpd_shared_attention_workspace_bytes", "fpd_evict_workspace_bytes", "fpd_shared_workspace_bytes"):
+        ps = ctypes.POINTER(PagedStore)
+        l.fpd_page_bytes.argtypes = [ci] * 4
+        l.fpd_paged_append.argtypes = [ci, ci, ps, ci, vp, ci, vp, ci, vp, vp, vp, vp, vp, ci, vp]
+        l.fpd_paged_read.argtypes = [ci, ci, ps, ci, vp, vp, vp, vp, vp, vp]
+        l.fpd_paged_attention.argtypes = [ci, ci, ci, ps, ci, vp, vp, vp, vp, ci, ci, ci, vp, vp, vp, sz, vp]
+        l.fpd_paged_attention_workspace_bytes.argtypes = [ci, ci, ci, ps]
+        l.fpd_verify_sampled.argtypes = [ci, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp]
+        for f in ("fpd_shared_attention_workspace_bytes", "fpd_evict_workspace_bytes", "fpd_shared_workspace_bytes",
+                  "fpd_page_bytes", "fpd_paged_attention_workspace_bytes"):
             getattr(l, f).restype = sz
         for f in ("fpd_model_create", "fpd_model_enable_fp8", "fpd_quantize_fp8", "fpd_prepare_context", "fpd_prepare_context_rows", "fpd_draft_block",
                   "fpd_constrain_argmax", "fpd_constrain_argmax_noalloc", "fpd_verify", "fpd_sd_advance",
                   "fpd_grid_to_text", "fpd_verify_prefix", "fpd_shared_attention", "fpd_context_weights",
-                  "fpd_evict_context", "fpd_prepare_context_at", "fpd_draft_block_shared",
-                  "fpd_device_status"):
+                  "fpd_evict_context", "fpd_prepare_context_at", "fpd_draft_block_shared", "fpd_paged_append", "fpd_paged_read",
+                  "fpd_paged_attention", "fpd_verify_sampled", "fpd_device_status"):
             getattr(l, f).restype = ctypes.c_int
         _lib = l
     return _lib
@@ -306,4 +323,6 @@ def fpd_device_status(stream=None) -> int:
 from .context import (_arg, fpd_context_weights, fpd_draft_block_shared, fpd_evict_context,  # noqa: E402
                       fpd_evict_workspace_bytes, fpd_prepare_context_at, fpd_shared_attention,
                       fpd_shared_attention_workspace_bytes, fpd_shared_workspace_bytes, shared_context)
+from .paged import (fpd_page_bytes, fpd_paged_append, fpd_paged_attention, fpd_paged_attention_workspace_bytes,  # noqa: E402
+                    fpd_paged_read, fpd_verify_sampled, paged_store, rope_table)
 from .drafter import Drafter, SharedDraft  # noqa: E402  (convenience wrapper over the calls above)

@@ -25,6 +25,7 @@ enum DeviceCheck : int32_t {
   kCheckBadContext = 5,      // a ctx_len outside [0, t_cap] (clamped)
   kCheckBadPosition = 6,     // a context row's position outside [0, t_cap) (row skipped)
   kCheckCtxOverflow = 7,     // an accepted append would pass t_cap (count capped)
+  kCheckBadPage = 8,         // a page id outside the pool
 };
 extern __device__ int32_t g_device_check;
 

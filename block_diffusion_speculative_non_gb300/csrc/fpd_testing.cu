@@ -2,6 +2,7 @@
 #include "../../include/fpd_testing.h"
 #include "fpd_context.cuh"
 #include "fpd_kernels.cuh"
+#include "paged_sched.cuh"
 #include "weights_share.cuh"
 
 using namespace fpd;
@@ -308,5 +309,49 @@ extern "C" int fpd_test_weight_shares(int batch, int nkv, const int32_t* counted
     for (int i = 0; i < 4; i++) units[4 * n + i] = u[i];
   }
   *n_units = n;
+  return FPD_OK;
+}
+
+extern "C" int fpd_test_paged_walk(int batch, int L, int block_keys, int group, int nkv, int rows, int window, int sinks, int causal,
+                                   int key_tile, const int32_t* counted, const int32_t* walked, int runs, int run, int max_parts,
+                                   int32_t* parts, int32_t* n_parts) {
+  if (batch < 1 || L < 1 || group < 1 || nkv < 1 || rows < 1 || key_tile < 1 || run < 0 || run >= runs || !counted || !walked || !parts || !n_parts)
+    return FPD_ERR_SHAPE;
+  struct Lens {
+    const int32_t* v;
+    int operator()(int b) const { return v[b]; }
+  };
+  const PagedShape s{L, block_keys, group, nkv, rows, ceil_div(L * group, rows), window, sinks, causal, key_tile};
+  long long sums[kSchedEntries + 1] = {0};
+  const int each = ceil_div(batch, kSchedEntries);
+  for (int e = 0; e < kSchedEntries; e++) {
+    sums[e + 1] = sums[e];
+    for (int b = e * each; b < std::min(batch, (e + 1) * each); b++) sums[e + 1] += nkv * request_tiles(s, counted[b]);
+  }
+  PagedWalk<Lens> walk(s, Lens{walked}, sums, batch, runs, run);
+  PagedUnit u;
+  int n = 0, t0, t1, last;
+  for (; walk.next(u, t0, t1, last); n++) {
+    if (n == max_parts) return FPD_ERR_CAPACITY;
+    const int32_t v[7] = {u.b, u.g, u.rt, t0, t1, u.len(), last};
+    for (int i = 0; i < 7; i++) parts[7 * n + i] = v[i];
+  }
+  *n_parts = n;
+  return FPD_OK;
+}
+
+extern "C" int fpd_test_paged_tiles(int L, int block_keys, int group, int rows, int window, int sinks, int causal, int key_tile,
+                                    int ctx_len, int row_tile, int max_tiles, int32_t* tiles, int32_t* n_tiles) {
+  if (L < 1 || group < 1 || rows < 1 || key_tile < 1 || row_tile < 0 || row_tile * rows >= L * group || !tiles || !n_tiles) return FPD_ERR_SHAPE;
+  const PagedShape s{L, block_keys, group, 1, rows, ceil_div(L * group, rows), window, sinks, causal, key_tile};
+  PagedUnit u;
+  unit_tiles(s, ctx_len, row_tile, u);
+  if (u.tiles() > max_tiles) return FPD_ERR_CAPACITY;
+  for (int i = 0; i < u.tiles(); i++) {
+    const PagedTile t = tile_at(u, key_tile, i);
+    const int32_t v[5] = {t.ctx, t.k0, t.valid, t.pos, tile_full(s, u, t)};
+    for (int j = 0; j < 5; j++) tiles[5 * i + j] = v[j];
+  }
+  *n_tiles = u.tiles();
   return FPD_OK;
 }

@@ -1,0 +1,190 @@
+// paged_sched.cuh — how the key tiles of a paged attention call are shared out (internal to libfpd).
+//
+// A unit is a row tile of one request and kv head: rows (position, head) rt R .. of the L positions' heads that share the kv
+// head.  It has the key tiles that hold a key some row of it sees: those of the first `sinks` positions, those from the first
+// row's window to the end, then the block's keys.  The lengths are known on the device alone, and requests differ in them, so
+// every CTA adds them up and takes an even run of all units' tiles, [c total / G, (c + 1) total / G): whatever the lengths, the
+// SMs finish together.  A unit inside one run is finished there; of a unit that runs share, each leaves a partial: the run
+// that starts it in slot 2 c + 1, the ones that go on with it in slot 2 c.  A unit without a key counts as one empty tile, so
+// that its rows are written too.
+#pragma once
+
+#include "fpd_paged.cuh"
+
+namespace fpd {
+
+constexpr int kSchedEntries = 128;   // running sums kept in shared memory, over ceil(batch / 128) requests each
+
+struct PagedUnit {
+  int b, g, rt;
+  int T, n, p0, p1;          // context length, keys, positions of the tile's first and last row
+  int ce, be;                // context slots and block keys before the end of what the rows see
+  int ns, cfirst, nm;        // tiles of the sinks; first tile behind them and their number
+  int bfirst, nb;            // first tile of the block and their number
+  __host__ __device__ int tiles() const { return ns + nm + nb; }
+  __host__ __device__ int len() const { return tiles() > 0 ? tiles() : 1; }
+};
+
+struct PagedTile {
+  bool ctx;
+  int k0, valid, pos;   // first slot or block key, keys, position of the first
+};
+
+// What decides a unit's tiles.
+struct PagedShape {
+  int L, lb, grp, nkv, rows, tiles, window, sinks, causal, kt;   // rows of a row tile, row tiles of a request and kv head
+};
+
+__host__ __device__ inline int imin(int a, int b) { return a < b ? a : b; }
+__host__ __device__ inline int imax(int a, int b) { return a > b ? a : b; }
+
+__host__ __device__ inline void unit_tiles(const PagedShape& s, int T, int rt, PagedUnit& u) {
+  u.rt = rt;
+  u.T = T;
+  u.n = T + s.lb;
+  const int last = imin(s.L * s.grp, (rt + 1) * s.rows) - 1;
+  u.p0 = u.n - s.L + rt * s.rows / s.grp;
+  u.p1 = u.n - s.L + last / s.grp;
+  const int end = s.causal ? imin(u.n, imax(0, u.p1 + 1)) : u.n;
+  const int start = s.window ? imin(end, imax(0, u.p0 - s.window + 1)) : 0;
+  const int s_end = imin(s.sinks, start);
+  u.ce = imin(end, T);
+  u.be = imax(0, end - T);
+  u.ns = (imin(s_end, u.ce) + s.kt - 1) / s.kt;
+  u.cfirst = imax(start / s.kt, u.ns);
+  u.nm = start < u.ce ? imax(0, (u.ce + s.kt - 1) / s.kt - u.cfirst) : 0;
+  u.bfirst = s_end > T ? 0 : imax(0, start - T) / s.kt;
+  u.nb = imax(0, (u.be + s.kt - 1) / s.kt - u.bfirst);
+}
+
+__host__ __device__ inline PagedTile tile_at(const PagedUnit& u, int kt, int i) {
+  PagedTile t;
+  t.ctx = i < u.ns + u.nm;
+  const int idx = i < u.ns ? i : t.ctx ? u.cfirst + i - u.ns : u.bfirst + i - u.ns - u.nm;
+  t.k0 = idx * kt;
+  t.valid = imin(kt, (t.ctx ? u.ce : u.be) - t.k0);
+  t.pos = t.ctx ? t.k0 : u.T + t.k0;
+  return t;
+}
+// Whether every row of the unit sees every key of the tile.
+__host__ __device__ inline bool tile_full(const PagedShape& s, const PagedUnit& u, const PagedTile& t) {
+  const int last = t.pos + s.kt - 1;
+  return t.valid == s.kt && (!s.window || last < s.sinks || u.p1 - t.pos < s.window) && (!s.causal || last <= u.p0);
+}
+
+// Tiles of a request in one kv head.
+__host__ __device__ inline long long request_tiles(const PagedShape& s, int T) {
+  PagedUnit u;
+  if (!s.window && !s.causal) {
+    unit_tiles(s, T, 0, u);
+    return (long long)s.tiles * u.len();
+  }
+  long long n = 0;
+  for (int rt = 0; rt < s.tiles; rt++) {
+    unit_tiles(s, T, rt, u);
+    n += u.len();
+  }
+  return n;
+}
+
+// One run of a CTA over the units.  Lens: the length of request b, clamped.
+template <class Lens>
+struct PagedWalk {
+  const PagedShape& s;
+  Lens lens;
+  int c, G, batch, b, g, rt, off;
+  long long x, x_end, total;
+
+  // `sums` holds running sums of the entries' tiles (kSchedEntries + 1 of them), complete when the walk is made
+  __host__ __device__ PagedWalk(const PagedShape& s_, Lens lens_, const long long* sums, int batch_, int runs, int c_)
+      : s(s_), lens(lens_), c(c_), batch(batch_) {
+    total = sums[kSchedEntries];
+    G = total < runs ? (int)total : runs;
+    x = c < G ? run_start(c) : total;
+    x_end = c < G ? run_start(c + 1) : total;
+    if (x >= x_end) return;
+    int lo = 0, hi = kSchedEntries;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] <= x) lo = mid; else hi = mid;
+    }
+    const int each = (batch + kSchedEntries - 1) / kSchedEntries;
+    long long rest = x - sums[lo], per;
+    for (b = lo * each;; b++) {
+      per = request_tiles(s, lens(b));
+      if (rest < per * s.nkv || b + 1 >= batch) break;
+      rest -= per * s.nkv;
+    }
+    // lengths that another stream changes meanwhile give a wrong result, never a unit that is not there
+    g = (int)imin((int)(rest / per), s.nkv - 1);
+    rest -= g * per;
+    PagedUnit u;
+    if (!s.window && !s.causal) {
+      unit_tiles(s, lens(b), 0, u);
+      rt = imin((int)(rest / u.len()), s.tiles - 1);
+      rest -= (long long)rt * u.len();
+    } else {
+      for (rt = 0; rt + 1 < s.tiles; rt++) {
+        unit_tiles(s, lens(b), rt, u);
+        if (rest < u.len()) break;
+        rest -= u.len();
+      }
+    }
+    off = (int)rest;
+  }
+  __host__ __device__ long long run_start(int i) const { return (long long)i * total / G; }
+  __host__ __device__ int run_of(long long t) const { return (int)(((t + 1) * G - 1) / total); }
+
+  // The next part [t0, t1) of a unit's tiles; last_run: the run that ends the unit.
+  __host__ __device__ bool next(PagedUnit& u, int& t0, int& t1, int& last_run) {
+    if (x >= x_end || b >= batch) return false;
+    unit_tiles(s, lens(b), rt, u);
+    u.b = b;
+    u.g = g;
+    const int len = u.len();
+    if (off >= len) off = len - 1;
+    t0 = off;
+    t1 = (int)(x_end - x < len - off ? off + (x_end - x) : len);
+    last_run = t1 == len ? c : imin(run_of(x + (len - off) - 1), G - 1);
+    x += t1 - t0;
+    off = 0;
+    if (++rt == s.tiles) {
+      rt = 0;
+      if (++g == s.nkv) {
+        g = 0;
+        b++;
+      }
+    }
+    return true;
+  }
+};
+
+#ifdef __CUDACC__
+struct DeviceLens {
+  const int32_t* ctx_len;
+  int cap;
+  __device__ int operator()(int b) const { return clamp_ctx(ctx_len[b], cap); }
+};
+// Running sums over the requests' tiles, by the first 128 threads of a CTA; the caller synchronises after it.
+__device__ __forceinline__ void sched_sums(const PagedShape& s, DeviceLens lens, int batch, long long* sums, int tid) {
+  const int each = (batch + kSchedEntries - 1) / kSchedEntries, lane = tid & 31;
+  long long v = 0;
+  if (tid < kSchedEntries)
+    for (int b = tid * each; b < min(batch, (tid + 1) * each); b++) v += s.nkv * request_tiles(s, lens(b));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  if (tid < kSchedEntries) sums[tid + 1] = v;   // sums within a warp
+  if (tid == 0) sums[0] = 0;
+}
+// After a barrier: adds the warps before; another barrier follows.
+__device__ __forceinline__ long long sched_before(const long long* sums, int tid) {
+  long long v = 0;
+  for (int w = 0; w < (tid >> 5); w++) v += sums[(w + 1) * 32];
+  return v;
+}
+#endif
+
+}  // namespace fpd

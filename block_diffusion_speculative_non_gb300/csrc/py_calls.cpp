@@ -1,4 +1,4 @@
-// py_calls.cpp — Python calls of the operators on a context store, as a module of CPython's own C interface.
+// py_calls.cpp — Python calls of the operators on a context store and on pages, as a module of CPython's own C interface.
 //
 // These operators take 3 to 10 us on the GPU for short contexts, and ctypes with the checks of ten tensors in Python took 6 to
 // 8 us of the host for each call, more than its launches (3 to 4 us).  Here the arguments go straight from the tensors to
@@ -21,6 +21,12 @@ struct Entries {
   decltype(&fpd_context_weights) context_weights;
   decltype(&fpd_evict_context) evict_context;
 } g_entries;
+struct PagedEntries {
+  decltype(&fpd_paged_append) append;
+  decltype(&fpd_paged_read) read;
+  decltype(&fpd_paged_attention) attention;
+  decltype(&fpd_verify_sampled) verify_sampled;
+} g_paged;
 
 int64_t product(std::initializer_list<int64_t> f) {   // as large as it gets where 64 bits do not hold it
   int64_t r = 1;
@@ -31,7 +37,7 @@ int64_t product(std::initializer_list<int64_t> f) {   // as large as it gets whe
 
 // Device address of a tensor that must be contiguous, of the given type, on device `dev` and hold at least n elements; an int
 // address or None is passed on.  False with the Python error set.
-bool address(PyObject* o, at::ScalarType type, int64_t n, const char* what, int dev, void** out) {
+bool address(PyObject* o, at::ScalarType type, int64_t n, const char* what, int dev, void** out, bool contiguous = true) {
   *out = nullptr;
   if (o == Py_None) return true;
   if (PyLong_CheckExact(o)) {
@@ -47,7 +53,7 @@ bool address(PyObject* o, at::ScalarType type, int64_t n, const char* what, int 
     PyObject* got = PyObject_GetAttrString(o, "dtype");
     if (got) PyErr_Format(PyExc_ValueError, "%s must be %S, got %S", what, (PyObject*)torch::getTHPDtype(type), got);
     Py_XDECREF(got);
-  } else if (!t.is_contiguous()) {
+  } else if (contiguous && !t.is_contiguous()) {
     PyErr_Format(PyExc_ValueError, "%s must be contiguous (row-major)", what);
   } else if (t.numel() < n) {
     PyErr_Format(PyExc_ValueError, "%s holds %lld elements, the call needs %lld", what, (long long)t.numel(), (long long)n);
@@ -60,17 +66,38 @@ bool address(PyObject* o, at::ScalarType type, int64_t n, const char* what, int 
   return false;
 }
 
+// The same of a tensor whose rows lie ld elements apart and hold at least `width` consecutive elements each.
+bool rows_address(PyObject* o, at::ScalarType type, int64_t rows, int64_t ld, int64_t width, const char* what, int dev, void** out) {
+  if (!THPVariable_Check(o) || THPVariable_Unpack(o).is_contiguous())
+    return address(o, type, rows > 0 ? std::max(product({rows - 1, ld}), (int64_t)0) + width : 0, what, dev, out);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  int64_t inner = 1;
+  for (int64_t d = t.dim() - 1; d > 0; d--) {
+    if (t.size(d) != 1 && t.stride(d) != inner) {
+      PyErr_Format(PyExc_ValueError, "the rows of %s must be contiguous", what);
+      return false;
+    }
+    inner *= t.size(d);
+  }
+  if (t.dim() < 2 || t.size(0) < rows || inner < width || (rows > 1 && t.stride(0) != ld)) {
+    PyErr_Format(PyExc_ValueError, "%s must have %lld rows of at least %lld elements, %lld elements apart", what, (long long)rows,
+                 (long long)width, (long long)ld);
+    return false;
+  }
+  return address(o, type, 0, what, dev, out, false);
+}
+
 // The arguments of a call, read in turn; after a failure the rest reads as zero and the Python error stands.
 struct Reader {
   PyObject* const* a;
   Py_ssize_t n, k = 0;
   int dev = 0;
   bool ok = true;
-  Reader(PyObject* const* args, Py_ssize_t nargs, Py_ssize_t want) : a(args), n(nargs) {
+  Reader(PyObject* const* args, Py_ssize_t nargs, Py_ssize_t want, bool bound = g_entries.shared_attention != nullptr) : a(args), n(nargs) {
     if (nargs != want) {
       PyErr_Format(PyExc_TypeError, "%zd arguments, the call takes %zd", nargs, want);
       ok = false;
-    } else if (!g_entries.shared_attention) {
+    } else if (!bound) {
       PyErr_SetString(PyExc_RuntimeError, "the library's entry points are not bound");
       ok = false;
     } else {
@@ -215,6 +242,107 @@ PyObject* evict_context(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   });
 }
 
+const fpd_paged_store* store_at(Reader& r) { return (const fpd_paged_store*)r.stream(); }   // the address of the caller's struct
+
+PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  return call([&]() -> PyObject* {
+    Reader r(args, nargs, 16, g_paged.append != nullptr);
+    const int batch = r.i(), rows = r.i();
+    const fpd_paged_store* st = store_at(r);
+    const int layer = r.i();
+    const int64_t width = r.ok ? product({st->n_kv_heads, st->head_dim}) : 0;
+    PyObject* ko = r.ok ? args[r.k++] : nullptr;
+    const int k_ld = r.i();
+    PyObject* vo = r.ok ? args[r.k++] : nullptr;
+    const int v_ld = r.i();
+    void *k = nullptr, *v = nullptr;
+    if (r.ok) r.ok = rows_address(ko, kBf16, rows, k_ld, width, "k", r.dev, &k) && rows_address(vo, kBf16, rows, v_ld, width, "v", r.dev, &v);
+    const int32_t* off = (const int32_t*)r.at(kI32, {(int64_t)batch + 1}, "row_off");
+    const int32_t* cnt = (const int32_t*)r.at(kI32, {batch}, "row_cnt");
+    const int32_t* start = (const int32_t*)r.at(kI32, {batch}, "pos_start");
+    const int32_t* offset = (const int32_t*)r.at(kI32, {batch}, "pos_offset");
+    PyObject* table = r.ok ? args[r.k++] : nullptr;
+    const int max_pos = r.i();
+    void* rope = nullptr;
+    if (r.ok) r.ok = address(table, kF32, product({max_pos, st->head_dim}), "rope", r.dev, &rope);
+    void* stream = r.stream();
+    return run(r, [&] {
+      return (int)g_paged.append(batch, rows, st, layer, k, k_ld, v, v_ld, off, cnt, start, offset, (const float*)rope, max_pos, stream);
+    });
+  });
+}
+
+PyObject* paged_read(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  return call([&]() -> PyObject* {
+    Reader r(args, nargs, 11, g_paged.read != nullptr);
+    const int batch = r.i(), rows = r.i();
+    const fpd_paged_store* st = store_at(r);
+    const int layer = r.i();
+    const int32_t* off = (const int32_t*)r.at(kI32, {(int64_t)batch + 1}, "row_off");
+    const int32_t* cnt = (const int32_t*)r.at(kI32, {batch}, "row_cnt");
+    const int32_t* start = (const int32_t*)r.at(kI32, {batch}, "pos_start");
+    const int64_t nkv = r.ok ? st->n_kv_heads : 0, h = r.ok ? st->head_dim : 0;
+    void* k = r.at(kBf16, {rows, nkv, h}, "k");
+    void* v = r.at(kBf16, {rows, nkv, h}, "v");
+    void* stream = r.stream();
+    return run(r, [&] { return (int)g_paged.read(batch, rows, st, layer, off, cnt, start, k, v, stream); });
+  });
+}
+
+PyObject* paged_attention(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  return call([&]() -> PyObject* {
+    Reader r(args, nargs, 18, g_paged.attention != nullptr);
+    const int batch = r.i(), L = r.i(), nq = r.i();
+    const fpd_paged_store* st = store_at(r);
+    const int layer = r.i();
+    const int64_t nkv = r.ok ? st->n_kv_heads : 0, h = r.ok ? st->head_dim : 0;
+    const void* q = r.at(kBf16, {batch, L, nq, h}, "q");
+    const void* k_blk = r.at(kBf16, {batch, nkv, L, h}, "k_blk");
+    const void* v_blk = r.at(kBf16, {batch, nkv, L, h}, "v_blk");
+    const int32_t* ctx_len = (const int32_t*)r.at(kI32, {batch}, "ctx_len");
+    const int window = r.i(), sinks = r.i(), causal = r.i();
+    void* out = r.at(kBf16, {batch, L, nq, h}, "out");
+    float* lse = (float*)r.at(kF32, {batch, L, nq}, "lse");
+    PyObject* work = r.ok ? args[r.k++] : nullptr;
+    const size_t bytes = r.size();
+    void* ws = nullptr;
+    if (r.ok) r.ok = address(work, kU8, (int64_t)std::min<size_t>(bytes, INT64_MAX), "workspace", r.dev, &ws);
+    void* stream = r.stream();
+    return run(r, [&] {
+      return (int)g_paged.attention(batch, L, nq, st, layer, q, k_blk, v_blk, ctx_len, window, sinks, causal, out, lse, ws, bytes, stream);
+    });
+  });
+}
+
+PyObject* verify_sampled(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  return call([&]() -> PyObject* {
+    Reader r(args, nargs, 12, g_paged.verify_sampled != nullptr);
+    const int batch = r.i(), L = r.i(), vocab = r.i();
+    const int64_t L1 = L > 0 ? L - 1 : 0;
+    const int32_t* draft = (const int32_t*)r.at(kI32, {batch, L1}, "draft");
+    const float* target = (const float*)r.at(kF32, {batch, L, vocab}, "target");
+    const float* probs = (const float*)r.at(kF32, {batch, L1, vocab}, "draft_probs");
+    const float* uniform = (const float*)r.at(kF32, {batch, L}, "uniform");
+    int32_t* accept = (int32_t*)r.at(kI32, {batch}, "accept_len");
+    int32_t* committed = (int32_t*)r.at(kI32, {batch, L}, "committed");
+    int32_t* valid = (int32_t*)r.at(kI32, {batch}, "valid_out");
+    void* stream = r.stream();
+    return run(r, [&] { return (int)g_paged.verify_sampled(batch, L, vocab, draft, target, probs, uniform, accept, committed, valid, stream); });
+  });
+}
+
+// bind_paged(append, read, attention, verify_sampled): addresses of the entry points
+PyObject* bind_paged(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  if (nargs != 4) {
+    PyErr_SetString(PyExc_TypeError, "bind_paged takes four addresses");
+    return nullptr;
+  }
+  g_paged = {(decltype(&fpd_paged_append))PyLong_AsVoidPtr(a[0]), (decltype(&fpd_paged_read))PyLong_AsVoidPtr(a[1]),
+             (decltype(&fpd_paged_attention))PyLong_AsVoidPtr(a[2]), (decltype(&fpd_verify_sampled))PyLong_AsVoidPtr(a[3])};
+  if (PyErr_Occurred()) return nullptr;
+  Py_RETURN_NONE;
+}
+
 // arg(tensor, dtype, n, what, device): the check alone
 PyObject* arg(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   return call([&]() -> PyObject* {
@@ -247,6 +375,11 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 PyMethodDef g_methods[] = {{"shared_attention", (PyCFunction)(void (*)(void))shared_attention, METH_FASTCALL, nullptr},
                            {"context_weights", (PyCFunction)(void (*)(void))context_weights, METH_FASTCALL, nullptr},
                            {"evict_context", (PyCFunction)(void (*)(void))evict_context, METH_FASTCALL, nullptr},
+                           {"paged_append", (PyCFunction)(void (*)(void))paged_append, METH_FASTCALL, nullptr},
+                           {"paged_read", (PyCFunction)(void (*)(void))paged_read, METH_FASTCALL, nullptr},
+                           {"paged_attention", (PyCFunction)(void (*)(void))paged_attention, METH_FASTCALL, nullptr},
+                           {"verify_sampled", (PyCFunction)(void (*)(void))verify_sampled, METH_FASTCALL, nullptr},
+                           {"bind_paged", (PyCFunction)(void (*)(void))bind_paged, METH_FASTCALL, nullptr},
                            {"arg", (PyCFunction)(void (*)(void))arg, METH_FASTCALL, nullptr},
                            {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

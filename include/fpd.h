@@ -66,7 +66,8 @@ enum {
   FPD_CHECK_BAD_CLASS = 4,      /* a pos_class entry outside [0, n_class) */
   FPD_CHECK_BAD_CONTEXT = 5,    /* a ctx_len outside [0, t_cap] (clamped) */
   FPD_CHECK_BAD_POSITION = 6,   /* a context row's position pos_start[b] + i outside [0, t_cap) (row skipped) */
-  FPD_CHECK_CTX_OVERFLOW = 7    /* fpd_sd_advance: ctx_len + accepted rows would pass t_cap (rows capped) */
+  FPD_CHECK_CTX_OVERFLOW = 7,   /* fpd_sd_advance: ctx_len + accepted rows would pass t_cap (rows capped) */
+  FPD_CHECK_BAD_PAGE = 8        /* a page id outside the pool (a row for it is skipped; its positions read as zeros) */
 };
 
 /* Drafter shape.  The layer form is a pre-norm transformer layer with per-head q/k RMSNorm, rotate-half
@@ -433,6 +434,94 @@ fpd_status fpd_draft_block_shared(fpd_model* model, int batch, int block_len, co
                                   void* workspace, size_t workspace_bytes, void* stream);
 /* 0 for sizes that the call refuses. */
 size_t fpd_shared_workspace_bytes(const fpd_model* model, int batch, int max_block_len, int prefix_cap, int t_cap);
+
+/* ---- a paged context cache ----------------------------------------------------------------------------------------
+ * Requests of very different lengths waste stores of one capacity each.  Here the contexts live in pages of one pool, and a
+ * table says which page holds which positions of a request; pages may be shared by requests that start alike, as long as
+ * nobody appends to them.  The operators take one layer of the pool and need no model.
+ *
+ * A page of a layer holds page_size positions as [K|V][kv_head] slabs (fpd_page_bytes in all); a slab is
+ *   FPD_PAGE_BF16   [page_size][head_dim] bf16
+ *   FPD_PAGE_INT4   [page_size][head_dim / 2] bytes of codes, dim 2 i in the lower half of byte i, followed by
+ *                   [page_size][head_dim / 16] scale bytes.  16 consecutive dims share a scale s; a code n + 8 stands for n s,
+ *                   -7 <= n <= 7.  The scale byte holds 5 exponent bits e and 3 mantissa bits m: (8 + m) 2^(e - 18), and
+ *                   m 2^-17 for e = 0 (an fp16 number without its sign and lower bits).  Written: the smallest s <= 2^13 with
+ *                   7 s >= the group's largest magnitude, n = x / s rounded to nearest, ties to even, within -7..7; an
+ *                   infinity becomes +-7, a NaN 0.
+ * The pool is [n_layers][n_pages] pages.  page_size is 16, 32, 64 or 128; head_dim 64 or 128.  Page ids outside [0, n_pages)
+ * are never followed: FPD_CHECK_BAD_PAGE is recorded, an append skips the row, the attention takes zeros. */
+enum { FPD_PAGE_BF16 = 0, FPD_PAGE_INT4 = 1 };
+typedef struct fpd_paged_store {
+  void* pages;           /* device, 16-byte aligned */
+  const int32_t* table;  /* device [batch][table_width]: positions [i page_size, (i + 1) page_size) of a request are in page table[b][i] */
+  int32_t format, n_layers, n_pages, page_size, n_kv_heads, head_dim;
+  int32_t table_width;   /* at most 2^30 / page_size */
+} fpd_paged_store;
+/* Bytes of one page of one layer; 0 for what the calls refuse. */
+size_t fpd_page_bytes(int format, int page_size, int n_kv_heads, int head_dim);
+
+/* Appends keys and values, the keys rotated on the way.  Rows are packed as in fpd_prepare_context_rows: rows
+ * [row_off[b], row_off[b] + row_cnt[b]) of request b go to slots pos_start[b] + i; the key is rotated (rotate-half) for position
+ * pos_offset[b] + pos_start[b] + i, which must lie in [0, max_pos), rounded to fp32 and to bf16; a 4-bit page holds the codes of the
+ * bf16 values.  Rows whose slot lies outside the table or whose position outside [0, max_pos) are skipped
+ * (FPD_CHECK_BAD_POSITION); no other row of a page is written.  Two rows of one call must not name the same slot of a page.
+ *   k, v         device, row r at k + r k_ld: [kv_head][head_dim] bf16 (slices of a wider projection's rows); 16-byte aligned,
+ *                k_ld, v_ld >= n_kv_heads head_dim, multiples of 8
+ *   row_cnt      device [batch] or NULL for row_off[b + 1] - row_off[b]
+ *   pos_start    device [batch] or NULL for 0, pos_offset device [batch] or NULL for 0
+ *   rope         device [max_pos][head_dim / 2] (cos, sin) fp32, or NULL (max_pos ignored): the keys are rotated already */
+fpd_status fpd_paged_append(int batch, int total_rows, const fpd_paged_store* store, int layer, const void* k, int k_ld,
+                            const void* v, int v_ld, const int32_t* row_off, const int32_t* row_cnt, const int32_t* pos_start,
+                            const int32_t* pos_offset, const float* rope, int max_pos, void* stream);
+/* The rows that an append with the same offsets wrote, as bf16 (a 4-bit row as what it stands for, exactly): to move a context
+ * into a contiguous store, or to see what a cache holds.  Rows that an append would skip are left as they are.
+ *   k, v   device [total_rows][kv_head][head_dim] bf16 */
+fpd_status fpd_paged_read(int batch, int total_rows, const fpd_paged_store* store, int layer, const int32_t* row_off,
+                          const int32_t* row_cnt, const int32_t* pos_start, void* k, void* v, void* stream);
+
+/* Attention of blocks over their requests' pages and the blocks themselves.  With n = ctx_len[b], plus block_len when block keys
+ * are given, request b's keys stand at positions 0..n-1 (the pages' slots, then the block) and its query row j at position
+ * r = n - block_len + j.  The row sees key t where
+ *   (window == 0 or t < sinks or r - t < window) and (not causal or t <= r)
+ * so a window holds the row's own position and the window - 1 before it, and the first `sinks` positions stay visible behind it;
+ * without causal the positions after the row are visible (the drafter's blocks).  Over those keys
+ *   lse = log sum_t exp(q . k_t / sqrt(h)),   out = sum_t exp(q . k_t / sqrt(h) - lse) v_t
+ * A row that sees no key (or scores of -inf alone) gives out 0 and lse -inf.  Keys that no row of a request sees, and slots from
+ * ctx_len on, are not touched by the result whatever they hold; a key or value that is not finite reaches the rows that see it,
+ * and may reach other rows of the same request and call where a window or causal hides it from them alone.
+ * Sums are fp32; weights of bf16 pages enter the second product as two bf16 terms, those of 4-bit pages as fp16; out is rounded
+ * once.  batch * block_len * n_q_heads <= 2^26, at most 128 query heads per kv head.  Lengths outside [0, table_width page_size]
+ * are clamped (FPD_CHECK_BAD_CONTEXT).  Calls that share a workspace must not overlap on the GPU.
+ *   q, out       device [batch * block_len, n_q_heads, h] bf16; q normed and rotated
+ *   k_blk, v_blk device [batch, n_kv_heads, block_len, h] bf16, or both NULL: no block keys (the block's own have been appended)
+ *   lse          device [batch * block_len, n_q_heads] fp32 or NULL
+ *   window       0: none; sinks: ignored without a window
+ *   workspace    fpd_paged_attention_workspace_bytes bytes for the same sizes on the current device */
+fpd_status fpd_paged_attention(int batch, int block_len, int n_q_heads, const fpd_paged_store* store, int layer, const void* q,
+                               const void* k_blk, const void* v_blk, const int32_t* ctx_len, int window, int sinks, int causal,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+/* Asks the current device for its SM count; 0 for what the call refuses or without a device. */
+size_t fpd_paged_attention_workspace_bytes(int batch, int block_len, int n_q_heads, const fpd_paged_store* store);
+
+/* ---- sampled verification --------------------------------------------------------------------------------------------
+ * fpd_verify keeps what the target's greedy ids agree with; this call keeps drafted ids so that the committed ids are distributed
+ * as samples of the target, whatever the drafter proposed.  With p_i = target[b][i] (the target's probabilities of the id at block
+ * position i + 1 behind the anchor and d_1..d_i), q_i = draft_probs[b][i] (those that d_{i+1} was drawn from; all of it on d_{i+1}
+ * where draft_probs is NULL: the ids of an argmax) and given random numbers u in [0, 1):
+ *   d_{i+1} is kept while u_i q_i(d_{i+1}) < p_i(d_{i+1});  n = the ids kept before the first refusal
+ *   the last id comes from r = max(p_n - q_n, 0) after a refusal (from p_n where that is 0 everywhere), from p_{L-1} when all were
+ *   kept: the lowest id whose running sum r(0) + .. + r(id) exceeds u_{L-1} times the sum over all ids
+ *   accept_len = n + 1, committed = d_1..d_n and the last id, then -1; valid = (n == L - 1), as fpd_verify's text mode
+ * Probabilities need not sum to 1; entries that are negative or NaN count as 0.  p - q is taken exactly and sums to about 2^-44.
+ * A row without any probability gives id -1 (FPD_CHECK_NO_LEGAL_ID); a drafted id outside [0, vocab) is refused
+ * (FPD_CHECK_BAD_TOKEN).
+ *   draft        device [B, L - 1] int32
+ *   target       device [B, L, vocab] fp32, finite; draft_probs device [B, L - 1, vocab] fp32, finite, or NULL
+ *   uniform      device [B, L] fp32
+ *   accept_len, committed [B, L], valid_out (or NULL): as fpd_verify */
+fpd_status fpd_verify_sampled(int batch, int block_len, int vocab, const int32_t* draft, const float* target,
+                              const float* draft_probs, const float* uniform, int32_t* accept_len, int32_t* committed,
+                              int32_t* valid_out, void* stream);
 
 /* ---- diagnostics ---------------------------------------------------------------------------------------- */
 const char* fpd_last_error(void);          /* thread-local message of the last failing call */
