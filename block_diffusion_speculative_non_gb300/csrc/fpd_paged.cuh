@@ -82,12 +82,13 @@ struct PagedAttn {
   int4* desc;                   // [runs]: request, kv head, row tile and last run of the unit that a run leaves unfinished
   int batch, L, lb, nq, window, sinks, causal;   // lb: block keys, L or 0
 };
+enum PagedKernel { kPagedMma, kPagedStream };
 struct PagedPlan {
-  bool tc;             // k_paged_attention_tc.cu, else k_paged_attention.cu
+  PagedKernel kernel;
   int rows, tiles;     // rows of a row tile, row tiles of a request and kv head
-  int runs;            // CTAs that share the key tiles
+  int grid, runs;      // CTAs, and the runs that share the key tiles (of CTAs, or of their warps)
 };
-PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int h, int format, int num_sms);
+PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int h, int format, int t_cap, int num_sms);
 cudaError_t paged_attn_init_attributes();
 cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cudaStream_t st);
 

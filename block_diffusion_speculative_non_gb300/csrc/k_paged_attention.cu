@@ -368,16 +368,16 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
 
 template <int H, bool INT4>
 auto mma_kernel(int rows) {
-  return rows == 16 ? paged_mma_kernel<H, 1, INT4> : rows == 32 ? paged_mma_kernel<H, 2, INT4> : paged_mma_kernel<H, 4, INT4>;
+  return rows == 32 ? paged_mma_kernel<H, 2, INT4> : paged_mma_kernel<H, 4, INT4>;
 }
 template <int H>
 size_t mma_smem(int rows) {
-  return rows == 16 ? sizeof(Mem<H, 1>) : rows == 32 ? sizeof(Mem<H, 2>) : sizeof(Mem<H, 4>);
+  return rows == 32 ? sizeof(Mem<H, 2>) : sizeof(Mem<H, 4>);
 }
 
 template <int H>
 cudaError_t attributes() {
-  for (int rows : {16, 32, 64}) {
+  for (int rows : {32, 64}) {
     cudaError_t e = cudaFuncSetAttribute(mma_kernel<H, false>(rows), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mma_smem<H>(rows));
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(mma_kernel<H, true>(rows), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mma_smem<H>(rows));
@@ -388,26 +388,36 @@ cudaError_t attributes() {
 
 template <int H>
 cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
-  auto k = p.a.pg.format == FPD_PAGE_INT4 ? mma_kernel<H, true>(pl.rows) : mma_kernel<H, false>(pl.rows);
-  cudaError_t e = launch_k(k, pl.runs, kThreads, mma_smem<H>(pl.rows), st, p);
+  cudaError_t e;
+  if (pl.kernel == kPagedStream) {
+    e = launch_paged_stream(p.a, p.s, pl, st);
+  } else {
+    auto k = p.a.pg.format == FPD_PAGE_INT4 ? mma_kernel<H, true>(pl.rows) : mma_kernel<H, false>(pl.rows);
+    e = launch_k(k, pl.runs, kThreads, mma_smem<H>(pl.rows), st, p);
+  }
   if (e != cudaSuccess) return e;
   return launch_k(paged_merge_kernel<H>, dim3(pl.runs, ceil_div(std::min(pl.rows, p.a.L * p.s.grp), 4)), 128, 0, st, p);
 }
 
 }  // namespace
 
-PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int h, int format, int num_sms) {
+PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int h, int format, int t_cap, int num_sms) {
   PagedPlan pl{};
   const int n = L * (nq / nkv);
-  pl.rows = n <= 16 ? 16 : n <= 32 ? 32 : 64;
+  pl.kernel = n <= 16 ? kPagedStream : kPagedMma;
+  pl.rows = n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
   pl.tiles = ceil_div(n, pl.rows);
-  pl.runs = 2 * num_sms;
+  // no more runs than there can be tiles
+  const long long most = (long long)batch * nkv * pl.tiles * (ceil_div(t_cap, kPagedTile) + ceil_div(L, kPagedTile));
+  pl.runs = (int)std::min<long long>(most, (long long)num_sms * (pl.kernel == kPagedStream ? paged_stream_warps() : 2));
+  pl.grid = pl.kernel == kPagedStream ? std::min(num_sms, pl.runs) : pl.runs;
   return pl;
 }
 
 cudaError_t paged_attn_init_attributes() {
-  const cudaError_t e = attributes<128>();
-  return e != cudaSuccess ? e : attributes<64>();
+  cudaError_t e = attributes<128>();
+  if (e == cudaSuccess) e = attributes<64>();
+  return e != cudaSuccess ? e : paged_stream_init_attributes();
 }
 
 cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cudaStream_t st) {

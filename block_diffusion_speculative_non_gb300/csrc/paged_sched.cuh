@@ -13,6 +13,7 @@
 
 namespace fpd {
 
+constexpr int kPagedTile = 64;       // keys of a tile of the mma.sync kernels
 constexpr int kSchedEntries = 128;   // running sums kept in shared memory, over ceil(batch / 128) requests each
 
 struct PagedUnit {
@@ -158,6 +159,10 @@ struct PagedWalk {
     return true;
   }
 };
+
+cudaError_t paged_stream_init_attributes();
+int paged_stream_warps();   // runs per SM
+cudaError_t launch_paged_stream(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, cudaStream_t st);
 
 #ifdef __CUDACC__
 struct DeviceLens {
