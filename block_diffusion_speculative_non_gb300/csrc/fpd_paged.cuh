@@ -82,7 +82,7 @@ struct PagedAttn {
   int4* desc;                   // [runs]: request, kv head, row tile and last run of the unit that a run leaves unfinished
   int batch, L, lb, nq, window, sinks, causal;   // lb: block keys, L or 0
 };
-enum PagedKernel { kPagedMma, kPagedStream };
+enum PagedKernel { kPagedMma, kPagedStream, kPagedTc };
 struct PagedPlan {
   PagedKernel kernel;
   int rows, tiles;     // rows of a row tile, row tiles of a request and kv head

@@ -391,6 +391,8 @@ cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
   cudaError_t e;
   if (pl.kernel == kPagedStream) {
     e = launch_paged_stream(p.a, p.s, pl, st);
+  } else if (pl.kernel == kPagedTc) {
+    e = launch_paged_tc(p.a, p.s, pl, st);
   } else {
     auto k = p.a.pg.format == FPD_PAGE_INT4 ? mma_kernel<H, true>(pl.rows) : mma_kernel<H, false>(pl.rows);
     e = launch_k(k, pl.runs, kThreads, mma_smem<H>(pl.rows), st, p);
@@ -404,12 +406,13 @@ cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
 PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int h, int format, int t_cap, int num_sms) {
   PagedPlan pl{};
   const int n = L * (nq / nkv);
-  pl.kernel = n <= 16 ? kPagedStream : kPagedMma;
-  pl.rows = n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
+  const int grp = nq / nkv;
+  pl.kernel = n <= 16 ? kPagedStream : kPagedTc;
+  pl.rows = n <= 8 ? 8 : n <= 16 ? 16 : 2 * (128 / grp * grp);
   pl.tiles = ceil_div(n, pl.rows);
   // no more runs than there can be tiles
   const long long most = (long long)batch * nkv * pl.tiles * (ceil_div(t_cap, kPagedTile) + ceil_div(L, kPagedTile));
-  pl.runs = (int)std::min<long long>(most, (long long)num_sms * (pl.kernel == kPagedStream ? paged_stream_warps() : 2));
+  pl.runs = (int)std::min<long long>(most, (long long)num_sms * (pl.kernel == kPagedStream ? paged_stream_warps() : pl.kernel == kPagedTc ? 1 : 2));
   pl.grid = pl.kernel == kPagedStream ? std::min(num_sms, pl.runs) : pl.runs;
   return pl;
 }
@@ -417,7 +420,8 @@ PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int h, int format, 
 cudaError_t paged_attn_init_attributes() {
   cudaError_t e = attributes<128>();
   if (e == cudaSuccess) e = attributes<64>();
-  return e != cudaSuccess ? e : paged_stream_init_attributes();
+  if (e == cudaSuccess) e = paged_stream_init_attributes();
+  return e != cudaSuccess ? e : paged_tc_init_attributes();
 }
 
 cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cudaStream_t st) {

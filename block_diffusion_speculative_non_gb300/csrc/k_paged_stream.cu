@@ -20,6 +20,8 @@
 
 #include "attn_body.cuh"
 #include "attn_tc_prims.cuh"
+#include "paged_decode.cuh"
+#include "paged_repair.cuh"
 #include "paged_sched.cuh"
 
 namespace fpd {
@@ -48,47 +50,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-template <uint32_t MASK, uint32_t OR>
-__device__ __forceinline__ uint32_t and_or(uint32_t v) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "n"(MASK), "n"(OR));   // (a & b) | c
-  return r;
-}
-constexpr uint32_t h2(uint32_t bits) { return bits * 0x10001u; }
-
-// Two scales (fp16 bits, a pair) as what the codes' multiply-adds need.
-struct Scale2 {
-  uint32_t s, o24, o264;
-  __device__ __forceinline__ explicit Scale2(uint32_t raw) {
-    s = hmul2(raw, h2(0x2000));       // 2^-7
-    o24 = hmul2(s, h2(0xCE00));       // -24
-    o264 = hmul2(s, h2(0xDC20));      // -264
-  }
-};
-// Nibble k of the lower and of the upper half of w as a pair n s', k = 0..3.
-__device__ __forceinline__ void decode4(uint32_t w, const Scale2& s, uint32_t (&r)[4]) {
-  const uint32_t a = w << 2, b = w >> 6;
-  r[0] = hfma2(and_or<0x003C003Cu, 0x5C005C00u>(a), s.s, s.o264);
-  r[1] = hfma2(and_or<0x03C003C0u, 0x4C004C00u>(a), s.s, s.o24);
-  r[2] = hfma2(and_or<0x003C003Cu, 0x5C005C00u>(b), s.s, s.o264);
-  r[3] = hfma2(and_or<0x03C003C0u, 0x4C004C00u>(b), s.s, s.o24);
-}
-
 // Query rows of a warp: NT columns tiles of 8.  State of the softmax for rows 8 j + 2 c + e; O^T of dims by rows.
 template <int H, int NT>
 struct State {
@@ -264,9 +225,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
     for (int j = 0; j < NT; j++)
 #pragma unroll
       for (int e = 0; e < 2; e++) pos_row[j][e] = u.n - a.L + (u.rt * R + 8 * j + 2 * c + e) / sh.grp;
-    auto see = [&](int pos, int row) {
-      return (!sh.window || pos < sh.sinks || row - pos < sh.window) && (!sh.causal || pos <= row);
-    };
+    auto see = [&](int pos, int row) { return row_sees(sh, row, pos); };
 
     if constexpr (!INT4) {
       // ---- bf16: slots of 16 keys; a tile is up to four of them ----
@@ -323,9 +282,12 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
         ok = attn_tc::wait_bar(bars + 8 * s, (cnt / ST) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (t.valid < 16) {   // V rows past the last key -> 0: 0 x a stale non-finite value would be NaN
-          for (int q = lane; q < (16 - t.valid) * (H / 8); q += 32) {
-            const int r = t.valid + q / (H / 8), ch = q % (H / 8);
+        int h_lo, h_hi;
+        hidden_from_all(sh, u, t, h_lo, h_hi);
+        if (t.valid < 16 || h_hi > h_lo) {
+          // V rows past the last key, and those that no row sees -> 0: 0 x a value that is not finite would be NaN
+          for (int q = lane; q < (16 - t.valid + h_hi - h_lo) * (H / 8); q += 32) {
+            const int z = q / (H / 8), r = z < h_hi - h_lo ? h_lo + z : t.valid + z - (h_hi - h_lo), ch = q % (H / 8);
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vs + (ch >> 3) * 2048 + r * 128 + (ch & 7) * 16), "r"(0) : "memory");
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -590,6 +552,8 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
     // ---- the rows' sums, and out ----
     const bool whole = t0 == 0 && t1 == u.len();
     const int slot = 2 * run + (t0 == 0 ? 1 : 0);
+    unsigned bad = 0;   // rows without numbers whose weights are numbers, under a mask (paged_repair.cuh)
+    float l_row[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -598,6 +562,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         const int r = 8 * j + 2 * c + e, qi = u.rt * R + r;
+        l_row[j][e] = l;
         if (qi >= nrows) continue;
         const float ul = INT4 ? l * 6.103515625e-05f : l;   // 2^-14
         const bool none = l == 0.f;
@@ -608,6 +573,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
         for (int i = 0; i < MT; i++) {
           x[2 * i] = none ? 0.f : st.o[i][j][e] * by;
           x[2 * i + 1] = none ? 0.f : st.o[i][j][2 + e] * by;
+          if (!(fabsf(x[2 * i]) < INFINITY && fabsf(x[2 * i + 1]) < INFINITY) && fabsf(l) < INFINITY) bad |= 1u << r;
         }
         if (whole) {
           bf16* dst = a.out + row * H;
@@ -632,6 +598,31 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
           if (g == 0) a.ml[row] = make_float2(st.m[j][e], ul);
         }
       }
+    bad = sh.window || sh.causal ? __reduce_or_sync(0xffffffffu, bad) : 0;
+    if (bad) __syncwarp();   // behind the rows' own stores
+    while (bad) {
+      const int r = __ffs(bad) - 1, qi = u.rt * R + r;
+      bad &= bad - 1;
+      float m = 0.f, l = 1.f, acc[H / 32];
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float mr = __shfl_sync(0xffffffffu, st.m[j][e], (r & 7) >> 1), lr = __shfl_sync(0xffffffffu, l_row[j][e], (r & 7) >> 1);
+          if (r == 8 * j + ((r & 7) & ~1) + e) {
+            m = mr;
+            l = lr;
+          }
+        }
+      repair_row<H>(a, sh, u, t0, nt, qi, m, acc);
+      const float by = whole ? (INT4 ? 16384.f : 1.f) / l : 1.f;
+      const size_t row = whole ? (size_t)(u.b * a.L + qi / sh.grp) * a.nq + u.g * sh.grp + qi % sh.grp : (size_t)slot * R + r;
+#pragma unroll
+      for (int j = 0; j < H / 32; j++) {
+        if (whole) a.out[row * H + lane + 32 * j] = __float2bfloat16_rn(acc[j] * by);
+        else a.o_part[row * H + lane + 32 * j] = acc[j];
+      }
+    }
     if (t0 == 0 && t1 < u.len()) left = make_int4(u.b, u.g, u.rt, last_run);
   }
   if (lane == 0) a.desc[run] = left;

@@ -1,0 +1,750 @@
+// k_paged_tc.cu — attention over pages for many rows, on the 5th-generation tensor cores.  Formulas and cut of the work as in
+// k_paged_attention.cu and paged_sched.cuh, with tiles of 128 keys.
+//
+// A CTA works on two "lanes", each a 128-row S / P / O set in tensor memory with a softmax warpgroup of its own (one thread per
+// query row), so that one lane's softmax runs while the tensor core works for the other.  A lane's rows are whole positions, the kv
+// head's heads of each.  A unit has the rows of two lanes, which share every K/V tile; where it has one lane's rows only (a text
+// block, the last rows of a long one) both lanes hold them and take the even and the odd key tiles, and their halves of O are put
+// together from tensor memory: a thread of either lane reaches both accumulators of its row.
+//
+// bf16 pages: TMA, one box per page and 64 dims (a coordinate past the pool, which reads zeros, for a page that is none); P enters as
+// two bf16 terms.
+// 4-bit pages: three warps decode tiles into the swizzled layout, K as bf16 and V as fp16 (7 bits either way, exact), a row of a
+// tile per thread.  The pairs that decode together are dims i and i + 4 of 8, so
+// Q is stored in that order too, and O comes out in it.  P enters as one fp16 term, p 2^7 (p stays below 2^8; weights down to 2^-31
+// count); the block's own keys are bf16 and take the bf16 products.
+#include <cstring>
+
+#include "attn_tc_prims.cuh"
+#include "paged_decode.cuh"
+#include "paged_repair.cuh"
+#include "paged_sched.cuh"
+
+namespace fpd {
+
+namespace {
+using namespace attn_tc;
+
+constexpr int QR = 128, KT = 128;
+constexpr int KST = 2, VST = 3;
+constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
+constexpr uint32_t kTmemO = 256;
+constexpr float kRescaleLog2 = 8.f;
+constexpr int ATOM_BYTES = KT * 64 * 2;
+
+struct TcArgs {
+  CUtensorMap tm_q, tm_pages, tm_kblk, tm_vblk;
+  PagedAttn a;
+  PagedShape s;
+  int runs, npt, rpt;   // positions and rows of a lane
+};
+
+template <int HD>
+struct Lay {
+  static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64;
+  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, STAT = V + VST * TILE, SUMS = STAT,   // the running sums are read before the statistics are written
+                       BAR = STAT + (kSchedEntries + 1) * 8;
+  static_assert(2 * QR * 4 <= (kSchedEntries + 1) * 8, "the lanes' statistics");
+};
+enum {
+  B_Q = 0,
+  B_QE = B_Q + 2,
+  B_KF = B_QE + 2,
+  B_KE = B_KF + KST,
+  B_VF = B_KE + KST,
+  B_VE = B_VF + VST,
+  B_SF = B_VE + VST,
+  B_PF = B_SF + 2,
+  B_PV = B_PF + 2,
+  B_END = B_PV + 2,
+  B_X = B_END + 1,   // the softmax warps, in units whose keys the lanes share
+  B_N = B_X + 1
+};
+template <int HD>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)Lay<HD>::BAR + 8 * B_N + 16;
+}
+static_assert(smem_bytes<128>() <= 232448, "tile set exceeds the shared memory of one CTA");
+
+// bf16: 11 warps, 0 and 2 TMA producers of K and Q, and of V, 1 the products, 3.. softmax.  4 bits: 12 warps, 0, 2 and 3 decode, 4..
+// softmax.
+template <bool INT4>
+struct Roles {
+  static constexpr int THREADS = INT4 ? 384 : 352, SOFTMAX = INT4 ? 4 : 3;
+};
+
+__device__ __forceinline__ void split_trunc(float a, float b, uint32_t& hi, uint32_t& lo) {   // a, b >= 0: hi + lo to 2^-16
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  hi = __byte_perm(ua, ub, 0x7632);
+  const uint64_t rest = add2(pack2(a, b), pack2(-__uint_as_float(ua & 0xFFFF0000u), -__uint_as_float(ub & 0xFFFF0000u)));
+  float ra, rb;
+  unpack2(rest, ra, rb);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb), "f"(ra));
+}
+constexpr uint32_t idesc_f16(int M, int N, int b_mn) {   // fp16 A and B, fp32 accumulator
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// A part of a unit as this kernel walks it.
+struct Seg {
+  PagedUnit u;
+  bool keys, whole, first;   // keys: one lane's rows; first: the unit starts here
+  int t0, n_tiles, row0, slot, last_run;
+  __device__ PagedTile tile(int i) const { return tile_at(u, KT, t0 + i); }
+  __device__ int lane_tiles(int t) const { return keys ? (n_tiles - t + 1) / 2 : n_tiles; }
+};
+
+template <int HD, bool INT4>
+__global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const __grid_constant__ TcArgs p) {
+  using S = Lay<HD>;
+  using Ro = Roles<INT4>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_N);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  long long* sums = reinterpret_cast<long long*>(smem + S::SUMS);
+  const uint32_t bar0 = tc::smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8 * i; };
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const PagedAttn& a = p.a;
+  const PagedShape& sh = p.s;
+  const int grp = sh.grp, nrows = a.L * grp;
+  constexpr int kFill = INT4 ? 4 : 1;   // arrivals that fill a tile: the decoding warps, or the one that issues its copies
+
+  if (tid == 0) {
+    for (int t = 0; t < 2; t++) {
+      tc::mbar_init(bar(B_Q + t), kFill);
+      tc::mbar_init(bar(B_QE + t), 1);
+      tc::mbar_init(bar(B_SF + t), 1);
+      tc::mbar_init(bar(B_PF + t), 4);
+      tc::mbar_init(bar(B_PV + t), 1);
+    }
+    for (int s = 0; s < KST; s++) {
+      tc::mbar_init(bar(B_KF + s), kFill);
+      tc::mbar_init(bar(B_KE + s), 1);
+    }
+    for (int s = 0; s < VST; s++) {
+      tc::mbar_init(bar(B_VF + s), kFill);
+      tc::mbar_init(bar(B_VE + s), 1);
+    }
+    tc::mbar_init(bar(B_END), 1);
+    tc::mbar_init(bar(B_X), 8);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+    if (!INT4) {
+      tc::tma_prefetch(&p.tm_q);
+      tc::tma_prefetch(&p.tm_pages);
+      if (a.lb) {
+        tc::tma_prefetch(&p.tm_kblk);
+        tc::tma_prefetch(&p.tm_vblk);
+      }
+    }
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmemCols);
+    tc::tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  const DeviceLens lens{a.ctx_len, a.pg.cap()};
+  sched_sums(sh, lens, a.batch, sums, tid);
+  __syncwarp();   // a CTA barrier counts a whole warp: single-lane roles reconverge before every one
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const long long before = tid < kSchedEntries ? sched_before(sums, tid) : 0;
+  __syncthreads();
+  if (tid < kSchedEntries) sums[tid + 1] += before;
+  __syncthreads();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+  PagedWalk<DeviceLens> walk(sh, lens, sums, a.batch, p.runs, blockIdx.x);
+  auto next = [&](Seg& s) {
+    int t1;
+    if (!walk.next(s.u, s.t0, t1, s.last_run)) return false;
+    s.whole = s.t0 == 0 && t1 == s.u.len();
+    s.first = s.t0 == 0;
+    s.n_tiles = max(0, min(t1, s.u.tiles()) - s.t0);   // an empty unit has none
+    s.row0 = s.u.rt * sh.rows;
+    s.keys = nrows - s.row0 <= p.rpt;
+    s.slot = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
+    return true;
+  };
+  Seg sg;
+  __syncthreads();
+
+  if (!INT4 && (warp == 0 || warp == 2)) {
+    // ---------------- TMA producers: K and Q (warp 0), V (warp 2); lane i copies a tile's page i ----------------
+    const bool is_v = warp == 2;
+    const int ST = is_v ? VST : KST, full = is_v ? B_VF : B_KF, empty = is_v ? B_VE : B_KE;
+    const uint32_t ring = tc::smem_u32(smem + (is_v ? S::V : S::K));
+    const int bp = min(KT, a.pg.page);   // rows of a box
+    int n = 0, nq[2] = {0, 0};
+    auto page_for = [&](const Seg& s, int i) {   // of this lane's part of tile i
+      if (i >= s.n_tiles) return 0;
+      const PagedTile t = s.tile(i);
+      return t.ctx && lane * bp < t.valid ? page_of(a.pg, s.u.b, t.k0 + lane * bp) : 0;
+    };
+    bool ok = true;
+    while (ok && !*abort_flag && next(sg)) {
+      int id = page_for(sg, 0);
+      for (int i = 0; i < sg.n_tiles && ok; i++) {
+        const int s = n % ST;
+        const PagedTile t = sg.tile(i);
+        const int id_now = id;
+        id = page_for(sg, i + 1);
+        if (n >= ST) ok = wait_bar(bar(empty + s), ((n / ST) & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        const bool mine = t.ctx ? lane * bp < t.valid : lane == 0;
+        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar(full + s), t.ctx ? boxes * bp * HD * 2 : S::TILE);
+        __syncwarp();
+        if (mine) {
+          for (int h = 0; h < S::ATOMS; h++) {
+            const uint32_t dst = ring + s * S::TILE + h * ATOM_BYTES;
+            if (t.ctx)
+              tc::tma_load_3d(dst + lane * bp * 128, &p.tm_pages, h * 64,
+                              ((is_v ? a.pg.nkv : 0) + sg.u.g) * a.pg.page + ((t.k0 + lane * bp) & (a.pg.page - 1)),
+                              id_now < 0 ? a.pg.n_pages : id_now, bar(full + s));
+            else
+              tc::tma_load_2d(dst, is_v ? &p.tm_vblk : &p.tm_kblk, h * 64, (sg.u.b * a.pg.nkv + sg.u.g) * a.lb + t.k0, bar(full + s));
+          }
+        }
+        n++;
+        if (is_v || i > 0) continue;
+        // Q behind the first K tile, whose slot is free one S before Q's (with the last S of the run before)
+        for (int l = 0; l < 2 && ok; l++) {
+          if (sg.lane_tiles(l) == 0) continue;
+          if (nq[l] > 0) ok = wait_bar(bar(B_QE + l), (nq[l] & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(bar(B_Q + l), p.rpt * HD * 2);
+            for (int h = 0; h < S::ATOMS; h++)
+              tc::tma_load_3d(tc::smem_u32(smem + S::Q) + l * S::TILE + h * ATOM_BYTES, &p.tm_q, h * 64, sg.u.g * grp,
+                              sg.u.b * a.L + (sg.row0 + (sg.keys ? 0 : l * p.rpt)) / grp, bar(B_Q + l));
+          }
+          nq[l]++;
+        }
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (*abort_flag) {   // a wait ran out: let the copies in flight land before the CTA's memory goes
+      for (int i = max(0, n - ST); i < n; i++) tc::mbar_wait(bar(full + i % ST), (i / ST) & 1);
+      for (int t = 0; t < 2; t++)
+        if (nq[t] > 0) tc::mbar_wait(bar(B_Q + t), (nq[t] & 1) ^ 1);
+    }
+  } else if (INT4 && warp < Ro::SOFTMAX && warp != 1) {
+    // ---------------- decoding warps ----------------
+    // A tile is eight items, 32 rows of K or of V each; the three warps take turns at them, a thread a row, and have requested the
+    // codes of their next three.
+    const int w3 = warp == 0 ? 0 : warp - 1;
+    uint8_t *qs = smem + S::Q, *ks = smem + S::K, *vs = smem + S::V;
+    int n = 0, nq[2] = {0, 0};
+    struct Raw {
+      uint4 code[HD / 32];
+      uint32_t scale[HD / 64];
+    };
+    auto fetch = [&](const Seg& s, int e, Raw& w) {   // a row of a context tile; zeros where there is none
+#pragma unroll
+      for (int j = 0; j < HD / 32; j++) w.code[j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < HD / 64; j++) w.scale[j] = 0;
+      if (e >= 8 * s.n_tiles) return;
+      const PagedTile t = s.tile(e >> 3);
+      const int r = (e & 3) * 32 + lane;
+      if (!t.ctx || r >= t.valid) return;
+      const int id = page_of(a.pg, s.u.b, t.k0 + r);
+      if (id < 0) return;
+      const int in = (t.k0 + r) & (a.pg.page - 1);
+      const uint8_t* slab = slab_of(a.pg, id, (e >> 2) & 1, s.u.g);
+      const uint4* code = reinterpret_cast<const uint4*>(slab + in * (HD / 2));
+      const uint32_t* scale = reinterpret_cast<const uint32_t*>(slab + a.pg.page * (HD / 2) + in * (HD / 16));
+#pragma unroll
+      for (int j = 0; j < HD / 32; j++) w.code[j] = __ldg(code + j);
+#pragma unroll
+      for (int j = 0; j < HD / 64; j++) w.scale[j] = __ldg(scale + j);
+    };
+    // chunk of 8 dims ch of row r in a tile of 64-dim atoms
+    auto put = [&](uint8_t* tile, int r, int ch, uint4 v) {
+      *reinterpret_cast<uint4*>(tile + (ch >> 3) * ATOM_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+    };
+    auto put_bf16 = [&](uint8_t* tile, int r, const bf16* row) {   // a bf16 row (null: zeros) in the order of the decoded ones
+#pragma unroll 4
+      for (int ch = 0; ch < HD / 8; ch++) {
+        const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(row) + ch) : make_uint4(0, 0, 0, 0);
+        put(tile, r, ch, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                                    __byte_perm(v.y, v.w, 0x7632)));
+      }
+    };
+    auto put_codes = [&](uint8_t* tile, int r, const Raw& w, bool is_v) {
+#pragma unroll
+      for (int q = 0; q < HD / 16; q++) {   // a group of 16 dims: two words
+        const uint32_t byte = (w.scale[q / 4] >> (8 * (q & 3))) & 0xFF;
+        const uint32_t c0 = q & 1 ? w.code[q / 2].z : w.code[q / 2].x, c1 = q & 1 ? w.code[q / 2].w : w.code[q / 2].y;
+        uint32_t x[4], y[4];
+        if (is_v) {
+          const Scale2 s(byte * 0x00800080u);
+          decode4(c0, s, x);
+          decode4(c1, s, y);
+        } else {
+          const Scale2Bf s(byte);
+          decode4_bf16(c0, s, x);
+          decode4_bf16(c1, s, y);
+        }
+        put(tile, r, 2 * q, make_uint4(x[0], x[1], x[2], x[3]));
+        put(tile, r, 2 * q + 1, make_uint4(y[0], y[1], y[2], y[3]));
+      }
+    };
+    auto done = [&](int b) {   // this warp's rows are written, for the tensor core to read
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(b));
+    };
+    bool ok = true;
+    auto wait = [&](int b, uint32_t parity) {
+      ok = wait_bar(bar(b), parity);
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      return ok;
+    };
+    while (ok && !*abort_flag && next(sg)) {
+      Raw raw[3];
+#pragma unroll
+      for (int d = 0; d < 3; d++) fetch(sg, w3 + 3 * d, raw[d]);
+      const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
+      bool q_done = false;
+      for (int e0 = w3; e0 < 8 * sg.n_tiles && ok; e0 += 9) {
+#pragma unroll
+        for (int d = 0; d < 3; d++) {
+          const int e = e0 + 3 * d;
+          if (e >= 8 * sg.n_tiles || !ok) break;
+          if (!q_done && e >= 4) {   // Q behind the first K tile
+            q_done = true;
+            for (int l = 0; l < 2 && ok; l++) {
+              if (sg.lane_tiles(l) == 0) continue;
+              if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
+              for (int k = w3; k < 4; k += 3) {
+                const int r = k * 32 + lane, qi = sg.row0 + (sg.keys ? 0 : l * p.rpt) + r;
+                const bool has = r < p.rpt && qi < nrows;
+                put_bf16(qs + l * S::TILE, r, has ? a.q + ((size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp) * HD : nullptr);
+                done(B_Q + l);
+              }
+              nq[l]++;
+            }
+            if (!ok) break;
+          }
+          const PagedTile t = sg.tile(e >> 3);
+          const bool is_v = (e >> 2) & 1;
+          const int i = n + (e >> 3), ST = is_v ? VST : KST, s = i % ST, r = (e & 3) * 32 + lane;
+          if (i >= ST && !wait((is_v ? B_VE : B_KE) + s, ((i / ST) & 1) ^ 1)) break;
+          uint8_t* tile = (is_v ? vs : ks) + s * S::TILE;
+          if (t.ctx) put_codes(tile, r, raw[d], is_v);
+          else put_bf16(tile, r, r < t.valid ? (is_v ? a.vblk : a.kblk) + (blk + t.k0 + r) * HD : nullptr);
+          done((is_v ? B_VF : B_KF) + s);
+          fetch(sg, e + 9, raw[d]);
+        }
+      }
+      n += sg.n_tiles;
+    }
+    if (!ok) *abort_flag = 1;
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    const uint32_t on = elect_one();
+    constexpr uint32_t id_s = idesc_bf16(QR, KT, 0);   // Q x K, both K-major in shared memory
+    constexpr uint32_t id_o = idesc_bf16(QR, HD, 1);   // P (tensor memory) x V (MN-major in shared memory)
+    constexpr uint32_t id_h = idesc_f16(QR, HD, 1);
+    const uint64_t dq = tc::sw128_kmajor_desc(tc::smem_u32(smem + S::Q)), dk = tc::sw128_kmajor_desc(tc::smem_u32(smem + S::K));
+    const uint64_t dv = sw128_mn_desc(tc::smem_u32(smem + S::V), ATOM_BYTES);
+    int n0 = 0, nq[2] = {0, 0}, nl[2] = {0, 0};        // ring tiles, Q loads, lane tiles so far
+    auto fail = [&]() { *abort_flag = 1; return false; };
+    auto wait_k = [&](int n) { return wait_bar(bar(B_KF + n % KST), (n / KST) & 1) || fail(); };
+    auto wait_v = [&](int n) { return wait_bar(bar(B_VF + n % VST), (n / VST) & 1) || fail(); };
+    auto issue_s = [&](int t, int slot) {   // S_t = Q_t K^T, K from the slot
+      const uint64_t da = dq + t * (S::TILE >> 4), db = dk + slot * (S::TILE >> 4);
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; kk++) {
+        const uint64_t step = ((kk >> 2) * ATOM_BYTES + (kk & 3) * 32) >> 4;   // stays inside the address field
+        umma_ss_if(on, tmem + t * KT, da + step, db + step, id_s, kk > 0 ? 1u : 0u);
+      }
+      commit_if(on, bar(B_SF + t));
+    };
+    auto pv = [&](int t, int slot, uint32_t accumulate, bool half) {   // O_t (+)= P_t V
+      if (!wait_bar(bar(B_PF + t), nl[t] & 1)) return fail();
+      nl[t]++;
+      tc::tc_fence_after();
+      const uint64_t dvs = dv + slot * (S::TILE >> 4);
+      const uint32_t pt = tmem + t * KT;
+      if (INT4 && half) {   // one fp16 term: keys 16 kk .. in columns 8 kk ..
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; kk++)
+          umma_ts_if(on, tmem + kTmemO + t * 128, pt + 8 * kk, dvs + (kk * 16 * 128 >> 4), id_h, kk > 0 ? 1u : accumulate);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; kk++) {
+          // keys 16 kk .. 16 kk + 15: chunk kk / 2, half kk % 2 -> hi at 32 c + 8 h, lo at 32 c + 16 + 8 h
+          const uint32_t col = 32 * (kk >> 1) + 8 * (kk & 1);
+          const uint64_t db = dvs + (kk * 16 * 128 >> 4);
+          umma_ts_if(on, tmem + kTmemO + t * 128, pt + col, db, id_o, kk > 0 ? 1u : accumulate);
+          umma_ts_if(on, tmem + kTmemO + t * 128, pt + col + 16, db, id_o, 1u);
+        }
+      }
+      commit_if(on, bar(B_PV + t));
+      return true;
+    };
+    auto uni = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    bool ok = true;
+    while (ok && !*abort_flag && next(sg)) {
+      const int nt = sg.n_tiles;
+      if (nt == 0) continue;
+      for (int t = 0; t < 2 && ok; t++) {
+        if (sg.lane_tiles(t) == 0) continue;
+        ok = wait_bar(bar(B_Q + t), nq[t] & 1) || fail();
+        nq[t]++;
+      }
+      tc::tc_fence_after();
+      const int nc = sg.u.ns + sg.u.nm - sg.t0;   // tiles of the pages; the block's follow
+      // Between a lane's P and its product stands nothing but the wait for P: a pair's other waits are done while the tensor
+      // core still has work.
+      if (!sg.keys) {
+        // a lane's next S follows its own product, so no lane waits for the other's softmax
+        if (ok && (ok = wait_k(n0))) {
+          tc::tc_fence_after();
+          const int k0 = uni(n0 % KST);
+          issue_s(0, k0);
+          issue_s(1, k0);
+          commit_if(on, bar(B_KE + k0));
+        }
+        if (nt == 1) {
+          commit_if(on, bar(B_QE + 0));
+          commit_if(on, bar(B_QE + 1));
+        }
+        if (ok) ok = wait_v(n0);
+        for (int i = 0; i < nt && ok && !*abort_flag; i++) {
+          const int n = n0 + i, vs = uni(n % VST), ks = uni((n + 1) % KST), acc = uni(i > 0);
+          const bool more = i + 1 < nt, half = i < nc;
+          if (!(ok = pv(0, vs, acc, half))) break;
+          if (more) {   // these copies started a whole tile ago
+            if (!(ok = wait_k(n + 1) && wait_v(n + 1))) break;
+            tc::tc_fence_after();
+            issue_s(0, ks);
+            if (i + 2 == nt) commit_if(on, bar(B_QE + 0));
+          }
+          if (!(ok = pv(1, vs, acc, half))) break;
+          commit_if(on, bar(B_VE + vs));
+          if (more) {
+            issue_s(1, ks);
+            commit_if(on, bar(B_KE + ks));
+            if (i + 2 == nt) commit_if(on, bar(B_QE + 1));
+          }
+        }
+      } else {
+        for (int i = 0; i < min(2, nt) && ok; i++) {
+          if (!(ok = wait_k(n0 + i))) break;
+          tc::tc_fence_after();
+          const int ks = uni((n0 + i) % KST);
+          issue_s(i, ks);
+          commit_if(on, bar(B_KE + ks));
+          if (i + 2 >= nt) commit_if(on, bar(B_QE + i));
+        }
+        for (int i = 0; i < nt && ok && !*abort_flag; i++) {
+          const int n = n0 + i, t = i & 1, vs = uni(n % VST), ks = uni((n + 2) % KST), acc = uni(i > 1);
+          if (!(ok = wait_v(n) && pv(t, vs, acc, i < nc))) break;
+          commit_if(on, bar(B_VE + vs));
+          if (i + 2 < nt) {
+            if (!(ok = wait_k(n + 2))) break;
+            tc::tc_fence_after();
+            issue_s(t, ks);
+            commit_if(on, bar(B_KE + ks));
+            if (i + 4 >= nt) commit_if(on, bar(B_QE + t));   // the lane's last S
+          }
+        }
+      }
+      n0 += nt;
+    }
+    // everything issued is done before tensor memory is freed (at once, unless a wait ran out)
+    commit_if(on, bar(B_END));
+    tc::mbar_wait(bar(B_END), 0);
+  } else if (warp >= Ro::SOFTMAX) {
+    // ---------------- softmax of lane t: thread = query row = TMEM lane ----------------
+    const int t = (warp - Ro::SOFTMAX) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t st = tmem + lane_off + t * KT, o_mine = tmem + lane_off + kTmemO + t * 128;
+    float* stat = reinterpret_cast<float*>(smem + S::STAT);   // [lane][row]: m, then l, of units whose keys the lanes share
+    int4 left = make_int4(-1, 0, 0, 0);
+    int met = 0;
+    auto meet = [&]() {   // with the other lane's warps; bounded, as every wait
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(B_X));
+      if (!wait_bar(bar(B_X), met++ & 1)) *abort_flag = 1;
+    };
+    int cnt = 0, other = 0, base = 0;   // tiles of this lane and of the other so far: phases of S, P and PV; of both: V slots
+    while (!*abort_flag && next(sg)) {
+      const int lrow0 = sg.row0 + (sg.keys ? 0 : t * p.rpt);
+      const bool warp_rows = quarter * 32 < p.rpt && lrow0 + quarter * 32 < nrows;   // else padding
+      const int i0 = sg.keys ? t : 0, step = sg.keys ? 2 : 1;
+      const int row_pos = sg.u.n - a.L + (lrow0 + r) / grp;
+      float m_ref = -INFINITY, l = 0.f;
+      bool first_tile = true;
+      for (int i = i0; i < sg.n_tiles && !*abort_flag; i += step, cnt++) {
+        const PagedTile tl = sg.tile(i);
+        const bool half = INT4 && tl.ctx;   // P as one fp16 term
+        if (!wait_bar(bar(B_SF + t), cnt & 1)) *abort_flag = 1;
+        tc::tc_fence_after();
+        if (warp_rows) {
+          float sv[KT];
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) tmem_ld32_nowait(st + c, sv + c);
+#pragma unroll
+          for (int c = 0; c < KT; c += 32) wait_ld32(sv + c);
+          if (!tile_full(sh, sg.u, tl)) {   // keys before `hi` that lie before `lo_end` or from `start` on
+            const int hi = sh.causal ? min(tl.valid, row_pos - tl.pos + 1) : tl.valid;
+            const int lo_end = sh.window ? sh.sinks - tl.pos : 0, start = sh.window ? row_pos - sh.window + 1 - tl.pos : 0;
+#pragma unroll
+            for (int e = 0; e < KT; e++)
+              if (e >= hi || (e >= lo_end && e < start)) sv[e] = -INFINITY;
+          }
+          float mq[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int e = 4; e + 7 < KT; e += 8)
+#pragma unroll
+            for (int u = 0; u < 4; u++) mq[u] = max3(mq[u], sv[e + u], sv[e + 4 + u]);
+#pragma unroll
+          for (int u = 0; u < 4; u++) mq[u] = fmaxf(mq[u], sv[KT - 4 + u]);
+          const float mx = max3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * sl2;
+          const bool need = mx > m_ref + kRescaleLog2;
+          if (__any_sync(0xffffffffu, need)) {   // tcgen05.ld/st are warp-wide: every lane takes part
+            const float m_new = need ? mx : m_ref;
+            const float cf = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
+            if (!first_tile) {
+              // O may only be rescaled once every product into it has finished
+              if (!wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
+              tc::tc_fence_after();
+#pragma unroll 1
+              for (int c0 = 0; c0 < HD; c0 += 16) {
+                float o[16];
+                tc::tmem_ld16(o_mine + c0, o);
+#pragma unroll
+                for (int e = 0; e < 16; e++) o[e] *= cf;
+                tmem_st16(o_mine + c0, o);
+              }
+            }
+            l *= cf;
+            m_ref = m_new;
+          }
+          // every score so far -inf: weight 0, not NaN.  fp16 weights are p 2^7, and V has 2^-7
+          const float nm = m_ref == -INFINITY ? 0.f : (half ? 7.f : 0.f) - m_ref;
+          const uint64_t sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
+          uint64_t lq[2] = {0ull, 0ull};
+          if (half) {
+#pragma unroll
+            for (int c0 = 0; c0 < KT; c0 += 16) {
+              uint32_t hi[8];
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float x0, x1;
+                unpack2(fma2(pack2(sv[c0 + e], sv[c0 + e + 1]), sl22, nm2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
+                hi[e / 2] = pack_f16(p0, p1);
+              }
+              tmem_st8(st + c0 / 2, hi);
+            }
+          } else {
+#pragma unroll
+            for (int c0 = 0; c0 < KT; c0 += 16) {
+              uint32_t hi[8], lo[8];
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float x0, x1;
+                unpack2(fma2(pack2(sv[c0 + e], sv[c0 + e + 1]), sl22, nm2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
+                split_trunc(p0, p1, hi[e / 2], lo[e / 2]);
+              }
+              const uint32_t pt = st + (c0 & ~31) + (c0 & 16) / 2;   // 32 keys: 16 columns of hi, 16 of lo
+              tmem_st8(pt, hi);
+              tmem_st8(pt + 16, lo);
+            }
+          }
+          float la, lb;
+          unpack2(add2(lq[0], lq[1]), la, lb);
+          l += half ? (la + lb) * 0.0078125f : la + lb;
+          tmem_wait_st();
+        }
+        first_tile = false;
+        int h_lo, h_hi;
+        hidden_from_all(sh, sg.u, tl, h_lo, h_hi);
+        if (!INT4 && (tl.valid < KT || h_hi > h_lo) && (sg.keys || t == 0)) {
+          // V rows past the last key, and those that no row sees -> 0 before the product: 0 x a value that is not finite would be
+          // NaN.  A pair's lane 1 comes after lane 0's product.  Row k: 128 bytes at k * 128 in each 64-dim atom (the swizzle
+          // permutes within a row).
+          const int n = base + i, s = n % VST;
+          if (!wait_bar(bar(B_VF + s), (n / VST) & 1)) *abort_flag = 1;
+          uint8_t* tile = smem + S::V + s * S::TILE;
+          const int rows = KT - tl.valid + h_hi - h_lo;
+          for (int c = r; c < rows * 8 * S::ATOMS; c += QR) {
+            const int z = c / (8 * S::ATOMS), k = z < h_hi - h_lo ? h_lo + z : tl.valid + z - (h_hi - h_lo);
+            const int h = (c >> 3) & (S::ATOMS - 1), q = c & 7;
+            *reinterpret_cast<uint4*>(tile + h * ATOM_BYTES + k * 128 + q * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B_PF + t));
+      }
+      other += sg.lane_tiles(1 - t);
+      base += sg.n_tiles;
+      if (!first_tile && !wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
+      float w_mine = 1.f, w_other = 0.f;
+      const bool shared_keys = sg.keys && sg.n_tiles > 1;
+      if (shared_keys) {   // the lanes' halves of a row: either lane puts together one half of the dims
+        stat[t * QR + r] = m_ref;
+        if (!wait_bar(bar(B_PV + 1 - t), (other - 1) & 1)) *abort_flag = 1;
+        meet();
+        const float m_other = stat[(1 - t) * QR + r];
+        meet();
+        stat[t * QR + r] = l;
+        meet();
+        const float l_other = stat[(1 - t) * QR + r];
+        const float mx = fmaxf(m_ref, m_other);
+        w_mine = m_ref == -INFINITY ? (l == l ? 0.f : 1.f) : ex2(m_ref - mx);   // a NaN sum counts
+        w_other = m_other == -INFINITY ? (l_other == l_other ? 0.f : 1.f) : ex2(m_other - mx);
+        l = l * w_mine + l_other * w_other;
+        m_ref = mx;
+      }
+      tc::tc_fence_after();
+      if (warp_rows && !(sg.keys && !shared_keys && t == 1)) {
+        const bool has = r < p.rpt && lrow0 + r < nrows, none = l == 0.f;
+        const int qi = lrow0 + r;
+        const size_t orow = has ? (size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp : 0;
+        const size_t prow = (size_t)sg.slot * sh.rows + (sg.keys ? r : t * p.rpt + r);
+        const float by = sg.whole ? (none ? 0.f : 1.f / l) : 1.f;
+        const int from = shared_keys ? t * (HD / 2) : 0, to = shared_keys ? from + HD / 2 : HD;
+        bool spoilt = false;
+#pragma unroll 1
+        for (int c0 = from; c0 < to; c0 += 32) {
+          float o[32];
+          if (sg.n_tiles > 0) {
+            tmem_ld32_nowait(o_mine + c0, o);
+            wait_ld32(o);
+          }
+          if (shared_keys) {
+            float q[32];
+            tmem_ld32_nowait(tmem + lane_off + kTmemO + (1 - t) * 128 + c0, q);
+            wait_ld32(q);
+#pragma unroll
+            for (int e = 0; e < 32; e++) o[e] = (w_mine == 0.f ? 0.f : o[e] * w_mine) + (w_other == 0.f ? 0.f : q[e] * w_other);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e++) o[e] = none ? 0.f : o[e] * by;
+          float x[32];   // in the order of the dims
+#pragma unroll
+          for (int e = 0; e < 32; e++) x[INT4 ? (e & ~7) + ((e & 7) >> 1) + 4 * (e & 1) : e] = o[e];
+#pragma unroll
+          for (int e = 0; e < 32; e++) spoilt |= !(fabsf(x[e]) < INFINITY);
+          if (!has) continue;
+          if (sg.whole) {
+            bf16* dst = a.out + orow * HD + c0;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[e + 2 * i + 1]), "f"(x[e + 2 * i]));
+              *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float* dst = a.o_part + prow * HD + c0;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+        }
+        // a row without numbers whose weights are numbers, under a mask (paged_repair.cuh)
+        unsigned bad = (sh.window || sh.causal) ? __ballot_sync(0xffffffffu, has && spoilt && fabsf(l) < INFINITY && !none) : 0;
+        if (bad) __syncwarp();   // behind the rows' own stores
+        while (bad) {
+          const int e = __ffs(bad) - 1;
+          bad &= bad - 1;
+          float acc[HD / 32];
+          repair_row<HD>(a, sh, sg.u, sg.t0, sg.t0 + sg.n_tiles, __shfl_sync(0xffffffffu, qi, e), __shfl_sync(0xffffffffu, m_ref, e), acc);
+          const float scale = __shfl_sync(0xffffffffu, by, e);
+          const size_t orow_e = __shfl_sync(0xffffffffu, (unsigned long long)orow, e), prow_e = __shfl_sync(0xffffffffu, (unsigned long long)prow, e);
+#pragma unroll
+          for (int j = 0; j < HD / 32; j++) {
+            const int d = lane + 32 * j;
+            if (d < from || d >= to) continue;
+            if (sg.whole) a.out[orow_e * HD + d] = __float2bfloat16_rn(acc[j] * scale);
+            else a.o_part[prow_e * HD + d] = acc[j];
+          }
+        }
+        if (has && (!shared_keys || t == 0)) {
+          if (!sg.whole) a.ml[prow] = make_float2(m_ref, l);
+          else if (a.lse) a.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+        }
+      }
+      if (sg.first && !sg.whole) left = make_int4(sg.u.b, sg.u.g, sg.u.rt, sg.last_run);
+      tc::tc_fence_before();   // O has been read: the next run's first product follows this lane's next P
+      if (shared_keys) meet();
+    }
+    if (warp == Ro::SOFTMAX && lane == 0) a.desc[blockIdx.x] = left;
+  }
+
+  __syncwarp();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int HD, bool INT4>
+cudaError_t attribute() {
+  return cudaFuncSetAttribute(paged_tc_kernel<HD, INT4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<HD>());
+}
+
+}  // namespace
+
+cudaError_t paged_tc_init_attributes() {
+  cudaError_t e = attribute<128, false>();
+  if (e == cudaSuccess) e = attribute<128, true>();
+  if (e == cudaSuccess) e = attribute<64, false>();
+  if (e == cudaSuccess) e = attribute<64, true>();
+  return e;
+}
+
+cudaError_t launch_paged_tc(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, cudaStream_t st) {
+  TcArgs p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  p.s = s;
+  p.s.kt = KT;
+  p.runs = pl.runs;
+  p.npt = QR / s.grp;
+  p.rpt = p.npt * s.grp;
+  const uint64_t h = a.pg.h;
+  if (a.pg.format == FPD_PAGE_BF16) {
+    const uint64_t qd[3] = {h, (uint64_t)a.nq, (uint64_t)a.batch * a.L}, qs[2] = {h * 2, h * 2 * a.nq};
+    const uint32_t qb[3] = {64u, (uint32_t)s.grp, (uint32_t)p.npt};
+    cudaError_t e = make_tmap_nd(&p.tm_q, a.q, 3, qd, qs, qb);
+    const uint64_t dims[3] = {h, (uint64_t)2 * a.pg.nkv * a.pg.page, (uint64_t)a.pg.n_pages}, strides[2] = {h * 2, a.pg.page_bytes};
+    const uint32_t box[3] = {64u, (uint32_t)std::min(KT, a.pg.page), 1u};
+    if (e == cudaSuccess) e = make_tmap_nd(&p.tm_pages, a.pg.base, 3, dims, strides, box);
+    if (a.lb) {
+      const uint64_t bd[2] = {h, (uint64_t)a.batch * a.pg.nkv * a.lb}, bs[1] = {h * 2};
+      const uint32_t bb[2] = {64u, (uint32_t)KT};
+      if (e == cudaSuccess) e = make_tmap_nd(&p.tm_kblk, a.kblk, 2, bd, bs, bb);
+      if (e == cudaSuccess) e = make_tmap_nd(&p.tm_vblk, a.vblk, 2, bd, bs, bb);
+    }
+    if (e != cudaSuccess) return e;
+    return h == 128 ? launch_k(paged_tc_kernel<128, false>, pl.grid, Roles<false>::THREADS, smem_bytes<128>(), st, p)
+                    : launch_k(paged_tc_kernel<64, false>, pl.grid, Roles<false>::THREADS, smem_bytes<64>(), st, p);
+  }
+  return h == 128 ? launch_k(paged_tc_kernel<128, true>, pl.grid, Roles<true>::THREADS, smem_bytes<128>(), st, p)
+                  : launch_k(paged_tc_kernel<64, true>, pl.grid, Roles<true>::THREADS, smem_bytes<64>(), st, p);
+}
+
+}  // namespace fpd

@@ -164,6 +164,9 @@ cudaError_t paged_stream_init_attributes();
 int paged_stream_warps();   // runs per SM
 cudaError_t launch_paged_stream(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, cudaStream_t st);
 
+cudaError_t paged_tc_init_attributes();
+cudaError_t launch_paged_tc(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, cudaStream_t st);
+
 #ifdef __CUDACC__
 struct DeviceLens {
   const int32_t* ctx_len;

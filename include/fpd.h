@@ -486,9 +486,8 @@ fpd_status fpd_paged_read(int batch, int total_rows, const fpd_paged_store* stor
  * so a window holds the row's own position and the window - 1 before it, and the first `sinks` positions stay visible behind it;
  * without causal the positions after the row are visible (the drafter's blocks).  Over those keys
  *   lse = log sum_t exp(q . k_t / sqrt(h)),   out = sum_t exp(q . k_t / sqrt(h) - lse) v_t
- * A row that sees no key (or scores of -inf alone) gives out 0 and lse -inf.  Keys that no row of a request sees, and slots from
- * ctx_len on, are not touched by the result whatever they hold; a key or value that is not finite reaches the rows that see it,
- * and may reach other rows of the same request and call where a window or causal hides it from them alone.
+ * A row that sees no key (or scores of -inf alone) gives out 0 and lse -inf.  What a row does not see does not touch it, finite or
+ * not (rows beside which a mask hides something that is not finite take the sum twice, slowly).
  * Sums are fp32; weights of bf16 pages enter the second product as two bf16 terms, those of 4-bit pages as fp16; out is rounded
  * once.  batch * block_len * n_q_heads <= 2^26, at most 128 query heads per kv head.  Lengths outside [0, table_width page_size]
  * are clamped (FPD_CHECK_BAD_CONTEXT).  Calls that share a workspace must not overlap on the GPU.

@@ -219,6 +219,43 @@ def test_what_is_not_finite_reaches_rows_that_see_it_and_no_other_request(pkg, n
     assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
 
 
+@pytest.mark.parametrize("form", ["bf16", "int4"])
+@pytest.mark.parametrize("mask", ["window_sinks", "sinks_causal", "causal", "appended_window"])
+@pytest.mark.parametrize("name", ["tokens_128", "text", "group_5", "primitive_64", "group_16"])
+def test_values_that_are_not_finite_stay_where_they_are_seen(pkg, name, mask, form):
+    """Infinite and NaN values behind a window's start and later in a causal block: rows that do not see them are as they were, rows
+    that do have no number in those dims."""
+    p = Problem(pkg, form, **CASES[name], **MASKS[mask])
+    window, sinks, causal = p.mask
+    nkv, h, L, grp = p.pool.nkv, p.pool.h, p.L, p.nq // p.pool.nkv
+    clean, wlse, vmax = p.want()
+    sees = torch.zeros(p.B, L, p.nq, h, dtype=torch.bool, device=DEV)
+    for b, n in enumerate(p.pool.lens):
+        total = n + (L if p.kb is not None else 0)
+        if total == 0:
+            continue
+        vis = torch.from_numpy(ref.visible(L, total, window, sinks, causal)).to(DEV)
+        for t in {total - 1, total - L // 2 - 1, total - L - window + 1, total - L - window + L // 2, n // 3} & set(range(total)):
+            value, dims = (math.nan, slice(0, h)) if t % 2 else (-math.inf, slice(3, h // 2))
+            if t < n:
+                if form == "int4":
+                    continue   # a stored 4-bit value is finite
+                v = p.pool.values[b][:1, t:t + 1].clone()
+                v[..., dims] = value
+                page = int(p.pool.table[b, t // p.pool.page])
+                p.pool.pages[-1, page, 1].view(nkv, p.pool.page, h)[0, t % p.pool.page] = v[0, 0].to(BF)
+            else:
+                p.vb[b, 0, t - n, dims] = value
+            sees[b, :, :grp, dims] |= vis[:, t, None, None]
+    out, lse = p.run()
+    sees = sees.view(p.B * L, p.nq, h)
+    assert not out[sees].isfinite().any()
+    tol = (2 * 2.0 ** -14 + (2.0 ** -11 if form == "int4" else 0)) * vmax[..., None] + 2.0 ** -8 * clean.abs()
+    assert bool(((out.double() - clean).abs() <= tol)[~sees].all())
+    live = wlse > -math.inf
+    assert bool(((lse.double() - wlse).abs()[live] <= 2.0 ** -14).all()) and pkg.fpd_device_status() == 0
+
+
 def test_scores_of_minus_infinity(pkg):
     """Infinite keys that give every visible key of a row the score -inf: weight 0, not NaN, beside keys that count."""
     p = Problem(pkg, "bf16", lens=[40, 70], L=2, nq=4, nkv=2, h=64, page=16, blk=False)
