@@ -81,9 +81,16 @@ __device__ __forceinline__ void split_trunc(float a, float b, uint32_t& hi, uint
   unpack2(rest, ra, rb);
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb), "f"(ra));
 }
+__device__ __forceinline__ void st8(void* dst, const uint32_t* v) {   // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {   // fp16 A and B, fp32 accumulator
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }   // bits 0 .. n - 1
 
 // A part of a unit as this kernel walks it.
 struct Seg {
@@ -247,18 +254,19 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       uint4 code[HD / 32];
       uint32_t scale[HD / 64];
     };
-    auto fetch = [&](const Seg& s, int e, Raw& w) {   // a row of a context tile; zeros where there is none
+    auto page_for = [&](const Seg& s, int e) {   // of this thread's row of item e; -1: none
+      if (e >= 8 * s.n_tiles) return -1;
+      const PagedTile t = s.tile(e >> 3);
+      const int r = (e & 3) * 32 + lane;
+      return t.ctx && r < t.valid ? page_of(a.pg, s.u.b, t.k0 + r) : -1;
+    };
+    auto fetch = [&](const Seg& s, int e, int id, Raw& w) {   // a row of a context tile; zeros where there is none
 #pragma unroll
       for (int j = 0; j < HD / 32; j++) w.code[j] = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < HD / 64; j++) w.scale[j] = 0;
-      if (e >= 8 * s.n_tiles) return;
-      const PagedTile t = s.tile(e >> 3);
-      const int r = (e & 3) * 32 + lane;
-      if (!t.ctx || r >= t.valid) return;
-      const int id = page_of(a.pg, s.u.b, t.k0 + r);
       if (id < 0) return;
-      const int in = (t.k0 + r) & (a.pg.page - 1);
+      const int in = (s.tile(e >> 3).k0 + (e & 3) * 32 + lane) & (a.pg.page - 1);
       const uint8_t* slab = slab_of(a.pg, id, (e >> 2) & 1, s.u.g);
       const uint4* code = reinterpret_cast<const uint4*>(slab + in * (HD / 2));
       const uint32_t* scale = reinterpret_cast<const uint32_t*>(slab + a.pg.page * (HD / 2) + in * (HD / 16));
@@ -311,8 +319,14 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     };
     while (ok && !*abort_flag && next(sg)) {
       Raw raw[3];
+      int id[3];   // pages of the items behind those whose codes are on their way
 #pragma unroll
-      for (int d = 0; d < 3; d++) fetch(sg, w3 + 3 * d, raw[d]);
+      for (int d = 0; d < 3; d++) id[d] = page_for(sg, w3 + 3 * d);
+#pragma unroll
+      for (int d = 0; d < 3; d++) {
+        fetch(sg, w3 + 3 * d, id[d], raw[d]);
+        id[d] = page_for(sg, w3 + 3 * d + 9);
+      }
       const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
       bool q_done = false;
       for (int e0 = w3; e0 < 8 * sg.n_tiles && ok; e0 += 9) {
@@ -343,7 +357,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           if (t.ctx) put_codes(tile, r, raw[d], is_v);
           else put_bf16(tile, r, r < t.valid ? (is_v ? a.vblk : a.kblk) + (blk + t.k0 + r) * HD : nullptr);
           done((is_v ? B_VF : B_KF) + s);
-          fetch(sg, e + 9, raw[d]);
+          fetch(sg, e + 9, id[d], raw[d]);
+          id[d] = page_for(sg, e + 18);
         }
       }
       n += sg.n_tiles;
@@ -485,7 +500,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       const int lrow0 = sg.row0 + (sg.keys ? 0 : t * p.rpt);
       const bool warp_rows = quarter * 32 < p.rpt && lrow0 + quarter * 32 < nrows;   // else padding
       const int i0 = sg.keys ? t : 0, step = sg.keys ? 2 : 1;
-      const int row_pos = sg.u.n - a.L + (lrow0 + r) / grp;
+      const int row_pos = sg.u.n - a.L + sh.by_grp.div(lrow0 + r);
       float m_ref = -INFINITY, l = 0.f;
       bool first_tile = true;
       for (int i = i0; i < sg.n_tiles && !*abort_flag; i += step, cnt++) {
@@ -499,12 +514,15 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           for (int c = 0; c < KT; c += 32) tmem_ld32_nowait(st + c, sv + c);
 #pragma unroll
           for (int c = 0; c < KT; c += 32) wait_ld32(sv + c);
-          if (!tile_full(sh, sg.u, tl)) {   // keys before `hi` that lie before `lo_end` or from `start` on
+          if (!tile_full(sh, sg.u, tl)) {   // keys before `hi` that lie before `lo_end` or from `start` on, as bits
             const int hi = sh.causal ? min(tl.valid, row_pos - tl.pos + 1) : tl.valid;
-            const int lo_end = sh.window ? sh.sinks - tl.pos : 0, start = sh.window ? row_pos - sh.window + 1 - tl.pos : 0;
+            const int lo_end = sh.window ? sh.sinks - tl.pos : KT, start = sh.window ? row_pos - sh.window + 1 - tl.pos : 0;
 #pragma unroll
-            for (int e = 0; e < KT; e++)
-              if (e >= hi || (e >= lo_end && e < start)) sv[e] = -INFINITY;
+            for (int w = 0; w < KT / 32; w++) {
+              const uint32_t see = below(hi - 32 * w) & (below(lo_end - 32 * w) | ~below(start - 32 * w));
+#pragma unroll
+              for (int e = 0; e < 32; e++) sv[32 * w + e] = (see >> e) & 1 ? sv[32 * w + e] : -INFINITY;
+            }
           }
           float mq[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
@@ -650,16 +668,16 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           if (sg.whole) {
             bf16* dst = a.out + orow * HD + c0;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[e + 2 * i + 1]), "f"(x[e + 2 * i]));
-              *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 8; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[e + 2 * i + 1]), "f"(x[e + 2 * i]));
+              st8(dst + e, w);
             }
           } else {
             float* dst = a.o_part + prow * HD + c0;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            for (int e = 0; e < 32; e += 8) st8(dst + e, reinterpret_cast<const uint32_t*>(x + e));
           }
         }
         // a row without numbers whose weights are numbers, under a mask (paged_repair.cuh)
@@ -721,7 +739,8 @@ cudaError_t launch_paged_tc(const PagedAttn& a, const PagedShape& s, const Paged
   memset(&p, 0, sizeof(p));
   p.a = a;
   p.s = s;
-  p.s.kt = KT;
+  p.s.kt_shift = 7;
+  static_assert(KT == 1 << 7, "keys of a tile");
   p.runs = pl.runs;
   p.npt = QR / s.grp;
   p.rpt = p.npt * s.grp;

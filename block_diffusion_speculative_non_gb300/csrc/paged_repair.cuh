@@ -52,7 +52,7 @@ struct KeyRow {
 // acc[j], dim lane + 32 j: sum over the keys of tiles [t0, t1) that the row sees of 2^(s log2(e) / sqrt(h) - m) v, by one warp.  qi: the
 // row among the unit's request and kv head; m: the row's maximum in base 2.
 template <int H>
-__device__ __noinline__ void repair_row(const PagedAttn& a, const PagedShape& s, const PagedUnit& u, int t0, int t1, int qi, float m,
+__device__ __noinline__ void repair_row(const PagedAttn& a, const PagedShape& s, const PagedUnit u, int t0, int t1, int qi, float m,
                                         float (&acc)[H / 32]) {
   const int lane = threadIdx.x & 31, row = u.n - a.L + qi / s.grp;
   const bf16* q = a.q + ((size_t)(u.b * a.L + qi / s.grp) * a.nq + u.g * s.grp + qi % s.grp) * H;
@@ -60,7 +60,7 @@ __device__ __noinline__ void repair_row(const PagedAttn& a, const PagedShape& s,
 #pragma unroll
   for (int j = 0; j < H / 32; j++) acc[j] = 0.f;
   for (int i = t0; i < t1; i++) {
-    const PagedTile t = tile_at(u, s.kt, i);
+    const PagedTile t = tile_at(u, s.kt(), i);
     for (int k0 = 0; k0 < t.valid; k0 += 32) {   // a key per lane, then the keys' values one after the other
       const int k = k0 + lane;
       const bool see = k < t.valid && row_sees(s, row, t.pos + k);

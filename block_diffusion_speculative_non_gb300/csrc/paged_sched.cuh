@@ -3,8 +3,8 @@
 // A unit is a row tile of one request and kv head: rows (position, head) rt R .. of the L positions' heads that share the kv
 // head.  It has the key tiles that hold a key some row of it sees: those of the first `sinks` positions, those from the first
 // row's window to the end, then the block's keys.  The lengths are known on the device alone, and requests differ in them, so
-// every CTA adds them up and takes an even run of all units' tiles, [c total / G, (c + 1) total / G): whatever the lengths, the
-// SMs finish together.  A unit inside one run is finished there; of a unit that runs share, each leaves a partial: the run
+// every CTA adds them up and takes an even run of all units' tiles (the first runs one tile more than the others): whatever the
+// lengths, the SMs finish together.  A unit inside one run is finished there; of a unit that runs share, each leaves a partial: the run
 // that starts it in slot 2 c + 1, the ones that go on with it in slot 2 c.  A unit without a key counts as one empty tile, so
 // that its rows are written too.
 #pragma once
@@ -31,31 +31,67 @@ struct PagedTile {
   int k0, valid, pos;   // first slot or block key, keys, position of the first
 };
 
-// What decides a unit's tiles.
-struct PagedShape {
-  int L, lb, grp, nkv, rows, tiles, window, sinks, causal, kt;   // rows of a row tile, row tiles of a request and kv head
-};
-
 __host__ __device__ inline int imin(int a, int b) { return a < b ? a : b; }
 __host__ __device__ inline int imax(int a, int b) { return a > b ? a : b; }
 
+// Division of 0 <= x < 2^31 by a number known on the host (Granlund and Montgomery's multiply, add and shift): the walk divides by
+// the group several times a unit, and the compiler's division by a variable is some 30 instructions.
+struct GroupDiv {
+  uint32_t d, m, s1, s2;
+  void set(uint32_t n) {
+    d = n;
+    uint32_t l = 0;
+    while ((1ull << l) < n) l++;
+    m = (uint32_t)(((1ull << 32) * ((1ull << l) - n)) / n + 1);
+    s1 = l > 0 ? 1 : 0;
+    s2 = l > 0 ? l - 1 : 0;
+  }
+  __host__ __device__ int div(int x) const {
+#ifdef __CUDA_ARCH__
+    const uint32_t t = __umulhi(m, (uint32_t)x);
+#else
+    const uint32_t t = (uint32_t)(((uint64_t)m * (uint32_t)x) >> 32);
+#endif
+    return (int)((t + (((uint32_t)x - t) >> s1)) >> s2);
+  }
+};
+
+// What decides a unit's tiles.
+struct PagedShape {
+  int L, lb, grp, nkv, rows, tiles, window, sinks, causal;   // rows of a row tile, row tiles of a request and kv head
+  int kt_shift;                                              // tiles of 2^kt_shift keys
+  GroupDiv by_grp;
+  __host__ __device__ int kt() const { return 1 << kt_shift; }
+};
+inline PagedShape paged_shape(int L, int lb, int grp, int nkv, int rows, int window, int sinks, int causal, int kt) {
+  PagedShape s{L, lb, grp, nkv, rows, ceil_div(L * grp, rows), window, sinks, causal, 0, {}};
+  while (s.kt() < kt) s.kt_shift++;
+  s.by_grp.set(grp);
+  return s;
+}
+// 64-bit quotients, by the 32-bit division where it holds them (several times shorter)
+__host__ __device__ inline long long quotient(long long x, long long y) {
+  return (((unsigned long long)x | (unsigned long long)y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 __host__ __device__ inline void unit_tiles(const PagedShape& s, int T, int rt, PagedUnit& u) {
+  const int sh = s.kt_shift, up = s.kt() - 1;
   u.rt = rt;
   u.T = T;
   u.n = T + s.lb;
   const int last = imin(s.L * s.grp, (rt + 1) * s.rows) - 1;
-  u.p0 = u.n - s.L + rt * s.rows / s.grp;
-  u.p1 = u.n - s.L + last / s.grp;
+  u.p0 = u.n - s.L + s.by_grp.div(rt * s.rows);
+  u.p1 = u.n - s.L + s.by_grp.div(last);
   const int end = s.causal ? imin(u.n, imax(0, u.p1 + 1)) : u.n;
   const int start = s.window ? imin(end, imax(0, u.p0 - s.window + 1)) : 0;
   const int s_end = imin(s.sinks, start);
   u.ce = imin(end, T);
   u.be = imax(0, end - T);
-  u.ns = (imin(s_end, u.ce) + s.kt - 1) / s.kt;
-  u.cfirst = imax(start / s.kt, u.ns);
-  u.nm = start < u.ce ? imax(0, (u.ce + s.kt - 1) / s.kt - u.cfirst) : 0;
-  u.bfirst = s_end > T ? 0 : imax(0, start - T) / s.kt;
-  u.nb = imax(0, (u.be + s.kt - 1) / s.kt - u.bfirst);
+  u.ns = (imin(s_end, u.ce) + up) >> sh;
+  u.cfirst = imax(start >> sh, u.ns);
+  u.nm = start < u.ce ? imax(0, ((u.ce + up) >> sh) - u.cfirst) : 0;
+  u.bfirst = s_end > T ? 0 : imax(0, start - T) >> sh;
+  u.nb = imax(0, ((u.be + up) >> sh) - u.bfirst);
 }
 
 __host__ __device__ inline PagedTile tile_at(const PagedUnit& u, int kt, int i) {
@@ -69,8 +105,8 @@ __host__ __device__ inline PagedTile tile_at(const PagedUnit& u, int kt, int i) 
 }
 // Whether every row of the unit sees every key of the tile.
 __host__ __device__ inline bool tile_full(const PagedShape& s, const PagedUnit& u, const PagedTile& t) {
-  const int last = t.pos + s.kt - 1;
-  return t.valid == s.kt && (!s.window || last < s.sinks || u.p1 - t.pos < s.window) && (!s.causal || last <= u.p0);
+  const int last = t.pos + s.kt() - 1;
+  return t.valid == s.kt() && (!s.window || last < s.sinks || u.p1 - t.pos < s.window) && (!s.causal || last <= u.p0);
 }
 
 // Tiles of a request in one kv head.
@@ -94,13 +130,15 @@ struct PagedWalk {
   const PagedShape& s;
   Lens lens;
   int c, G, batch, b, g, rt, off;
-  long long x, x_end, total;
+  long long x, x_end, total, each_run, longer;   // runs of each_run tiles, the first `longer` of them one more
 
   // `sums` holds running sums of the entries' tiles (kSchedEntries + 1 of them), complete when the walk is made
   __host__ __device__ PagedWalk(const PagedShape& s_, Lens lens_, const long long* sums, int batch_, int runs, int c_)
       : s(s_), lens(lens_), c(c_), batch(batch_) {
     total = sums[kSchedEntries];
     G = total < runs ? (int)total : runs;
+    each_run = quotient(total, G);
+    longer = total - each_run * G;
     x = c < G ? run_start(c) : total;
     x_end = c < G ? run_start(c + 1) : total;
     if (x >= x_end) return;
@@ -111,18 +149,23 @@ struct PagedWalk {
     }
     const int each = (batch + kSchedEntries - 1) / kSchedEntries;
     long long rest = x - sums[lo], per;
-    for (b = lo * each;; b++) {
-      per = request_tiles(s, lens(b));
-      if (rest < per * s.nkv || b + 1 >= batch) break;
-      rest -= per * s.nkv;
+    b = lo * each;
+    if (each == 1) {
+      per = quotient(sums[lo + 1] - sums[lo], s.nkv);
+    } else {
+      for (;; b++) {
+        per = request_tiles(s, lens(b));
+        if (rest < per * s.nkv || b + 1 >= batch) break;
+        rest -= per * s.nkv;
+      }
     }
     // lengths that another stream changes meanwhile give a wrong result, never a unit that is not there
-    g = (int)imin((int)(rest / per), s.nkv - 1);
+    g = imin((int)quotient(rest, per), s.nkv - 1);
     rest -= g * per;
     PagedUnit u;
     if (!s.window && !s.causal) {
       unit_tiles(s, lens(b), 0, u);
-      rt = imin((int)(rest / u.len()), s.tiles - 1);
+      rt = imin((int)quotient(rest, u.len()), s.tiles - 1);
       rest -= (long long)rt * u.len();
     } else {
       for (rt = 0; rt + 1 < s.tiles; rt++) {
@@ -133,8 +176,11 @@ struct PagedWalk {
     }
     off = (int)rest;
   }
-  __host__ __device__ long long run_start(int i) const { return (long long)i * total / G; }
-  __host__ __device__ int run_of(long long t) const { return (int)(((t + 1) * G - 1) / total); }
+  __host__ __device__ long long run_start(int i) const { return i * each_run + (i < longer ? i : longer); }
+  __host__ __device__ int run_of(long long t) const {
+    const long long before = longer * (each_run + 1);   // tiles of the longer runs
+    return (int)(t < before ? quotient(t, each_run + 1) : longer + quotient(t - before, each_run));
+  }
 
   // The next part [t0, t1) of a unit's tiles; last_run: the run that ends the unit.
   __host__ __device__ bool next(PagedUnit& u, int& t0, int& t1, int& last_run) {
