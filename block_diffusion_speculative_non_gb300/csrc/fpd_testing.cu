@@ -328,7 +328,10 @@ extern "C" int fpd_test_paged_walk(int batch, int L, int block_keys, int group, 
     sums[e + 1] = sums[e];
     for (int b = e * each; b < std::min(batch, (e + 1) * each); b++) sums[e + 1] += nkv * request_tiles(s, counted[b]);
   }
-  PagedWalk<Lens> walk(s, Lens{walked}, sums, batch, runs, run);
+  PagedWalk<Lens> walk(s, Lens{walked}, batch, sums[kSchedEntries], runs, run);
+  int e = 0;
+  while (e + 1 < kSchedEntries && sums[e + 1] <= walk.x) e++;
+  if (walk.x < walk.x_end) walk.locate(e, sums[e], sums[e + 1] - sums[e]);
   PagedUnit u;
   int n = 0, t0, t1, last;
   for (; walk.next(u, t0, t1, last); n++) {

@@ -106,12 +106,11 @@ __device__ __forceinline__ void tile_math(uint32_t ks, uint32_t vs, const uint32
   }
 }
 
-// Shared memory: Q of 16 WM rows, two K and V tiles, the running sums.  The keys' shares of O meet in the K and V tiles.
+// Shared memory: Q of 16 WM rows, two K and V tiles.  The keys' shares of O meet in the K and V tiles.
 template <int H, int WM>
 struct Mem {
   bf16 q[WM * 16 * H];
   bf16 kv[2][2][KT * H];
-  long long sums[kSchedEntries + 1];
 };
 
 template <int H, int WM, bool INT4>
@@ -125,14 +124,7 @@ __global__ void __launch_bounds__(kThreads) paged_mma_kernel(const __grid_consta
   const int nrows = a.L * sh.grp, cap = a.pg.cap();
   pdl_wait();
   pdl_trigger();
-  const DeviceLens lens{a.ctx_len, cap};
-  sched_sums(sh, lens, a.batch, sm.sums, tid);
-  __syncthreads();
-  const long long before = sched_before(sm.sums, tid);
-  __syncthreads();
-  sm.sums[tid + 1] += before;
-  __syncthreads();
-  PagedWalk<DeviceLens> walk(sh, lens, sm.sums, a.batch, p.runs, blockIdx.x);
+  PagedWalk<DeviceLens> walk = make_walk(sh, DeviceLens{a.ctx_len, cap}, a.batch, p.runs, blockIdx.x);
   const float sl2 = rsqrtf((float)H) * 1.4426950408889634f;
   const uint32_t q_s = smem_addr(sm.q);
   int4 left = make_int4(-1, 0, 0, 0);   // the unit that this run leaves unfinished
@@ -308,62 +300,82 @@ __global__ void __launch_bounds__(kThreads) paged_mma_kernel(const __grid_consta
   if (tid == 0) a.desc[blockIdx.x] = left;
 }
 
-// The units that runs share: CTA (c, y) puts together rows 4 y .. of the unit that run c starts and leaves unfinished, from slots
-// 2 c + 1, 2 (c + 1), .. in that order; one warp a row.
-template <int H>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ Args p) {
-  constexpr int DPL = H / 32;
+// The units that runs share: CTA (c, y) puts together rows of the unit that run c starts and leaves unfinished, from slots
+// 2 c + 1, 2 (c + 1), .. in that order; a warp has RPW rows.  The partials are requested with their weights, not behind them.
+constexpr int kMergeWarps = 4;
+template <int H, int RPW>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ Args p) {
+  constexpr int DPL = H / 32, U = 8 / RPW;
   pdl_wait();
   pdl_trigger();
   const PagedAttn& a = p.a;
-  const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5), R = p.s.rows, grp = p.s.grp;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, R = p.s.rows, grp = p.s.grp;
   const int4 d = a.desc[c];
-  const int qi = d.z * R + r;
-  if (d.x < 0 || r >= R || qi >= a.L * grp) return;
+  const int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * RPW, rows = min(R, a.L * grp - d.z * R);
+  if (d.x < 0 || r0 >= rows) return;
   const int pieces = d.w - c + 1;
-  auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R + r; };
-  float mx = -INFINITY;
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
-    const float2 v = i0 + lane < pieces ? __ldcg(a.ml + slot(i0 + lane)) : make_float2(-INFINITY, 0.f);
-    mx = fmaxf(mx, warp_max(v.y == 0.f ? -INFINITY : v.x));
+  auto slot = [&](int i, int r) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R + min(r, rows - 1); };
+  float mx[RPW], den[RPW], num[RPW][DPL];
+#pragma unroll
+  for (int q = 0; q < RPW; q++) {
+    mx[q] = -INFINITY;
+    den[q] = 0.f;
+#pragma unroll
+    for (int e = 0; e < DPL; e++) num[q][e] = 0.f;
   }
-  float den = 0.f, num[DPL];
+  for (int i0 = 0; i0 < pieces; i0 += U) {   // the softmax of the partials, U at a time
+    float t[RPW][U][DPL];
+    float2 v[RPW][U];
 #pragma unroll
-  for (int e = 0; e < DPL; e++) num[e] = 0.f;
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
-    const float2 v = i0 + lane < pieces ? __ldcg(a.ml + slot(i0 + lane)) : make_float2(-INFINITY, 0.f);
-    const float wl = v.y == 0.f ? 0.f : exp2f(v.x - mx);
-    den += warp_sum(v.y == 0.f ? 0.f : v.y * wl);
-    for (int u0 = 0; u0 < min(32, pieces - i0); u0 += 8) {
-      float t[8][DPL], wgt[8];
+    for (int q = 0; q < RPW; q++)
 #pragma unroll
-      for (int u = 0; u < 8; u++) {
-        wgt[u] = __shfl_sync(0xffffffffu, wl, u0 + u);
-#pragma unroll
-        for (int e = 0; e < DPL; e++) t[u][e] = 0.f;
-        if (wgt[u] != 0.f) {
-          const float* op = a.o_part + slot(i0 + u0 + u) * H + lane * DPL;
-#pragma unroll
-          for (int e = 0; e < DPL; e += 2) {
-            const float2 f = __ldcg(reinterpret_cast<const float2*>(op + e));
-            t[u][e] = f.x;
-            t[u][e + 1] = f.y;
-          }
+      for (int u = 0; u < U; u++) {
+        const size_t at = slot(min(i0 + u, pieces - 1), r0 + q);
+        v[q][u] = __ldcg(a.ml + at);
+        const float* op = a.o_part + at * H + lane * DPL;
+        if constexpr (DPL == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(op));
+          t[q][u][0] = f.x, t[q][u][1] = f.y, t[q][u][2] = f.z, t[q][u][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(op));
+          t[q][u][0] = f.x, t[q][u][1] = f.y;
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; u++)
+    for (int q = 0; q < RPW; q++) {
+      float m = mx[q];
 #pragma unroll
-        for (int e = 0; e < DPL; e++) num[e] += wgt[u] != 0.f ? t[u][e] * wgt[u] : 0.f;
+      for (int u = 0; u < U; u++) {
+        if (i0 + u >= pieces) v[q][u].y = 0.f;   // l = 0: no weight, whatever the rest holds
+        if (v[q][u].y != 0.f) m = fmaxf(m, v[q][u].x);
+      }
+      const float back = den[q] == 0.f ? 0.f : ex2_approx(mx[q] - m);
+      mx[q] = m;
+      den[q] *= back;
+#pragma unroll
+      for (int e = 0; e < DPL; e++) num[q][e] = back == 0.f ? 0.f : num[q][e] * back;
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const float w = v[q][u].y == 0.f ? 0.f : ex2_approx(v[q][u].x - m);
+        den[q] += v[q][u].y == 0.f ? 0.f : v[q][u].y * w;
+#pragma unroll
+        for (int e = 0; e < DPL; e++) num[q][e] += w != 0.f ? t[q][u][e] * w : 0.f;
+      }
     }
   }
-  const bool none = den == 0.f;
-  const size_t row = (size_t)(d.x * a.L + qi / grp) * a.nq + d.y * grp + qi % grp;
-  bf16* dst = a.out + row * H + lane * DPL;
 #pragma unroll
-  for (int e = 0; e < DPL; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(none ? 0.f : num[e] / den, none ? 0.f : num[e + 1] / den);
-  if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
+  for (int q = 0; q < RPW; q++) {
+    if (r0 + q >= rows) break;
+    const int qi = d.z * R + r0 + q, j = p.s.by_grp.div(qi);
+    const bool none = den[q] == 0.f;
+    const float by = 1.f / den[q];
+    const size_t row = (size_t)(d.x * a.L + j) * a.nq + d.y * grp + qi - j * grp;
+    bf16* dst = a.out + row * H + lane * DPL;
+#pragma unroll
+    for (int e = 0; e < DPL; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(none ? 0.f : num[q][e] * by, none ? 0.f : num[q][e + 1] * by);
+    if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (mx[q] + log2f(den[q])) * 0.69314718055994531f;
+  }
 }
 
 template <int H, bool INT4>
@@ -398,7 +410,9 @@ cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
     e = launch_k(k, pl.runs, kThreads, mma_smem<H>(pl.rows), st, p);
   }
   if (e != cudaSuccess) return e;
-  return launch_k(paged_merge_kernel<H>, dim3(pl.runs, ceil_div(std::min(pl.rows, p.a.L * p.s.grp), 4)), 128, 0, st, p);
+  const int rows = std::min(pl.rows, p.a.L * p.s.grp);
+  if (pl.kernel == kPagedStream) return launch_k(paged_merge_kernel<H, 1>, dim3(pl.runs, ceil_div(rows, kMergeWarps)), kMergeWarps * 32, 0, st, p);
+  return launch_k(paged_merge_kernel<H, 2>, dim3(pl.runs, ceil_div(rows, 2 * kMergeWarps)), kMergeWarps * 32, 0, st, p);
 }
 
 }  // namespace

@@ -123,8 +123,8 @@ struct Ring {
   static constexpr int HALF = INT4 ? KT * (H / 2 + H / 16) : 16 * H * 2;   // bytes of a slot's K or V: 64 or 16 keys
   static constexpr int SLOT = 2 * HALF;
   static constexpr int WARPS = 8, SLOTS = 3;
-  static constexpr int BARS = 1024 + WARPS * SLOTS * SLOT, SUMS = BARS + WARPS * SLOTS * 8;
-  static constexpr size_t BYTES = SUMS + (kSchedEntries + 1) * 8;
+  static constexpr int BARS = WARPS * SLOTS * SLOT;
+  static constexpr size_t BYTES = 1024 + BARS + WARPS * SLOTS * 8;
 };
 
 template <int H, int NT, bool INT4>
@@ -138,8 +138,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
   const int g = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * ST * Rg::SLOT;
   const uint32_t ring_s = tc::smem_u32(ring);
-  const uint32_t bars = tc::smem_u32(smem + (Rg::BARS - 1024)) + warp * ST * 8;
-  long long* sums = reinterpret_cast<long long*>(smem + (Rg::SUMS - 1024));
+  const uint32_t bars = tc::smem_u32(smem + Rg::BARS) + warp * ST * 8;
   const PagedAttn& a = p.a;
   const PagedShape& sh = p.s;
   const int nrows = a.L * sh.grp;
@@ -147,18 +146,12 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
     for (int i = 0; i < ST; i++) tc::mbar_init(bars + 8 * i, 1);
     tc::fence_barrier_init();
   }
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
-  const DeviceLens lens{a.ctx_len, a.pg.cap()};
-  sched_sums(sh, lens, a.batch, sums, tid);
-  __syncthreads();
-  const long long before = tid < kSchedEntries ? sched_before(sums, tid) : 0;
-  __syncthreads();
-  if (tid < kSchedEntries) sums[tid + 1] += before;
-  __syncthreads();
   const int run = blockIdx.x + warp * gridDim.x;
   if (run >= p.runs) return;
-  PagedWalk<DeviceLens> walk(sh, lens, sums, a.batch, p.runs, run);
+  PagedWalk<DeviceLens> walk = make_walk(sh, DeviceLens{a.ctx_len, a.pg.cap()}, a.batch, p.runs, run);
   const float sl2 = rsqrtf((float)H) * 1.4426950408889634f;
   int4 left = make_int4(-1, 0, 0, 0);
   int cnt = 0;      // slots filled and emptied so far: place in the ring and phase

@@ -42,9 +42,7 @@ struct TcArgs {
 template <int HD>
 struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64;
-  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, STAT = V + VST * TILE, SUMS = STAT,   // the running sums are read before the statistics are written
-                       BAR = STAT + (kSchedEntries + 1) * 8;
-  static_assert(2 * QR * 4 <= (kSchedEntries + 1) * 8, "the lanes' statistics");
+  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, STAT = V + VST * TILE, BAR = STAT + 2 * QR * 4;
 };
 enum {
   B_Q = 0,
@@ -66,11 +64,11 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<128>() <= 232448, "tile set exceeds the shared memory of one CTA");
 
-// bf16: 11 warps, 0 and 2 TMA producers of K and Q, and of V, 1 the products, 3.. softmax.  4 bits: 12 warps, 0, 2 and 3 decode, 4..
-// softmax.
+// bf16: 11 warps, 0 and 2 TMA producers of K and Q, and of V, 1 the products, 3.. softmax.  4 bits: 16 warps, 0 and
+// 2..7 decode, 8.. softmax, which takes the scores in two halves (128 registers a thread).
 template <bool INT4>
 struct Roles {
-  static constexpr int THREADS = INT4 ? 384 : 352, SOFTMAX = INT4 ? 4 : 3;
+  static constexpr int THREADS = INT4 ? 512 : 352, SOFTMAX = INT4 ? 8 : 3;
 };
 
 __device__ __forceinline__ void split_trunc(float a, float b, uint32_t& hi, uint32_t& lo) {   // a, b >= 0: hi + lo to 2^-16
@@ -110,7 +108,6 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_N);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  long long* sums = reinterpret_cast<long long*>(smem + S::SUMS);
   const uint32_t bar0 = tc::smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * i; };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -154,19 +151,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   }
   pdl_wait();
   pdl_trigger();
-  const DeviceLens lens{a.ctx_len, a.pg.cap()};
-  sched_sums(sh, lens, a.batch, sums, tid);
+  PagedWalk<DeviceLens> walk = make_walk(sh, DeviceLens{a.ctx_len, a.pg.cap()}, a.batch, p.runs, blockIdx.x);
   __syncwarp();   // a CTA barrier counts a whole warp: single-lane roles reconverge before every one
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const long long before = tid < kSchedEntries ? sched_before(sums, tid) : 0;
-  __syncthreads();
-  if (tid < kSchedEntries) sums[tid + 1] += before;
-  __syncthreads();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  PagedWalk<DeviceLens> walk(sh, lens, sums, a.batch, p.runs, blockIdx.x);
   auto next = [&](Seg& s) {
     int t1;
     if (!walk.next(s.u, s.t0, t1, s.last_run)) return false;
@@ -179,7 +170,6 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     return true;
   };
   Seg sg;
-  __syncthreads();
 
   if (!INT4 && (warp == 0 || warp == 2)) {
     // ---------------- TMA producers: K and Q (warp 0), V (warp 2); lane i copies a tile's page i ----------------
@@ -245,10 +235,11 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     }
   } else if (INT4 && warp < Ro::SOFTMAX && warp != 1) {
     // ---------------- decoding warps ----------------
-    // A tile is eight items, 32 rows of K or of V each; the three warps take turns at them, a thread a row, and have requested the
-    // codes of their next three.
-    const int w3 = warp == 0 ? 0 : warp - 1;
-    uint8_t *qs = smem + S::Q, *ks = smem + S::K, *vs = smem + S::V;
+    // A tile is eight items, 32 rows of K or of V each; the warps take turns at them, a thread a row, and have requested the codes
+    // of their next two.
+    constexpr int NW = 7, DEEP = 2;
+    const int wd = warp == 0 ? 0 : warp - 1;
+    const uint32_t qs = tc::smem_u32(smem + S::Q), ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V);
     int n = 0, nq[2] = {0, 0};
     struct Raw {
       uint4 code[HD / 32];
@@ -276,18 +267,21 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       for (int j = 0; j < HD / 64; j++) w.scale[j] = __ldg(scale + j);
     };
     // chunk of 8 dims ch of row r in a tile of 64-dim atoms
-    auto put = [&](uint8_t* tile, int r, int ch, uint4 v) {
-      *reinterpret_cast<uint4*>(tile + (ch >> 3) * ATOM_BYTES + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+    auto put = [&](uint32_t row, int ch, uint4 v) {
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"((row ^ ((ch & 7) << 4)) + (ch >> 3) * ATOM_BYTES), "r"(v.x), "r"(v.y),
+                   "r"(v.z), "r"(v.w)
+                   : "memory");
     };
-    auto put_bf16 = [&](uint8_t* tile, int r, const bf16* row) {   // a bf16 row (null: zeros) in the order of the decoded ones
+    auto row_at = [&](uint32_t tile, int r) { return tile + r * 128 + ((r & 7) << 4); };   // its chunk 0; chunk c at c ^ (r & 7)
+    auto put_bf16 = [&](uint32_t to, const bf16* row) {   // a bf16 row (null: zeros) in the order of the decoded ones
 #pragma unroll 4
       for (int ch = 0; ch < HD / 8; ch++) {
         const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(row) + ch) : make_uint4(0, 0, 0, 0);
-        put(tile, r, ch, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                                    __byte_perm(v.y, v.w, 0x7632)));
+        put(to, ch, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                               __byte_perm(v.y, v.w, 0x7632)));
       }
     };
-    auto put_codes = [&](uint8_t* tile, int r, const Raw& w, bool is_v) {
+    auto put_codes = [&](uint32_t to, const Raw& w, bool is_v) {
 #pragma unroll
       for (int q = 0; q < HD / 16; q++) {   // a group of 16 dims: two words
         const uint32_t byte = (w.scale[q / 4] >> (8 * (q & 3))) & 0xFF;
@@ -302,8 +296,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           decode4_bf16(c0, s, x);
           decode4_bf16(c1, s, y);
         }
-        put(tile, r, 2 * q, make_uint4(x[0], x[1], x[2], x[3]));
-        put(tile, r, 2 * q + 1, make_uint4(y[0], y[1], y[2], y[3]));
+        put(to, 2 * q, make_uint4(x[0], x[1], x[2], x[3]));
+        put(to, 2 * q + 1, make_uint4(y[0], y[1], y[2], y[3]));
       }
     };
     auto done = [&](int b) {   // this warp's rows are written, for the tensor core to read
@@ -318,31 +312,31 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       return ok;
     };
     while (ok && !*abort_flag && next(sg)) {
-      Raw raw[3];
-      int id[3];   // pages of the items behind those whose codes are on their way
+      Raw raw[DEEP];
+      int id[DEEP];   // pages of the items behind those whose codes are on their way
 #pragma unroll
-      for (int d = 0; d < 3; d++) id[d] = page_for(sg, w3 + 3 * d);
+      for (int d = 0; d < DEEP; d++) id[d] = page_for(sg, wd + NW * d);
 #pragma unroll
-      for (int d = 0; d < 3; d++) {
-        fetch(sg, w3 + 3 * d, id[d], raw[d]);
-        id[d] = page_for(sg, w3 + 3 * d + 9);
+      for (int d = 0; d < DEEP; d++) {
+        fetch(sg, wd + NW * d, id[d], raw[d]);
+        id[d] = page_for(sg, wd + NW * (d + DEEP));
       }
       const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
       bool q_done = false;
-      for (int e0 = w3; e0 < 8 * sg.n_tiles && ok; e0 += 9) {
+      for (int e0 = wd; e0 < 8 * sg.n_tiles && ok; e0 += NW * DEEP) {
 #pragma unroll
-        for (int d = 0; d < 3; d++) {
-          const int e = e0 + 3 * d;
+        for (int d = 0; d < DEEP; d++) {
+          const int e = e0 + NW * d;
           if (e >= 8 * sg.n_tiles || !ok) break;
-          if (!q_done && e >= 4) {   // Q behind the first K tile
+          if (!q_done && (e >= 4 || wd < 4)) {   // the warps that start with the first K tile take Q first
             q_done = true;
             for (int l = 0; l < 2 && ok; l++) {
               if (sg.lane_tiles(l) == 0) continue;
               if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
-              for (int k = w3; k < 4; k += 3) {
+              for (int k = wd; k < 4; k += NW) {
                 const int r = k * 32 + lane, qi = sg.row0 + (sg.keys ? 0 : l * p.rpt) + r;
                 const bool has = r < p.rpt && qi < nrows;
-                put_bf16(qs + l * S::TILE, r, has ? a.q + ((size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp) * HD : nullptr);
+                put_bf16(row_at(qs + l * S::TILE, r), has ? a.q + ((size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp) * HD : nullptr);
                 done(B_Q + l);
               }
               nq[l]++;
@@ -353,12 +347,12 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           const bool is_v = (e >> 2) & 1;
           const int i = n + (e >> 3), ST = is_v ? VST : KST, s = i % ST, r = (e & 3) * 32 + lane;
           if (i >= ST && !wait((is_v ? B_VE : B_KE) + s, ((i / ST) & 1) ^ 1)) break;
-          uint8_t* tile = (is_v ? vs : ks) + s * S::TILE;
-          if (t.ctx) put_codes(tile, r, raw[d], is_v);
-          else put_bf16(tile, r, r < t.valid ? (is_v ? a.vblk : a.kblk) + (blk + t.k0 + r) * HD : nullptr);
+          const uint32_t to = row_at((is_v ? vs : ks) + s * S::TILE, r);
+          if (t.ctx) put_codes(to, raw[d], is_v);
+          else put_bf16(to, r < t.valid ? (is_v ? a.vblk : a.kblk) + (blk + t.k0 + r) * HD : nullptr);
           done((is_v ? B_VF : B_KF) + s);
-          fetch(sg, e + 9, id[d], raw[d]);
-          id[d] = page_for(sg, e + 18);
+          fetch(sg, e + NW * DEEP, id[d], raw[d]);
+          id[d] = page_for(sg, e + 2 * NW * DEEP);
         }
       }
       n += sg.n_tiles;
@@ -509,28 +503,35 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         if (!wait_bar(bar(B_SF + t), cnt & 1)) *abort_flag = 1;
         tc::tc_fence_after();
         if (warp_rows) {
-          float sv[KT];
-#pragma unroll
-          for (int c = 0; c < KT; c += 32) tmem_ld32_nowait(st + c, sv + c);
-#pragma unroll
-          for (int c = 0; c < KT; c += 32) wait_ld32(sv + c);
-          if (!tile_full(sh, sg.u, tl)) {   // keys before `hi` that lie before `lo_end` or from `start` on, as bits
+          constexpr int W = INT4 ? KT / 2 : KT;   // scores held at a time
+          float sv[W];
+          uint32_t see[KT / 32];   // keys before `hi` that lie before `lo_end` or from `start` on, as bits
+          const bool full = tile_full(sh, sg.u, tl);
+          if (!full) {
             const int hi = sh.causal ? min(tl.valid, row_pos - tl.pos + 1) : tl.valid;
             const int lo_end = sh.window ? sh.sinks - tl.pos : KT, start = sh.window ? row_pos - sh.window + 1 - tl.pos : 0;
 #pragma unroll
-            for (int w = 0; w < KT / 32; w++) {
-              const uint32_t see = below(hi - 32 * w) & (below(lo_end - 32 * w) | ~below(start - 32 * w));
-#pragma unroll
-              for (int e = 0; e < 32; e++) sv[32 * w + e] = (see >> e) & 1 ? sv[32 * w + e] : -INFINITY;
-            }
+            for (int w = 0; w < KT / 32; w++) see[w] = below(hi - 32 * w) & (below(lo_end - 32 * w) | ~below(start - 32 * w));
           }
-          float mq[4] = {sv[0], sv[1], sv[2], sv[3]};
+          auto load = [&](int k0) {
 #pragma unroll
-          for (int e = 4; e + 7 < KT; e += 8)
+            for (int c = 0; c < W; c += 32) tmem_ld32_nowait(st + k0 + c, sv + c);
 #pragma unroll
-            for (int u = 0; u < 4; u++) mq[u] = max3(mq[u], sv[e + u], sv[e + 4 + u]);
+            for (int c = 0; c < W; c += 32) wait_ld32(sv + c);
+            if (!full) {
 #pragma unroll
-          for (int u = 0; u < 4; u++) mq[u] = fmaxf(mq[u], sv[KT - 4 + u]);
+              for (int e = 0; e < W; e++) sv[e] = (see[(k0 + e) >> 5] >> (e & 31)) & 1 ? sv[e] : -INFINITY;
+            }
+          };
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k0 = KT - W; k0 >= 0; k0 -= W) {   // the first keys' scores stay for what follows
+            load(k0);
+#pragma unroll
+            for (int e = 0; e < W; e += 8)
+#pragma unroll
+              for (int u = 0; u < 4; u++) mq[u] = max3(mq[u], sv[e + u], sv[e + 4 + u]);
+          }
           const float mx = max3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * sl2;
           const bool need = mx > m_ref + kRescaleLog2;
           if (__any_sync(0xffffffffu, need)) {   // tcgen05.ld/st are warp-wide: every lane takes part
@@ -556,35 +557,40 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           const float nm = m_ref == -INFINITY ? 0.f : (half ? 7.f : 0.f) - m_ref;
           const uint64_t sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
           uint64_t lq[2] = {0ull, 0ull};
-          if (half) {
 #pragma unroll
-            for (int c0 = 0; c0 < KT; c0 += 16) {
-              uint32_t hi[8];
+          for (int k0 = 0; k0 < KT; k0 += W) {
+            if (k0 > 0) load(k0);
+            if (half) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float x0, x1;
-                unpack2(fma2(pack2(sv[c0 + e], sv[c0 + e + 1]), sl22, nm2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
-                hi[e / 2] = pack_f16(p0, p1);
+              for (int c0 = 0; c0 < W; c0 += 16) {
+                uint32_t hi[8];
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  float x0, x1;
+                  unpack2(fma2(pack2(sv[c0 + e], sv[c0 + e + 1]), sl22, nm2), x0, x1);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
+                  hi[e / 2] = pack_f16(p0, p1);
+                }
+                tmem_st8(st + (k0 + c0) / 2, hi);
               }
-              tmem_st8(st + c0 / 2, hi);
-            }
-          } else {
+            } else {
 #pragma unroll
-            for (int c0 = 0; c0 < KT; c0 += 16) {
-              uint32_t hi[8], lo[8];
+              for (int c0 = 0; c0 < W; c0 += 16) {
+                uint32_t hi[8], lo[8];
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float x0, x1;
-                unpack2(fma2(pack2(sv[c0 + e], sv[c0 + e + 1]), sl22, nm2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
-                split_trunc(p0, p1, hi[e / 2], lo[e / 2]);
+                for (int e = 0; e < 16; e += 2) {
+                  float x0, x1;
+                  unpack2(fma2(pack2(sv[c0 + e], sv[c0 + e + 1]), sl22, nm2), x0, x1);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
+                  split_trunc(p0, p1, hi[e / 2], lo[e / 2]);
+                }
+                const int c = k0 + c0;
+                const uint32_t pt = st + (c & ~31) + (c & 16) / 2;   // 32 keys: 16 columns of hi, 16 of lo
+                tmem_st8(pt, hi);
+                tmem_st8(pt + 16, lo);
               }
-              const uint32_t pt = st + (c0 & ~31) + (c0 & 16) / 2;   // 32 keys: 16 columns of hi, 16 of lo
-              tmem_st8(pt, hi);
-              tmem_st8(pt + 16, lo);
             }
           }
           float la, lb;

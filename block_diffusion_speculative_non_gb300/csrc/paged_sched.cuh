@@ -14,7 +14,7 @@
 namespace fpd {
 
 constexpr int kPagedTile = 64;       // keys of a tile of the mma.sync kernels
-constexpr int kSchedEntries = 128;   // running sums kept in shared memory, over ceil(batch / 128) requests each
+constexpr int kSchedEntries = 32;    // the lanes of a warp add up ceil(batch / 32) requests each
 
 struct PagedUnit {
   int b, g, rt;
@@ -132,26 +132,21 @@ struct PagedWalk {
   int c, G, batch, b, g, rt, off;
   long long x, x_end, total, each_run, longer;   // runs of each_run tiles, the first `longer` of them one more
 
-  // `sums` holds running sums of the entries' tiles (kSchedEntries + 1 of them), complete when the walk is made
-  __host__ __device__ PagedWalk(const PagedShape& s_, Lens lens_, const long long* sums, int batch_, int runs, int c_)
-      : s(s_), lens(lens_), c(c_), batch(batch_) {
-    total = sums[kSchedEntries];
+  __host__ __device__ PagedWalk(const PagedShape& s_, Lens lens_, int batch_, long long total_, int runs, int c_)
+      : s(s_), lens(lens_), c(c_), batch(batch_), b(0), g(0), rt(0), off(0), total(total_) {
     G = total < runs ? (int)total : runs;
     each_run = quotient(total, G);
     longer = total - each_run * G;
     x = c < G ? run_start(c) : total;
     x_end = c < G ? run_start(c + 1) : total;
-    if (x >= x_end) return;
-    int lo = 0, hi = kSchedEntries;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sums[mid] <= x) lo = mid; else hi = mid;
-    }
+  }
+  // Finds the run's first unit: entry lo, which starts at tile `base` and holds `size` of them, is the one with tile x.
+  __host__ __device__ void locate(int lo, long long base, long long size) {
     const int each = (batch + kSchedEntries - 1) / kSchedEntries;
-    long long rest = x - sums[lo], per;
+    long long rest = x - base, per;
     b = lo * each;
     if (each == 1) {
-      per = quotient(sums[lo + 1] - sums[lo], s.nkv);
+      per = quotient(size, s.nkv);
     } else {
       for (;; b++) {
         per = request_tiles(s, lens(b));
@@ -219,25 +214,23 @@ struct DeviceLens {
   int cap;
   __device__ int operator()(int b) const { return clamp_ctx(ctx_len[b], cap); }
 };
-// Running sums over the requests' tiles, by the first 128 threads of a CTA; the caller synchronises after it.
-__device__ __forceinline__ void sched_sums(const PagedShape& s, DeviceLens lens, int batch, long long* sums, int tid) {
-  const int each = (batch + kSchedEntries - 1) / kSchedEntries, lane = tid & 31;
+// The walk of run c, by a whole warp (every warp that walks makes its own; no shared memory, no barrier).
+__device__ __forceinline__ PagedWalk<DeviceLens> make_walk(const PagedShape& s, DeviceLens lens, int batch, int runs, int c) {
+  const int each = (batch + kSchedEntries - 1) / kSchedEntries, lane = threadIdx.x & 31;
   long long v = 0;
-  if (tid < kSchedEntries)
-    for (int b = tid * each; b < min(batch, (tid + 1) * each); b++) v += s.nkv * request_tiles(s, lens(b));
+  for (int b = lane * each; b < min(batch, (lane + 1) * each); b++) v += s.nkv * request_tiles(s, lens(b));
+  long long up = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
+    const long long t = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += t;
   }
-  if (tid < kSchedEntries) sums[tid + 1] = v;   // sums within a warp
-  if (tid == 0) sums[0] = 0;
-}
-// After a barrier: adds the warps before; another barrier follows.
-__device__ __forceinline__ long long sched_before(const long long* sums, int tid) {
-  long long v = 0;
-  for (int w = 0; w < (tid >> 5); w++) v += sums[(w + 1) * 32];
-  return v;
+  PagedWalk<DeviceLens> w(s, lens, batch, __shfl_sync(0xffffffffu, up, 31), runs, c);
+  const unsigned m = __ballot_sync(0xffffffffu, up > w.x);
+  const int e = m ? __ffs(m) - 1 : 31;
+  const long long base = __shfl_sync(0xffffffffu, up - v, e), size = __shfl_sync(0xffffffffu, v, e);
+  if (w.x < w.x_end) w.locate(e, base, size);
+  return w;
 }
 #endif
 
