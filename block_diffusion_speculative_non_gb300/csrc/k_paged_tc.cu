@@ -26,11 +26,13 @@ namespace {
 using namespace attn_tc;
 
 constexpr int QR = 128, KT = 128;
-constexpr int KST = 2, VST = 3;
+constexpr int KST = 2, VST = 2;
 constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
 constexpr uint32_t kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int ATOM_BYTES = KT * 64 * 2;
+
+constexpr int kOutBytes = 32 * 32 * 4;   // a softmax warp's rows by 32 dims, on their way out
 
 struct TcArgs {
   CUtensorMap tm_q, tm_pages, tm_kblk, tm_vblk;
@@ -42,7 +44,7 @@ struct TcArgs {
 template <int HD>
 struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64;
-  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, STAT = V + VST * TILE, BAR = STAT + 2 * QR * 4;
+  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, OUT = V + VST * TILE, BAR = OUT + 8 * kOutBytes;   // OUT: 32 dims of each row
 };
 enum {
   B_Q = 0,
@@ -78,11 +80,6 @@ __device__ __forceinline__ void split_trunc(float a, float b, uint32_t& hi, uint
   float ra, rb;
   unpack2(rest, ra, rb);
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb), "f"(ra));
-}
-__device__ __forceinline__ void st8(void* dst, const uint32_t* v) {   // 32-byte aligned
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-               "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {   // fp16 A and B, fp32 accumulator
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -481,7 +478,9 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lane_off + t * KT, o_mine = tmem + lane_off + kTmemO + t * 128;
-    float* stat = reinterpret_cast<float*>(smem + S::STAT);   // [lane][row]: m, then l, of units whose keys the lanes share
+    uint8_t* stage = smem + S::OUT + (warp - Ro::SOFTMAX) * kOutBytes;
+    float2* stat = reinterpret_cast<float2*>(stage);   // (m, l) of units whose keys the lanes share
+    const float2* stat_other = reinterpret_cast<const float2*>(smem + S::OUT + ((warp - Ro::SOFTMAX) ^ 4) * kOutBytes);
     int4 left = make_int4(-1, 0, 0, 0);
     int met = 0;
     auto meet = [&]() {   // with the other lane's warps; bounded, as every wait
@@ -626,14 +625,11 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       float w_mine = 1.f, w_other = 0.f;
       const bool shared_keys = sg.keys && sg.n_tiles > 1;
       if (shared_keys) {   // the lanes' halves of a row: either lane puts together one half of the dims
-        stat[t * QR + r] = m_ref;
+        stat[lane] = make_float2(m_ref, l);
         if (!wait_bar(bar(B_PV + 1 - t), (other - 1) & 1)) *abort_flag = 1;
         meet();
-        const float m_other = stat[(1 - t) * QR + r];
-        meet();
-        stat[t * QR + r] = l;
-        meet();
-        const float l_other = stat[(1 - t) * QR + r];
+        const float m_other = stat_other[lane].x, l_other = stat_other[lane].y;
+        meet();   // both have read: the rows go through the same bytes
         const float mx = fmaxf(m_ref, m_other);
         w_mine = m_ref == -INFINITY ? (l == l ? 0.f : 1.f) : ex2(m_ref - mx);   // a NaN sum counts
         w_other = m_other == -INFINITY ? (l_other == l_other ? 0.f : 1.f) : ex2(m_other - mx);
@@ -646,6 +642,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         const int qi = lrow0 + r;
         const size_t orow = has ? (size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp : 0;
         const size_t prow = (size_t)sg.slot * sh.rows + (sg.keys ? r : t * p.rpt + r);
+        const long long row_out = has ? (long long)(sg.whole ? orow : prow) : -1;
         const float by = sg.whole ? (none ? 0.f : 1.f / l) : 1.f;
         const int from = shared_keys ? t * (HD / 2) : 0, to = shared_keys ? from + HD / 2 : HD;
         bool spoilt = false;
@@ -664,26 +661,44 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
             for (int e = 0; e < 32; e++) o[e] = (w_mine == 0.f ? 0.f : o[e] * w_mine) + (w_other == 0.f ? 0.f : q[e] * w_other);
           }
 #pragma unroll
-          for (int e = 0; e < 32; e++) o[e] = none ? 0.f : o[e] * by;
-          float x[32];   // in the order of the dims
-#pragma unroll
-          for (int e = 0; e < 32; e++) x[INT4 ? (e & ~7) + ((e & 7) >> 1) + 4 * (e & 1) : e] = o[e];
-#pragma unroll
-          for (int e = 0; e < 32; e++) spoilt |= !(fabsf(x[e]) < INFINITY);
-          if (!has) continue;
+          for (int e = 0; e < 32; e++) {
+            o[e] = none ? 0.f : o[e] * by;
+            spoilt |= !(fabsf(o[e]) < INFINITY);
+          }
+          // dim e of 8 in its place: 4-bit pages leave the dims in the order 0 4 1 5 2 6 3 7
+          auto dim = [&](int e) { return INT4 ? o[(e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1)] : o[e]; };
+          // through shared memory (16-byte chunk q of row r at q ^ (r & 7)), so that a store has whole lines: a row per lane took
+          // the store unit 4 times as long
+          __syncwarp();
           if (sg.whole) {
-            bf16* dst = a.out + orow * HD + c0;
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              uint32_t w[8];
+            for (int q = 0; q < 4; q++) {
+              uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 8; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[e + 2 * i + 1]), "f"(x[e + 2 * i]));
-              st8(dst + e, w);
+              for (int i = 0; i < 4; i++)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dim(8 * q + 2 * i + 1)), "f"(dim(8 * q + 2 * i)));
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              const int e = 8 * i + (lane >> 2), q = lane & 3;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + e * 128 + ((q ^ (e & 7)) << 4));
+              const long long row = __shfl_sync(0xffffffffu, row_out, e);
+              if (row >= 0) *reinterpret_cast<uint4*>(a.out + row * HD + c0 + 8 * q) = v;
             }
           } else {
-            float* dst = a.o_part + prow * HD + c0;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) st8(dst + e, reinterpret_cast<const uint32_t*>(x + e));
+            for (int q = 0; q < 8; q++)
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_float4(dim(4 * q), dim(4 * q + 1), dim(4 * q + 2), dim(4 * q + 3));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const int e = 4 * i + (lane >> 3), q = lane & 7;
+              const float4 v = *reinterpret_cast<const float4*>(stage + e * 128 + ((q ^ (e & 7)) << 4));
+              const long long row = __shfl_sync(0xffffffffu, row_out, e);
+              if (row >= 0) *reinterpret_cast<float4*>(a.o_part + row * HD + c0 + 4 * q) = v;
+            }
           }
         }
         // a row without numbers whose weights are numbers, under a mask (paged_repair.cuh)
@@ -695,13 +710,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           float acc[HD / 32];
           repair_row<HD>(a, sh, sg.u, sg.t0, sg.t0 + sg.n_tiles, __shfl_sync(0xffffffffu, qi, e), __shfl_sync(0xffffffffu, m_ref, e), acc);
           const float scale = __shfl_sync(0xffffffffu, by, e);
-          const size_t orow_e = __shfl_sync(0xffffffffu, (unsigned long long)orow, e), prow_e = __shfl_sync(0xffffffffu, (unsigned long long)prow, e);
+          const size_t row = (size_t)__shfl_sync(0xffffffffu, row_out, e);
 #pragma unroll
           for (int j = 0; j < HD / 32; j++) {
             const int d = lane + 32 * j;
             if (d < from || d >= to) continue;
-            if (sg.whole) a.out[orow_e * HD + d] = __float2bfloat16_rn(acc[j] * scale);
-            else a.o_part[prow_e * HD + d] = acc[j];
+            if (sg.whole) a.out[row * HD + d] = __float2bfloat16_rn(acc[j] * scale);
+            else a.o_part[row * HD + d] = acc[j];
           }
         }
         if (has && (!shared_keys || t == 0)) {
