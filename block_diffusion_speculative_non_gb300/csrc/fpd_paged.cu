@@ -102,18 +102,21 @@ struct AttnWs {
   float* o_part;
   float2* ml;
   int4* desc;
+  uint32_t* spoilt;
   size_t bytes;
 };
 AttnWs carve(void* base, int batch, int L, int nq, const fpd_paged_store* s, int sms) {
   AttnWs w{};
-  w.plan = paged_attn_plan(batch, L, nq, s->n_kv_heads, s->head_dim, s->format, s->table_width * s->page_size, sms);
+  w.plan = paged_attn_plan(batch, L, nq, s->n_kv_heads, s->table_width * s->page_size, sms);
   const size_t n = (size_t)2 * w.plan.runs * w.plan.rows;
   const size_t lead = align_up((uintptr_t)base, 256) - (uintptr_t)base;   // the workspace itself is 16-byte aligned
   const size_t ml_at = align_up(n * s->head_dim * sizeof(float), 256), desc_at = ml_at + align_up(n * sizeof(float2), 256);
   w.o_part = (float*)((char*)base + lead);
   w.ml = (float2*)((char*)base + lead + ml_at);
   w.desc = (int4*)((char*)base + lead + desc_at);
-  w.bytes = 256 + desc_at + (size_t)w.plan.runs * sizeof(int4);
+  const size_t spoilt_at = desc_at + align_up((size_t)w.plan.runs * sizeof(int4), 256);
+  w.spoilt = (uint32_t*)((char*)base + lead + spoilt_at);
+  w.bytes = 256 + spoilt_at + (size_t)w.plan.runs * 8 * sizeof(uint32_t);
   return w;
 }
 
@@ -212,6 +215,7 @@ fpd_status fpd_paged_attention(int batch, int block_len, int n_q_heads, const fp
   a.o_part = w.o_part;
   a.ml = w.ml;
   a.desc = w.desc;
+  a.spoilt = w.spoilt;
   a.batch = batch;
   a.L = block_len;
   a.lb = k_blk ? block_len : 0;

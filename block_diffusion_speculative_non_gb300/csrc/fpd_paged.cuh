@@ -80,15 +80,16 @@ struct PagedAttn {
   float* o_part;                // [2 runs][rows of a tile][h]
   float2* ml;                   // [2 runs][rows of a tile]: running maximum (base 2) and sum
   int4* desc;                   // [runs]: request, kv head, row tile and last run of the unit that a run leaves unfinished
+  uint32_t* spoilt;             // [runs][words]: which of a run's parts came out with something that is no number
   int batch, L, lb, nq, window, sinks, causal;   // lb: block keys, L or 0
 };
-enum PagedKernel { kPagedMma, kPagedStream, kPagedTc };
+enum PagedKernel { kPagedStream, kPagedTc };
 struct PagedPlan {
   PagedKernel kernel;
   int rows, tiles;     // rows of a row tile, row tiles of a request and kv head
   int grid, runs;      // CTAs, and the runs that share the key tiles (of CTAs, or of their warps)
 };
-PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int h, int format, int t_cap, int num_sms);
+PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int t_cap, int num_sms);
 cudaError_t paged_attn_init_attributes();
 cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cudaStream_t st);
 

@@ -21,7 +21,7 @@
 #include "attn_body.cuh"
 #include "attn_tc_prims.cuh"
 #include "paged_decode.cuh"
-#include "paged_repair.cuh"
+#include "paged_masks.cuh"
 #include "paged_sched.cuh"
 
 namespace fpd {
@@ -156,6 +156,8 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
   int4 left = make_int4(-1, 0, 0, 0);
   int cnt = 0;      // slots filled and emptied so far: place in the ring and phase
   bool ok = true;
+  unsigned spoilt_units = 0;   // parts of the run, from 31 on together, that came out whole and with something that is no number
+  int n_units = 0;
 
   PagedUnit u;
   int t0, t1, last_run;
@@ -545,8 +547,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
     // ---- the rows' sums, and out ----
     const bool whole = t0 == 0 && t1 == u.len();
     const int slot = 2 * run + (t0 == 0 ? 1 : 0);
-    unsigned bad = 0;   // rows without numbers whose weights are numbers, under a mask (paged_repair.cuh)
-    float l_row[NT][2];
+    bool spoilt = false;
 #pragma unroll
     for (int j = 0; j < NT; j++)
 #pragma unroll
@@ -555,7 +556,6 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         const int r = 8 * j + 2 * c + e, qi = u.rt * R + r;
-        l_row[j][e] = l;
         if (qi >= nrows) continue;
         const float ul = INT4 ? l * 6.103515625e-05f : l;   // 2^-14
         const bool none = l == 0.f;
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
         for (int i = 0; i < MT; i++) {
           x[2 * i] = none ? 0.f : st.o[i][j][e] * by;
           x[2 * i + 1] = none ? 0.f : st.o[i][j][2 + e] * by;
-          if (!(fabsf(x[2 * i]) < INFINITY && fabsf(x[2 * i + 1]) < INFINITY) && fabsf(l) < INFINITY) bad |= 1u << r;
+          spoilt |= !(fabsf(x[2 * i]) < INFINITY && fabsf(x[2 * i + 1]) < INFINITY);
         }
         if (whole) {
           bf16* dst = a.out + row * H;
@@ -591,34 +591,14 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
           if (g == 0) a.ml[row] = make_float2(st.m[j][e], ul);
         }
       }
-    bad = sh.window || sh.causal ? __reduce_or_sync(0xffffffffu, bad) : 0;
-    if (bad) __syncwarp();   // behind the rows' own stores
-    while (bad) {
-      const int r = __ffs(bad) - 1, qi = u.rt * R + r;
-      bad &= bad - 1;
-      float m = 0.f, l = 1.f, acc[H / 32];
-#pragma unroll
-      for (int j = 0; j < NT; j++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          const float mr = __shfl_sync(0xffffffffu, st.m[j][e], (r & 7) >> 1), lr = __shfl_sync(0xffffffffu, l_row[j][e], (r & 7) >> 1);
-          if (r == 8 * j + ((r & 7) & ~1) + e) {
-            m = mr;
-            l = lr;
-          }
-        }
-      repair_row<H>(a, sh, u, t0, nt, qi, m, acc);
-      const float by = whole ? (INT4 ? 16384.f : 1.f) / l : 1.f;
-      const size_t row = whole ? (size_t)(u.b * a.L + qi / sh.grp) * a.nq + u.g * sh.grp + qi % sh.grp : (size_t)slot * R + r;
-#pragma unroll
-      for (int j = 0; j < H / 32; j++) {
-        if (whole) a.out[row * H + lane + 32 * j] = __float2bfloat16_rn(acc[j] * by);
-        else a.o_part[row * H + lane + 32 * j] = acc[j];
-      }
-    }
+    if (whole && __any_sync(0xffffffffu, spoilt)) spoilt_units |= 1u << min(n_units, 31);
+    n_units++;
     if (t0 == 0 && t1 < u.len()) left = make_int4(u.b, u.g, u.rt, last_run);
   }
-  if (lane == 0) a.desc[run] = left;
+  if (lane == 0) {
+    a.desc[run] = left;
+    a.spoilt[run] = spoilt_units;
+  }
 }
 
 template <int H, int NT, bool INT4>

@@ -17,7 +17,7 @@
 
 #include "attn_tc_prims.cuh"
 #include "paged_decode.cuh"
-#include "paged_repair.cuh"
+#include "paged_masks.cuh"
 #include "paged_sched.cuh"
 
 namespace fpd {
@@ -25,14 +25,12 @@ namespace fpd {
 namespace {
 using namespace attn_tc;
 
-constexpr int QR = 128, KT = 128;
-constexpr int KST = 2, VST = 2;
+constexpr int QR = 128, KT = kPagedTcTile;
+constexpr int KST = 2, VST = 3;
 constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
 constexpr uint32_t kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int ATOM_BYTES = KT * 64 * 2;
-
-constexpr int kOutBytes = 32 * 32 * 4;   // a softmax warp's rows by 32 dims, on their way out
 
 struct TcArgs {
   CUtensorMap tm_q, tm_pages, tm_kblk, tm_vblk;
@@ -44,7 +42,7 @@ struct TcArgs {
 template <int HD>
 struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64;
-  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, OUT = V + VST * TILE, BAR = OUT + 8 * kOutBytes;   // OUT: 32 dims of each row
+  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, STAT = V + VST * TILE, BAR = STAT + 2 * QR * 4;
 };
 enum {
   B_Q = 0,
@@ -80,6 +78,11 @@ __device__ __forceinline__ void split_trunc(float a, float b, uint32_t& hi, uint
   float ra, rb;
   unpack2(rest, ra, rb);
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb), "f"(ra));
+}
+__device__ __forceinline__ void st8(void* dst, const uint32_t (&v)[8]) {   // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {   // fp16 A and B, fp32 accumulator
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -478,11 +481,10 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lane_off + t * KT, o_mine = tmem + lane_off + kTmemO + t * 128;
-    uint8_t* stage = smem + S::OUT + (warp - Ro::SOFTMAX) * kOutBytes;
-    float2* stat = reinterpret_cast<float2*>(stage);   // (m, l) of units whose keys the lanes share
-    const float2* stat_other = reinterpret_cast<const float2*>(smem + S::OUT + ((warp - Ro::SOFTMAX) ^ 4) * kOutBytes);
+    float* stat = reinterpret_cast<float*>(smem + S::STAT);   // [lane][row]: m, then l, of units whose keys the lanes share
     int4 left = make_int4(-1, 0, 0, 0);
-    int met = 0;
+    unsigned spoilt_units = 0;   // parts of the run, from 31 on together, that came out whole and with something that is no number
+    int n_units = 0, met = 0;
     auto meet = [&]() {   // with the other lane's warps; bounded, as every wait
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(B_X));
@@ -625,11 +627,14 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       float w_mine = 1.f, w_other = 0.f;
       const bool shared_keys = sg.keys && sg.n_tiles > 1;
       if (shared_keys) {   // the lanes' halves of a row: either lane puts together one half of the dims
-        stat[lane] = make_float2(m_ref, l);
+        stat[t * QR + r] = m_ref;
         if (!wait_bar(bar(B_PV + 1 - t), (other - 1) & 1)) *abort_flag = 1;
         meet();
-        const float m_other = stat_other[lane].x, l_other = stat_other[lane].y;
-        meet();   // both have read: the rows go through the same bytes
+        const float m_other = stat[(1 - t) * QR + r];
+        meet();
+        stat[t * QR + r] = l;
+        meet();
+        const float l_other = stat[(1 - t) * QR + r];
         const float mx = fmaxf(m_ref, m_other);
         w_mine = m_ref == -INFINITY ? (l == l ? 0.f : 1.f) : ex2(m_ref - mx);   // a NaN sum counts
         w_other = m_other == -INFINITY ? (l_other == l_other ? 0.f : 1.f) : ex2(m_other - mx);
@@ -642,83 +647,48 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         const int qi = lrow0 + r;
         const size_t orow = has ? (size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp : 0;
         const size_t prow = (size_t)sg.slot * sh.rows + (sg.keys ? r : t * p.rpt + r);
-        const long long row_out = has ? (long long)(sg.whole ? orow : prow) : -1;
         const float by = sg.whole ? (none ? 0.f : 1.f / l) : 1.f;
         const int from = shared_keys ? t * (HD / 2) : 0, to = shared_keys ? from + HD / 2 : HD;
         bool spoilt = false;
+        // 16 dims at a time, in a loop that stays short: unrolled, its code took longer to fetch than to run
 #pragma unroll 1
-        for (int c0 = from; c0 < to; c0 += 32) {
-          float o[32];
+        for (int c0 = from; c0 < to; c0 += 16) {
+          float o[16];
           if (sg.n_tiles > 0) {
-            tmem_ld32_nowait(o_mine + c0, o);
-            wait_ld32(o);
+            tmem_ld16_nowait(o_mine + c0, o);
+            wait_ld16(o);
           }
           if (shared_keys) {
-            float q[32];
-            tmem_ld32_nowait(tmem + lane_off + kTmemO + (1 - t) * 128 + c0, q);
-            wait_ld32(q);
+            float q[16];
+            tmem_ld16_nowait(tmem + lane_off + kTmemO + (1 - t) * 128 + c0, q);
+            wait_ld16(q);
 #pragma unroll
-            for (int e = 0; e < 32; e++) o[e] = (w_mine == 0.f ? 0.f : o[e] * w_mine) + (w_other == 0.f ? 0.f : q[e] * w_other);
+            for (int e = 0; e < 16; e++) o[e] = (w_mine == 0.f ? 0.f : o[e] * w_mine) + (w_other == 0.f ? 0.f : q[e] * w_other);
           }
 #pragma unroll
-          for (int e = 0; e < 32; e++) {
+          for (int e = 0; e < 16; e++) {
             o[e] = none ? 0.f : o[e] * by;
             spoilt |= !(fabsf(o[e]) < INFINITY);
           }
+          if (!has) continue;
           // dim e of 8 in its place: 4-bit pages leave the dims in the order 0 4 1 5 2 6 3 7
           auto dim = [&](int e) { return INT4 ? o[(e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1)] : o[e]; };
-          // through shared memory (16-byte chunk q of row r at q ^ (r & 7)), so that a store has whole lines: a row per lane took
-          // the store unit 4 times as long
-          __syncwarp();
           if (sg.whole) {
+            uint32_t w[8];
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; i++)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dim(8 * q + 2 * i + 1)), "f"(dim(8 * q + 2 * i)));
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              const int e = 8 * i + (lane >> 2), q = lane & 3;
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + e * 128 + ((q ^ (e & 7)) << 4));
-              const long long row = __shfl_sync(0xffffffffu, row_out, e);
-              if (row >= 0) *reinterpret_cast<uint4*>(a.out + row * HD + c0 + 8 * q) = v;
-            }
+            for (int i = 0; i < 8; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dim(2 * i + 1)), "f"(dim(2 * i)));
+            st8(a.out + orow * HD + c0, w);
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; q++)
-              *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_float4(dim(4 * q), dim(4 * q + 1), dim(4 * q + 2), dim(4 * q + 3));
-            __syncwarp();
+            for (int h = 0; h < 16; h += 8) {
+              uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-              const int e = 4 * i + (lane >> 3), q = lane & 7;
-              const float4 v = *reinterpret_cast<const float4*>(stage + e * 128 + ((q ^ (e & 7)) << 4));
-              const long long row = __shfl_sync(0xffffffffu, row_out, e);
-              if (row >= 0) *reinterpret_cast<float4*>(a.o_part + row * HD + c0 + 4 * q) = v;
+              for (int i = 0; i < 8; i++) w[i] = __float_as_uint(dim(h + i));
+              st8(a.o_part + prow * HD + c0 + h, w);
             }
           }
         }
-        // a row without numbers whose weights are numbers, under a mask (paged_repair.cuh)
-        unsigned bad = (sh.window || sh.causal) ? __ballot_sync(0xffffffffu, has && spoilt && fabsf(l) < INFINITY && !none) : 0;
-        if (bad) __syncwarp();   // behind the rows' own stores
-        while (bad) {
-          const int e = __ffs(bad) - 1;
-          bad &= bad - 1;
-          float acc[HD / 32];
-          repair_row<HD>(a, sh, sg.u, sg.t0, sg.t0 + sg.n_tiles, __shfl_sync(0xffffffffu, qi, e), __shfl_sync(0xffffffffu, m_ref, e), acc);
-          const float scale = __shfl_sync(0xffffffffu, by, e);
-          const size_t row = (size_t)__shfl_sync(0xffffffffu, row_out, e);
-#pragma unroll
-          for (int j = 0; j < HD / 32; j++) {
-            const int d = lane + 32 * j;
-            if (d < from || d >= to) continue;
-            if (sg.whole) a.out[row * HD + d] = __float2bfloat16_rn(acc[j] * scale);
-            else a.o_part[row * HD + d] = acc[j];
-          }
-        }
+        if (sg.whole && has && spoilt) spoilt_units |= 1u << min(n_units, 31);
         if (has && (!shared_keys || t == 0)) {
           if (!sg.whole) a.ml[prow] = make_float2(m_ref, l);
           else if (a.lse) a.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
@@ -727,7 +697,10 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       if (sg.first && !sg.whole) left = make_int4(sg.u.b, sg.u.g, sg.u.rt, sg.last_run);
       tc::tc_fence_before();   // O has been read: the next run's first product follows this lane's next P
       if (shared_keys) meet();
+      n_units++;
     }
+    spoilt_units = __reduce_or_sync(0xffffffffu, spoilt_units);
+    if (lane == 0) a.spoilt[blockIdx.x * 8 + warp - Ro::SOFTMAX] = spoilt_units;
     if (warp == Ro::SOFTMAX && lane == 0) a.desc[blockIdx.x] = left;
   }
 
@@ -760,8 +733,6 @@ cudaError_t launch_paged_tc(const PagedAttn& a, const PagedShape& s, const Paged
   memset(&p, 0, sizeof(p));
   p.a = a;
   p.s = s;
-  p.s.kt_shift = 7;
-  static_assert(KT == 1 << 7, "keys of a tile");
   p.runs = pl.runs;
   p.npt = QR / s.grp;
   p.rpt = p.npt * s.grp;

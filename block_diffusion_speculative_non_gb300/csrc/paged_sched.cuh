@@ -13,7 +13,7 @@
 
 namespace fpd {
 
-constexpr int kPagedTile = 64;       // keys of a tile of the mma.sync kernels
+constexpr int kPagedTile = 64, kPagedTcTile = 128;   // keys of a tile of k_paged_stream.cu and of k_paged_tc.cu
 constexpr int kSchedEntries = 32;    // the lanes of a warp add up ceil(batch / 32) requests each
 
 struct PagedUnit {
