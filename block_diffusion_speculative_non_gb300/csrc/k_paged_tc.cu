@@ -235,9 +235,10 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     }
   } else if (INT4 && warp < Ro::SOFTMAX && warp != 1) {
     // ---------------- decoding warps ----------------
-    // A tile is eight items, 32 rows of K or of V each; the warps take turns at them, a thread a row, and have requested the codes
-    // of their next two.
-    constexpr int NW = 7, DEEP = 2;
+    // A tile is eight items, 32 rows of K or of V each; the warps take turns at them, a thread a row.  An item's page is looked up
+    // three turns ahead, its codes are requested into L2 two turns ahead and into registers one turn ahead.  One copy of the
+    // code for all turns: unrolled, a third of the stalls were for instructions.
+    constexpr int NW = 7;
     const int wd = warp == 0 ? 0 : warp - 1;
     const uint32_t qs = tc::smem_u32(smem + S::Q), ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V);
     int n = 0, nq[2] = {0, 0};
@@ -265,6 +266,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       for (int j = 0; j < HD / 32; j++) w.code[j] = __ldg(code + j);
 #pragma unroll
       for (int j = 0; j < HD / 64; j++) w.scale[j] = __ldg(scale + j);
+    };
+    auto to_l2 = [&](const Seg& s, int e, int id) {
+      if (id < 0) return;
+      const int in = (s.tile(e >> 3).k0 + (e & 3) * 32 + lane) & (a.pg.page - 1);
+      const uint8_t* slab = slab_of(a.pg, id, (e >> 2) & 1, s.u.g);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(slab + in * (HD / 2)));
+      if ((lane & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(slab + a.pg.page * (HD / 2) + in * (HD / 16)));
     };
     // chunk of 8 dims ch of row r in a tile of 64-dim atoms
     auto put = [&](uint32_t row, int ch, uint4 v) {
@@ -312,22 +320,21 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       return ok;
     };
     while (ok && !*abort_flag && next(sg)) {
-      Raw raw[DEEP];
-      int id[DEEP];   // pages of the items behind those whose codes are on their way
-#pragma unroll
-      for (int d = 0; d < DEEP; d++) id[d] = page_for(sg, wd + NW * d);
-#pragma unroll
-      for (int d = 0; d < DEEP; d++) {
-        fetch(sg, wd + NW * d, id[d], raw[d]);
-        id[d] = page_for(sg, wd + NW * (d + DEEP));
-      }
+      Raw raw, ahead;
+      int id1 = page_for(sg, wd), id2 = page_for(sg, wd + NW), id3 = page_for(sg, wd + 2 * NW);
+      fetch(sg, wd, id1, raw);
+      id1 = id2;
+      id2 = id3;
+      id3 = page_for(sg, wd + 3 * NW);
       const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
       bool q_done = false;
-      for (int e0 = wd; e0 < 8 * sg.n_tiles && ok; e0 += NW * DEEP) {
-#pragma unroll
-        for (int d = 0; d < DEEP; d++) {
-          const int e = e0 + NW * d;
-          if (e >= 8 * sg.n_tiles || !ok) break;
+#pragma unroll 1
+      for (int e = wd; e < 8 * sg.n_tiles && ok; e += NW) {
+          fetch(sg, e + NW, id1, ahead);
+          to_l2(sg, e + 2 * NW, id2);
+          id1 = id2;
+          id2 = id3;
+          id3 = page_for(sg, e + 4 * NW);
           if (!q_done && (e >= 4 || wd < 4)) {   // the warps that start with the first K tile take Q first
             q_done = true;
             for (int l = 0; l < 2 && ok; l++) {
@@ -345,15 +352,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           }
           const PagedTile t = sg.tile(e >> 3);
           const bool is_v = (e >> 2) & 1;
-          const int i = n + (e >> 3), ST = is_v ? VST : KST, s = i % ST, r = (e & 3) * 32 + lane;
-          if (i >= ST && !wait((is_v ? B_VE : B_KE) + s, ((i / ST) & 1) ^ 1)) break;
+          const int i = n + (e >> 3), turn = is_v ? i / VST : i / KST, s = i - turn * (is_v ? VST : KST), r = (e & 3) * 32 + lane;
+          if (turn > 0 && !wait((is_v ? B_VE : B_KE) + s, (turn & 1) ^ 1)) break;
           const uint32_t to = row_at((is_v ? vs : ks) + s * S::TILE, r);
-          if (t.ctx) put_codes(to, raw[d], is_v);
+          if (t.ctx) put_codes(to, raw, is_v);
           else put_bf16(to, r < t.valid ? (is_v ? a.vblk : a.kblk) + (blk + t.k0 + r) * HD : nullptr);
           done((is_v ? B_VF : B_KF) + s);
-          fetch(sg, e + NW * DEEP, id[d], raw[d]);
-          id[d] = page_for(sg, e + 2 * NW * DEEP);
-        }
+          raw = ahead;
       }
       n += sg.n_tiles;
     }
@@ -521,11 +526,15 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
             for (int c = 0; c < W; c += 32) wait_ld32(sv + c);
             if (!full) {
 #pragma unroll
-              for (int e = 0; e < W; e++) sv[e] = (see[(k0 + e) >> 5] >> (e & 31)) & 1 ? sv[e] : -INFINITY;
+              for (int w = 0; w < W / 32; w++) {
+                const uint32_t bits = W == KT || k0 == 0 ? see[w] : see[KT / 32 - W / 32 + w];
+#pragma unroll
+                for (int e = 0; e < 32; e++) sv[32 * w + e] = (bits >> e) & 1 ? sv[32 * w + e] : -INFINITY;
+              }
             }
           };
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
           for (int k0 = KT - W; k0 >= 0; k0 -= W) {   // the first keys' scores stay for what follows
             load(k0);
 #pragma unroll
@@ -558,7 +567,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           const float nm = m_ref == -INFINITY ? 0.f : (half ? 7.f : 0.f) - m_ref;
           const uint64_t sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
           uint64_t lq[2] = {0ull, 0ull};
-#pragma unroll
+#pragma unroll 1
           for (int k0 = 0; k0 < KT; k0 += W) {
             if (k0 > 0) load(k0);
             if (half) {
