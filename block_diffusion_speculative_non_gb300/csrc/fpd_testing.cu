@@ -313,15 +313,15 @@ extern "C" int fpd_test_weight_shares(int batch, int nkv, const int32_t* counted
 }
 
 extern "C" int fpd_test_paged_walk(int batch, int L, int block_keys, int group, int nkv, int rows, int window, int sinks, int causal,
-                                   int key_tile, const int32_t* counted, const int32_t* walked, int runs, int run, int max_parts,
+                                   int key_tile, int unit_cost, const int32_t* counted, const int32_t* walked, int runs, int run, int max_parts,
                                    int32_t* parts, int32_t* n_parts) {
-  if (batch < 1 || L < 1 || group < 1 || nkv < 1 || rows < 1 || key_tile < 1 || run < 0 || run >= runs || !counted || !walked || !parts || !n_parts)
+  if (batch < 1 || L < 1 || group < 1 || nkv < 1 || rows < 1 || key_tile < 1 || unit_cost < 0 || run < 0 || run >= runs || !counted || !walked || !parts || !n_parts)
     return FPD_ERR_SHAPE;
   struct Lens {
     const int32_t* v;
     int operator()(int b) const { return v[b]; }
   };
-  const PagedShape s = paged_shape(L, block_keys, group, nkv, rows, window, sinks, causal, key_tile);
+  const PagedShape s = paged_shape(L, block_keys, group, nkv, rows, window, sinks, causal, key_tile, unit_cost);
   long long sums[kSchedEntries + 1] = {0};
   const int each = ceil_div(batch, kSchedEntries);
   for (int e = 0; e < kSchedEntries; e++) {
@@ -346,7 +346,7 @@ extern "C" int fpd_test_paged_walk(int batch, int L, int block_keys, int group, 
 extern "C" int fpd_test_paged_tiles(int L, int block_keys, int group, int rows, int window, int sinks, int causal, int key_tile,
                                     int ctx_len, int row_tile, int max_tiles, int32_t* tiles, int32_t* n_tiles) {
   if (L < 1 || group < 1 || rows < 1 || key_tile < 1 || row_tile < 0 || row_tile * rows >= L * group || !tiles || !n_tiles) return FPD_ERR_SHAPE;
-  const PagedShape s = paged_shape(L, block_keys, group, 1, rows, window, sinks, causal, key_tile);
+  const PagedShape s = paged_shape(L, block_keys, group, 1, rows, window, sinks, causal, key_tile, 0);
   PagedUnit u;
   unit_tiles(s, ctx_len, row_tile, u);
   if (u.tiles() > max_tiles) return FPD_ERR_CAPACITY;

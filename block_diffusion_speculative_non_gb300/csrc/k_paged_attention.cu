@@ -182,7 +182,7 @@ cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cuda
   // positions stay below 2^30 + 2^26: a longer window hides nothing
   constexpr int kFar = 1200000000;
   p.s = paged_shape(a.L, a.lb, a.nq / a.pg.nkv, a.pg.nkv, pl.rows, a.window > kFar ? 0 : a.window, std::min(a.sinks, kFar), a.causal,
-                    pl.kernel == kPagedTc ? kPagedTcTile : kPagedTile);
+                    pl.kernel == kPagedTc ? kPagedTcTile : kPagedTile, 2);
   p.runs = pl.runs;
   p.spoilt_words = pl.kernel == kPagedStream ? 1 : 8;
   return a.pg.h == 128 ? launch<128>(p, pl, st) : launch<64>(p, pl, st);

@@ -84,6 +84,11 @@ __device__ __forceinline__ void st8(void* dst, const uint32_t (&v)[8]) {   // 32
                "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {   // fp16 A and B, fp32 accumulator
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
@@ -281,12 +286,23 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
                    : "memory");
     };
     auto row_at = [&](uint32_t tile, int r) { return tile + r * 128 + ((r & 7) << 4); };   // its chunk 0; chunk c at c ^ (r & 7)
-    auto put_bf16 = [&](uint32_t to, const bf16* row) {   // a bf16 row (null: zeros) in the order of the decoded ones
-#pragma unroll 4
-      for (int ch = 0; ch < HD / 8; ch++) {
-        const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(row) + ch) : make_uint4(0, 0, 0, 0);
-        put(to, ch, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                               __byte_perm(v.y, v.w, 0x7632)));
+    // 32 bf16 rows from row r0 of a tile on, in the order of the decoded ones; from(r): a row's address, null for zeros.  A warp's load
+    // has whole rows.
+    auto put_bf16 = [&](uint32_t tile, int r0, auto from) {
+      constexpr int PER = HD / 8, RPL = 32 / PER;   // chunks of a row, rows of a load
+      const int ch = lane % PER, r_in = lane / PER;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 / RPL; i0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const bf16* row = from(r0 + (i0 + i) * RPL + r_in);
+          v[i] = row ? __ldg(reinterpret_cast<const uint4*>(row) + ch) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          put(row_at(tile, r0 + (i0 + i) * RPL + r_in), ch, make_uint4(__byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
+                                                                       __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632)));
       }
     };
     auto put_codes = [&](uint32_t to, const Raw& w, bool is_v) {
@@ -341,9 +357,11 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
               if (sg.lane_tiles(l) == 0) continue;
               if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
               for (int k = wd; k < 4; k += NW) {
-                const int r = k * 32 + lane, qi = sg.row0 + (sg.keys ? 0 : l * p.rpt) + r;
-                const bool has = r < p.rpt && qi < nrows;
-                put_bf16(row_at(qs + l * S::TILE, r), has ? a.q + ((size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp) * HD : nullptr);
+                const int q0 = sg.row0 + (sg.keys ? 0 : l * p.rpt);
+                put_bf16(qs + l * S::TILE, k * 32, [&](int r) -> const bf16* {
+                  const int qi = q0 + r, j = sh.by_grp.div(qi);
+                  return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg.u.b * a.L + j) * a.nq + sg.u.g * grp + qi - j * grp) * HD : nullptr;
+                });
                 done(B_Q + l);
               }
               nq[l]++;
@@ -352,11 +370,15 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           }
           const PagedTile t = sg.tile(e >> 3);
           const bool is_v = (e >> 2) & 1;
-          const int i = n + (e >> 3), turn = is_v ? i / VST : i / KST, s = i - turn * (is_v ? VST : KST), r = (e & 3) * 32 + lane;
+          const int i = n + (e >> 3), turn = is_v ? i / VST : i / KST, s = i - turn * (is_v ? VST : KST);
           if (turn > 0 && !wait((is_v ? B_VE : B_KE) + s, (turn & 1) ^ 1)) break;
-          const uint32_t to = row_at((is_v ? vs : ks) + s * S::TILE, r);
-          if (t.ctx) put_codes(to, raw, is_v);
-          else put_bf16(to, r < t.valid ? (is_v ? a.vblk : a.kblk) + (blk + t.k0 + r) * HD : nullptr);
+          const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
+          if (t.ctx) {
+            put_codes(row_at(tile, (e & 3) * 32 + lane), raw, is_v);
+          } else {
+            const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
+            put_bf16(tile, (e & 3) * 32, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
+          }
           done((is_v ? B_VF : B_KF) + s);
           raw = ahead;
       }
@@ -533,43 +555,63 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
               }
             }
           };
-          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int k0 = KT - W; k0 >= 0; k0 -= W) {   // the first keys' scores stay for what follows
-            load(k0);
-#pragma unroll
-            for (int e = 0; e < W; e += 8)
-#pragma unroll
-              for (int u = 0; u < 4; u++) mq[u] = max3(mq[u], sv[e + u], sv[e + 4 + u]);
-          }
-          const float mx = max3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * sl2;
-          const bool need = mx > m_ref + kRescaleLog2;
-          if (__any_sync(0xffffffffu, need)) {   // tcgen05.ld/st are warp-wide: every lane takes part
-            const float m_new = need ? mx : m_ref;
-            const float cf = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
-            if (!first_tile) {
-              // O may only be rescaled once every product into it has finished
-              if (!wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
-              tc::tc_fence_after();
-#pragma unroll 1
-              for (int c0 = 0; c0 < HD; c0 += 16) {
-                float o[16];
-                tc::tmem_ld16(o_mine + c0, o);
-#pragma unroll
-                for (int e = 0; e < 16; e++) o[e] *= cf;
-                tmem_st16(o_mine + c0, o);
-              }
-            }
-            l *= cf;
-            m_ref = m_new;
-          }
-          // every score so far -inf: weight 0, not NaN.  fp16 weights are p 2^7, and V has 2^-7
-          const float nm = m_ref == -INFINITY ? 0.f : (half ? 7.f : 0.f) - m_ref;
-          const uint64_t sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
           uint64_t lq[2] = {0ull, 0ull};
 #pragma unroll 1
           for (int k0 = 0; k0 < KT; k0 += W) {
-            if (k0 > 0) load(k0);
+            load(k0);
+            float mq[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+            for (int e = 4; e + 7 < W; e += 8)
+#pragma unroll
+              for (int u = 0; u < 4; u++) mq[u] = max3(mq[u], sv[e + u], sv[e + 4 + u]);
+#pragma unroll
+            for (int u = 0; u < 4; u++) mq[u] = fmaxf(mq[u], sv[W - 4 + u]);
+            const float mx = max3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * sl2;
+            const bool need = mx > m_ref + kRescaleLog2;
+            if (__any_sync(0xffffffffu, need)) {   // tcgen05.ld/st are warp-wide: every lane takes part
+              // by a power of two where there is something to bring along: exact, for the weights of the first half too
+              const float m_new = !need ? m_ref : m_ref == -INFINITY ? mx : m_ref + ceilf(mx - m_ref);
+              const float cf = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
+              if (!first_tile) {
+                // O may only be rescaled once every product into it has finished
+                if (!wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < HD; c0 += 16) {
+                  float o[16];
+                  tc::tmem_ld16(o_mine + c0, o);
+#pragma unroll
+                  for (int e = 0; e < 16; e++) o[e] *= cf;
+                  tmem_st16(o_mine + c0, o);
+                }
+              }
+              if (k0 > 0) {   // weights already written: pairs of fp16, or of bf16
+                float la, lb;
+                unpack2(lq[0], la, lb);
+                lq[0] = pack2(la * cf, lb * cf);
+                unpack2(lq[1], la, lb);
+                lq[1] = pack2(la * cf, lb * cf);
+                const uint32_t by = half ? pack_f16(cf, cf) : __float_as_uint(cf) >> 16 | (__float_as_uint(cf) & 0xFFFF0000u);
+#pragma unroll 1
+                for (int c0 = 0; c0 < (half ? k0 / 2 : k0); c0 += 16) {
+                  float w[16];
+                  tmem_wait_st();
+                  tc::tmem_ld16(st + c0, w);
+                  uint32_t v[16];
+#pragma unroll
+                  for (int e = 0; e < 16; e++) {
+                    const uint32_t x = __float_as_uint(w[e]);
+                    v[e] = half ? hmul2(x, by) : mul_bf16x2(x, by);
+                  }
+                  tmem_st16(st + c0, v);
+                }
+              }
+              l *= cf;
+              m_ref = m_new;
+            }
+            // every score so far -inf: weight 0, not NaN.  fp16 weights are p 2^7, and V has 2^-7
+            const float nm = m_ref == -INFINITY ? 0.f : (half ? 7.f : 0.f) - m_ref;
+            const uint64_t sl22 = pack2(sl2, sl2), nm2 = pack2(nm, nm);
             if (half) {
 #pragma unroll
               for (int c0 = 0; c0 < W; c0 += 16) {
@@ -596,8 +638,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
                   lq[(e >> 1) & 1] = add2(lq[(e >> 1) & 1], pack2(p0, p1));
                   split_trunc(p0, p1, hi[e / 2], lo[e / 2]);
                 }
-                const int c = k0 + c0;
-                const uint32_t pt = st + (c & ~31) + (c & 16) / 2;   // 32 keys: 16 columns of hi, 16 of lo
+                const uint32_t pt = st + k0 + (c0 & ~31) + (c0 & 16) / 2;   // 32 keys: 16 columns of hi, 16 of lo
                 tmem_st8(pt, hi);
                 tmem_st8(pt + 16, lo);
               }

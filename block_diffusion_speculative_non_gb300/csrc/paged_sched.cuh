@@ -4,7 +4,8 @@
 // head.  It has the key tiles that hold a key some row of it sees: those of the first `sinks` positions, those from the first
 // row's window to the end, then the block's keys.  The lengths are known on the device alone, and requests differ in them, so
 // every CTA adds them up and takes an even run of all units' tiles (the first runs one tile more than the others): whatever the
-// lengths, the SMs finish together.  A unit inside one run is finished there; of a unit that runs share, each leaves a partial: the run
+// lengths, the SMs finish together.  A unit also counts for what it costs besides its tiles (its queries, its way out).  A unit inside one run is
+// finished there; of a unit that runs share, each leaves a partial: the run
 // that starts it in slot 2 c + 1, the ones that go on with it in slot 2 c.  A unit without a key counts as one empty tile, so
 // that its rows are written too.
 #pragma once
@@ -60,11 +61,13 @@ struct GroupDiv {
 struct PagedShape {
   int L, lb, grp, nkv, rows, tiles, window, sinks, causal;   // rows of a row tile, row tiles of a request and kv head
   int kt_shift;                                              // tiles of 2^kt_shift keys
+  int unit_cost;                                             // what a unit costs besides its tiles, in tiles
   GroupDiv by_grp;
   __host__ __device__ int kt() const { return 1 << kt_shift; }
 };
-inline PagedShape paged_shape(int L, int lb, int grp, int nkv, int rows, int window, int sinks, int causal, int kt) {
-  PagedShape s{L, lb, grp, nkv, rows, ceil_div(L * grp, rows), window, sinks, causal, 0, {}};
+inline PagedShape paged_shape(int L, int lb, int grp, int nkv, int rows, int window, int sinks, int causal, int kt,
+                              int unit_cost) {
+  PagedShape s{L, lb, grp, nkv, rows, ceil_div(L * grp, rows), window, sinks, causal, 0, unit_cost, {}};
   while (s.kt() < kt) s.kt_shift++;
   s.by_grp.set(grp);
   return s;
@@ -109,17 +112,17 @@ __host__ __device__ inline bool tile_full(const PagedShape& s, const PagedUnit& 
   return t.valid == s.kt() && (!s.window || last < s.sinks || u.p1 - t.pos < s.window) && (!s.causal || last <= u.p0);
 }
 
-// Tiles of a request in one kv head.
+// Tiles of a request in one kv head, with what its units cost besides.
 __host__ __device__ inline long long request_tiles(const PagedShape& s, int T) {
   PagedUnit u;
   if (!s.window && !s.causal) {
     unit_tiles(s, T, 0, u);
-    return (long long)s.tiles * u.len();
+    return (long long)s.tiles * (u.len() + s.unit_cost);
   }
   long long n = 0;
   for (int rt = 0; rt < s.tiles; rt++) {
     unit_tiles(s, T, rt, u);
-    n += u.len();
+    n += u.len() + s.unit_cost;
   }
   return n;
 }
@@ -160,16 +163,31 @@ struct PagedWalk {
     PagedUnit u;
     if (!s.window && !s.causal) {
       unit_tiles(s, lens(b), 0, u);
-      rt = imin((int)quotient(rest, u.len()), s.tiles - 1);
-      rest -= (long long)rt * u.len();
+      rt = imin((int)quotient(rest, u.len() + s.unit_cost), s.tiles - 1);
+      rest -= (long long)rt * (u.len() + s.unit_cost);
     } else {
       for (rt = 0; rt + 1 < s.tiles; rt++) {
         unit_tiles(s, lens(b), rt, u);
-        if (rest < u.len()) break;
-        rest -= u.len();
+        if (rest < u.len() + s.unit_cost) break;
+        rest -= u.len() + s.unit_cost;
       }
+      unit_tiles(s, lens(b), rt, u);
     }
     off = (int)rest;
+    if (off >= u.len()) {   // among what the unit costs besides: the run starts with the next one
+      x += imax(1, u.len() + s.unit_cost - off);
+      step();
+    }
+  }
+  __host__ __device__ void step() {   // to the next unit
+    off = 0;
+    if (++rt == s.tiles) {
+      rt = 0;
+      if (++g == s.nkv) {
+        g = 0;
+        b++;
+      }
+    }
   }
   __host__ __device__ long long run_start(int i) const { return i * each_run + (i < longer ? i : longer); }
   __host__ __device__ int run_of(long long t) const {
@@ -187,15 +205,13 @@ struct PagedWalk {
     if (off >= len) off = len - 1;
     t0 = off;
     t1 = (int)(x_end - x < len - off ? off + (x_end - x) : len);
-    last_run = t1 == len ? c : imin(run_of(x + (len - off) - 1), G - 1);
-    x += t1 - t0;
-    off = 0;
-    if (++rt == s.tiles) {
-      rt = 0;
-      if (++g == s.nkv) {
-        g = 0;
-        b++;
-      }
+    if (t1 == len) {
+      last_run = c;
+      x += len + s.unit_cost - off;
+      step();
+    } else {
+      last_run = imin(run_of(x + (len - off) - 1), G - 1);
+      x = x_end;
     }
     return true;
   }

@@ -89,9 +89,9 @@ int fpd_test_weight_shares(int batch, int nkv, const int32_t* counted, const int
                            int32_t* units, int32_t* n_units);
 /* Host only: the parts of units that run `run` of `runs` of fpd_paged_attention walks, {request, kv head, row tile, first tile,
  * tile behind the last, the unit's tiles (1 for one without a key), the run that ends the unit} each.  rows: of a row tile;
- * key_tile: keys of a tile; counted, walked: as above. */
+ * key_tile: keys of a tile; unit_cost: tiles that a unit counts for besides its own; counted, walked: as above. */
 int fpd_test_paged_walk(int batch, int L, int block_keys, int group, int nkv, int rows, int window, int sinks, int causal,
-                        int key_tile, const int32_t* counted, const int32_t* walked, int runs, int run, int max_parts,
+                        int key_tile, int unit_cost, const int32_t* counted, const int32_t* walked, int runs, int run, int max_parts,
                         int32_t* parts, int32_t* n_parts);
 /* Host only: the key tiles of one unit, {in the pages (1) or the block (0), first slot or block key, keys, position of the first
  * key, every row sees every key of the whole tile} each. */

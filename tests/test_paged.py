@@ -156,14 +156,14 @@ def test_binding_checks_tensors(fpd):
 
 # ---- how the key tiles are shared out ------------------------------------------------------------------------------------
 
-def walk(fpd, lens, L, lb, grp, nkv, rows, window, sinks, causal, kt, runs, walked=None, most=4000):
+def walk(fpd, lens, L, lb, grp, nkv, rows, window, sinks, causal, kt, cost, runs, walked=None, most=4000):
     f, P, I = fpd.lib().fpd_test_paged_walk, ctypes.POINTER(ctypes.c_int32), ctypes.c_int
-    f.argtypes = [I] * 10 + [P, P, I, I, I, P, P]
+    f.argtypes = [I] * 11 + [P, P, I, I, I, P, P]
     a, b = ((ctypes.c_int32 * len(lens))(*v) for v in (lens, walked or lens))
     out, n = (ctypes.c_int32 * (7 * most))(), ctypes.c_int32()
     got = []
     for c in range(runs):
-        assert f(len(lens), L, lb, grp, nkv, rows, window, sinks, causal, kt, a, b, runs, c, most, out, ctypes.byref(n)) == 0
+        assert f(len(lens), L, lb, grp, nkv, rows, window, sinks, causal, kt, cost, a, b, runs, c, most, out, ctypes.byref(n)) == 0
         got.append([tuple(out[7 * i:7 * i + 7]) for i in range(n.value)])
     return got
 
@@ -208,13 +208,14 @@ def test_a_units_tiles_hold_what_its_rows_see(fpd, shape, blk):
                             assert see[j0:j1 + 1, pos:pos + valid].any()
 
 
+@pytest.mark.parametrize("cost", [0, 3])
 @pytest.mark.parametrize("lens", [[0], [1], [130, 0, 64, 1000], [5] * 300, [(97 * i) % 700 for i in range(75)]])
-def test_walks_cover_every_tile_once(fpd, lens):
+def test_walks_cover_every_tile_once(fpd, lens, cost):
     for L, lb, grp, rows, nkv, (window, sinks, causal), kt in [
             (1, 1, 4, 16, 2, (0, 0, 0), 64), (16, 16, 4, 64, 8, (0, 0, 0), 128), (30, 0, 5, 64, 1, (100, 70, 1), 64),
             (30, 30, 5, 64, 3, (0, 0, 1), 64)]:
         for runs in (1, 7, 304):
-            got = walk(fpd, lens, L, lb, grp, nkv, rows, window, sinks, causal, kt, runs)
+            got = walk(fpd, lens, L, lb, grp, nkv, rows, window, sinks, causal, kt, cost, runs)
             flat = [(p, c) for c, parts in enumerate(got) for p in parts]
             want = [(b, g, rt, max(1, len(tiles(fpd, T, rt, L, lb, grp, rows, window, sinks, causal, kt))))
                     for b, T in enumerate(lens) for g in range(nkv) for rt in range(-(-L * grp // rows))]
@@ -229,8 +230,9 @@ def test_walks_cover_every_tile_once(fpd, lens):
                     ends = [e for (p, e) in flat if p[:3] == (b, g, rt) and p[4] == n]
                     assert ends == [last]
             assert i == len(want) and at == 0
-            per = [sum(p[4] - p[3] for p in parts) for parts in got]
-            assert max(per) - min(p for p in per if p or runs > sum(per)) <= 1
+            # a run's tiles and the ends of its units, within the even share
+            share = -(-sum(w[3] + cost for w in want) // min(runs, sum(w[3] + cost for w in want)))
+            assert max(sum(p[4] - p[3] for p in parts) + cost * sum(p[4] == p[5] for p in parts[:-1]) for parts in got) <= share
 
 
 def test_walks_stay_in_bounds_under_lengths_that_change(fpd):
@@ -240,7 +242,7 @@ def test_walks_stay_in_bounds_under_lengths_that_change(fpd):
         lens = rng.integers(0, 2000, n).tolist()
         other = [0] * n if k % 3 == 0 else rng.integers(0, 2000, n).tolist()
         for window, sinks, causal in ((0, 0, 0), (50, 3, 1)):
-            for c, parts in enumerate(walk(fpd, lens, 20, 20, 5, 2, 64, window, sinks, causal, 64, 9, other)):
+            for c, parts in enumerate(walk(fpd, lens, 20, 20, 5, 2, 64, window, sinks, causal, 64, k % 4, 9, other)):
                 for b, g, rt, t0, t1, m, last in parts:
                     assert 0 <= b < n and 0 <= g < 2 and 0 <= rt < 2 and 0 <= t0 < t1 <= m and c <= last < 9
 
