@@ -26,7 +26,10 @@ namespace {
 using namespace attn_tc;
 
 constexpr int QR = 128, KT = kPagedTcTile;
-constexpr int KST = 2, VST = 3;
+constexpr int KST = 2;
+template <bool INT4>
+constexpr int kVst = INT4 ? 2 : 3;     // V slots; 4-bit pages leave one to the codes
+constexpr int kRawSlots = 3;           // codes and scales of a tile's K or V
 constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
 constexpr uint32_t kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
@@ -39,10 +42,11 @@ struct TcArgs {
   int runs, npt, rpt;   // positions and rows of a lane
 };
 
-template <int HD>
+template <int HD, bool INT4>
 struct Lay {
-  static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64;
-  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, STAT = V + VST * TILE, BAR = STAT + 2 * QR * 4;
+  static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64, VST = kVst<INT4>;
+  static constexpr int RAW_BYTES = KT * (HD / 2 + HD / 16);
+  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, RAW = V + VST * TILE, STAT = RAW + (INT4 ? kRawSlots * RAW_BYTES : 0), BAR = STAT + 2 * QR * 4;
 };
 enum {
   B_Q = 0,
@@ -50,22 +54,24 @@ enum {
   B_KF = B_QE + 2,
   B_KE = B_KF + KST,
   B_VF = B_KE + KST,
-  B_VE = B_VF + VST,
-  B_SF = B_VE + VST,
+  B_VE = B_VF + 3,
+  B_SF = B_VE + 3,
   B_PF = B_SF + 2,
   B_PV = B_PF + 2,
   B_END = B_PV + 2,
   B_X = B_END + 1,   // the softmax warps, in units whose keys the lanes share
-  B_N = B_X + 1
+  B_RF = B_X + 1,    // codes: full, empty [slot]
+  B_RE = B_RF + kRawSlots,
+  B_N = B_RE + kRawSlots
 };
-template <int HD>
+template <int HD, bool INT4>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)Lay<HD>::BAR + 8 * B_N + 16;
+  return 1024 + (size_t)Lay<HD, INT4>::BAR + 8 * B_N + 16;
 }
-static_assert(smem_bytes<128>() <= 232448, "tile set exceeds the shared memory of one CTA");
+static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<128, true>() <= 232448, "tile set exceeds the shared memory of one CTA");
 
-// bf16: 11 warps, 0 and 2 TMA producers of K and Q, and of V, 1 the products, 3.. softmax.  4 bits: 16 warps, 0 and
-// 2..7 decode, 8.. softmax, which takes the scores in two halves (128 registers a thread).
+// bf16: 11 warps, 0 and 2 TMA producers of K and Q, and of V, 1 the products, 3.. softmax.  4 bits: 16 warps, 0
+// copies codes, 2..7 decode, 8.. softmax, which takes the scores in two halves (128 registers a thread).
 template <bool INT4>
 struct Roles {
   static constexpr int THREADS = INT4 ? 512 : 352, SOFTMAX = INT4 ? 8 : 3;
@@ -106,7 +112,8 @@ struct Seg {
 
 template <int HD, bool INT4>
 __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const __grid_constant__ TcArgs p) {
-  using S = Lay<HD>;
+  using S = Lay<HD, INT4>;
+  constexpr int VST = S::VST;
   using Ro = Roles<INT4>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -136,6 +143,10 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     for (int s = 0; s < VST; s++) {
       tc::mbar_init(bar(B_VF + s), kFill);
       tc::mbar_init(bar(B_VE + s), 1);
+    }
+    for (int s = 0; s < kRawSlots; s++) {
+      tc::mbar_init(bar(B_RF + s), 1);
+      tc::mbar_init(bar(B_RE + s), 4);
     }
     tc::mbar_init(bar(B_END), 1);
     tc::mbar_init(bar(B_X), 8);
@@ -238,47 +249,61 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       for (int t = 0; t < 2; t++)
         if (nq[t] > 0) tc::mbar_wait(bar(B_Q + t), (nq[t] & 1) ^ 1);
     }
+  } else if (INT4 && warp == 0) {
+    // ---------------- codes of the context tiles, K and V in turn, by bulk copies: lanes 2 i + part copy from page i ----------------
+    const int kp = min(KT, a.pg.page), part = lane & 1, pi = lane >> 1;   // part: codes, scales
+    const uint32_t ring = tc::smem_u32(smem + S::RAW);
+    const uint32_t w = part ? HD / 16 : HD / 2;
+    int h = 0;   // halves of tiles so far
+    bool ok = true;
+    auto page_for = [&](const Seg& s, int i) {
+      if (i >= s.n_tiles || pi >= KT / 16) return 0;
+      const PagedTile t = s.tile(i);
+      return t.ctx && pi * kp < t.valid ? page_of(a.pg, s.u.b, t.k0 + pi * kp) : 0;
+    };
+    while (ok && !*abort_flag && next(sg)) {
+      int id = page_for(sg, 0);
+#pragma unroll 1
+      for (int i = 0; i < sg.n_tiles && ok; i++) {
+        const PagedTile t = sg.tile(i);
+        if (!t.ctx) break;
+        const int id_now = id, in = t.k0 & (a.pg.page - 1);
+        id = page_for(sg, i + 1);
+        const int rows = pi < KT / 16 ? min(kp, ceil_div(t.valid, 16) * 16 - pi * kp) : 0;   // whole groups of 16 positions
+        const uint32_t bytes = rows > 0 && id_now >= 0 ? rows * w : 0, total = __reduce_add_sync(0xffffffffu, bytes);
+        const uint32_t at = (part ? KT * (HD / 2) : 0) + pi * kp * w;
+#pragma unroll 1
+        for (int v = 0; v < 2; v++, h++) {
+          const int s = h % kRawSlots;
+          if (h >= kRawSlots) ok = wait_bar(bar(B_RE + s), ((h / kRawSlots) & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+          if (!ok) break;
+          if (rows > 0 && id_now < 0) {   // a page that is none: zeros
+            for (uint32_t j = 0; j < rows * w; j += 16)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + s * S::RAW_BYTES + at + j), "r"(0) : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar(B_RF + s), total);
+          __syncwarp();
+          if (bytes)
+            tc::bulk_load(ring + s * S::RAW_BYTES + at, slab_of(a.pg, id_now, v, sg.u.g) + (part ? a.pg.page * (HD / 2) : 0) + in * w, bytes,
+                          bar(B_RF + s));
+        }
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (*abort_flag)
+      for (int i = max(0, h - kRawSlots); i < h; i++) tc::mbar_wait(bar(B_RF + i % kRawSlots), (i / kRawSlots) & 1);
   } else if (INT4 && warp < Ro::SOFTMAX && warp != 1) {
     // ---------------- decoding warps ----------------
-    // A tile is eight items, 32 rows of K or of V each; the warps take turns at them, a thread a row.  An item's page is looked up
-    // three turns ahead, its codes are requested into L2 two turns ahead and into registers one turn ahead.  One copy of the
-    // code for all turns: unrolled, a third of the stalls were for instructions.
-    constexpr int NW = 7;
-    const int wd = warp == 0 ? 0 : warp - 1;
+    // A tile's K is four items of 32 rows, then its V; the six warps take turns at them, a thread a row.  One copy of the code for
+    // all turns, and loops over a row's chunks: unrolled, a third of the stalls were for instructions.
+    constexpr int NW = 6;
+    const int wd = warp - 2;
     const uint32_t qs = tc::smem_u32(smem + S::Q), ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V);
-    int n = 0, nq[2] = {0, 0};
-    struct Raw {
-      uint4 code[HD / 32];
-      uint32_t scale[HD / 64];
-    };
-    auto page_for = [&](const Seg& s, int e) {   // of this thread's row of item e; -1: none
-      if (e >= 8 * s.n_tiles) return -1;
-      const PagedTile t = s.tile(e >> 3);
-      const int r = (e & 3) * 32 + lane;
-      return t.ctx && r < t.valid ? page_of(a.pg, s.u.b, t.k0 + r) : -1;
-    };
-    auto fetch = [&](const Seg& s, int e, int id, Raw& w) {   // a row of a context tile; zeros where there is none
-#pragma unroll
-      for (int j = 0; j < HD / 32; j++) w.code[j] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < HD / 64; j++) w.scale[j] = 0;
-      if (id < 0) return;
-      const int in = (s.tile(e >> 3).k0 + (e & 3) * 32 + lane) & (a.pg.page - 1);
-      const uint8_t* slab = slab_of(a.pg, id, (e >> 2) & 1, s.u.g);
-      const uint4* code = reinterpret_cast<const uint4*>(slab + in * (HD / 2));
-      const uint32_t* scale = reinterpret_cast<const uint32_t*>(slab + a.pg.page * (HD / 2) + in * (HD / 16));
-#pragma unroll
-      for (int j = 0; j < HD / 32; j++) w.code[j] = __ldg(code + j);
-#pragma unroll
-      for (int j = 0; j < HD / 64; j++) w.scale[j] = __ldg(scale + j);
-    };
-    auto to_l2 = [&](const Seg& s, int e, int id) {
-      if (id < 0) return;
-      const int in = (s.tile(e >> 3).k0 + (e & 3) * 32 + lane) & (a.pg.page - 1);
-      const uint8_t* slab = slab_of(a.pg, id, (e >> 2) & 1, s.u.g);
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(slab + in * (HD / 2)));
-      if ((lane & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(slab + a.pg.page * (HD / 2) + in * (HD / 16)));
-    };
+    const uint32_t rs = tc::smem_u32(smem + S::RAW);
+    int n = 0, nh = 0, nq[2] = {0, 0};   // tiles, halves of context tiles and Q loads so far
     // chunk of 8 dims ch of row r in a tile of 64-dim atoms
     auto put = [&](uint32_t row, int ch, uint4 v) {
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"((row ^ ((ch & 7) << 4)) + (ch >> 3) * ATOM_BYTES), "r"(v.x), "r"(v.y),
@@ -305,23 +330,42 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
                                                                        __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632)));
       }
     };
-    auto put_codes = [&](uint32_t to, const Raw& w, bool is_v) {
-#pragma unroll
-      for (int q = 0; q < HD / 16; q++) {   // a group of 16 dims: two words
-        const uint32_t byte = (w.scale[q / 4] >> (8 * (q & 3))) & 0xFF;
-        const uint32_t c0 = q & 1 ? w.code[q / 2].z : w.code[q / 2].x, c1 = q & 1 ? w.code[q / 2].w : w.code[q / 2].y;
-        uint32_t x[4], y[4];
+    // row r of the codes in a slot (past `valid`: zeros) into row r of a tile.  A row is HD / 32 chunks of 16 bytes; lanes begin at
+    // different ones, so that a load of 8 rows has no bank twice.
+    auto put_codes = [&](uint32_t tile, uint32_t raw, int r, bool valid, bool is_v) {
+      constexpr int CH = HD / 32;
+      const uint32_t to = row_at(tile, r);
+      unsigned long long scales;   // a byte for 16 dims
+      if constexpr (HD == 128) {
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(scales) : "r"(raw + KT * (HD / 2) + r * 8));
+      } else {
+        uint32_t x;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(raw + KT * (HD / 2) + r * 4));
+        scales = x;
+      }
+      if (!valid) scales = 0;   // what is stale stands for nothing
+#pragma unroll 1
+      for (int j = 0; j < CH; j++) {
+        const int ch = (j + (HD == 128 ? r >> 1 : r >> 2)) & (CH - 1);
+        uint32_t c[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + r * (HD / 2) + ch * 16));
+        const uint32_t two = (uint32_t)(scales >> (16 * ch)) & 0xFFFF;
+        uint32_t x[4][4];
         if (is_v) {
-          const Scale2 s(byte * 0x00800080u);
-          decode4(c0, s, x);
-          decode4(c1, s, y);
+          const Scale2 s0((two & 0xFF) * 0x00800080u), s1((two >> 8) * 0x00800080u);
+          decode4(c[0], s0, x[0]);
+          decode4(c[1], s0, x[1]);
+          decode4(c[2], s1, x[2]);
+          decode4(c[3], s1, x[3]);
         } else {
-          const Scale2Bf s(byte);
-          decode4_bf16(c0, s, x);
-          decode4_bf16(c1, s, y);
+          const Scale2Bf s0(two & 0xFF), s1(two >> 8);
+          decode4_bf16(c[0], s0, x[0]);
+          decode4_bf16(c[1], s0, x[1]);
+          decode4_bf16(c[2], s1, x[2]);
+          decode4_bf16(c[3], s1, x[3]);
         }
-        put(to, 2 * q, make_uint4(x[0], x[1], x[2], x[3]));
-        put(to, 2 * q + 1, make_uint4(y[0], y[1], y[2], y[3]));
+#pragma unroll
+        for (int i = 0; i < 4; i++) put(to, 4 * ch + i, make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]));
       }
     };
     auto done = [&](int b) {   // this warp's rows are written, for the tensor core to read
@@ -336,53 +380,48 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       return ok;
     };
     while (ok && !*abort_flag && next(sg)) {
-      Raw raw, ahead;
-      int id1 = page_for(sg, wd), id2 = page_for(sg, wd + NW), id3 = page_for(sg, wd + 2 * NW);
-      fetch(sg, wd, id1, raw);
-      id1 = id2;
-      id2 = id3;
-      id3 = page_for(sg, wd + 3 * NW);
       const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
+      const int nc = min(sg.n_tiles, max(0, sg.u.ns + sg.u.nm - sg.t0));   // context tiles; the block's follow
       bool q_done = false;
 #pragma unroll 1
       for (int e = wd; e < 8 * sg.n_tiles && ok; e += NW) {
-          fetch(sg, e + NW, id1, ahead);
-          to_l2(sg, e + 2 * NW, id2);
-          id1 = id2;
-          id2 = id3;
-          id3 = page_for(sg, e + 4 * NW);
-          if (!q_done && (e >= 4 || wd < 4)) {   // the warps that start with the first K tile take Q first
-            q_done = true;
-            for (int l = 0; l < 2 && ok; l++) {
-              if (sg.lane_tiles(l) == 0) continue;
-              if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
-              for (int k = wd; k < 4; k += NW) {
-                const int q0 = sg.row0 + (sg.keys ? 0 : l * p.rpt);
-                put_bf16(qs + l * S::TILE, k * 32, [&](int r) -> const bf16* {
-                  const int qi = q0 + r, j = sh.by_grp.div(qi);
-                  return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg.u.b * a.L + j) * a.nq + sg.u.g * grp + qi - j * grp) * HD : nullptr;
-                });
-                done(B_Q + l);
-              }
-              nq[l]++;
-            }
-            if (!ok) break;
+        if (!q_done) {   // Q beside the first K tile: its eight items of 32 rows, from the last warp on
+          q_done = true;
+          for (int i = 0; i < 8 && ok; i++) {
+            const int l = i >> 2, k = i & 3;
+            if (sg.lane_tiles(l) == 0 || NW - 1 - i % NW != wd) continue;
+            if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
+            const int q0 = sg.row0 + (sg.keys ? 0 : l * p.rpt);
+            put_bf16(qs + l * S::TILE, k * 32, [&](int r) -> const bf16* {
+              const int qi = q0 + r, j = sh.by_grp.div(qi);
+              return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg.u.b * a.L + j) * a.nq + sg.u.g * grp + qi - j * grp) * HD : nullptr;
+            });
+            done(B_Q + l);
           }
-          const PagedTile t = sg.tile(e >> 3);
-          const bool is_v = (e >> 2) & 1;
-          const int i = n + (e >> 3), turn = is_v ? i / VST : i / KST, s = i - turn * (is_v ? VST : KST);
-          if (turn > 0 && !wait((is_v ? B_VE : B_KE) + s, (turn & 1) ^ 1)) break;
-          const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
-          if (t.ctx) {
-            put_codes(row_at(tile, (e & 3) * 32 + lane), raw, is_v);
-          } else {
-            const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
-            put_bf16(tile, (e & 3) * 32, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
-          }
-          done((is_v ? B_VF : B_KF) + s);
-          raw = ahead;
+          for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
+          if (!ok) break;
+        }
+        const PagedTile t = sg.tile(e >> 3);
+        const bool is_v = (e >> 2) & 1;
+        const int i = n + (e >> 3), turn = is_v ? i / VST : i / KST, s = i - turn * (is_v ? VST : KST), r0 = (e & 3) * 32;
+        if (turn > 0 && !wait((is_v ? B_VE : B_KE) + s, (turn & 1) ^ 1)) break;
+        const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
+        if (t.ctx) {
+          const int h = nh + (e >> 2), slot = h % kRawSlots;
+          if (!wait(B_RF + slot, (h / kRawSlots) & 1)) break;
+          put_codes(tile, rs + slot * S::RAW_BYTES, r0 + lane, r0 + lane < t.valid, is_v);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(B_RE + slot));
+        } else {
+          const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
+          put_bf16(tile, r0, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
+        }
+        done((is_v ? B_VF : B_KF) + s);
       }
+      if (!q_done)   // fewer items than warps
+        for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
       n += sg.n_tiles;
+      nh += 2 * nc;
     }
     if (!ok) *abort_flag = 1;
   } else if (warp == 1) {
@@ -765,7 +804,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
 
 template <int HD, bool INT4>
 cudaError_t attribute() {
-  return cudaFuncSetAttribute(paged_tc_kernel<HD, INT4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<HD>());
+  return cudaFuncSetAttribute(paged_tc_kernel<HD, INT4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<HD, INT4>());
 }
 
 }  // namespace
@@ -801,11 +840,11 @@ cudaError_t launch_paged_tc(const PagedAttn& a, const PagedShape& s, const Paged
       if (e == cudaSuccess) e = make_tmap_nd(&p.tm_vblk, a.vblk, 2, bd, bs, bb);
     }
     if (e != cudaSuccess) return e;
-    return h == 128 ? launch_k(paged_tc_kernel<128, false>, pl.grid, Roles<false>::THREADS, smem_bytes<128>(), st, p)
-                    : launch_k(paged_tc_kernel<64, false>, pl.grid, Roles<false>::THREADS, smem_bytes<64>(), st, p);
+    return h == 128 ? launch_k(paged_tc_kernel<128, false>, pl.grid, Roles<false>::THREADS, smem_bytes<128, false>(), st, p)
+                    : launch_k(paged_tc_kernel<64, false>, pl.grid, Roles<false>::THREADS, smem_bytes<64, false>(), st, p);
   }
-  return h == 128 ? launch_k(paged_tc_kernel<128, true>, pl.grid, Roles<true>::THREADS, smem_bytes<128>(), st, p)
-                  : launch_k(paged_tc_kernel<64, true>, pl.grid, Roles<true>::THREADS, smem_bytes<64>(), st, p);
+  return h == 128 ? launch_k(paged_tc_kernel<128, true>, pl.grid, Roles<true>::THREADS, smem_bytes<128, true>(), st, p)
+                  : launch_k(paged_tc_kernel<64, true>, pl.grid, Roles<true>::THREADS, smem_bytes<64, true>(), st, p);
 }
 
 }  // namespace fpd
