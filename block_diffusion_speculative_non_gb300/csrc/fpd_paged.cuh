@@ -100,7 +100,6 @@ struct VerifySampled {
   int32_t *accept, *committed, *valid;
   int batch, L, vocab;
 };
-cudaError_t verify_sampled_init_attributes();
 cudaError_t launch_verify_sampled(const VerifySampled& a, cudaStream_t st);
 
 }  // namespace fpd

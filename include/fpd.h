@@ -511,7 +511,7 @@ size_t fpd_paged_attention_workspace_bytes(int batch, int block_len, int n_q_hea
  *   the last id comes from r = max(p_n - q_n, 0) after a refusal (from p_n where that is 0 everywhere), from p_{L-1} when all were
  *   kept: the lowest id whose running sum r(0) + .. + r(id) exceeds u_{L-1} times the sum over all ids
  *   accept_len = n + 1, committed = d_1..d_n and the last id, then -1; valid = (n == L - 1), as fpd_verify's text mode
- * Probabilities need not sum to 1; entries that are negative or NaN count as 0.  p - q is taken exactly and sums to about 2^-44.
+ * Probabilities need not sum to 1; entries that are negative or NaN count as 0.  p - q is taken exactly, sums to about 2^-44.
  * A row without any probability gives id -1 (FPD_CHECK_NO_LEGAL_ID); a drafted id outside [0, vocab) is refused
  * (FPD_CHECK_BAD_TOKEN).
  *   draft        device [B, L - 1] int32
