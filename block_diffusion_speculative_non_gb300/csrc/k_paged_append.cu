@@ -2,8 +2,8 @@
 //
 //   key of row r at position pos:  k'_i = k_i cos_i - k_{i + h/2} sin_i,  k'_{i + h/2} = k_{i + h/2} cos_i + k_i sin_i,  i < h/2
 //
-// A thread has 16 dims of one row and kv head, 8 of each half, so that a rotation stays inside it; two neighbours have a 4-bit
-// group.  The loads go out before the row's request, slot and page are known.  Bound by the copy: 4 h bytes in and 2 h (or
+// A thread has 16 dims of a row, 8 of each half, so that a rotation stays inside it, in one or more kv heads of K and V; two
+// neighbours have a 4-bit group.  The first loads go out before the row's request, slot and page are known.  Bound by the copy: 4 h bytes in and 2 h (or
 // 9 h / 16) bytes out per row and kv head, K or V.
 #include "fpd_paged.cuh"
 
@@ -78,64 +78,85 @@ __device__ __forceinline__ uint32_t quant8(const float (&x)[8], int& byte) {
   return w;
 }
 
+// Thread: 16 dims (e) of row r, in slabs (K, then V heads) s0 .. of the row, four at a time.
 template <int H, bool INT4>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ PagedRows a, int row_threads, int rows_per_cta) {
+__global__ void __launch_bounds__(kThreads, INT4 ? 2 : 3) append_kernel(const __grid_constant__ PagedRows a, int per) {
   pdl_wait();
   pdl_trigger();
-  constexpr int E = H / 16;   // threads of a row and kv head
-  const int nkv = a.pg.nkv;
-  const int rr = threadIdx.x / row_threads, in_row = threadIdx.x - rr * row_threads;
-  const int r = blockIdx.x * rows_per_cta + rr;
-  const int item = blockIdx.y * row_threads + in_row;        // (K|V, kv head, e) of the row
-  const int slab = item / E, e = item % E;
-  bool ok = rr < rows_per_cta && r < a.total_rows && slab < 2 * nkv;
-  const bool is_v = slab >= nkv;
-  const int g = is_v ? slab - nkv : slab;
-  uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-  if (ok) {
-    const bf16* src = (is_v ? a.v + (size_t)r * a.v_ld : a.k + (size_t)r * a.k_ld) + (size_t)g * H + 8 * e;
-    u0 = __ldcs(reinterpret_cast<const uint4*>(src));
-    u1 = __ldcs(reinterpret_cast<const uint4*>(src + H / 2));
-  }
-  Place w;
-  ok = ok && place_of(a, r, a.rope != nullptr, w);
-  float x0[8], x1[8];
-  unpack8(u0, x0);
-  unpack8(u1, x1);
-  if (ok && !is_v && a.rope) {
-    const float4* cs = reinterpret_cast<const float4*>(a.rope + (size_t)w.pos * (H / 2) + 8 * e);
+  constexpr int E = H / 16, U = 4;   // threads of a row, slabs in flight
+  const int nkv = a.pg.nkv, e = threadIdx.x % E, r = blockIdx.x * (kThreads / E) + threadIdx.x / E;
+  const int s0 = blockIdx.y * per, s1 = min(2 * nkv, s0 + per);
+  const bool here = r < a.total_rows;
+  uint4 u[U][2];
+  auto load = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float4 t = __ldg(cs + i / 2);
-      const float a0 = x0[i], b0 = x1[i], a1 = x0[i + 1], b1 = x1[i + 1];
-      x0[i] = dot2(a0, t.x, b0, -t.y);
-      x1[i] = dot2(b0, t.x, a0, t.y);
-      x0[i + 1] = dot2(a1, t.z, b1, -t.w);
-      x1[i + 1] = dot2(b1, t.z, a1, t.w);
+    for (int i = 0; i < U; i++) {
+      const int g = s + i < nkv ? s + i : s + i - nkv;
+      u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+      if (here && s + i < s1) {
+        const bf16* src = (s + i >= nkv ? a.v + (size_t)r * a.v_ld : a.k + (size_t)r * a.k_ld) + (size_t)g * H + 8 * e;
+        u[i][0] = __ldcs(reinterpret_cast<const uint4*>(src));
+        u[i][1] = __ldcs(reinterpret_cast<const uint4*>(src + H / 2));
+      }
     }
-    u0 = pack8(x0);
-    u1 = pack8(x1);
+  };
+  load(s0);
+  Place w;
+  const bool ok = here && place_of(a, r, a.rope != nullptr, w);
+  const bool turn = ok && a.rope && s0 < nkv;
+  float4 cs[4];   // (cos, sin) of dims 8 e ..
+  if (turn) {
+    const float4* at = reinterpret_cast<const float4*>(a.rope + (size_t)w.pos * (H / 2) + 8 * e);
+#pragma unroll
+    for (int i = 0; i < 4; i++) cs[i] = __ldg(at + i);
   }
-  if (!INT4) {
-    if (!ok) return;
-    bf16* dst = reinterpret_cast<bf16*>(slab_of(a.pg, w.id, is_v, g)) + (size_t)w.in_page * H + 8 * e;
-    *reinterpret_cast<uint4*>(dst) = u0;
-    *reinterpret_cast<uint4*>(dst + H / 2) = u1;
-  } else {
-    unpack8(u0, x0);   // as rounded to bf16
-    unpack8(u1, x1);
-    int s0, s1;
-    const uint32_t c0 = quant8(x0, s0), c1 = quant8(x1, s1);   // every thread: neighbours exchange their maxima
-    if (!ok) return;
-    uint8_t* p = slab_of(a.pg, w.id, is_v, g);
-    uint8_t* code = p + w.in_page * (H / 2) + 4 * e;
-    *reinterpret_cast<uint32_t*>(code) = c0;
-    *reinterpret_cast<uint32_t*>(code + H / 4) = c1;
-    if ((e & 1) == 0) {
-      uint8_t* sc = p + a.pg.page * (H / 2) + w.in_page * (H / 16) + e / 2;
-      sc[0] = (uint8_t)s0;
-      sc[H / 32] = (uint8_t)s1;
+  uint8_t* page = ok ? slab_of(a.pg, w.id, 0, 0) : nullptr;   // the slabs of a page follow one another
+  for (int s = s0; s < s1; s += U) {
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+      if (s + i >= s1) break;   // the same for all threads
+      uint4 u0 = u[i][0], u1 = u[i][1];
+      float x0[8], x1[8];
+      if (turn && s + i < nkv) {
+        unpack8(u0, x0);
+        unpack8(u1, x1);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float4 t = cs[j / 2];
+          const float a0 = x0[j], b0 = x1[j], a1 = x0[j + 1], b1 = x1[j + 1];
+          x0[j] = dot2(a0, t.x, b0, -t.y);
+          x1[j] = dot2(b0, t.x, a0, t.y);
+          x0[j + 1] = dot2(a1, t.z, b1, -t.w);
+          x1[j + 1] = dot2(b1, t.z, a1, t.w);
+        }
+        u0 = pack8(x0);
+        u1 = pack8(x1);
+      }
+      uint8_t* slab = page + (size_t)(s + i) * a.pg.slab_bytes;
+      if (!INT4) {
+        if (ok) {
+          bf16* dst = reinterpret_cast<bf16*>(slab) + (size_t)w.in_page * H + 8 * e;
+          *reinterpret_cast<uint4*>(dst) = u0;
+          *reinterpret_cast<uint4*>(dst + H / 2) = u1;
+        }
+      } else {
+        unpack8(u0, x0);   // as rounded to bf16
+        unpack8(u1, x1);
+        int c0, c1;
+        const uint32_t w0 = quant8(x0, c0), w1 = quant8(x1, c1);   // every thread: neighbours exchange their maxima
+        if (ok) {
+          uint8_t* code = slab + w.in_page * (H / 2) + 4 * e;
+          *reinterpret_cast<uint32_t*>(code) = w0;
+          *reinterpret_cast<uint32_t*>(code + H / 4) = w1;
+          if ((e & 1) == 0) {
+            uint8_t* sc = slab + a.pg.page * (H / 2) + w.in_page * (H / 16) + e / 2;
+            sc[0] = (uint8_t)c0;
+            sc[H / 32] = (uint8_t)c1;
+          }
+        }
+      }
     }
+    if (s + U < s1) load(s + U);
   }
 }
 
@@ -186,8 +207,13 @@ cudaError_t launch_rows(K kernel, const PagedRows& a, cudaStream_t st) {
 
 cudaError_t launch_paged_append(const PagedRows& a, cudaStream_t st) {
   const bool q = a.pg.format == FPD_PAGE_INT4;
-  if (a.pg.h == 128) return launch_rows(q ? append_kernel<128, true> : append_kernel<128, false>, a, st);
-  return launch_rows(q ? append_kernel<64, true> : append_kernel<64, false>, a, st);
+  // few rows: a thread for each slab; many: a thread keeps its angles for a row's slabs, as long as the GPU stays full
+  const int slabs = 2 * a.pg.nkv, e = a.pg.h / 16;
+  const int per = (int)std::min<long long>(slabs, std::max<long long>(1, (long long)a.total_rows * e * slabs / (152 * 1024)));
+  const dim3 grid(ceil_div(a.total_rows, kThreads / e), ceil_div(slabs, per));
+  auto go = [&](auto k) { return launch_k(k, grid, kThreads, 0, st, a, per); };
+  if (a.pg.h == 128) return go(q ? append_kernel<128, true> : append_kernel<128, false>);
+  return go(q ? append_kernel<64, true> : append_kernel<64, false>);
 }
 
 cudaError_t launch_paged_read(const PagedRows& a, cudaStream_t st) {

@@ -137,7 +137,7 @@ __device__ __forceinline__ int pick(float2 mine, float2 x, float2& start, int la
 }
 
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_sampled_kernel(const __grid_constant__ VerifySampled a, int ctas, int range) {
+__global__ void __launch_bounds__(kThreads, 4) verify_sampled_kernel(const __grid_constant__ VerifySampled a, int ctas, int range) {
   pdl_wait();
   pdl_trigger();
   __shared__ float2 cta_sum, part[kWarps], part2[kWarps];
