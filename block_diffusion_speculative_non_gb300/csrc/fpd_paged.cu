@@ -107,7 +107,7 @@ struct AttnWs {
 };
 AttnWs carve(void* base, int batch, int L, int nq, const fpd_paged_store* s, int sms) {
   AttnWs w{};
-  w.plan = paged_attn_plan(batch, L, nq, s->n_kv_heads, s->table_width * s->page_size, sms);
+  w.plan = paged_attn_plan(batch, L, nq, s->n_kv_heads, s->format, s->table_width * s->page_size, sms);
   const size_t n = (size_t)2 * w.plan.runs * w.plan.rows;
   const size_t lead = align_up((uintptr_t)base, 256) - (uintptr_t)base;   // the workspace itself is 16-byte aligned
   const size_t ml_at = align_up(n * s->head_dim * sizeof(float), 256), desc_at = ml_at + align_up(n * sizeof(float2), 256);

@@ -87,9 +87,9 @@ enum PagedKernel { kPagedStream, kPagedTc };
 struct PagedPlan {
   PagedKernel kernel;
   int rows, tiles;     // rows of a row tile, row tiles of a request and kv head
-  int grid, runs;      // CTAs, and the runs that share the key tiles (of CTAs, or of their warps)
+  int sms, grid, runs; // SMs, CTAs, and the runs that share the key tiles (of CTAs, or of their warps)
 };
-PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int t_cap, int num_sms);
+PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int format, int t_cap, int num_sms);
 cudaError_t paged_attn_init_attributes();
 cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cudaStream_t st);
 

@@ -147,10 +147,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
   }
 }
 
+// Few short units: a CTA each, whose warps have at most four tiles, does without partials and the merge's launch.  (Rows of one position
+// see the same keys, so nothing needs a repair.)
+bool unit_per_cta(const Args& p, const PagedPlan& pl) {
+  const PagedShape& s = p.s;
+  if (s.L > 1 && (s.window || s.causal)) return false;
+  const int kt = s.kt();
+  long long keys_tiles = ceil_div(p.a.pg.cap(), kt);
+  if (s.window) keys_tiles = std::min(keys_tiles, ((long long)s.window + s.L) / kt + 2 + ceil_div(std::min(s.sinks, 1 << 29), kt));
+  const long long units = (long long)p.a.batch * s.nkv * s.tiles;
+  return units <= pl.sms && keys_tiles + ceil_div(s.lb, kt) <= 4 * paged_stream_warps(s.rows, p.a.pg.format);
+}
+
 template <int H>
 cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
-  const cudaError_t e = pl.kernel == kPagedStream ? launch_paged_stream(p.a, p.s, pl, st) : launch_paged_tc(p.a, p.s, pl, st);
-  if (e != cudaSuccess) return e;
+  const bool alone = pl.kernel == kPagedStream && unit_per_cta(p, pl);
+  const cudaError_t e = pl.kernel == kPagedStream ? launch_paged_stream(p.a, p.s, pl, alone, st) : launch_paged_tc(p.a, p.s, pl, st);
+  if (e != cudaSuccess || alone) return e;
   const int rows = std::min(pl.rows, p.a.L * p.s.grp);
   if (pl.kernel == kPagedStream) return launch_k(paged_merge_kernel<H, 1>, dim3(pl.runs, ceil_div(rows, kMergeWarps)), kMergeWarps * 32, 0, st, p);
   return launch_k(paged_merge_kernel<H, 2>, dim3(pl.runs, ceil_div(rows, 2 * kMergeWarps)), kMergeWarps * 32, 0, st, p);
@@ -158,15 +171,16 @@ cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
 
 }  // namespace
 
-PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int t_cap, int num_sms) {
+PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int format, int t_cap, int num_sms) {
   PagedPlan pl{};
+  pl.sms = num_sms;
   const int grp = nq / nkv, n = L * grp;
   pl.kernel = n <= 16 ? kPagedStream : kPagedTc;
   pl.rows = n <= 8 ? 8 : n <= 16 ? 16 : 2 * (128 / grp * grp);
   pl.tiles = ceil_div(n, pl.rows);
   // no more runs than there can be tiles
   const long long most = (long long)batch * nkv * pl.tiles * (ceil_div(t_cap, kPagedTile) + ceil_div(L, kPagedTile));
-  pl.runs = (int)std::min<long long>(most, (long long)num_sms * (pl.kernel == kPagedStream ? paged_stream_warps() : 1));
+  pl.runs = (int)std::min<long long>(most, (long long)num_sms * (pl.kernel == kPagedStream ? paged_stream_warps(pl.rows, format) : 1));
   pl.grid = std::min(num_sms, pl.runs);
   return pl;
 }
@@ -179,9 +193,9 @@ cudaError_t paged_attn_init_attributes() {
 cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cudaStream_t st) {
   Args p;
   p.a = a;
-  // positions stay below 2^30 + 2^26: a longer window hides nothing
+  // positions stay below 2^30 + 2^26: a longer window hides nothing; nor does causal from the only, last position
   constexpr int kFar = 1200000000;
-  p.s = paged_shape(a.L, a.lb, a.nq / a.pg.nkv, a.pg.nkv, pl.rows, a.window > kFar ? 0 : a.window, std::min(a.sinks, kFar), a.causal,
+  p.s = paged_shape(a.L, a.lb, a.nq / a.pg.nkv, a.pg.nkv, pl.rows, a.window > kFar ? 0 : a.window, std::min(a.sinks, kFar), a.causal && a.L > 1,
                     pl.kernel == kPagedTc ? kPagedTcTile : kPagedTile, 2);
   p.runs = pl.runs;
   p.spoilt_words = pl.kernel == kPagedStream ? 1 : 8;

@@ -37,6 +37,7 @@ struct Args {
   PagedAttn a;
   PagedShape s;
   int runs;
+  bool per_cta;   // a CTA has a unit, its warps share the unit's tiles and put it together; no runs, no partials
 };
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -122,7 +123,7 @@ template <int H, int NT, bool INT4>
 struct Ring {
   static constexpr int HALF = INT4 ? KT * (H / 2 + H / 16) : 16 * H * 2;   // bytes of a slot's K or V: 64 or 16 keys
   static constexpr int SLOT = 2 * HALF;
-  static constexpr int WARPS = 8, SLOTS = 3;
+  static constexpr int WARPS = INT4 && NT == 1 ? 12 : 8, SLOTS = INT4 && NT == 1 ? 2 : 3;
   static constexpr int BARS = WARPS * SLOTS * SLOT;
   static constexpr size_t BYTES = 1024 + BARS + WARPS * SLOTS * 8;
 };
@@ -149,9 +150,10 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
   __syncwarp();
   pdl_wait();
   pdl_trigger();
+  const DeviceLens lens{a.ctx_len, a.pg.cap()};
   const int run = blockIdx.x + warp * gridDim.x;
-  if (run >= p.runs) return;
-  PagedWalk<DeviceLens> walk = make_walk(sh, DeviceLens{a.ctx_len, a.pg.cap()}, a.batch, p.runs, run);
+  if (!p.per_cta && run >= p.runs) return;
+  PagedWalk<DeviceLens> walk = p.per_cta ? PagedWalk<DeviceLens>(sh, lens, a.batch, 1, 1, 1) : make_walk(sh, lens, a.batch, p.runs, run);
   const float sl2 = rsqrtf((float)H) * 1.4426950408889634f;
   int4 left = make_int4(-1, 0, 0, 0);
   int cnt = 0;      // slots filled and emptied so far: place in the ring and phase
@@ -161,7 +163,19 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
 
   PagedUnit u;
   int t0, t1, last_run;
-  while (ok && walk.next(u, t0, t1, last_run)) {
+  bool more;
+  if (p.per_cta) {
+    const int bg = blockIdx.x / sh.tiles;
+    u.b = bg / sh.nkv;
+    u.g = bg - u.b * sh.nkv;
+    unit_tiles(sh, lens(u.b), blockIdx.x - bg * sh.tiles, u);
+    t0 = warp * u.tiles() / Rg::WARPS;
+    t1 = (warp + 1) * u.tiles() / Rg::WARPS;
+    more = true;
+  } else {
+    more = walk.next(u, t0, t1, last_run);
+  }
+  for (; ok && more; more = !p.per_cta && walk.next(u, t0, t1, last_run)) {
     const int nt = min(t1, u.tiles());
     State<H, NT> st;
     st.clear();
@@ -545,7 +559,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
     }
 
     // ---- the rows' sums, and out ----
-    const bool whole = t0 == 0 && t1 == u.len();
+    const bool whole = !p.per_cta && t0 == 0 && t1 == u.len();
     const int slot = 2 * run + (t0 == 0 ? 1 : 0);
     bool spoilt = false;
 #pragma unroll
@@ -580,7 +594,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
           }
           if (a.lse && g == 0) a.lse[row] = none ? -INFINITY : (st.m[j][e] + log2f(ul)) * 0.69314718055994531f;
         } else {
-          float* dst = a.o_part + row * H;
+          float* dst = p.per_cta ? reinterpret_cast<float*>(ring) + r * H : a.o_part + row * H;
           if constexpr (INT4) {
 #pragma unroll
             for (int i = 0; i < H / 8; i += 4) *reinterpret_cast<float4*>(dst + H / 8 * g + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
@@ -588,16 +602,47 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
 #pragma unroll
             for (int i = 0; i < H / 8; i++) dst[16 * (i >> 1) + g + 8 * (i & 1)] = x[i];
           }
-          if (g == 0) a.ml[row] = make_float2(st.m[j][e], ul);
+          if (g == 0) (p.per_cta ? reinterpret_cast<float2*>(ring + R * H * 4)[r] : a.ml[row]) = make_float2(st.m[j][e], ul);
         }
       }
     if (whole && __any_sync(0xffffffffu, spoilt)) spoilt_units |= 1u << min(n_units, 31);
     n_units++;
     if (t0 == 0 && t1 < u.len()) left = make_int4(u.b, u.g, u.rt, last_run);
   }
-  if (lane == 0) {
-    a.desc[run] = left;
-    a.spoilt[run] = spoilt_units;
+  if (!p.per_cta) {
+    if (lane == 0) {
+      a.desc[run] = left;
+      a.spoilt[run] = spoilt_units;
+    }
+    return;
+  }
+  __syncthreads();   // the warps' shares, each in its own ring
+  for (int i = tid; i < min(R, nrows - u.rt * R) * (H / 4); i += Rg::WARPS * 32) {
+    const int r = i / (H / 4), d = 4 * (i % (H / 4)), qi = u.rt * R + r;
+    float2 v[Rg::WARPS];
+    float mx = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int w = 0; w < Rg::WARPS; w++) {
+      v[w] = reinterpret_cast<const float2*>(smem + w * ST * Rg::SLOT + R * H * 4)[r];
+      if (v[w].y != 0.f) mx = fmaxf(mx, v[w].x);
+    }
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < Rg::WARPS; w++) {
+      const float by = v[w].y == 0.f ? 0.f : ex2_approx(v[w].x - mx);
+      if (by == 0.f) continue;
+      den += v[w].y * by;
+      const float4 o = *reinterpret_cast<const float4*>(smem + w * ST * Rg::SLOT + (r * H + d) * 4);
+      sum.x += o.x * by, sum.y += o.y * by, sum.z += o.z * by, sum.w += o.w * by;
+    }
+    const bool none = den == 0.f;
+    const float by = none ? 0.f : 1.f / den;
+    const size_t row = (size_t)(u.b * a.L + sh.by_grp.div(qi)) * a.nq + u.g * sh.grp + qi - sh.by_grp.div(qi) * sh.grp;
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(none ? 0.f : sum.y * by), "f"(none ? 0.f : sum.x * by));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(none ? 0.f : sum.w * by), "f"(none ? 0.f : sum.z * by));
+    *reinterpret_cast<uint2*>(a.out + row * H + d) = w;
+    if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
   }
 }
 
@@ -615,14 +660,16 @@ cudaError_t attributes() {
 
 template <int H, bool INT4>
 cudaError_t launch(const Args& p, int num_sms, cudaStream_t st) {
-  const int grid = std::min(p.runs, num_sms);
+  const int grid = p.per_cta ? p.a.batch * p.s.nkv * p.s.tiles : std::min(p.runs, num_sms);
   if (p.s.rows == 8) return launch_k(paged_stream_kernel<H, 1, INT4>, grid, Ring<H, 1, INT4>::WARPS * 32, Ring<H, 1, INT4>::BYTES, st, p);
   return launch_k(paged_stream_kernel<H, 2, INT4>, grid, Ring<H, 2, INT4>::WARPS * 32, Ring<H, 2, INT4>::BYTES, st, p);
 }
 
 }  // namespace
 
-int paged_stream_warps() { return Ring<128, 1, false>::WARPS; }
+int paged_stream_warps(int rows, int format) {
+  return rows == 8 && format == FPD_PAGE_INT4 ? Ring<128, 1, true>::WARPS : Ring<128, 1, false>::WARPS;
+}
 
 cudaError_t paged_stream_init_attributes() {
   cudaError_t e = attributes<128, false>();
@@ -632,12 +679,13 @@ cudaError_t paged_stream_init_attributes() {
   return e;
 }
 
-cudaError_t launch_paged_stream(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, cudaStream_t st) {
+cudaError_t launch_paged_stream(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, bool per_cta, cudaStream_t st) {
   Args p;
   memset(&p, 0, sizeof(p));
   p.a = a;
   p.s = s;
   p.runs = pl.runs;
+  p.per_cta = per_cta;
   const uint64_t h = a.pg.h;
   cudaError_t e = cudaSuccess;
   if (a.pg.format == FPD_PAGE_BF16) {

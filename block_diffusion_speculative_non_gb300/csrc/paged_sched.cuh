@@ -218,8 +218,9 @@ struct PagedWalk {
 };
 
 cudaError_t paged_stream_init_attributes();
-int paged_stream_warps();   // runs per SM
-cudaError_t launch_paged_stream(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, cudaStream_t st);
+int paged_stream_warps(int rows, int format);   // runs per SM
+// per_cta: a CTA for each unit, which leaves no partial
+cudaError_t launch_paged_stream(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, bool per_cta, cudaStream_t st);
 
 cudaError_t paged_tc_init_attributes();
 cudaError_t launch_paged_tc(const PagedAttn& a, const PagedShape& s, const PagedPlan& pl, cudaStream_t st);
