@@ -185,7 +185,8 @@ size_t fpd_paged_attention_workspace_bytes(int batch, int block_len, int n_q_hea
   if (check_store_sizes(store) || check_queries(batch, block_len, n_q_heads, store->n_kv_heads)) return 0;
   int sms = 0;
   if (device_ready(&sms) != cudaSuccess) return 0;
-  return carve(nullptr, batch, block_len, n_q_heads, store, sms).bytes;
+  const AttnWs w = carve(nullptr, batch, block_len, n_q_heads, store, sms);
+  return w.plan.too_large ? 0 : w.bytes;
 }
 
 fpd_status fpd_paged_attention(int batch, int block_len, int n_q_heads, const fpd_paged_store* store, int layer, const void* q,
@@ -205,6 +206,7 @@ fpd_status fpd_paged_attention(int batch, int block_len, int n_q_heads, const fp
   cudaError_t e = device_ready(&sms);
   if (e != cudaSuccess) return cuda_error(e, "device query");
   const AttnWs w = carve(workspace, batch, block_len, n_q_heads, store, sms);
+  if (w.plan.too_large) return refuse(FPD_ERR_SHAPE, "batch %d of %d pages: more key tiles than 31 bits hold", batch, store->table_width);
   if (w.bytes > workspace_bytes) return refuse(FPD_ERR_CAPACITY, "workspace %zu < %zu bytes", workspace_bytes, w.bytes);
   a.q = (const bf16*)q;
   a.kblk = (const bf16*)k_blk;

@@ -322,7 +322,7 @@ extern "C" int fpd_test_paged_walk(int batch, int L, int block_keys, int group, 
     int operator()(int b) const { return v[b]; }
   };
   const PagedShape s = paged_shape(L, block_keys, group, nkv, rows, window, sinks, causal, key_tile, unit_cost);
-  long long sums[kSchedEntries + 1] = {0};
+  int sums[kSchedEntries + 1] = {0};
   const int each = ceil_div(batch, kSchedEntries);
   for (int e = 0; e < kSchedEntries; e++) {
     sums[e + 1] = sums[e];

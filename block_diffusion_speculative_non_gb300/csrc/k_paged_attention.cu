@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
   }
 }
 
+constexpr int kUnitCost = 2;   // what a unit costs besides its tiles, in tiles (0 and 2: 103 and 97 us at four trajectories with a window)
+
 // Few short units: a CTA each, whose warps have at most four tiles, does without partials and the merge's launch.  (Rows of one position
 // see the same keys, so nothing needs a repair.)
 bool unit_per_cta(const Args& p, const PagedPlan& pl) {
@@ -180,6 +182,7 @@ PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int format, int t_c
   pl.tiles = ceil_div(n, pl.rows);
   // no more runs than there can be tiles
   const long long most = (long long)batch * nkv * pl.tiles * (ceil_div(t_cap, kPagedTile) + ceil_div(L, kPagedTile));
+  pl.too_large = most + 2ll * batch * nkv * pl.tiles * (1 + kUnitCost) > INT32_MAX;
   pl.runs = (int)std::min<long long>(most, (long long)num_sms * (pl.kernel == kPagedStream ? paged_stream_warps(pl.rows, format) : 1));
   pl.grid = std::min(num_sms, pl.runs);
   return pl;
@@ -196,7 +199,7 @@ cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cuda
   // positions stay below 2^30 + 2^26: a longer window hides nothing; nor does causal from the only, last position
   constexpr int kFar = 1200000000;
   p.s = paged_shape(a.L, a.lb, a.nq / a.pg.nkv, a.pg.nkv, pl.rows, a.window > kFar ? 0 : a.window, std::min(a.sinks, kFar), a.causal && a.L > 1,
-                    pl.kernel == kPagedTc ? kPagedTcTile : kPagedTile, 2);
+                    pl.kernel == kPagedTc ? kPagedTcTile : kPagedTile, kUnitCost);
   p.runs = pl.runs;
   p.spoilt_words = pl.kernel == kPagedStream ? 1 : 8;
   return a.pg.h == 128 ? launch<128>(p, pl, st) : launch<64>(p, pl, st);

@@ -148,6 +148,13 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
     tc::fence_barrier_init();
   }
   __syncwarp();
+  if (!INT4 && tid == 0) {
+    tc::tma_prefetch(&p.tm_pages);
+    if (a.lb) {
+      tc::tma_prefetch(&p.tm_kblk);
+      tc::tma_prefetch(&p.tm_vblk);
+    }
+  }
   pdl_wait();
   pdl_trigger();
   const DeviceLens lens{a.ctx_len, a.pg.cap()};
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
   if (!p.per_cta && run >= p.runs) return;
   PagedWalk<DeviceLens> walk = p.per_cta ? PagedWalk<DeviceLens>(sh, lens, a.batch, 1, 1, 1) : make_walk(sh, lens, a.batch, p.runs, run);
   const float sl2 = rsqrtf((float)H) * 1.4426950408889634f;
-  int4 left = make_int4(-1, 0, 0, 0);
+  if (!p.per_cta && lane == 0) a.desc[run] = make_int4(-1, 0, 0, 0);
   int cnt = 0;      // slots filled and emptied so far: place in the ring and phase
   bool ok = true;
   unsigned spoilt_units = 0;   // parts of the run, from 31 on together, that came out whole and with something that is no number
@@ -181,54 +188,56 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
     st.clear();
     // ---- queries: row 8 j + g of the tile in the lanes 4 g + c ----
     const bf16* qrow[NT];
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const int qi = u.rt * R + 8 * j + g;
-      qrow[j] = qi < nrows ? a.q + ((size_t)(u.b * a.L + qi / sh.grp) * a.nq + u.g * sh.grp + qi % sh.grp) * H : nullptr;
-    }
     float sc[NT][2];
     uint32_t qf[MT][NT][2];
-    if constexpr (!INT4) {
+    auto load_q = [&]() {   // behind the first copies' requests
 #pragma unroll
       for (int j = 0; j < NT; j++) {
-        sc[j][0] = sc[j][1] = sl2;
-#pragma unroll
-        for (int k = 0; k < MT; k++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) qf[k][j][e] = qrow[j] ? __ldg(reinterpret_cast<const uint32_t*>(qrow[j] + 16 * k + 8 * e + 2 * c)) : 0u;
+        const int qi = u.rt * R + 8 * j + g;
+        qrow[j] = qi < nrows ? a.q + ((size_t)(u.b * a.L + qi / sh.grp) * a.nq + u.g * sh.grp + qi % sh.grp) * H : nullptr;
       }
-    } else {
+      if constexpr (!INT4) {
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-        // dims H / 4 c ..: 8 of them per word of codes; product 2 w + e takes dims (2 e, 2 e + 4) and (2 e + 1, 2 e + 5) of word w
-        float x[H / 4], big = 0.f;
+        for (int j = 0; j < NT; j++) {
+          sc[j][0] = sc[j][1] = sl2;
 #pragma unroll
-        for (int w = 0; w < H / 32; w++) {
-          const uint4 v = qrow[j] ? __ldg(reinterpret_cast<const uint4*>(qrow[j] + H / 4 * c + 8 * w)) : make_uint4(0, 0, 0, 0);
-          const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+          for (int k = 0; k < MT; k++)
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            x[8 * w + 2 * i] = __uint_as_float(r[i] << 16);
-            x[8 * w + 2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-          }
+            for (int e = 0; e < 2; e++) qf[k][j][e] = qrow[j] ? __ldg(reinterpret_cast<const uint32_t*>(qrow[j] + 16 * k + 8 * e + 2 * c)) : 0u;
         }
+      } else {
 #pragma unroll
-        for (int i = 0; i < H / 4; i++) big = fmaxf(big, fabsf(x[i]));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100);   // the scale and its inverse stay normal
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23), back = __uint_as_float((uint32_t)(127 + ex) << 23) * 128.f;
+        for (int j = 0; j < NT; j++) {
+          // dims H / 4 c ..: 8 of them per word of codes; product 2 w + e takes dims (2 e, 2 e + 4) and (2 e + 1, 2 e + 5) of word w
+          float x[H / 4], big = 0.f;
 #pragma unroll
-        for (int w = 0; w < H / 32; w++)
+          for (int w = 0; w < H / 32; w++) {
+            const uint4 v = qrow[j] ? __ldg(reinterpret_cast<const uint4*>(qrow[j] + H / 4 * c + 8 * w)) : make_uint4(0, 0, 0, 0);
+            const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            qf[2 * w + e][j][0] = pack_f16(x[8 * w + 2 * e] * down, x[8 * w + 2 * e + 4] * down);
-            qf[2 * w + e][j][1] = pack_f16(x[8 * w + 2 * e + 1] * down, x[8 * w + 2 * e + 5] * down);
+            for (int i = 0; i < 4; i++) {
+              x[8 * w + 2 * i] = __uint_as_float(r[i] << 16);
+              x[8 * w + 2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+            }
           }
-        sc[j][0] = sl2 * __shfl_sync(0xffffffffu, back, 8 * c);       // row 2 c is lane group 2 c
-        sc[j][1] = sl2 * __shfl_sync(0xffffffffu, back, 8 * c + 4);
+#pragma unroll
+          for (int i = 0; i < H / 4; i++) big = fmaxf(big, fabsf(x[i]));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100);   // the scale and its inverse stay normal
+          const float down = __uint_as_float((uint32_t)(127 - ex) << 23), back = __uint_as_float((uint32_t)(127 + ex) << 23) * 128.f;
+#pragma unroll
+          for (int w = 0; w < H / 32; w++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              qf[2 * w + e][j][0] = pack_f16(x[8 * w + 2 * e] * down, x[8 * w + 2 * e + 4] * down);
+              qf[2 * w + e][j][1] = pack_f16(x[8 * w + 2 * e + 1] * down, x[8 * w + 2 * e + 5] * down);
+            }
+          sc[j][0] = sl2 * __shfl_sync(0xffffffffu, back, 8 * c);       // row 2 c is lane group 2 c
+          sc[j][1] = sl2 * __shfl_sync(0xffffffffu, back, 8 * c + 4);
+        }
       }
-    }
+    };
     int pos_row[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; j++)
@@ -284,6 +293,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
         }
       };
       for (int i = 0; i < ST; i++) fill();
+      load_q();
       for (int i = 0; i < steps && ok; i++) {
         PagedTile t;
         if (!keys_of(i, t)) continue;
@@ -386,6 +396,7 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
         filled++;
       };
       for (int i = 0; i < ST; i++) fill();
+      load_q();
       const int kk = (g >> 1) + 4 * (g & 1);   // row g of a product is key kk of its 16, row g + 8 key kk + 8
       for (int i = t0; i < nc && ok; i++) {
         const PagedTile t = tile_at(u, KT, i);
@@ -607,13 +618,10 @@ __global__ void __launch_bounds__(Ring<H, NT, INT4>::WARPS * 32, 1) paged_stream
       }
     if (whole && __any_sync(0xffffffffu, spoilt)) spoilt_units |= 1u << min(n_units, 31);
     n_units++;
-    if (t0 == 0 && t1 < u.len()) left = make_int4(u.b, u.g, u.rt, last_run);
+    if (!p.per_cta && lane == 0 && t0 == 0 && t1 < u.len()) a.desc[run] = make_int4(u.b, u.g, u.rt, last_run);   // left to others
   }
   if (!p.per_cta) {
-    if (lane == 0) {
-      a.desc[run] = left;
-      a.spoilt[run] = spoilt_units;
-    }
+    if (lane == 0) a.spoilt[run] = spoilt_units;
     return;
   }
   __syncthreads();   // the warps' shares, each in its own ring

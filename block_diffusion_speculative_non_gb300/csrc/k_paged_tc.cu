@@ -548,7 +548,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lane_off + t * KT, o_mine = tmem + lane_off + kTmemO + t * 128;
     float* stat = reinterpret_cast<float*>(smem + S::STAT);   // [lane][row]: m, then l, of units whose keys the lanes share
-    int4 left = make_int4(-1, 0, 0, 0);
+    const bool speaks = warp == Ro::SOFTMAX && lane == 0;
+    if (speaks) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     unsigned spoilt_units = 0;   // parts of the run, from 31 on together, that came out whole and with something that is no number
     int n_units = 0, met = 0;
     auto meet = [&]() {   // with the other lane's warps; bounded, as every wait
@@ -783,14 +784,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           else if (a.lse) a.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         }
       }
-      if (sg.first && !sg.whole) left = make_int4(sg.u.b, sg.u.g, sg.u.rt, sg.last_run);
+      if (speaks && sg.first && !sg.whole) a.desc[blockIdx.x] = make_int4(sg.u.b, sg.u.g, sg.u.rt, sg.last_run);   // left to others
       tc::tc_fence_before();   // O has been read: the next run's first product follows this lane's next P
       if (shared_keys) meet();
       n_units++;
     }
     spoilt_units = __reduce_or_sync(0xffffffffu, spoilt_units);
     if (lane == 0) a.spoilt[blockIdx.x * 8 + warp - Ro::SOFTMAX] = spoilt_units;
-    if (warp == Ro::SOFTMAX && lane == 0) a.desc[blockIdx.x] = left;
   }
 
   __syncwarp();

@@ -72,10 +72,6 @@ inline PagedShape paged_shape(int L, int lb, int grp, int nkv, int rows, int win
   s.by_grp.set(grp);
   return s;
 }
-// 64-bit quotients, by the 32-bit division where it holds them (several times shorter)
-__host__ __device__ inline long long quotient(long long x, long long y) {
-  return (((unsigned long long)x | (unsigned long long)y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
-}
 
 __host__ __device__ inline void unit_tiles(const PagedShape& s, int T, int rt, PagedUnit& u) {
   const int sh = s.kt_shift, up = s.kt() - 1;
@@ -113,13 +109,13 @@ __host__ __device__ inline bool tile_full(const PagedShape& s, const PagedUnit& 
 }
 
 // Tiles of a request in one kv head, with what its units cost besides.
-__host__ __device__ inline long long request_tiles(const PagedShape& s, int T) {
+__host__ __device__ inline int request_tiles(const PagedShape& s, int T) {
   PagedUnit u;
   if (!s.window && !s.causal) {
     unit_tiles(s, T, 0, u);
-    return (long long)s.tiles * (u.len() + s.unit_cost);
+    return s.tiles * (u.len() + s.unit_cost);
   }
-  long long n = 0;
+  int n = 0;
   for (int rt = 0; rt < s.tiles; rt++) {
     unit_tiles(s, T, rt, u);
     n += u.len() + s.unit_cost;
@@ -127,29 +123,29 @@ __host__ __device__ inline long long request_tiles(const PagedShape& s, int T) {
   return n;
 }
 
-// One run of a CTA over the units.  Lens: the length of request b, clamped.
+// One run over the units.  Lens: the length of request b, clamped.  The host sees to it that all tiles fit 31 bits.
 template <class Lens>
 struct PagedWalk {
   const PagedShape& s;
   Lens lens;
   int c, G, batch, b, g, rt, off;
-  long long x, x_end, total, each_run, longer;   // runs of each_run tiles, the first `longer` of them one more
+  int x, x_end, each_run, longer;   // runs of each_run tiles, the first `longer` of them one more
 
-  __host__ __device__ PagedWalk(const PagedShape& s_, Lens lens_, int batch_, long long total_, int runs, int c_)
-      : s(s_), lens(lens_), c(c_), batch(batch_), b(0), g(0), rt(0), off(0), total(total_) {
-    G = total < runs ? (int)total : runs;
-    each_run = quotient(total, G);
+  __host__ __device__ PagedWalk(const PagedShape& s_, Lens lens_, int batch_, int total, int runs, int c_)
+      : s(s_), lens(lens_), c(c_), batch(batch_), b(0), g(0), rt(0), off(0) {
+    G = imin(total, runs);
+    each_run = (int)((unsigned)total / (unsigned)G);
     longer = total - each_run * G;
     x = c < G ? run_start(c) : total;
     x_end = c < G ? run_start(c + 1) : total;
   }
   // Finds the run's first unit: entry lo, which starts at tile `base` and holds `size` of them, is the one with tile x.
-  __host__ __device__ void locate(int lo, long long base, long long size) {
+  __host__ __device__ void locate(int lo, int base, int size) {
     const int each = (batch + kSchedEntries - 1) / kSchedEntries;
-    long long rest = x - base, per;
+    int rest = x - base, per;
     b = lo * each;
     if (each == 1) {
-      per = quotient(size, s.nkv);
+      per = (int)((unsigned)size / (unsigned)s.nkv);
     } else {
       for (;; b++) {
         per = request_tiles(s, lens(b));
@@ -158,13 +154,13 @@ struct PagedWalk {
       }
     }
     // lengths that another stream changes meanwhile give a wrong result, never a unit that is not there
-    g = imin((int)quotient(rest, per), s.nkv - 1);
+    g = imin((int)((unsigned)rest / (unsigned)per), s.nkv - 1);
     rest -= g * per;
     PagedUnit u;
     if (!s.window && !s.causal) {
       unit_tiles(s, lens(b), 0, u);
-      rt = imin((int)quotient(rest, u.len() + s.unit_cost), s.tiles - 1);
-      rest -= (long long)rt * (u.len() + s.unit_cost);
+      rt = imin((int)((unsigned)rest / (unsigned)(u.len() + s.unit_cost)), s.tiles - 1);
+      rest -= rt * (u.len() + s.unit_cost);
     } else {
       for (rt = 0; rt + 1 < s.tiles; rt++) {
         unit_tiles(s, lens(b), rt, u);
@@ -173,7 +169,7 @@ struct PagedWalk {
       }
       unit_tiles(s, lens(b), rt, u);
     }
-    off = (int)rest;
+    off = rest;
     if (off >= u.len()) {   // among what the unit costs besides: the run starts with the next one
       x += imax(1, u.len() + s.unit_cost - off);
       step();
@@ -189,10 +185,10 @@ struct PagedWalk {
       }
     }
   }
-  __host__ __device__ long long run_start(int i) const { return i * each_run + (i < longer ? i : longer); }
-  __host__ __device__ int run_of(long long t) const {
-    const long long before = longer * (each_run + 1);   // tiles of the longer runs
-    return (int)(t < before ? quotient(t, each_run + 1) : longer + quotient(t - before, each_run));
+  __host__ __device__ int run_start(int i) const { return i * each_run + imin(i, longer); }
+  __host__ __device__ int run_of(int t) const {
+    const int before = longer * (each_run + 1);   // tiles of the longer runs
+    return (int)(t < before ? (unsigned)t / (unsigned)(each_run + 1) : longer + (unsigned)(t - before) / (unsigned)each_run);
   }
 
   // The next part [t0, t1) of a unit's tiles; last_run: the run that ends the unit.
@@ -204,7 +200,7 @@ struct PagedWalk {
     const int len = u.len();
     if (off >= len) off = len - 1;
     t0 = off;
-    t1 = (int)(x_end - x < len - off ? off + (x_end - x) : len);
+    t1 = imin(len, off + (x_end - x));
     if (t1 == len) {
       last_run = c;
       x += len + s.unit_cost - off;
@@ -234,18 +230,18 @@ struct DeviceLens {
 // The walk of run c, by a whole warp (every warp that walks makes its own; no shared memory, no barrier).
 __device__ __forceinline__ PagedWalk<DeviceLens> make_walk(const PagedShape& s, DeviceLens lens, int batch, int runs, int c) {
   const int each = (batch + kSchedEntries - 1) / kSchedEntries, lane = threadIdx.x & 31;
-  long long v = 0;
+  int v = 0;
   for (int b = lane * each; b < min(batch, (lane + 1) * each); b++) v += s.nkv * request_tiles(s, lens(b));
-  long long up = v;
+  int up = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, up, o);
+    const int t = __shfl_up_sync(0xffffffffu, up, o);
     if (lane >= o) up += t;
   }
   PagedWalk<DeviceLens> w(s, lens, batch, __shfl_sync(0xffffffffu, up, 31), runs, c);
   const unsigned m = __ballot_sync(0xffffffffu, up > w.x);
   const int e = m ? __ffs(m) - 1 : 31;
-  const long long base = __shfl_sync(0xffffffffu, up - v, e), size = __shfl_sync(0xffffffffu, v, e);
+  const int base = __shfl_sync(0xffffffffu, up - v, e), size = __shfl_sync(0xffffffffu, v, e);
   if (w.x < w.x_end) w.locate(e, base, size);
   return w;
 }
