@@ -126,6 +126,10 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   const PagedAttn& a = p.a;
   const PagedShape& sh = p.s;
   const int grp = sh.grp, nrows = a.L * grp;
+  // 4 bits: quarters of the lanes that no unit's rows reach (a text block's 64) decode instead
+  const int live = INT4 ? min(4, (min(nrows, p.rpt) + 31) / 32) : 4;
+  const int quarter = warp & 3;
+  const bool helps = INT4 && warp >= Ro::SOFTMAX && quarter >= live;
   constexpr int kFill = INT4 ? 4 : 1;   // arrivals that fill a tile: the decoding warps, or the one that issues its copies
 
   if (tid == 0) {
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       tc::mbar_init(bar(B_Q + t), kFill);
       tc::mbar_init(bar(B_QE + t), 1);
       tc::mbar_init(bar(B_SF + t), 1);
-      tc::mbar_init(bar(B_PF + t), 4);
+      tc::mbar_init(bar(B_PF + t), live);
       tc::mbar_init(bar(B_PV + t), 1);
     }
     for (int s = 0; s < KST; s++) {
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       tc::mbar_init(bar(B_RE + s), 4);
     }
     tc::mbar_init(bar(B_END), 1);
-    tc::mbar_init(bar(B_X), 8);
+    tc::mbar_init(bar(B_X), 2 * live);
     *abort_flag = 0;
     tc::fence_barrier_init();
     if (!INT4) {
@@ -295,12 +299,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     if (!ok) *abort_flag = 1;
     if (*abort_flag)
       for (int i = max(0, h - kRawSlots); i < h; i++) tc::mbar_wait(bar(B_RF + i % kRawSlots), (i / kRawSlots) & 1);
-  } else if (INT4 && warp < Ro::SOFTMAX && warp != 1) {
+  } else if (INT4 && ((warp < Ro::SOFTMAX && warp != 1) || helps)) {
     // ---------------- decoding warps ----------------
-    // A tile's K is four items of 32 rows, then its V; the six warps take turns at them, a thread a row.  One copy of the code for
+    // A tile's K is four items of 32 rows, then its V; the warps take turns at them, a thread a row.  One copy of the code for
     // all turns, and loops over a row's chunks: unrolled, a third of the stalls were for instructions.
-    constexpr int NW = 6;
-    const int wd = warp - 2;
+    const int NW = 6 + 2 * (4 - live);
+    const int wd = helps ? 6 + (warp >= Ro::SOFTMAX + 4 ? 4 - live : 0) + quarter - live : warp - 2;
+    if (helps && lane == 0) a.spoilt[blockIdx.x * 8 + warp - Ro::SOFTMAX] = 0;
     const uint32_t qs = tc::smem_u32(smem + S::Q), ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V);
     const uint32_t rs = tc::smem_u32(smem + S::RAW);
     int n = 0, nh = 0, nq[2] = {0, 0};   // tiles, halves of context tiles and Q loads so far
@@ -350,6 +355,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         uint32_t c[4];
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + r * (HD / 2) + ch * 16));
         const uint32_t two = (uint32_t)(scales >> (16 * ch)) & 0xFFFF;
+        const uint32_t half = (to ^ ((ch & 1) << 6)) + (ch >> 1) * ATOM_BYTES;   // chunks 4 ch ..
         uint32_t x[4][4];
         if (is_v) {
           const Scale2 s0((two & 0xFF) * 0x00800080u), s1((two >> 8) * 0x00800080u);
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           decode4_bf16(c[3], s1, x[3]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++) put(to, 4 * ch + i, make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]));
+        for (int i = 0; i < 4; i++) put(half, i, make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]));
       }
     };
     auto done = [&](int b) {   // this warp's rows are written, for the tensor core to read
@@ -382,44 +388,48 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     while (ok && !*abort_flag && next(sg)) {
       const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
       const int nc = min(sg.n_tiles, max(0, sg.u.ns + sg.u.nm - sg.t0));   // context tiles; the block's follow
-      bool q_done = false;
-#pragma unroll 1
-      for (int e = wd; e < 8 * sg.n_tiles && ok; e += NW) {
-        if (!q_done) {   // Q beside the first K tile: its eight items of 32 rows, from the last warp on
-          q_done = true;
-          for (int i = 0; i < 8 && ok; i++) {
-            const int l = i >> 2, k = i & 3;
-            if (sg.lane_tiles(l) == 0 || NW - 1 - i % NW != wd) continue;
-            if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
-            const int q0 = sg.row0 + (sg.keys ? 0 : l * p.rpt);
-            put_bf16(qs + l * S::TILE, k * 32, [&](int r) -> const bf16* {
-              const int qi = q0 + r, j = sh.by_grp.div(qi);
-              return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg.u.b * a.L + j) * a.nq + sg.u.g * grp + qi - j * grp) * HD : nullptr;
-            });
-            done(B_Q + l);
-          }
-          for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
-          if (!ok) break;
-        }
-        const PagedTile t = sg.tile(e >> 3);
-        const bool is_v = (e >> 2) & 1;
-        const int i = n + (e >> 3), turn = is_v ? i / VST : i / KST, s = i - turn * (is_v ? VST : KST), r0 = (e & 3) * 32;
-        if (turn > 0 && !wait((is_v ? B_VE : B_KE) + s, (turn & 1) ^ 1)) break;
-        const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
-        if (t.ctx) {
-          const int h = nh + (e >> 2), slot = h % kRawSlots;
-          if (!wait(B_RF + slot, (h / kRawSlots) & 1)) break;
-          put_codes(tile, rs + slot * S::RAW_BYTES, r0 + lane, r0 + lane < t.valid, is_v);
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar(B_RE + slot));
-        } else {
-          const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
-          put_bf16(tile, r0, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
-        }
-        done((is_v ? B_VF : B_KF) + s);
+      for (int i = 0; i < 8 && ok; i++) {   // Q beside the first K tile: eight items of 32 rows, from the second warp on
+        const int l = i >> 2, k = i & 3;
+        if (sg.lane_tiles(l) == 0 || (i + 1) % NW != wd) continue;
+        if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
+        const int q0 = sg.row0 + (sg.keys ? 0 : l * p.rpt);
+        put_bf16(qs + l * S::TILE, k * 32, [&](int r) -> const bf16* {
+          const int qi = q0 + r, j = sh.by_grp.div(qi);
+          return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg.u.b * a.L + j) * a.nq + sg.u.g * grp + qi - j * grp) * HD : nullptr;
+        });
+        done(B_Q + l);
       }
-      if (!q_done)   // fewer items than warps
-        for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
+      for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
+      // item k of a tile's K is turn 8 i + k, of its V turn 8 i + 4 + k; a warp has at most one of either.  It waits for every tile's K
+      // slot and codes whether or not it has an item there: a wait on a parity must not begin two phases early.  (V's slot needs
+      // none: the K slot is free behind the products that came before.)
+      int turn = wd;   // (wd - 8 i) mod NW
+#pragma unroll 1
+      for (int i = 0; i < sg.n_tiles && ok; i++) {
+        const PagedTile t = sg.tile(i);
+        const int at = n + i;
+#pragma unroll 1
+        for (int is_v = 0; is_v < 2 && ok; is_v++) {
+          const int k = is_v ? (turn >= 4 ? turn - 4 : turn - 4 + NW) : turn;
+          const int slots = is_v ? VST : KST, round = is_v ? at / VST : at / KST, s = at - round * slots, h = nh + 2 * i + is_v, slot = h % kRawSlots;
+          const bool mine = k < 4;
+          if (round > 0 && (mine || !is_v) && !wait((is_v ? B_VE : B_KE) + s, (round & 1) ^ 1)) break;
+          if (t.ctx && !wait(B_RF + slot, (h / kRawSlots) & 1)) break;
+          if (!mine) continue;
+          const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
+          if (t.ctx) {
+            put_codes(tile, rs + slot * S::RAW_BYTES, 32 * k + lane, 32 * k + lane < t.valid, is_v);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(B_RE + slot));
+          } else {
+            const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
+            put_bf16(tile, 32 * k, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
+          }
+          done((is_v ? B_VF : B_KF) + s);
+        }
+        turn -= 8 % NW;
+        if (turn < 0) turn += NW;
+      }
       n += sg.n_tiles;
       nh += 2 * nc;
     }
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     tc::mbar_wait(bar(B_END), 0);
   } else if (warp >= Ro::SOFTMAX) {
     // ---------------- softmax of lane t: thread = query row = TMEM lane ----------------
-    const int t = (warp - Ro::SOFTMAX) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int t = (warp - Ro::SOFTMAX) >> 2, r = quarter * 32 + lane;
     const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lane_off + t * KT, o_mine = tmem + lane_off + kTmemO + t * 128;

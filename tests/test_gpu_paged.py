@@ -158,6 +158,10 @@ CASES = {
     "group_128": dict(lens=[400, 3], L=3, nq=128, nkv=1, h=64, page=64),
     "primitive": dict(lens=[600, 37], L=385, nq=16, nkv=4, h=128, page=128),
     "primitive_64": dict(lens=[600, 37, 0], L=129, nq=8, nkv=2, h=64, page=16),
+    "many_texts": dict(lens=[(61 * i) % 600 for i in range(45)], L=16, nq=32, nkv=8, h=128, page=64),
+    "many_rows_24": dict(lens=[(61 * i) % 400 for i in range(60)], L=6, nq=16, nkv=4, h=64, page=32),
+    "many_rows_96": dict(lens=[(47 * i) % 500 for i in range(40)], L=12, nq=32, nkv=4, h=128, page=16),
+    "many_rows_160": dict(lens=[(83 * i) % 700 for i in range(30)], L=40, nq=16, nkv=4, h=64, page=128),
     "many": dict(lens=[(37 * i) % 90 for i in range(200)], L=2, nq=4, nkv=2, h=64, page=16),
 }
 MASKS = {"all": {}, "causal": dict(causal=True), "window": dict(window=50), "window_sinks": dict(window=33, sinks=5),
