@@ -130,27 +130,28 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   const int live = INT4 ? min(4, (min(nrows, p.rpt) + 31) / 32) : 4;
   const int quarter = warp & 3;
   const bool helps = INT4 && warp >= Ro::SOFTMAX && quarter >= live;
-  constexpr int kFill = INT4 ? 4 : 1;   // arrivals that fill a tile: the decoding warps, or the one that issues its copies
+  // arrivals that fill a tile, and Q: from every decoding warp (with rows in it or without), or from the one that issues its copies
+  const int NW = 6 + 2 * (4 - live), fill = INT4 ? NW : 1, fill_q = INT4 ? 4 : 1;
 
   if (tid == 0) {
     for (int t = 0; t < 2; t++) {
-      tc::mbar_init(bar(B_Q + t), kFill);
+      tc::mbar_init(bar(B_Q + t), fill_q);
       tc::mbar_init(bar(B_QE + t), 1);
       tc::mbar_init(bar(B_SF + t), 1);
       tc::mbar_init(bar(B_PF + t), live);
       tc::mbar_init(bar(B_PV + t), 1);
     }
     for (int s = 0; s < KST; s++) {
-      tc::mbar_init(bar(B_KF + s), kFill);
+      tc::mbar_init(bar(B_KF + s), fill);
       tc::mbar_init(bar(B_KE + s), 1);
     }
     for (int s = 0; s < VST; s++) {
-      tc::mbar_init(bar(B_VF + s), kFill);
+      tc::mbar_init(bar(B_VF + s), fill);
       tc::mbar_init(bar(B_VE + s), 1);
     }
     for (int s = 0; s < kRawSlots; s++) {
       tc::mbar_init(bar(B_RF + s), 1);
-      tc::mbar_init(bar(B_RE + s), 4);
+      tc::mbar_init(bar(B_RE + s), NW);
     }
     tc::mbar_init(bar(B_END), 1);
     tc::mbar_init(bar(B_X), 2 * live);
@@ -303,7 +304,6 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     // ---------------- decoding warps ----------------
     // A tile's K is four items of 32 rows, then its V; the warps take turns at them, a thread a row.  One copy of the code for
     // all turns, and loops over a row's chunks: unrolled, a third of the stalls were for instructions.
-    const int NW = 6 + 2 * (4 - live);
     const int wd = helps ? 6 + (warp >= Ro::SOFTMAX + 4 ? 4 - live : 0) + quarter - live : warp - 2;
     if (helps && lane == 0) a.spoilt[blockIdx.x * 8 + warp - Ro::SOFTMAX] = 0;
     const uint32_t qs = tc::smem_u32(smem + S::Q), ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V);
@@ -400,9 +400,9 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         done(B_Q + l);
       }
       for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
-      // item k of a tile's K is turn 8 i + k, of its V turn 8 i + 4 + k; a warp has at most one of either.  It waits for every tile's K
-      // slot and codes whether or not it has an item there: a wait on a parity must not begin two phases early.  (V's slot needs
-      // none: the K slot is free behind the products that came before.)
+      // item k of a tile's K is turn 8 i + k, of its V turn 8 i + 4 + k; a warp has at most one of either.  Whether or not it has one,
+      // it waits for every slot and for all codes, and its arrival fills and frees them: a wait on a parity must begin neither two
+      // phases early nor two late.
       int turn = wd;   // (wd - 8 i) mod NW
 #pragma unroll 1
       for (int i = 0; i < sg.n_tiles && ok; i++) {
@@ -412,16 +412,14 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         for (int is_v = 0; is_v < 2 && ok; is_v++) {
           const int k = is_v ? (turn >= 4 ? turn - 4 : turn - 4 + NW) : turn;
           const int slots = is_v ? VST : KST, round = is_v ? at / VST : at / KST, s = at - round * slots, h = nh + 2 * i + is_v, slot = h % kRawSlots;
-          const bool mine = k < 4;
-          if (round > 0 && (mine || !is_v) && !wait((is_v ? B_VE : B_KE) + s, (round & 1) ^ 1)) break;
+          if (round > 0 && !wait((is_v ? B_VE : B_KE) + s, (round & 1) ^ 1)) break;
           if (t.ctx && !wait(B_RF + slot, (h / kRawSlots) & 1)) break;
-          if (!mine) continue;
           const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
           if (t.ctx) {
-            put_codes(tile, rs + slot * S::RAW_BYTES, 32 * k + lane, 32 * k + lane < t.valid, is_v);
+            if (k < 4) put_codes(tile, rs + slot * S::RAW_BYTES, 32 * k + lane, 32 * k + lane < t.valid, is_v);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar(B_RE + slot));
-          } else {
+          } else if (k < 4) {
             const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
             put_bf16(tile, 32 * k, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
           }
