@@ -29,7 +29,7 @@ constexpr int QR = 128, KT = kPagedTcTile;
 constexpr int KST = 2;
 template <bool INT4>
 constexpr int kVst = INT4 ? 2 : 3;     // V slots; 4-bit pages leave one to the codes
-constexpr int kRawSlots = 3;           // codes and scales of a tile's K or V
+constexpr int kRawSlots = 3;           // a ring of codes and scales: slots, each a tile's K or V
 constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
 constexpr uint32_t kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
@@ -46,7 +46,10 @@ template <int HD, bool INT4>
 struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64, VST = kVst<INT4>;
   static constexpr int RAW_BYTES = KT * (HD / 2 + HD / 16);
-  static constexpr int Q = 0, K = 2 * TILE, V = K + KST * TILE, RAW = V + VST * TILE, STAT = RAW + (INT4 ? kRawSlots * RAW_BYTES : 0), BAR = STAT + 2 * QR * 4;
+  // lane 1's Q lies before the codes, which have its place where the lanes share one
+  static constexpr int Q = 0, K = TILE, V = K + KST * TILE, Q1 = V + VST * TILE, RAW = Q1 + TILE;
+  static constexpr int STAT = RAW + (INT4 ? kRawSlots * RAW_BYTES : 0), BAR = STAT + 2 * QR * 4;
+  static_assert(2 * kRawSlots * RAW_BYTES <= TILE + kRawSlots * RAW_BYTES, "two rings of codes");
 };
 enum {
   B_Q = 0,
@@ -61,8 +64,8 @@ enum {
   B_END = B_PV + 2,
   B_X = B_END + 1,   // the softmax warps, in units whose keys the lanes share
   B_RF = B_X + 1,    // codes: full, empty [slot]
-  B_RE = B_RF + kRawSlots,
-  B_N = B_RE + kRawSlots
+  B_RE = B_RF + 2 * kRawSlots,
+  B_N = B_RE + 2 * kRawSlots
 };
 template <int HD, bool INT4>
 constexpr size_t smem_bytes() {
@@ -126,12 +129,14 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   const PagedAttn& a = p.a;
   const PagedShape& sh = p.s;
   const int grp = sh.grp, nrows = a.L * grp;
-  // 4 bits: quarters of the lanes that no unit's rows reach (a text block's 64) decode instead
-  const int live = INT4 ? min(4, (min(nrows, p.rpt) + 31) / 32) : 4;
-  const int quarter = warp & 3;
-  const bool helps = INT4 && warp >= Ro::SOFTMAX && quarter >= live;
-  // arrivals that fill a tile, and Q: from every decoding warp (with rows in it or without), or from the one that issues its copies
-  const int NW = 6 + 2 * (4 - live), fill = INT4 ? NW : 1, fill_q = INT4 ? 4 : 1;
+  // 4 bits: quarters of the lanes that no unit's rows reach (a text block's 64) decode instead.  The decoding warps are then two
+  // teams, of K and of V, each with a ring of codes; else one.  The lanes of such units hold the same rows, in one copy.
+  const int live = INT4 && nrows <= min(p.rpt, 96) ? (nrows + 31) / 32 : 4;
+  const bool two = INT4 && live < 4;
+  const int quarter = warp & 3, teams = two ? 2 : 1;
+  const bool helps = two && warp >= Ro::SOFTMAX && quarter >= live;
+  // arrivals that fill a tile, and Q: from every warp of the team, or from the one that issues the copies
+  const int NW = (6 + 2 * (4 - live)) / teams, fill = INT4 ? NW : 1, fill_q = INT4 ? 4 : 1;
 
   if (tid == 0) {
     for (int t = 0; t < 2; t++) {
@@ -149,7 +154,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       tc::mbar_init(bar(B_VF + s), fill);
       tc::mbar_init(bar(B_VE + s), 1);
     }
-    for (int s = 0; s < kRawSlots; s++) {
+    for (int s = 0; s < 2 * kRawSlots; s++) {
       tc::mbar_init(bar(B_RF + s), 1);
       tc::mbar_init(bar(B_RE + s), NW);
     }
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           if (lane == 0) {
             tc::mbar_arrive_expect_tx(bar(B_Q + l), p.rpt * HD * 2);
             for (int h = 0; h < S::ATOMS; h++)
-              tc::tma_load_3d(tc::smem_u32(smem + S::Q) + l * S::TILE + h * ATOM_BYTES, &p.tm_q, h * 64, sg.u.g * grp,
+              tc::tma_load_3d(tc::smem_u32(smem + (l ? S::Q1 : S::Q)) + h * ATOM_BYTES, &p.tm_q, h * 64, sg.u.g * grp,
                               sg.u.b * a.L + (sg.row0 + (sg.keys ? 0 : l * p.rpt)) / grp, bar(B_Q + l));
           }
           nq[l]++;
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   } else if (INT4 && warp == 0) {
     // ---------------- codes of the context tiles, K and V in turn, by bulk copies: lanes 2 i + part copy from page i ----------------
     const int kp = min(KT, a.pg.page), part = lane & 1, pi = lane >> 1;   // part: codes, scales
-    const uint32_t ring = tc::smem_u32(smem + S::RAW);
+    const uint32_t ring = tc::smem_u32(smem + (two ? S::Q1 : S::RAW));
     const uint32_t w = part ? HD / 16 : HD / 2;
     int h = 0;   // halves of tiles so far
     bool ok = true;
@@ -279,8 +284,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         const uint32_t at = (part ? KT * (HD / 2) : 0) + pi * kp * w;
 #pragma unroll 1
         for (int v = 0; v < 2; v++, h++) {
-          const int s = h % kRawSlots;
-          if (h >= kRawSlots) ok = wait_bar(bar(B_RE + s), ((h / kRawSlots) & 1) ^ 1);
+          const int c = h / teams, s = c % kRawSlots + (two ? v * kRawSlots : 0);
+          if (c >= kRawSlots) ok = wait_bar(bar(B_RE + s), ((c / kRawSlots) & 1) ^ 1);
           ok = __all_sync(0xffffffffu, ok && !*abort_flag);
           if (!ok) break;
           if (rows > 0 && id_now < 0) {   // a page that is none: zeros
@@ -299,16 +304,19 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     }
     if (!ok) *abort_flag = 1;
     if (*abort_flag)
-      for (int i = max(0, h - kRawSlots); i < h; i++) tc::mbar_wait(bar(B_RF + i % kRawSlots), (i / kRawSlots) & 1);
+      for (int i = max(0, h - teams * kRawSlots); i < h; i++) {
+        const int c = i / teams;
+        tc::mbar_wait(bar(B_RF + c % kRawSlots + (two ? (i & 1) * kRawSlots : 0)), (c / kRawSlots) & 1);
+      }
   } else if (INT4 && ((warp < Ro::SOFTMAX && warp != 1) || helps)) {
     // ---------------- decoding warps ----------------
-    // A tile's K is four items of 32 rows, then its V; the warps take turns at them, a thread a row.  One copy of the code for
-    // all turns, and loops over a row's chunks: unrolled, a third of the stalls were for instructions.
-    const int wd = helps ? 6 + (warp >= Ro::SOFTMAX + 4 ? 4 - live : 0) + quarter - live : warp - 2;
+    // A tile's K or V is HD / 8 items, each 32 rows by 32 dims of every row; a team's warps take turns at them, a thread a row.  One
+    // copy of the code for all: unrolled, a third of the stalls were for instructions.
+    const int wall = helps ? 6 + (warp >= Ro::SOFTMAX + 4 ? 4 - live : 0) + quarter - live : warp - 2;
+    const int team = wall >= NW, wd = wall - (team ? NW : 0);
     if (helps && lane == 0) a.spoilt[blockIdx.x * 8 + warp - Ro::SOFTMAX] = 0;
-    const uint32_t qs = tc::smem_u32(smem + S::Q), ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V);
-    const uint32_t rs = tc::smem_u32(smem + S::RAW);
-    int n = 0, nh = 0, nq[2] = {0, 0};   // tiles, halves of context tiles and Q loads so far
+    const uint32_t ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V), rs = tc::smem_u32(smem + (two ? S::Q1 : S::RAW));
+    int n = 0, nc = 0, nq[2] = {0, 0};   // tiles, context tiles and Q loads so far
     // chunk of 8 dims ch of row r in a tile of 64-dim atoms
     auto put = [&](uint32_t row, int ch, uint4 v) {
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"((row ^ ((ch & 7) << 4)) + (ch >> 3) * ATOM_BYTES), "r"(v.x), "r"(v.y),
@@ -335,44 +343,32 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
                                                                        __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632)));
       }
     };
-    // row r of the codes in a slot (past `valid`: zeros) into row r of a tile.  A row is HD / 32 chunks of 16 bytes; lanes begin at
-    // different ones, so that a load of 8 rows has no bank twice.
-    auto put_codes = [&](uint32_t tile, uint32_t raw, int r, bool valid, bool is_v) {
+    // 32 dims of row r of the codes in a slot (past `valid`: zeros) into row r of a tile: the j-th of the row's HD / 32 chunks of 16
+    // bytes, counted from one that differs between rows, so that neither a load nor a store of 8 rows has a bank twice
+    auto put_codes = [&](uint32_t tile, uint32_t raw, int r, int j, bool valid, bool is_v) {
       constexpr int CH = HD / 32;
-      const uint32_t to = row_at(tile, r);
-      unsigned long long scales;   // a byte for 16 dims
-      if constexpr (HD == 128) {
-        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(scales) : "r"(raw + KT * (HD / 2) + r * 8));
+      const int ch = (j + (HD == 128 ? r >> 1 : r >> 2)) & (CH - 1);
+      uint32_t c[4], two_scales;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + r * (HD / 2) + ch * 16));
+      asm volatile("{\n .reg .u16 x;\n ld.shared.u16 x, [%1];\n cvt.u32.u16 %0, x;\n}" : "=r"(two_scales) : "r"(raw + KT * (HD / 2) + r * (HD / 16) + ch * 2));
+      if (!valid) two_scales = 0;   // what is stale stands for nothing
+      const uint32_t half = (row_at(tile, r) ^ ((ch & 1) << 6)) + (ch >> 1) * ATOM_BYTES;   // chunks 4 ch ..
+      uint32_t x[4][4];
+      if (is_v) {
+        const Scale2 s0((two_scales & 0xFF) * 0x00800080u), s1((two_scales >> 8) * 0x00800080u);
+        decode4(c[0], s0, x[0]);
+        decode4(c[1], s0, x[1]);
+        decode4(c[2], s1, x[2]);
+        decode4(c[3], s1, x[3]);
       } else {
-        uint32_t x;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(raw + KT * (HD / 2) + r * 4));
-        scales = x;
+        const Scale2Bf s0(two_scales & 0xFF), s1(two_scales >> 8);
+        decode4_bf16(c[0], s0, x[0]);
+        decode4_bf16(c[1], s0, x[1]);
+        decode4_bf16(c[2], s1, x[2]);
+        decode4_bf16(c[3], s1, x[3]);
       }
-      if (!valid) scales = 0;   // what is stale stands for nothing
-#pragma unroll 1
-      for (int j = 0; j < CH; j++) {
-        const int ch = (j + (HD == 128 ? r >> 1 : r >> 2)) & (CH - 1);
-        uint32_t c[4];
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + r * (HD / 2) + ch * 16));
-        const uint32_t two = (uint32_t)(scales >> (16 * ch)) & 0xFFFF;
-        const uint32_t half = (to ^ ((ch & 1) << 6)) + (ch >> 1) * ATOM_BYTES;   // chunks 4 ch ..
-        uint32_t x[4][4];
-        if (is_v) {
-          const Scale2 s0((two & 0xFF) * 0x00800080u), s1((two >> 8) * 0x00800080u);
-          decode4(c[0], s0, x[0]);
-          decode4(c[1], s0, x[1]);
-          decode4(c[2], s1, x[2]);
-          decode4(c[3], s1, x[3]);
-        } else {
-          const Scale2Bf s0(two & 0xFF), s1(two >> 8);
-          decode4_bf16(c[0], s0, x[0]);
-          decode4_bf16(c[1], s0, x[1]);
-          decode4_bf16(c[2], s1, x[2]);
-          decode4_bf16(c[3], s1, x[3]);
-        }
 #pragma unroll
-        for (int i = 0; i < 4; i++) put(half, i, make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]));
-      }
+      for (int i = 0; i < 4; i++) put(half, i, make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]));
     };
     auto done = [&](int b) {   // this warp's rows are written, for the tensor core to read
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -387,49 +383,46 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     };
     while (ok && !*abort_flag && next(sg)) {
       const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
-      const int nc = min(sg.n_tiles, max(0, sg.u.ns + sg.u.nm - sg.t0));   // context tiles; the block's follow
       for (int i = 0; i < 8 && ok; i++) {   // Q beside the first K tile: eight items of 32 rows, from the second warp on
         const int l = i >> 2, k = i & 3;
-        if (sg.lane_tiles(l) == 0 || (i + 1) % NW != wd) continue;
+        if (sg.lane_tiles(l) == 0 || (two && l) || (i + 1) % (teams * NW) != wall) continue;
         if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
         const int q0 = sg.row0 + (sg.keys ? 0 : l * p.rpt);
-        put_bf16(qs + l * S::TILE, k * 32, [&](int r) -> const bf16* {
+        put_bf16(tc::smem_u32(smem + (l ? S::Q1 : S::Q)), k * 32, [&](int r) -> const bf16* {
           const int qi = q0 + r, j = sh.by_grp.div(qi);
           return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg.u.b * a.L + j) * a.nq + sg.u.g * grp + qi - j * grp) * HD : nullptr;
         });
         done(B_Q + l);
       }
       for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
-      // item k of a tile's K is turn 8 i + k, of its V turn 8 i + 4 + k; a warp has at most one of either.  Whether or not it has one,
-      // it waits for every slot and for all codes, and its arrival fills and frees them: a wait on a parity must begin neither two
-      // phases early nor two late.
-      int turn = wd;   // (wd - 8 i) mod NW
+      // Whether or not it has an item, a warp waits for all slots and codes of its team, and its arrival fills and frees them: a wait
+      // on a parity must begin neither two phases early nor two late.
 #pragma unroll 1
-      for (int i = 0; i < sg.n_tiles && ok; i++) {
+      for (int i = 0; i < sg.n_tiles && ok; i++, n++) {
         const PagedTile t = sg.tile(i);
-        const int at = n + i;
 #pragma unroll 1
-        for (int is_v = 0; is_v < 2 && ok; is_v++) {
-          const int k = is_v ? (turn >= 4 ? turn - 4 : turn - 4 + NW) : turn;
-          const int slots = is_v ? VST : KST, round = is_v ? at / VST : at / KST, s = at - round * slots, h = nh + 2 * i + is_v, slot = h % kRawSlots;
+        for (int is_v = team; is_v < 2 && ok; is_v += teams) {
+          const int slots = is_v ? VST : KST, round = n / slots, s = n - round * slots;
           if (round > 0 && !wait((is_v ? B_VE : B_KE) + s, (round & 1) ^ 1)) break;
-          if (t.ctx && !wait(B_RF + slot, (h / kRawSlots) & 1)) break;
           const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
           if (t.ctx) {
-            if (k < 4) put_codes(tile, rs + slot * S::RAW_BYTES, 32 * k + lane, 32 * k + lane < t.valid, is_v);
+            const int c = two ? nc : 2 * nc + is_v, slot = c % kRawSlots + team * kRawSlots;
+            if (!wait(B_RF + slot, (c / kRawSlots) & 1)) break;
+#pragma unroll 1
+            for (int item = wd; item < HD / 8; item += NW) {
+              const int r = 32 * (item & 3) + lane;
+              put_codes(tile, rs + slot * S::RAW_BYTES, r, item >> 2, r < t.valid, is_v);
+            }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar(B_RE + slot));
-          } else if (k < 4) {
+          } else if (wd < 4) {
             const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
-            put_bf16(tile, 32 * k, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
+            put_bf16(tile, 32 * wd, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
           }
           done((is_v ? B_VF : B_KF) + s);
         }
-        turn -= 8 % NW;
-        if (turn < 0) turn += NW;
+        nc += t.ctx;
       }
-      n += sg.n_tiles;
-      nh += 2 * nc;
     }
     if (!ok) *abort_flag = 1;
   } else if (warp == 1) {
@@ -445,7 +438,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     auto wait_k = [&](int n) { return wait_bar(bar(B_KF + n % KST), (n / KST) & 1) || fail(); };
     auto wait_v = [&](int n) { return wait_bar(bar(B_VF + n % VST), (n / VST) & 1) || fail(); };
     auto issue_s = [&](int t, int slot) {   // S_t = Q_t K^T, K from the slot
-      const uint64_t da = dq + t * (S::TILE >> 4), db = dk + slot * (S::TILE >> 4);
+      const uint64_t da = dq + (t && !two ? S::Q1 >> 4 : 0), db = dk + slot * (S::TILE >> 4);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; kk++) {
         const uint64_t step = ((kk >> 2) * ATOM_BYTES + (kk & 3) * 32) >> 4;   // stays inside the address field
@@ -482,7 +475,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       const int nt = sg.n_tiles;
       if (nt == 0) continue;
       for (int t = 0; t < 2 && ok; t++) {
-        if (sg.lane_tiles(t) == 0) continue;
+        if (sg.lane_tiles(t) == 0 || (two && t)) continue;
         ok = wait_bar(bar(B_Q + t), nq[t] & 1) || fail();
         nq[t]++;
       }
@@ -523,13 +516,16 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           }
         }
       } else {
+        auto q_read = [&](int i, int t) {   // after S of tile i: the last one from a copy of Q
+          if (i + (two ? 1 : 2) >= nt) commit_if(on, bar(B_QE + (two ? 0 : t)));
+        };
         for (int i = 0; i < min(2, nt) && ok; i++) {
           if (!(ok = wait_k(n0 + i))) break;
           tc::tc_fence_after();
           const int ks = uni((n0 + i) % KST);
           issue_s(i, ks);
           commit_if(on, bar(B_KE + ks));
-          if (i + 2 >= nt) commit_if(on, bar(B_QE + i));
+          q_read(i, i);
         }
         for (int i = 0; i < nt && ok && !*abort_flag; i++) {
           const int n = n0 + i, t = i & 1, vs = uni(n % VST), ks = uni((n + 2) % KST), acc = uni(i > 1);
@@ -540,7 +536,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
             tc::tc_fence_after();
             issue_s(t, ks);
             commit_if(on, bar(B_KE + ks));
-            if (i + 4 >= nt) commit_if(on, bar(B_QE + t));   // the lane's last S
+            q_read(i + 2, t);
           }
         }
       }
