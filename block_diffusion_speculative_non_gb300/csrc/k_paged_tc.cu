@@ -42,13 +42,24 @@ struct TcArgs {
   int runs, npt, rpt;   // positions and rows of a lane
 };
 
+// A part of a unit as this kernel walks it.  Warp 0 walks, a few parts ahead, and leaves what it finds in shared memory: walks of their
+// own took every warp some 40 registers, spilled at each unit, and code to fetch.
+constexpr int kSegs = 4;
+struct Seg {
+  PagedUnit u;                              // u.b < 0: the run is over
+  int keys, whole, first;                   // keys: one lane's rows; first: the unit starts here
+  int t0, n_tiles, row0, last_run;
+  __device__ PagedTile tile(int i) const { return tile_at(u, KT, t0 + i); }
+  __device__ int lane_tiles(int t) const { return keys ? (n_tiles - t + 1) / 2 : n_tiles; }
+};
+
 template <int HD, bool INT4>
 struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64, VST = kVst<INT4>;
   static constexpr int RAW_BYTES = KT * (HD / 2 + HD / 16);
   // lane 1's Q lies before the codes, which have its place where the lanes share one
   static constexpr int Q = 0, K = TILE, V = K + KST * TILE, Q1 = V + VST * TILE, RAW = Q1 + TILE;
-  static constexpr int STAT = RAW + (INT4 ? kRawSlots * RAW_BYTES : 0), BAR = STAT + 2 * QR * 4;
+  static constexpr int STAT = RAW + (INT4 ? kRawSlots * RAW_BYTES : 0), SEG = STAT + 2 * QR * 4, BAR = SEG + kSegs * (int)sizeof(Seg);
   static_assert(2 * kRawSlots * RAW_BYTES <= TILE + kRawSlots * RAW_BYTES, "two rings of codes");
 };
 enum {
@@ -65,7 +76,9 @@ enum {
   B_X = B_END + 1,   // the softmax warps, in units whose keys the lanes share
   B_RF = B_X + 1,    // codes: full, empty [slot]
   B_RE = B_RF + 2 * kRawSlots,
-  B_N = B_RE + 2 * kRawSlots
+  B_GF = B_RE + 2 * kRawSlots,   // parts of units: full, empty [slot]
+  B_GE = B_GF + kSegs,
+  B_N = B_GE + kSegs
 };
 template <int HD, bool INT4>
 constexpr size_t smem_bytes() {
@@ -103,15 +116,6 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {   // fp16 A and B, fp32 a
 }
 
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }   // bits 0 .. n - 1
-
-// A part of a unit as this kernel walks it.
-struct Seg {
-  PagedUnit u;
-  bool keys, whole, first;   // keys: one lane's rows; first: the unit starts here
-  int t0, n_tiles, row0, slot, last_run;
-  __device__ PagedTile tile(int i) const { return tile_at(u, KT, t0 + i); }
-  __device__ int lane_tiles(int t) const { return keys ? (n_tiles - t + 1) / 2 : n_tiles; }
-};
 
 template <int HD, bool INT4>
 __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const __grid_constant__ TcArgs p) {
@@ -158,6 +162,10 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       tc::mbar_init(bar(B_RF + s), 1);
       tc::mbar_init(bar(B_RE + s), NW);
     }
+    for (int s = 0; s < kSegs; s++) {
+      tc::mbar_init(bar(B_GF + s), 1);
+      tc::mbar_init(bar(B_GE + s), Ro::THREADS / 32 - 1);
+    }
     tc::mbar_init(bar(B_END), 1);
     tc::mbar_init(bar(B_X), 2 * live);
     *abort_flag = 0;
@@ -177,25 +185,49 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   }
   pdl_wait();
   pdl_trigger();
-  PagedWalk<DeviceLens> walk = make_walk(sh, DeviceLens{a.ctx_len, a.pg.cap()}, a.batch, p.runs, blockIdx.x);
+  const DeviceLens lens{a.ctx_len, a.pg.cap()};
+  PagedWalk<DeviceLens> walk = warp == 0 ? make_walk(sh, lens, a.batch, p.runs, blockIdx.x) : PagedWalk<DeviceLens>(sh, lens, a.batch, 1, 1, 1);
   __syncwarp();   // a CTA barrier counts a whole warp: single-lane roles reconverge before every one
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  auto next = [&](Seg& s) {
+  Seg* const segs = reinterpret_cast<Seg*>(smem + S::SEG);
+  const Seg* sg = segs;
+  int n_seg = 0;
+  auto walk_next = [&]() {   // warp 0
+    const int s = n_seg % kSegs;
+    Seg w;
     int t1;
-    if (!walk.next(s.u, s.t0, t1, s.last_run)) return false;
-    s.whole = s.t0 == 0 && t1 == s.u.len();
-    s.first = s.t0 == 0;
-    s.n_tiles = max(0, min(t1, s.u.tiles()) - s.t0);   // an empty unit has none
-    s.row0 = s.u.rt * sh.rows;
-    s.keys = nrows - s.row0 <= p.rpt;
-    s.slot = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
-    return true;
+    if (walk.next(w.u, w.t0, t1, w.last_run)) {
+      w.whole = w.t0 == 0 && t1 == w.u.len();
+      w.first = w.t0 == 0;
+      w.n_tiles = max(0, min(t1, w.u.tiles()) - w.t0);   // an empty unit has none
+      w.row0 = w.u.rt * sh.rows;
+      w.keys = nrows - w.row0 <= p.rpt;
+    } else {
+      w.u.b = -1;
+    }
+    if (n_seg >= kSegs && !wait_bar(bar(B_GE + s), ((n_seg / kSegs) & 1) ^ 1)) *abort_flag = 1;
+    __syncwarp();
+    if (lane == 0) {
+      segs[s] = w;
+      tc::mbar_arrive(bar(B_GF + s));
+    }
+    __syncwarp();
+    sg = segs + s;
+    n_seg++;
+    return w.u.b >= 0;
   };
-  Seg sg;
+  auto next = [&]() {   // the others: done with the part before
+    __syncwarp();
+    if (n_seg > 0 && lane == 0) tc::mbar_arrive(bar(B_GE + (n_seg - 1) % kSegs));
+    if (!wait_bar(bar(B_GF + n_seg % kSegs), (n_seg / kSegs) & 1)) *abort_flag = 1;
+    sg = segs + n_seg % kSegs;
+    n_seg++;
+    return !*abort_flag && sg->u.b >= 0;
+  };
 
   if (!INT4 && (warp == 0 || warp == 2)) {
     // ---------------- TMA producers: K and Q (warp 0), V (warp 2); lane i copies a tile's page i ----------------
@@ -204,19 +236,19 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     const uint32_t ring = tc::smem_u32(smem + (is_v ? S::V : S::K));
     const int bp = min(KT, a.pg.page);   // rows of a box
     int n = 0, nq[2] = {0, 0};
-    auto page_for = [&](const Seg& s, int i) {   // of this lane's part of tile i
-      if (i >= s.n_tiles) return 0;
-      const PagedTile t = s.tile(i);
-      return t.ctx && lane * bp < t.valid ? page_of(a.pg, s.u.b, t.k0 + lane * bp) : 0;
+    auto page_for = [&](int i) {   // of this lane's part of tile i
+      if (i >= sg->n_tiles) return 0;
+      const PagedTile t = sg->tile(i);
+      return t.ctx && lane * bp < t.valid ? page_of(a.pg, sg->u.b, t.k0 + lane * bp) : 0;
     };
     bool ok = true;
-    while (ok && !*abort_flag && next(sg)) {
-      int id = page_for(sg, 0);
-      for (int i = 0; i < sg.n_tiles && ok; i++) {
+    while (ok && !*abort_flag && (is_v ? next() : walk_next())) {
+      int id = page_for(0);
+      for (int i = 0; i < sg->n_tiles && ok; i++) {
         const int s = n % ST;
-        const PagedTile t = sg.tile(i);
+        const PagedTile t = sg->tile(i);
         const int id_now = id;
-        id = page_for(sg, i + 1);
+        id = page_for(i + 1);
         if (n >= ST) ok = wait_bar(bar(empty + s), ((n / ST) & 1) ^ 1);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         if (!ok) break;
@@ -229,25 +261,25 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
             const uint32_t dst = ring + s * S::TILE + h * ATOM_BYTES;
             if (t.ctx)
               tc::tma_load_3d(dst + lane * bp * 128, &p.tm_pages, h * 64,
-                              ((is_v ? a.pg.nkv : 0) + sg.u.g) * a.pg.page + ((t.k0 + lane * bp) & (a.pg.page - 1)),
+                              ((is_v ? a.pg.nkv : 0) + sg->u.g) * a.pg.page + ((t.k0 + lane * bp) & (a.pg.page - 1)),
                               id_now < 0 ? a.pg.n_pages : id_now, bar(full + s));
             else
-              tc::tma_load_2d(dst, is_v ? &p.tm_vblk : &p.tm_kblk, h * 64, (sg.u.b * a.pg.nkv + sg.u.g) * a.lb + t.k0, bar(full + s));
+              tc::tma_load_2d(dst, is_v ? &p.tm_vblk : &p.tm_kblk, h * 64, (sg->u.b * a.pg.nkv + sg->u.g) * a.lb + t.k0, bar(full + s));
           }
         }
         n++;
         if (is_v || i > 0) continue;
         // Q behind the first K tile, whose slot is free one S before Q's (with the last S of the run before)
         for (int l = 0; l < 2 && ok; l++) {
-          if (sg.lane_tiles(l) == 0) continue;
+          if (sg->lane_tiles(l) == 0) continue;
           if (nq[l] > 0) ok = wait_bar(bar(B_QE + l), (nq[l] & 1) ^ 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) {
             tc::mbar_arrive_expect_tx(bar(B_Q + l), p.rpt * HD * 2);
             for (int h = 0; h < S::ATOMS; h++)
-              tc::tma_load_3d(tc::smem_u32(smem + (l ? S::Q1 : S::Q)) + h * ATOM_BYTES, &p.tm_q, h * 64, sg.u.g * grp,
-                              sg.u.b * a.L + (sg.row0 + (sg.keys ? 0 : l * p.rpt)) / grp, bar(B_Q + l));
+              tc::tma_load_3d(tc::smem_u32(smem + (l ? S::Q1 : S::Q)) + h * ATOM_BYTES, &p.tm_q, h * 64, sg->u.g * grp,
+                              sg->u.b * a.L + (sg->row0 + (sg->keys ? 0 : l * p.rpt)) / grp, bar(B_Q + l));
           }
           nq[l]++;
         }
@@ -266,19 +298,19 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     const uint32_t w = part ? HD / 16 : HD / 2;
     int h = 0;   // halves of tiles so far
     bool ok = true;
-    auto page_for = [&](const Seg& s, int i) {
-      if (i >= s.n_tiles || pi >= KT / 16) return 0;
-      const PagedTile t = s.tile(i);
-      return t.ctx && pi * kp < t.valid ? page_of(a.pg, s.u.b, t.k0 + pi * kp) : 0;
+    auto page_for = [&](int i) {
+      if (i >= sg->n_tiles || pi >= KT / 16) return 0;
+      const PagedTile t = sg->tile(i);
+      return t.ctx && pi * kp < t.valid ? page_of(a.pg, sg->u.b, t.k0 + pi * kp) : 0;
     };
-    while (ok && !*abort_flag && next(sg)) {
-      int id = page_for(sg, 0);
+    while (ok && !*abort_flag && walk_next()) {
+      int id = page_for(0);
 #pragma unroll 1
-      for (int i = 0; i < sg.n_tiles && ok; i++) {
-        const PagedTile t = sg.tile(i);
+      for (int i = 0; i < sg->n_tiles && ok; i++) {
+        const PagedTile t = sg->tile(i);
         if (!t.ctx) break;
         const int id_now = id, in = t.k0 & (a.pg.page - 1);
-        id = page_for(sg, i + 1);
+        id = page_for(i + 1);
         const int rows = pi < KT / 16 ? min(kp, ceil_div(t.valid, 16) * 16 - pi * kp) : 0;   // whole groups of 16 positions
         const uint32_t bytes = rows > 0 && id_now >= 0 ? rows * w : 0, total = __reduce_add_sync(0xffffffffu, bytes);
         const uint32_t at = (part ? KT * (HD / 2) : 0) + pi * kp * w;
@@ -297,7 +329,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           if (lane == 0) tc::mbar_arrive_expect_tx(bar(B_RF + s), total);
           __syncwarp();
           if (bytes)
-            tc::bulk_load(ring + s * S::RAW_BYTES + at, slab_of(a.pg, id_now, v, sg.u.g) + (part ? a.pg.page * (HD / 2) : 0) + in * w, bytes,
+            tc::bulk_load(ring + s * S::RAW_BYTES + at, slab_of(a.pg, id_now, v, sg->u.g) + (part ? a.pg.page * (HD / 2) : 0) + in * w, bytes,
                           bar(B_RF + s));
         }
       }
@@ -381,25 +413,25 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
       return ok;
     };
-    while (ok && !*abort_flag && next(sg)) {
-      const size_t blk = ((size_t)sg.u.b * a.pg.nkv + sg.u.g) * a.lb;
+    while (ok && !*abort_flag && next()) {
+      const size_t blk = ((size_t)sg->u.b * a.pg.nkv + sg->u.g) * a.lb;
       for (int i = 0; i < 8 && ok; i++) {   // Q beside the first K tile: eight items of 32 rows, from the second warp on
         const int l = i >> 2, k = i & 3;
-        if (sg.lane_tiles(l) == 0 || (two && l) || (i + 1) % (teams * NW) != wall) continue;
+        if (sg->lane_tiles(l) == 0 || (two && l) || (i + 1) % (teams * NW) != wall) continue;
         if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
-        const int q0 = sg.row0 + (sg.keys ? 0 : l * p.rpt);
+        const int q0 = sg->row0 + (sg->keys ? 0 : l * p.rpt);
         put_bf16(tc::smem_u32(smem + (l ? S::Q1 : S::Q)), k * 32, [&](int r) -> const bf16* {
           const int qi = q0 + r, j = sh.by_grp.div(qi);
-          return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg.u.b * a.L + j) * a.nq + sg.u.g * grp + qi - j * grp) * HD : nullptr;
+          return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg->u.b * a.L + j) * a.nq + sg->u.g * grp + qi - j * grp) * HD : nullptr;
         });
         done(B_Q + l);
       }
-      for (int l = 0; l < 2; l++) nq[l] += sg.lane_tiles(l) > 0;
+      for (int l = 0; l < 2; l++) nq[l] += sg->lane_tiles(l) > 0;
       // Whether or not it has an item, a warp waits for all slots and codes of its team, and its arrival fills and frees them: a wait
       // on a parity must begin neither two phases early nor two late.
 #pragma unroll 1
-      for (int i = 0; i < sg.n_tiles && ok; i++, n++) {
-        const PagedTile t = sg.tile(i);
+      for (int i = 0; i < sg->n_tiles && ok; i++, n++) {
+        const PagedTile t = sg->tile(i);
 #pragma unroll 1
         for (int is_v = team; is_v < 2 && ok; is_v += teams) {
           const int slots = is_v ? VST : KST, round = n / slots, s = n - round * slots;
@@ -471,19 +503,19 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     };
     auto uni = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     bool ok = true;
-    while (ok && !*abort_flag && next(sg)) {
-      const int nt = sg.n_tiles;
+    while (ok && !*abort_flag && next()) {
+      const int nt = sg->n_tiles;
       if (nt == 0) continue;
       for (int t = 0; t < 2 && ok; t++) {
-        if (sg.lane_tiles(t) == 0 || (two && t)) continue;
+        if (sg->lane_tiles(t) == 0 || (two && t)) continue;
         ok = wait_bar(bar(B_Q + t), nq[t] & 1) || fail();
         nq[t]++;
       }
       tc::tc_fence_after();
-      const int nc = sg.u.ns + sg.u.nm - sg.t0;   // tiles of the pages; the block's follow
+      const int nc = sg->u.ns + sg->u.nm - sg->t0;   // tiles of the pages; the block's follow
       // Between a lane's P and its product stands nothing but the wait for P: a pair's other waits are done while the tensor
       // core still has work.
-      if (!sg.keys) {
+      if (!sg->keys) {
         // a lane's next S follows its own product, so no lane waits for the other's softmax
         if (ok && (ok = wait_k(n0))) {
           tc::tc_fence_after();
@@ -562,15 +594,15 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       if (!wait_bar(bar(B_X), met++ & 1)) *abort_flag = 1;
     };
     int cnt = 0, other = 0, base = 0;   // tiles of this lane and of the other so far: phases of S, P and PV; of both: V slots
-    while (!*abort_flag && next(sg)) {
-      const int lrow0 = sg.row0 + (sg.keys ? 0 : t * p.rpt);
+    while (!*abort_flag && next()) {
+      const int lrow0 = sg->row0 + (sg->keys ? 0 : t * p.rpt);
       const bool warp_rows = quarter * 32 < p.rpt && lrow0 + quarter * 32 < nrows;   // else padding
-      const int i0 = sg.keys ? t : 0, step = sg.keys ? 2 : 1;
-      const int row_pos = sg.u.n - a.L + sh.by_grp.div(lrow0 + r);
+      const int i0 = sg->keys ? t : 0, step = sg->keys ? 2 : 1;
+      const int row_pos = sg->u.n - a.L + sh.by_grp.div(lrow0 + r);
       float m_ref = -INFINITY, l = 0.f;
       bool first_tile = true;
-      for (int i = i0; i < sg.n_tiles && !*abort_flag; i += step, cnt++) {
-        const PagedTile tl = sg.tile(i);
+      for (int i = i0; i < sg->n_tiles && !*abort_flag; i += step, cnt++) {
+        const PagedTile tl = sg->tile(i);
         const bool half = INT4 && tl.ctx;   // P as one fp16 term
         if (!wait_bar(bar(B_SF + t), cnt & 1)) *abort_flag = 1;
         tc::tc_fence_after();
@@ -578,7 +610,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           constexpr int W = INT4 ? KT / 2 : KT;   // scores held at a time
           float sv[W];
           uint32_t see[KT / 32];   // keys before `hi` that lie before `lo_end` or from `start` on, as bits
-          const bool full = tile_full(sh, sg.u, tl);
+          const bool full = tile_full(sh, sg->u, tl);
           if (!full) {
             const int hi = sh.causal ? min(tl.valid, row_pos - tl.pos + 1) : tl.valid;
             const int lo_end = sh.window ? sh.sinks - tl.pos : KT, start = sh.window ? row_pos - sh.window + 1 - tl.pos : 0;
@@ -695,8 +727,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         }
         first_tile = false;
         int h_lo, h_hi;
-        hidden_from_all(sh, sg.u, tl, h_lo, h_hi);
-        if (!INT4 && (tl.valid < KT || h_hi > h_lo) && (sg.keys || t == 0)) {
+        hidden_from_all(sh, sg->u, tl, h_lo, h_hi);
+        if (!INT4 && (tl.valid < KT || h_hi > h_lo) && (sg->keys || t == 0)) {
           // V rows past the last key, and those that no row sees -> 0 before the product: 0 x a value that is not finite would be
           // NaN.  A pair's lane 1 comes after lane 0's product.  Row k: 128 bytes at k * 128 in each 64-dim atom (the swizzle
           // permutes within a row).
@@ -715,11 +747,11 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(B_PF + t));
       }
-      other += sg.lane_tiles(1 - t);
-      base += sg.n_tiles;
+      other += sg->lane_tiles(1 - t);
+      base += sg->n_tiles;
       if (!first_tile && !wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
       float w_mine = 1.f, w_other = 0.f;
-      const bool shared_keys = sg.keys && sg.n_tiles > 1;
+      const bool shared_keys = sg->keys && sg->n_tiles > 1;
       if (shared_keys) {   // the lanes' halves of a row: either lane puts together one half of the dims
         stat[t * QR + r] = m_ref;
         if (!wait_bar(bar(B_PV + 1 - t), (other - 1) & 1)) *abort_flag = 1;
@@ -736,19 +768,20 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         m_ref = mx;
       }
       tc::tc_fence_after();
-      if (warp_rows && !(sg.keys && !shared_keys && t == 1)) {
+      if (warp_rows && !(sg->keys && !shared_keys && t == 1)) {
         const bool has = r < p.rpt && lrow0 + r < nrows, none = l == 0.f;
         const int qi = lrow0 + r;
-        const size_t orow = has ? (size_t)(sg.u.b * a.L + qi / grp) * a.nq + sg.u.g * grp + qi % grp : 0;
-        const size_t prow = (size_t)sg.slot * sh.rows + (sg.keys ? r : t * p.rpt + r);
-        const float by = sg.whole ? (none ? 0.f : 1.f / l) : 1.f;
+        const int j = sh.by_grp.div(qi);
+        const size_t orow = has ? (size_t)(sg->u.b * a.L + j) * a.nq + sg->u.g * grp + qi - j * grp : 0;
+        const size_t prow = (size_t)(2 * blockIdx.x + sg->first) * sh.rows + (sg->keys ? r : t * p.rpt + r);
+        const float by = sg->whole ? (none ? 0.f : 1.f / l) : 1.f;
         const int from = shared_keys ? t * (HD / 2) : 0, to = shared_keys ? from + HD / 2 : HD;
         bool spoilt = false;
         // 16 dims at a time, in a loop that stays short: unrolled, its code took longer to fetch than to run
 #pragma unroll 1
         for (int c0 = from; c0 < to; c0 += 16) {
           float o[16];
-          if (sg.n_tiles > 0) {
+          if (sg->n_tiles > 0) {
             tmem_ld16_nowait(o_mine + c0, o);
             wait_ld16(o);
           }
@@ -767,7 +800,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           if (!has) continue;
           // dim e of 8 in its place: 4-bit pages leave the dims in the order 0 4 1 5 2 6 3 7
           auto dim = [&](int e) { return INT4 ? o[(e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1)] : o[e]; };
-          if (sg.whole) {
+          if (sg->whole) {
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dim(2 * i + 1)), "f"(dim(2 * i)));
@@ -782,13 +815,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
             }
           }
         }
-        if (sg.whole && has && spoilt) spoilt_units |= 1u << min(n_units, 31);
+        if (sg->whole && has && spoilt) spoilt_units |= 1u << min(n_units, 31);
         if (has && (!shared_keys || t == 0)) {
-          if (!sg.whole) a.ml[prow] = make_float2(m_ref, l);
+          if (!sg->whole) a.ml[prow] = make_float2(m_ref, l);
           else if (a.lse) a.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         }
       }
-      if (speaks && sg.first && !sg.whole) a.desc[blockIdx.x] = make_int4(sg.u.b, sg.u.g, sg.u.rt, sg.last_run);   // left to others
+      if (speaks && sg->first && !sg->whole) a.desc[blockIdx.x] = make_int4(sg->u.b, sg->u.g, sg->u.rt, sg->last_run);   // left to others
       tc::tc_fence_before();   // O has been read: the next run's first product follows this lane's next P
       if (shared_keys) meet();
       n_units++;
