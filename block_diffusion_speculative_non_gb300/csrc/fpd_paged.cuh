@@ -87,6 +87,7 @@ enum PagedKernel { kPagedStream, kPagedTc };
 struct PagedPlan {
   PagedKernel kernel;
   int rows, tiles;     // rows of a row tile, row tiles of a request and kv head
+  bool solo;           // k_paged_tc.cu: row tiles of one lane
   bool too_large;      // more key tiles than 31 bits hold
   int sms, grid, runs; // SMs, CTAs, and the runs that share the key tiles (of CTAs, or of their warps)
 };

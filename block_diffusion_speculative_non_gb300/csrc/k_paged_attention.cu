@@ -178,13 +178,23 @@ PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int format, int t_c
   pl.sms = num_sms;
   const int grp = nq / nkv, n = L * grp;
   pl.kernel = n <= 16 ? kPagedStream : kPagedTc;
-  pl.rows = n <= 8 ? 8 : n <= 16 ? 16 : 2 * (128 / grp * grp);
+  // tcgen05: one lane's rows (4 bits: 96, so that warps are left to decode for either lane), or as few row tiles of two lanes as there
+  // can be, of even sizes
+  const int npt = 128 / grp, tiles = ceil_div(L, 2 * npt);
+  pl.solo = pl.kernel == kPagedTc && L <= npt && n <= (format == FPD_PAGE_INT4 ? 96 : 128);
+  pl.rows = n <= 8 ? 8 : n <= 16 ? 16 : pl.solo ? n : 2 * grp * ceil_div(L, 2 * tiles);
   pl.tiles = ceil_div(n, pl.rows);
   // no more runs than there can be tiles
   const long long most = (long long)batch * nkv * pl.tiles * (ceil_div(t_cap, kPagedTile) + ceil_div(L, kPagedTile));
   pl.too_large = most + 2ll * batch * nkv * pl.tiles * (1 + kUnitCost) > INT32_MAX;
-  pl.runs = (int)std::min<long long>(most, (long long)num_sms * (pl.kernel == kPagedStream ? paged_stream_warps(pl.rows, format) : 1));
-  pl.grid = std::min(num_sms, pl.runs);
+  if (pl.kernel == kPagedStream) {
+    pl.runs = (int)std::min<long long>(most, (long long)num_sms * paged_stream_warps(pl.rows, format));
+    pl.grid = std::min(num_sms, pl.runs);
+  } else {
+    const int lanes = pl.solo ? 2 : 1;   // runs of a CTA
+    pl.grid = (int)std::min<long long>(num_sms, (most + lanes - 1) / lanes);
+    pl.runs = pl.grid * lanes;
+  }
   return pl;
 }
 
@@ -201,7 +211,7 @@ cudaError_t launch_paged_attention(const PagedAttn& a, const PagedPlan& pl, cuda
   p.s = paged_shape(a.L, a.lb, a.nq / a.pg.nkv, a.pg.nkv, pl.rows, a.window > kFar ? 0 : a.window, std::min(a.sinks, kFar), a.causal && a.L > 1,
                     pl.kernel == kPagedTc ? kPagedTcTile : kPagedTile, kUnitCost);
   p.runs = pl.runs;
-  p.spoilt_words = pl.kernel == kPagedStream ? 1 : 8;
+  p.spoilt_words = pl.kernel == kPagedStream ? 1 : pl.solo ? 4 : 8;
   return a.pg.h == 128 ? launch<128>(p, pl, st) : launch<64>(p, pl, st);
 }
 

@@ -3,16 +3,15 @@
 //
 // A CTA works on two "lanes", each a 128-row S / P / O set in tensor memory with a softmax warpgroup of its own (one thread per
 // query row), so that one lane's softmax runs while the tensor core works for the other.  A lane's rows are whole positions, the kv
-// head's heads of each.  A unit has the rows of two lanes, which share every K/V tile; where it has one lane's rows only (a text
-// block, the last rows of a long one) both lanes hold them and take the even and the odd key tiles, and their halves of O are put
-// together from tensor memory: a thread of either lane reaches both accumulators of its row.
+// head's heads of each.  Where a unit has more rows than a lane, it has the rows of two, which share every K/V tile; where a request
+// has at most a lane's (a text block), each lane walks a run of its own, with its own tiles, warps and barriers: one's way out of a
+// unit and into the next is hidden behind the other's tiles.
 //
 // bf16 pages: TMA, one box per page and 64 dims (a coordinate past the pool, which reads zeros, for a page that is none); P enters as
 // two bf16 terms.
-// 4-bit pages: three warps decode tiles into the swizzled layout, K as bf16 and V as fp16 (7 bits either way, exact), a row of a
-// tile per thread.  The pairs that decode together are dims i and i + 4 of 8, so
-// Q is stored in that order too, and O comes out in it.  P enters as one fp16 term, p 2^7 (p stays below 2^8; weights down to 2^-31
-// count); the block's own keys are bf16 and take the bf16 products.
+// 4-bit pages: warps decode tiles into the swizzled layout, K as bf16 and V as fp16 (7 bits either way, exact).  The pairs that decode
+// together are dims i and i + 4 of 8, so Q is stored in that order too, and O comes out in it.  P enters as one fp16 term, p 2^7 (p
+// stays below 2^8; weights down to 2^-31 count); the block's own keys are bf16 and take the bf16 products.
 #include <cstring>
 
 #include "attn_tc_prims.cuh"
@@ -29,7 +28,7 @@ constexpr int QR = 128, KT = kPagedTcTile;
 constexpr int KST = 2;
 template <bool INT4>
 constexpr int kVst = INT4 ? 2 : 3;     // V slots; 4-bit pages leave one to the codes
-constexpr int kRawSlots = 3;           // a ring of codes and scales: slots, each a tile's K or V
+constexpr int kRawSlots = 3;           // most slots of a ring of codes and scales, each a tile's K or V
 constexpr int kTmemCols = 512;         // S/P of lane t at 128 t, O of lane t at 256 + 128 t
 constexpr uint32_t kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
@@ -39,28 +38,26 @@ struct TcArgs {
   CUtensorMap tm_q, tm_pages, tm_kblk, tm_vblk;
   PagedAttn a;
   PagedShape s;
-  int runs, npt, rpt;   // positions and rows of a lane
+  int runs, npt, rpt, solo;   // positions and rows of a lane; whether the lanes have runs of their own
 };
 
-// A part of a unit as this kernel walks it.  Warp 0 walks, a few parts ahead, and leaves what it finds in shared memory: walks of their
-// own took every warp some 40 registers, spilled at each unit, and code to fetch.
+// A part of a unit as this kernel walks it.  One warp walks a run, a few parts ahead, and leaves what it finds in shared memory: walks
+// of their own took every warp some 40 registers, spilled at each unit.
 constexpr int kSegs = 4;
 struct Seg {
   PagedUnit u;                              // u.b < 0: the run is over
-  int keys, whole, first;                   // keys: one lane's rows; first: the unit starts here
+  int whole, first;                         // first: the unit starts here
   int t0, n_tiles, row0, last_run;
   __device__ PagedTile tile(int i) const { return tile_at(u, KT, t0 + i); }
-  __device__ int lane_tiles(int t) const { return keys ? (n_tiles - t + 1) / 2 : n_tiles; }
 };
 
 template <int HD, bool INT4>
 struct Lay {
   static constexpr int TILE = KT * HD * 2, ATOMS = HD / 64, VST = kVst<INT4>;
   static constexpr int RAW_BYTES = KT * (HD / 2 + HD / 16);
-  // lane 1's Q lies before the codes, which have its place where the lanes share one
-  static constexpr int Q = 0, K = TILE, V = K + KST * TILE, Q1 = V + VST * TILE, RAW = Q1 + TILE;
-  static constexpr int STAT = RAW + (INT4 ? kRawSlots * RAW_BYTES : 0), SEG = STAT + 2 * QR * 4, BAR = SEG + kSegs * (int)sizeof(Seg);
-  static_assert(2 * kRawSlots * RAW_BYTES <= TILE + kRawSlots * RAW_BYTES, "two rings of codes");
+  // 4 bits, lanes on their own: the codes begin behind the rows of Q that are there
+  static constexpr int Q = 0, RAW = 2 * TILE, K = (RAW + (INT4 ? kRawSlots * RAW_BYTES : 0) + 1023) / 1024 * 1024;
+  static constexpr int V = K + KST * TILE, SEG = V + VST * TILE, BAR = SEG + 2 * kSegs * (int)sizeof(Seg);
 };
 enum {
   B_Q = 0,
@@ -73,12 +70,11 @@ enum {
   B_PF = B_SF + 2,
   B_PV = B_PF + 2,
   B_END = B_PV + 2,
-  B_X = B_END + 1,   // the softmax warps, in units whose keys the lanes share
-  B_RF = B_X + 1,    // codes: full, empty [slot]
+  B_RF = B_END + 2,    // codes: full, empty [ring][slot]
   B_RE = B_RF + 2 * kRawSlots,
-  B_GF = B_RE + 2 * kRawSlots,   // parts of units: full, empty [slot]
-  B_GE = B_GF + kSegs,
-  B_N = B_GE + kSegs
+  B_GF = B_RE + 2 * kRawSlots,   // parts of units: full, empty [run][slot]
+  B_GE = B_GF + 2 * kSegs,
+  B_N = B_GE + 2 * kSegs
 };
 template <int HD, bool INT4>
 constexpr size_t smem_bytes() {
@@ -86,11 +82,12 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<128, true>() <= 232448, "tile set exceeds the shared memory of one CTA");
 
-// bf16: 11 warps, 0 and 2 TMA producers of K and Q, and of V, 1 the products, 3.. softmax.  4 bits: 16 warps, 0
-// copies codes, 2..7 decode, 8.. softmax, which takes the scores in two halves (128 registers a thread).
+// Warp 1 issues the products, of both lanes or of lane 0, and warp 3 those of lane 1 on its own.  bf16: warps 0 and 2 copy, K with Q
+// and V, or all of a lane; softmax from 4 on.  4 bits: warp 0 copies codes (and warp 2 those of lane 1 on its own), the others below 8
+// decode, and softmax takes the scores in two halves (128 registers a thread).
 template <bool INT4>
 struct Roles {
-  static constexpr int THREADS = INT4 ? 512 : 352, SOFTMAX = INT4 ? 8 : 3;
+  static constexpr int THREADS = INT4 ? 512 : 384, SOFTMAX = INT4 ? 8 : 4;
 };
 
 __device__ __forceinline__ void split_trunc(float a, float b, uint32_t& hi, uint32_t& lo) {   // a, b >= 0: hi + lo to 2^-16
@@ -133,14 +130,16 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   const PagedAttn& a = p.a;
   const PagedShape& sh = p.s;
   const int grp = sh.grp, nrows = a.L * grp;
-  // 4 bits: quarters of the lanes that no unit's rows reach (a text block's 64) decode instead.  The decoding warps are then two
-  // teams, of K and of V, each with a ring of codes; else one.  The lanes of such units hold the same rows, in one copy.
-  const int live = INT4 && nrows <= min(p.rpt, 96) ? (nrows + 31) / 32 : 4;
-  const bool two = INT4 && live < 4;
-  const int quarter = warp & 3, teams = two ? 2 : 1;
-  const bool helps = two && warp >= Ro::SOFTMAX && quarter >= live;
-  // arrivals that fill a tile, and Q: from every warp of the team, or from the one that issues the copies
-  const int NW = (6 + 2 * (4 - live)) / teams, fill = INT4 ? NW : 1, fill_q = INT4 ? 4 : 1;
+  // 4 bits: quarters of the lanes that no unit's rows reach (a text block's 64) decode instead
+  const int live = INT4 ? (min(nrows, p.rpt) + 31) / 32 : 4;
+  const bool solo = p.solo;
+  const int quarter = warp & 3;
+  const bool helps = INT4 && warp >= Ro::SOFTMAX && quarter >= live;
+  const int own = solo ? 4 : 2;                                            // decoding warps from here to 7 beside the helpers
+  const int NW = (8 - own + 2 * (4 - live)) / (solo ? 2 : 1);              // decoding warps of a team: of a lane, or all
+  const int decodes = helps ? 8 - own + (warp >= Ro::SOFTMAX + 4 ? 4 - live : 0) + quarter - live : warp - own, team = solo ? decodes / NW : 0;
+  // arrivals that fill a tile, and Q: from every warp of the team, or from the one that issues the copies; and that read a part
+  const int fill = INT4 ? NW : 1, fill_q = INT4 ? live : 1, readers = 1 + (INT4 ? NW : solo ? 0 : 1) + (solo ? 1 : 2) * live;
 
   if (tid == 0) {
     for (int t = 0; t < 2; t++) {
@@ -162,12 +161,11 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       tc::mbar_init(bar(B_RF + s), 1);
       tc::mbar_init(bar(B_RE + s), NW);
     }
-    for (int s = 0; s < kSegs; s++) {
+    for (int s = 0; s < 2 * kSegs; s++) {
       tc::mbar_init(bar(B_GF + s), 1);
-      tc::mbar_init(bar(B_GE + s), Ro::THREADS / 32 - 1);
+      tc::mbar_init(bar(B_GE + s), readers);
     }
-    tc::mbar_init(bar(B_END), 1);
-    tc::mbar_init(bar(B_X), 2 * live);
+    for (int t = 0; t < 2; t++) tc::mbar_init(bar(B_END + t), 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
     if (!INT4) {
@@ -186,17 +184,23 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   pdl_wait();
   pdl_trigger();
   const DeviceLens lens{a.ctx_len, a.pg.cap()};
-  PagedWalk<DeviceLens> walk = warp == 0 ? make_walk(sh, lens, a.batch, p.runs, blockIdx.x) : PagedWalk<DeviceLens>(sh, lens, a.batch, 1, 1, 1);
+  const bool walks = warp == 0 || (solo && warp == 2);
+  PagedWalk<DeviceLens> walk =
+      walks ? make_walk(sh, lens, a.batch, p.runs, solo ? 2 * blockIdx.x + warp / 2 : blockIdx.x) : PagedWalk<DeviceLens>(sh, lens, a.batch, 1, 1, 1);
   __syncwarp();   // a CTA barrier counts a whole warp: single-lane roles reconverge before every one
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  Seg* const segs = reinterpret_cast<Seg*>(smem + S::SEG);
+  // the run of the warp: lane 1's on its own, or else the CTA's
+  const bool softmaxes = warp >= Ro::SOFTMAX && !helps;
+  const int ln = !solo ? 0 : softmaxes ? (warp - Ro::SOFTMAX) >> 2 : warp < 4 ? warp >> 1 : team;
+  Seg* const segs = reinterpret_cast<Seg*>(smem + S::SEG) + ln * kSegs;
+  const int b_gf = B_GF + ln * kSegs, b_ge = B_GE + ln * kSegs;
   const Seg* sg = segs;
   int n_seg = 0;
-  auto walk_next = [&]() {   // warp 0
+  auto walk_next = [&]() {
     const int s = n_seg % kSegs;
     Seg w;
     int t1;
@@ -205,15 +209,14 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       w.first = w.t0 == 0;
       w.n_tiles = max(0, min(t1, w.u.tiles()) - w.t0);   // an empty unit has none
       w.row0 = w.u.rt * sh.rows;
-      w.keys = nrows - w.row0 <= p.rpt;
     } else {
       w.u.b = -1;
     }
-    if (n_seg >= kSegs && !wait_bar(bar(B_GE + s), ((n_seg / kSegs) & 1) ^ 1)) *abort_flag = 1;
+    if (n_seg >= kSegs && !wait_bar(bar(b_ge + s), ((n_seg / kSegs) & 1) ^ 1)) *abort_flag = 1;
     __syncwarp();
     if (lane == 0) {
       segs[s] = w;
-      tc::mbar_arrive(bar(B_GF + s));
+      tc::mbar_arrive(bar(b_gf + s));
     }
     __syncwarp();
     sg = segs + s;
@@ -222,79 +225,88 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   };
   auto next = [&]() {   // the others: done with the part before
     __syncwarp();
-    if (n_seg > 0 && lane == 0) tc::mbar_arrive(bar(B_GE + (n_seg - 1) % kSegs));
-    if (!wait_bar(bar(B_GF + n_seg % kSegs), (n_seg / kSegs) & 1)) *abort_flag = 1;
+    if (n_seg > 0 && lane == 0) tc::mbar_arrive(bar(b_ge + (n_seg - 1) % kSegs));
+    if (!wait_bar(bar(b_gf + n_seg % kSegs), (n_seg / kSegs) & 1)) *abort_flag = 1;
     sg = segs + n_seg % kSegs;
     n_seg++;
     return !*abort_flag && sg->u.b >= 0;
   };
 
+  // 4 bits: Q of a lane on its own takes the rows that there are, and the codes' rings what that leaves
+  const int q_atom = INT4 && solo ? live * 32 * 128 : ATOM_BYTES, q_bytes = S::ATOMS * q_atom;
+  auto q_at = [&](int l) { return tc::smem_u32(smem + S::Q) + l * q_bytes; };
+  const int raw_slots = solo && live == 3 ? 2 : kRawSlots;
+  const uint32_t raws = tc::smem_u32(smem) + (solo ? 2 * q_bytes + ln * raw_slots * S::RAW_BYTES : S::RAW);
+  const int b_rf = B_RF + ln * kRawSlots, b_re = B_RE + ln * kRawSlots;
+
+  auto drain = [&](int first, int copies, int slots) {   // the copies into a ring that may still be in flight
+    for (int i = max(0, copies - slots); i < copies; i++) tc::mbar_wait(bar(first + i % slots), (i / slots) & 1);
+  };
+
   if (!INT4 && (warp == 0 || warp == 2)) {
-    // ---------------- TMA producers: K and Q (warp 0), V (warp 2); lane i copies a tile's page i ----------------
-    const bool is_v = warp == 2;
-    const int ST = is_v ? VST : KST, full = is_v ? B_VF : B_KF, empty = is_v ? B_VE : B_KE;
-    const uint32_t ring = tc::smem_u32(smem + (is_v ? S::V : S::K));
+    // ---------------- TMA producers: K and Q (warp 0) and V (warp 2), or all of a lane; lane i copies a tile's page i ----------------
     const int bp = min(KT, a.pg.page);   // rows of a box
-    int n = 0, nq[2] = {0, 0};
+    int n = 0, copied[2] = {0, 0}, nq[2] = {0, 0};   // tiles; copies of K and V; loads of Q
     auto page_for = [&](int i) {   // of this lane's part of tile i
       if (i >= sg->n_tiles) return 0;
       const PagedTile t = sg->tile(i);
       return t.ctx && lane * bp < t.valid ? page_of(a.pg, sg->u.b, t.k0 + lane * bp) : 0;
     };
     bool ok = true;
-    while (ok && !*abort_flag && (is_v ? next() : walk_next())) {
+    while (ok && !*abort_flag && (walks ? walk_next() : next())) {
       int id = page_for(0);
-      for (int i = 0; i < sg->n_tiles && ok; i++) {
-        const int s = n % ST;
+      for (int i = 0; i < sg->n_tiles && ok; i++, n++) {
         const PagedTile t = sg->tile(i);
         const int id_now = id;
         id = page_for(i + 1);
-        if (n >= ST) ok = wait_bar(bar(empty + s), ((n / ST) & 1) ^ 1);
-        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-        if (!ok) break;
-        const bool mine = t.ctx ? lane * bp < t.valid : lane == 0;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar(full + s), t.ctx ? boxes * bp * HD * 2 : S::TILE);
-        __syncwarp();
-        if (mine) {
-          for (int h = 0; h < S::ATOMS; h++) {
-            const uint32_t dst = ring + s * S::TILE + h * ATOM_BYTES;
-            if (t.ctx)
-              tc::tma_load_3d(dst + lane * bp * 128, &p.tm_pages, h * 64,
-                              ((is_v ? a.pg.nkv : 0) + sg->u.g) * a.pg.page + ((t.k0 + lane * bp) & (a.pg.page - 1)),
-                              id_now < 0 ? a.pg.n_pages : id_now, bar(full + s));
-            else
-              tc::tma_load_2d(dst, is_v ? &p.tm_vblk : &p.tm_kblk, h * 64, (sg->u.b * a.pg.nkv + sg->u.g) * a.lb + t.k0, bar(full + s));
-          }
-        }
-        n++;
-        if (is_v || i > 0) continue;
-        // Q behind the first K tile, whose slot is free one S before Q's (with the last S of the run before)
-        for (int l = 0; l < 2 && ok; l++) {
-          if (sg->lane_tiles(l) == 0) continue;
-          if (nq[l] > 0) ok = wait_bar(bar(B_QE + l), (nq[l] & 1) ^ 1);
-          ok = __all_sync(0xffffffffu, ok);
+        for (int is_v = !solo && warp == 2; is_v < (!solo && warp == 0 ? 1 : 2); is_v++) {
+          const int ST = is_v ? VST : KST, round = solo ? n : n / ST, s = solo ? ln : n - round * ST, full = (is_v ? B_VF : B_KF) + s;
+          if (round > 0) ok = wait_bar(bar((is_v ? B_VE : B_KE) + s), (round & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
           if (!ok) break;
-          if (lane == 0) {
-            tc::mbar_arrive_expect_tx(bar(B_Q + l), p.rpt * HD * 2);
-            for (int h = 0; h < S::ATOMS; h++)
-              tc::tma_load_3d(tc::smem_u32(smem + (l ? S::Q1 : S::Q)) + h * ATOM_BYTES, &p.tm_q, h * 64, sg->u.g * grp,
-                              sg->u.b * a.L + (sg->row0 + (sg->keys ? 0 : l * p.rpt)) / grp, bar(B_Q + l));
+          const bool mine = t.ctx ? lane * bp < t.valid : lane == 0;
+          const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar(full), t.ctx ? boxes * bp * HD * 2 : S::TILE);
+          __syncwarp();
+          if (mine) {
+            for (int h = 0; h < S::ATOMS; h++) {
+              const uint32_t dst = tc::smem_u32(smem + (is_v ? S::V : S::K)) + s * S::TILE + h * ATOM_BYTES;
+              if (t.ctx)
+                tc::tma_load_3d(dst + lane * bp * 128, &p.tm_pages, h * 64,
+                                ((is_v ? a.pg.nkv : 0) + sg->u.g) * a.pg.page + ((t.k0 + lane * bp) & (a.pg.page - 1)),
+                                id_now < 0 ? a.pg.n_pages : id_now, bar(full));
+              else
+                tc::tma_load_2d(dst, is_v ? &p.tm_vblk : &p.tm_kblk, h * 64, (sg->u.b * a.pg.nkv + sg->u.g) * a.lb + t.k0, bar(full));
+            }
           }
-          nq[l]++;
+          copied[is_v]++;
+          if (is_v || i > 0) continue;
+          // Q behind the first K tile, whose slot is free one S before Q's (with the last S of the part before)
+          for (int l = ln; l < (solo ? ln + 1 : 2) && ok; l++) {
+            if (nq[l] > 0) ok = wait_bar(bar(B_QE + l), (nq[l] & 1) ^ 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+              tc::mbar_arrive_expect_tx(bar(B_Q + l), p.rpt * HD * 2);
+              for (int h = 0; h < S::ATOMS; h++)
+                tc::tma_load_3d(tc::smem_u32(smem + S::Q) + l * S::TILE + h * ATOM_BYTES, &p.tm_q, h * 64, sg->u.g * grp,
+                                sg->u.b * a.L + (sg->row0 + (solo ? 0 : l * p.rpt)) / grp, bar(B_Q + l));
+            }
+            nq[l]++;
+          }
+          if (!ok) break;
         }
       }
     }
     if (!ok) *abort_flag = 1;
     if (*abort_flag) {   // a wait ran out: let the copies in flight land before the CTA's memory goes
-      for (int i = max(0, n - ST); i < n; i++) tc::mbar_wait(bar(full + i % ST), (i / ST) & 1);
-      for (int t = 0; t < 2; t++)
-        if (nq[t] > 0) tc::mbar_wait(bar(B_Q + t), (nq[t] & 1) ^ 1);
+      drain(B_KF + ln, copied[0], solo ? 1 : KST);
+      drain(B_VF + ln, copied[1], solo ? 1 : VST);
+      for (int l = 0; l < 2; l++) drain(B_Q + l, nq[l], 1);
     }
-  } else if (INT4 && warp == 0) {
+  } else if (INT4 && walks) {
     // ---------------- codes of the context tiles, K and V in turn, by bulk copies: lanes 2 i + part copy from page i ----------------
     const int kp = min(KT, a.pg.page), part = lane & 1, pi = lane >> 1;   // part: codes, scales
-    const uint32_t ring = tc::smem_u32(smem + (two ? S::Q1 : S::RAW));
     const uint32_t w = part ? HD / 16 : HD / 2;
     int h = 0;   // halves of tiles so far
     bool ok = true;
@@ -316,49 +328,44 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         const uint32_t at = (part ? KT * (HD / 2) : 0) + pi * kp * w;
 #pragma unroll 1
         for (int v = 0; v < 2; v++, h++) {
-          const int c = h / teams, s = c % kRawSlots + (two ? v * kRawSlots : 0);
-          if (c >= kRawSlots) ok = wait_bar(bar(B_RE + s), ((c / kRawSlots) & 1) ^ 1);
+          const int round = h / raw_slots, s = h - round * raw_slots, full = b_rf + s;
+          if (round > 0) ok = wait_bar(bar(b_re + s), (round & 1) ^ 1);
           ok = __all_sync(0xffffffffu, ok && !*abort_flag);
           if (!ok) break;
           if (rows > 0 && id_now < 0) {   // a page that is none: zeros
             for (uint32_t j = 0; j < rows * w; j += 16)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + s * S::RAW_BYTES + at + j), "r"(0) : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(raws + s * S::RAW_BYTES + at + j), "r"(0) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar(B_RF + s), total);
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar(full), total);
           __syncwarp();
           if (bytes)
-            tc::bulk_load(ring + s * S::RAW_BYTES + at, slab_of(a.pg, id_now, v, sg->u.g) + (part ? a.pg.page * (HD / 2) : 0) + in * w, bytes,
-                          bar(B_RF + s));
+            tc::bulk_load(raws + s * S::RAW_BYTES + at, slab_of(a.pg, id_now, v, sg->u.g) + (part ? a.pg.page * (HD / 2) : 0) + in * w, bytes,
+                          bar(full));
         }
       }
     }
     if (!ok) *abort_flag = 1;
-    if (*abort_flag)
-      for (int i = max(0, h - teams * kRawSlots); i < h; i++) {
-        const int c = i / teams;
-        tc::mbar_wait(bar(B_RF + c % kRawSlots + (two ? (i & 1) * kRawSlots : 0)), (c / kRawSlots) & 1);
-      }
-  } else if (INT4 && ((warp < Ro::SOFTMAX && warp != 1) || helps)) {
+    if (*abort_flag) drain(b_rf, h, raw_slots);
+  } else if (INT4 && ((warp < Ro::SOFTMAX && warp >= own) || helps)) {
     // ---------------- decoding warps ----------------
     // A tile's K or V is HD / 8 items, each 32 rows by 32 dims of every row; a team's warps take turns at them, a thread a row.  One
     // copy of the code for all: unrolled, a third of the stalls were for instructions.
-    const int wall = helps ? 6 + (warp >= Ro::SOFTMAX + 4 ? 4 - live : 0) + quarter - live : warp - 2;
-    const int team = wall >= NW, wd = wall - (team ? NW : 0);
+    const int wd = solo ? decodes - team * NW : decodes;
     if (helps && lane == 0) a.spoilt[blockIdx.x * 8 + warp - Ro::SOFTMAX] = 0;
-    const uint32_t ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V), rs = tc::smem_u32(smem + (two ? S::Q1 : S::RAW));
-    int n = 0, nc = 0, nq[2] = {0, 0};   // tiles, context tiles and Q loads so far
+    const uint32_t ks = tc::smem_u32(smem + S::K), vs = tc::smem_u32(smem + S::V);
+    int n = 0, nh = 0, nq = 0;   // tiles, halves of context tiles and Q loads so far
     // chunk of 8 dims ch of row r in a tile of 64-dim atoms
-    auto put = [&](uint32_t row, int ch, uint4 v) {
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"((row ^ ((ch & 7) << 4)) + (ch >> 3) * ATOM_BYTES), "r"(v.x), "r"(v.y),
+    auto put = [&](uint32_t row, int ch, uint4 v, int atom = ATOM_BYTES) {
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"((row ^ ((ch & 7) << 4)) + (ch >> 3) * atom), "r"(v.x), "r"(v.y),
                    "r"(v.z), "r"(v.w)
                    : "memory");
     };
     auto row_at = [&](uint32_t tile, int r) { return tile + r * 128 + ((r & 7) << 4); };   // its chunk 0; chunk c at c ^ (r & 7)
     // 32 bf16 rows from row r0 of a tile on, in the order of the decoded ones; from(r): a row's address, null for zeros.  A warp's load
     // has whole rows.
-    auto put_bf16 = [&](uint32_t tile, int r0, auto from) {
+    auto put_bf16 = [&](uint32_t tile, int r0, int atom, auto from) {
       constexpr int PER = HD / 8, RPL = 32 / PER;   // chunks of a row, rows of a load
       const int ch = lane % PER, r_in = lane / PER;
 #pragma unroll 1
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
 #pragma unroll
         for (int i = 0; i < 8; i++)
           put(row_at(tile, r0 + (i0 + i) * RPL + r_in), ch, make_uint4(__byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
-                                                                       __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632)));
+                                                                       __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632)), atom);
       }
     };
     // 32 dims of row r of the codes in a slot (past `valid`: zeros) into row r of a tile: the j-th of the row's HD / 32 chunks of 16
@@ -415,66 +422,70 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     };
     while (ok && !*abort_flag && next()) {
       const size_t blk = ((size_t)sg->u.b * a.pg.nkv + sg->u.g) * a.lb;
-      for (int i = 0; i < 8 && ok; i++) {   // Q beside the first K tile: eight items of 32 rows, from the second warp on
-        const int l = i >> 2, k = i & 3;
-        if (sg->lane_tiles(l) == 0 || (two && l) || (i + 1) % (teams * NW) != wall) continue;
-        if (nq[l] > 0 && !wait(B_QE + l, (nq[l] & 1) ^ 1)) break;
-        const int q0 = sg->row0 + (sg->keys ? 0 : l * p.rpt);
-        put_bf16(tc::smem_u32(smem + (l ? S::Q1 : S::Q)), k * 32, [&](int r) -> const bf16* {
-          const int qi = q0 + r, j = sh.by_grp.div(qi);
-          return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg->u.b * a.L + j) * a.nq + sg->u.g * grp + qi - j * grp) * HD : nullptr;
-        });
-        done(B_Q + l);
+      if (sg->n_tiles > 0) {   // Q beside the first K tile: an item for 32 rows, from the second warp on
+        const int lanes = solo ? 1 : 2;
+        for (int i = 0; i < lanes * live && ok; i++) {
+          const int l = i < live ? ln : 1, k = i < live ? i : i - live;
+          if ((i + 1) % NW != wd) continue;
+          if (nq > 0 && !wait(B_QE + l, (nq & 1) ^ 1)) break;
+          const int q0 = sg->row0 + (solo ? 0 : l * p.rpt);
+          put_bf16(q_at(l), k * 32, q_atom, [&](int r) -> const bf16* {
+            const int qi = q0 + r, j = sh.by_grp.div(qi);
+            return r < p.rpt && qi < nrows ? a.q + ((size_t)(sg->u.b * a.L + j) * a.nq + sg->u.g * grp + qi - j * grp) * HD : nullptr;
+          });
+          done(B_Q + l);
+        }
+        nq++;
       }
-      for (int l = 0; l < 2; l++) nq[l] += sg->lane_tiles(l) > 0;
       // Whether or not it has an item, a warp waits for all slots and codes of its team, and its arrival fills and frees them: a wait
       // on a parity must begin neither two phases early nor two late.
 #pragma unroll 1
       for (int i = 0; i < sg->n_tiles && ok; i++, n++) {
         const PagedTile t = sg->tile(i);
 #pragma unroll 1
-        for (int is_v = team; is_v < 2 && ok; is_v += teams) {
-          const int slots = is_v ? VST : KST, round = n / slots, s = n - round * slots;
+        for (int is_v = 0; is_v < 2 && ok; is_v++) {
+          const int slots = is_v ? VST : KST, round = solo ? n : n / slots, s = solo ? ln : n - round * slots;
           if (round > 0 && !wait((is_v ? B_VE : B_KE) + s, (round & 1) ^ 1)) break;
           const uint32_t tile = (is_v ? vs : ks) + s * S::TILE;
           if (t.ctx) {
-            const int c = two ? nc : 2 * nc + is_v, slot = c % kRawSlots + team * kRawSlots;
-            if (!wait(B_RF + slot, (c / kRawSlots) & 1)) break;
+            const int turn = nh / raw_slots, slot = nh - turn * raw_slots;
+            if (!wait(b_rf + slot, turn & 1)) break;
+            nh++;
 #pragma unroll 1
             for (int item = wd; item < HD / 8; item += NW) {
               const int r = 32 * (item & 3) + lane;
-              put_codes(tile, rs + slot * S::RAW_BYTES, r, item >> 2, r < t.valid, is_v);
+              put_codes(tile, raws + slot * S::RAW_BYTES, r, item >> 2, r < t.valid, is_v);
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(B_RE + slot));
-          } else if (wd < 4) {
+            if (lane == 0) tc::mbar_arrive(bar(b_re + slot));
+          } else {
             const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
-            put_bf16(tile, 32 * wd, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
+#pragma unroll 1
+            for (int k = wd; k < 4; k += NW) put_bf16(tile, 32 * k, ATOM_BYTES, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
           }
           done((is_v ? B_VF : B_KF) + s);
         }
-        nc += t.ctx;
       }
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp == 1) {
+  } else if (warp == 1 || (solo && warp == 3)) {
     // ---------------- MMA issuer ----------------
     const uint32_t on = elect_one();
     constexpr uint32_t id_s = idesc_bf16(QR, KT, 0);   // Q x K, both K-major in shared memory
     constexpr uint32_t id_o = idesc_bf16(QR, HD, 1);   // P (tensor memory) x V (MN-major in shared memory)
     constexpr uint32_t id_h = idesc_f16(QR, HD, 1);
-    const uint64_t dq = tc::sw128_kmajor_desc(tc::smem_u32(smem + S::Q)), dk = tc::sw128_kmajor_desc(tc::smem_u32(smem + S::K));
-    const uint64_t dv = sw128_mn_desc(tc::smem_u32(smem + S::V), ATOM_BYTES);
-    int n0 = 0, nq[2] = {0, 0}, nl[2] = {0, 0};        // ring tiles, Q loads, lane tiles so far
+    const uint64_t dk = tc::sw128_kmajor_desc(tc::smem_u32(smem + S::K)), dv = sw128_mn_desc(tc::smem_u32(smem + S::V), ATOM_BYTES);
+    int n0 = 0, nq = 0, nl[2] = {0, 0};        // ring tiles, Q loads, lane tiles so far
+    auto uni = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     auto fail = [&]() { *abort_flag = 1; return false; };
-    auto wait_k = [&](int n) { return wait_bar(bar(B_KF + n % KST), (n / KST) & 1) || fail(); };
-    auto wait_v = [&](int n) { return wait_bar(bar(B_VF + n % VST), (n / VST) & 1) || fail(); };
+    auto wait_k = [&](int n) { return (solo ? wait_bar(bar(B_KF + ln), n & 1) : wait_bar(bar(B_KF + n % KST), (n / KST) & 1)) || fail(); };
+    auto wait_v = [&](int n) { return (solo ? wait_bar(bar(B_VF + ln), n & 1) : wait_bar(bar(B_VF + n % VST), (n / VST) & 1)) || fail(); };
     auto issue_s = [&](int t, int slot) {   // S_t = Q_t K^T, K from the slot
-      const uint64_t da = dq + (t && !two ? S::Q1 >> 4 : 0), db = dk + slot * (S::TILE >> 4);
+      const uint64_t da = tc::sw128_kmajor_desc(q_at(t)), db = dk + slot * (S::TILE >> 4);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; kk++) {
-        const uint64_t step = ((kk >> 2) * ATOM_BYTES + (kk & 3) * 32) >> 4;   // stays inside the address field
-        umma_ss_if(on, tmem + t * KT, da + step, db + step, id_s, kk > 0 ? 1u : 0u);
+        const uint32_t in = (kk & 3) * 32;   // sums stay inside the address field
+        umma_ss_if(on, tmem + t * KT, da + (((kk >> 2) * q_atom + in) >> 4), db + (((kk >> 2) * ATOM_BYTES + in) >> 4), id_s, kk > 0 ? 1u : 0u);
       }
       commit_if(on, bar(B_SF + t));
     };
@@ -501,21 +512,17 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       commit_if(on, bar(B_PV + t));
       return true;
     };
-    auto uni = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     bool ok = true;
     while (ok && !*abort_flag && next()) {
       const int nt = sg->n_tiles;
       if (nt == 0) continue;
-      for (int t = 0; t < 2 && ok; t++) {
-        if (sg->lane_tiles(t) == 0 || (two && t)) continue;
-        ok = wait_bar(bar(B_Q + t), nq[t] & 1) || fail();
-        nq[t]++;
-      }
+      for (int l = ln; l < (solo ? ln + 1 : 2) && ok; l++) ok = wait_bar(bar(B_Q + l), nq & 1) || fail();
+      nq++;
       tc::tc_fence_after();
       const int nc = sg->u.ns + sg->u.nm - sg->t0;   // tiles of the pages; the block's follow
       // Between a lane's P and its product stands nothing but the wait for P: a pair's other waits are done while the tensor
       // core still has work.
-      if (!sg->keys) {
+      if (!solo) {
         // a lane's next S follows its own product, so no lane waits for the other's softmax
         if (ok && (ok = wait_k(n0))) {
           tc::tc_fence_after();
@@ -548,60 +555,44 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           }
         }
       } else {
-        auto q_read = [&](int i, int t) {   // after S of tile i: the last one from a copy of Q
-          if (i + (two ? 1 : 2) >= nt) commit_if(on, bar(B_QE + (two ? 0 : t)));
-        };
-        for (int i = 0; i < min(2, nt) && ok; i++) {
+        for (int i = 0; i <= nt && ok && !*abort_flag; i++) {   // S of tile i behind the product of tile i - 1
+          if (i > 0) {
+            const int vs = uni(ln), acc = uni(i > 1);
+            if (!(ok = wait_v(n0 + i - 1) && pv(ln, vs, acc, i - 1 < nc))) break;
+            commit_if(on, bar(B_VE + ln));
+          }
+          if (i == nt) break;
           if (!(ok = wait_k(n0 + i))) break;
           tc::tc_fence_after();
-          const int ks = uni((n0 + i) % KST);
-          issue_s(i, ks);
-          commit_if(on, bar(B_KE + ks));
-          q_read(i, i);
-        }
-        for (int i = 0; i < nt && ok && !*abort_flag; i++) {
-          const int n = n0 + i, t = i & 1, vs = uni(n % VST), ks = uni((n + 2) % KST), acc = uni(i > 1);
-          if (!(ok = wait_v(n) && pv(t, vs, acc, i < nc))) break;
-          commit_if(on, bar(B_VE + vs));
-          if (i + 2 < nt) {
-            if (!(ok = wait_k(n + 2))) break;
-            tc::tc_fence_after();
-            issue_s(t, ks);
-            commit_if(on, bar(B_KE + ks));
-            q_read(i + 2, t);
-          }
+          issue_s(ln, uni(ln));
+          commit_if(on, bar(B_KE + ln));
+          if (i + 1 == nt) commit_if(on, bar(B_QE + ln));
         }
       }
       n0 += nt;
     }
     // everything issued is done before tensor memory is freed (at once, unless a wait ran out)
-    commit_if(on, bar(B_END));
-    tc::mbar_wait(bar(B_END), 0);
-  } else if (warp >= Ro::SOFTMAX) {
+    commit_if(on, bar(B_END + ln));
+    tc::mbar_wait(bar(B_END + ln), 0);
+  } else if (softmaxes) {
     // ---------------- softmax of lane t: thread = query row = TMEM lane ----------------
     const int t = (warp - Ro::SOFTMAX) >> 2, r = quarter * 32 + lane;
     const float sl2 = rsqrtf((float)HD) * 1.4426950408889634f;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lane_off + t * KT, o_mine = tmem + lane_off + kTmemO + t * 128;
-    float* stat = reinterpret_cast<float*>(smem + S::STAT);   // [lane][row]: m, then l, of units whose keys the lanes share
-    const bool speaks = warp == Ro::SOFTMAX && lane == 0;
-    if (speaks) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    const int run = solo ? 2 * blockIdx.x + t : blockIdx.x;
+    const bool speaks = quarter == 0 && (solo || t == 0) && lane == 0;
+    if (speaks) a.desc[run] = make_int4(-1, 0, 0, 0);
     unsigned spoilt_units = 0;   // parts of the run, from 31 on together, that came out whole and with something that is no number
-    int n_units = 0, met = 0;
-    auto meet = [&]() {   // with the other lane's warps; bounded, as every wait
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(B_X));
-      if (!wait_bar(bar(B_X), met++ & 1)) *abort_flag = 1;
-    };
-    int cnt = 0, other = 0, base = 0;   // tiles of this lane and of the other so far: phases of S, P and PV; of both: V slots
+    int n_units = 0;
+    int cnt = 0;   // tiles so far: phases of S, P and PV
     while (!*abort_flag && next()) {
-      const int lrow0 = sg->row0 + (sg->keys ? 0 : t * p.rpt);
+      const int lrow0 = sg->row0 + (solo ? 0 : t * p.rpt);
       const bool warp_rows = quarter * 32 < p.rpt && lrow0 + quarter * 32 < nrows;   // else padding
-      const int i0 = sg->keys ? t : 0, step = sg->keys ? 2 : 1;
       const int row_pos = sg->u.n - a.L + sh.by_grp.div(lrow0 + r);
       float m_ref = -INFINITY, l = 0.f;
       bool first_tile = true;
-      for (int i = i0; i < sg->n_tiles && !*abort_flag; i += step, cnt++) {
+      for (int i = 0; i < sg->n_tiles && !*abort_flag; i++, cnt++) {
         const PagedTile tl = sg->tile(i);
         const bool half = INT4 && tl.ctx;   // P as one fp16 term
         if (!wait_bar(bar(B_SF + t), cnt & 1)) *abort_flag = 1;
@@ -728,12 +719,12 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         first_tile = false;
         int h_lo, h_hi;
         hidden_from_all(sh, sg->u, tl, h_lo, h_hi);
-        if (!INT4 && (tl.valid < KT || h_hi > h_lo) && (sg->keys || t == 0)) {
+        if (!INT4 && (tl.valid < KT || h_hi > h_lo) && (solo || t == 0)) {
           // V rows past the last key, and those that no row sees -> 0 before the product: 0 x a value that is not finite would be
           // NaN.  A pair's lane 1 comes after lane 0's product.  Row k: 128 bytes at k * 128 in each 64-dim atom (the swizzle
           // permutes within a row).
-          const int n = base + i, s = n % VST;
-          if (!wait_bar(bar(B_VF + s), (n / VST) & 1)) *abort_flag = 1;
+          const int round = solo ? cnt : cnt / VST, s = solo ? t : cnt - round * VST;
+          if (!wait_bar(bar(B_VF + s), round & 1)) *abort_flag = 1;
           uint8_t* tile = smem + S::V + s * S::TILE;
           const int rows = KT - tl.valid + h_hi - h_lo;
           for (int c = r; c < rows * 8 * S::ATOMS; c += QR) {
@@ -747,50 +738,23 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(B_PF + t));
       }
-      other += sg->lane_tiles(1 - t);
-      base += sg->n_tiles;
       if (!first_tile && !wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
-      float w_mine = 1.f, w_other = 0.f;
-      const bool shared_keys = sg->keys && sg->n_tiles > 1;
-      if (shared_keys) {   // the lanes' halves of a row: either lane puts together one half of the dims
-        stat[t * QR + r] = m_ref;
-        if (!wait_bar(bar(B_PV + 1 - t), (other - 1) & 1)) *abort_flag = 1;
-        meet();
-        const float m_other = stat[(1 - t) * QR + r];
-        meet();
-        stat[t * QR + r] = l;
-        meet();
-        const float l_other = stat[(1 - t) * QR + r];
-        const float mx = fmaxf(m_ref, m_other);
-        w_mine = m_ref == -INFINITY ? (l == l ? 0.f : 1.f) : ex2(m_ref - mx);   // a NaN sum counts
-        w_other = m_other == -INFINITY ? (l_other == l_other ? 0.f : 1.f) : ex2(m_other - mx);
-        l = l * w_mine + l_other * w_other;
-        m_ref = mx;
-      }
       tc::tc_fence_after();
-      if (warp_rows && !(sg->keys && !shared_keys && t == 1)) {
+      if (warp_rows) {
         const bool has = r < p.rpt && lrow0 + r < nrows, none = l == 0.f;
         const int qi = lrow0 + r;
         const int j = sh.by_grp.div(qi);
         const size_t orow = has ? (size_t)(sg->u.b * a.L + j) * a.nq + sg->u.g * grp + qi - j * grp : 0;
-        const size_t prow = (size_t)(2 * blockIdx.x + sg->first) * sh.rows + (sg->keys ? r : t * p.rpt + r);
+        const size_t prow = (size_t)(2 * run + sg->first) * sh.rows + (solo ? r : t * p.rpt + r);
         const float by = sg->whole ? (none ? 0.f : 1.f / l) : 1.f;
-        const int from = shared_keys ? t * (HD / 2) : 0, to = shared_keys ? from + HD / 2 : HD;
         bool spoilt = false;
         // 16 dims at a time, in a loop that stays short: unrolled, its code took longer to fetch than to run
 #pragma unroll 1
-        for (int c0 = from; c0 < to; c0 += 16) {
+        for (int c0 = 0; c0 < HD; c0 += 16) {
           float o[16];
           if (sg->n_tiles > 0) {
             tmem_ld16_nowait(o_mine + c0, o);
             wait_ld16(o);
-          }
-          if (shared_keys) {
-            float q[16];
-            tmem_ld16_nowait(tmem + lane_off + kTmemO + (1 - t) * 128 + c0, q);
-            wait_ld16(q);
-#pragma unroll
-            for (int e = 0; e < 16; e++) o[e] = (w_mine == 0.f ? 0.f : o[e] * w_mine) + (w_other == 0.f ? 0.f : q[e] * w_other);
           }
 #pragma unroll
           for (int e = 0; e < 16; e++) {
@@ -816,14 +780,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           }
         }
         if (sg->whole && has && spoilt) spoilt_units |= 1u << min(n_units, 31);
-        if (has && (!shared_keys || t == 0)) {
+        if (has) {
           if (!sg->whole) a.ml[prow] = make_float2(m_ref, l);
           else if (a.lse) a.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         }
       }
-      if (speaks && sg->first && !sg->whole) a.desc[blockIdx.x] = make_int4(sg->u.b, sg->u.g, sg->u.rt, sg->last_run);   // left to others
+      if (speaks && sg->first && !sg->whole) a.desc[run] = make_int4(sg->u.b, sg->u.g, sg->u.rt, sg->last_run);   // left to others
       tc::tc_fence_before();   // O has been read: the next run's first product follows this lane's next P
-      if (shared_keys) meet();
       n_units++;
     }
     spoilt_units = __reduce_or_sync(0xffffffffu, spoilt_units);
@@ -860,7 +823,8 @@ cudaError_t launch_paged_tc(const PagedAttn& a, const PagedShape& s, const Paged
   p.a = a;
   p.s = s;
   p.runs = pl.runs;
-  p.npt = QR / s.grp;
+  p.solo = pl.solo;
+  p.npt = pl.solo ? s.L : pl.rows / 2 / s.grp;
   p.rpt = p.npt * s.grp;
   const uint64_t h = a.pg.h;
   if (a.pg.format == FPD_PAGE_BF16) {
