@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
   }
 }
 
-constexpr int kUnitCost = 2;   // what a unit costs besides its tiles, in tiles (0 and 2: 103 and 97 us at four trajectories with a window)
+constexpr int kUnitCost = 3;   // what a unit costs besides its tiles, in tiles (0, 2 and 3: 103, 97 and 95 us at four trajectories with a window)
 
 // Few short units: a CTA each, whose warps have at most four tiles, does without partials and the merge's launch.  (Rows of one position
 // see the same keys, so nothing needs a repair.)

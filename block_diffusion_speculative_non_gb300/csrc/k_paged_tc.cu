@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
         if (!wait_bar(bar(B_SF + t), cnt & 1)) *abort_flag = 1;
         tc::tc_fence_after();
         if (warp_rows) {
-          constexpr int W = INT4 ? KT / 2 : KT;   // scores held at a time
+          constexpr int W = KT / 2;   // scores held at a time
           float sv[W];
           uint32_t see[KT / 32];   // keys before `hi` that lie before `lo_end` or from `start` on, as bits
           const bool full = tile_full(sh, sg->u, tl);
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
           };
           uint64_t lq[2] = {0ull, 0ull};
 #pragma unroll 1
-          for (int k0 = 0; k0 < KT; k0 += W) {
+          for (int k0 = 0; k0 < (tl.valid > W ? KT : W); k0 += W) {
             load(k0);
             float mq[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
@@ -710,6 +710,13 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
                 tmem_st8(pt + 16, lo);
               }
             }
+          }
+          if (tl.valid <= W) {   // no key in the second half
+            const uint32_t zero[16] = {};
+            const int from = half ? W / 2 : W;
+#pragma unroll
+            for (int c = 0; c < W; c += 16)
+              if (c < from) tmem_st16(st + from + c, zero);
           }
           float la, lb;
           unpack2(add2(lq[0], lq[1]), la, lb);
