@@ -416,8 +416,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
     };
     bool ok = true;
     auto wait = [&](int b, uint32_t parity) {
-      ok = wait_bar(bar(b), parity);
-      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity));
       return ok;
     };
     while (ok && !*abort_flag && next()) {
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
       // Whether or not it has an item, a warp waits for all slots and codes of its team, and its arrival fills and frees them: a wait
       // on a parity must begin neither two phases early nor two late.
 #pragma unroll 1
-      for (int i = 0; i < sg->n_tiles && ok; i++, n++) {
+      for (int i = 0, nt = sg->n_tiles; i < nt && ok && !*abort_flag; i++, n++) {
         const PagedTile t = sg->tile(i);
 #pragma unroll 1
         for (int is_v = 0; is_v < 2 && ok; is_v++) {
@@ -456,14 +455,14 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
               const int r = 32 * (item & 3) + lane;
               put_codes(tile, raws + slot * S::RAW_BYTES, r, item >> 2, r < t.valid, is_v);
             }
-            __syncwarp();
+            done((is_v ? B_VF : B_KF) + s);
             if (lane == 0) tc::mbar_arrive(bar(b_re + slot));
           } else {
             const bf16* first = (is_v ? a.vblk : a.kblk) + (blk + t.k0) * HD;
 #pragma unroll 1
             for (int k = wd; k < 4; k += NW) put_bf16(tile, 32 * k, ATOM_BYTES, [&](int r) { return r < t.valid ? first + (size_t)r * HD : nullptr; });
+            done((is_v ? B_VF : B_KF) + s);
           }
-          done((is_v ? B_VF : B_KF) + s);
         }
       }
     }
