@@ -207,7 +207,8 @@ cudaError_t launch_rows(K kernel, const PagedRows& a, cudaStream_t st) {
 
 cudaError_t launch_paged_append(const PagedRows& a, cudaStream_t st) {
   const bool q = a.pg.format == FPD_PAGE_INT4;
-  // few rows: a thread for each slab; many: a thread keeps its angles for a row's slabs, as long as the GPU stays full
+  // few rows: a thread for each slab; many: a thread keeps its angles for a row's slabs, as long as the GPU stays full (1024 threads on
+  // each of its 152 SMs; eight prompts, 36864 rows: 66.8 us with a thread for each slab, 53 so, 85 % of the copy rate)
   const int slabs = 2 * a.pg.nkv, e = a.pg.h / 16;
   const int per = (int)std::min<long long>(slabs, std::max<long long>(1, (long long)a.total_rows * e * slabs / (152 * 1024)));
   const dim3 grid(ceil_div(a.total_rows, kThreads / e), ceil_div(slabs, per));

@@ -149,8 +149,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
 
 constexpr int kUnitCost = 3;   // what a unit costs besides its tiles, in tiles (0, 2 and 3: 103, 97 and 95 us at four trajectories with a window)
 
-// Few short units: a CTA each, whose warps have at most four tiles, does without partials and the merge's launch.  (Rows of one position
-// see the same keys, so nothing needs a repair.)
+// Few short units: a CTA each, whose warps have at most two tiles, does without partials and the merge's launch.  (Rows of one position
+// see the same keys, so nothing needs a repair.)  4 tokens, 8 kv heads, us in runs and so: contexts to 512 16.4 and 11.1, to 1024 (three
+// tiles a warp) 13.4 and 15.9; 4 bits, to 1024 11.9 and 10.0, to 2048 (three tiles) 13.8 and 14.8.
 bool unit_per_cta(const Args& p, const PagedPlan& pl) {
   const PagedShape& s = p.s;
   if (s.L > 1 && (s.window || s.causal)) return false;
@@ -158,7 +159,7 @@ bool unit_per_cta(const Args& p, const PagedPlan& pl) {
   long long keys_tiles = ceil_div(p.a.pg.cap(), kt);
   if (s.window) keys_tiles = std::min(keys_tiles, ((long long)s.window + s.L) / kt + 2 + ceil_div(std::min(s.sinks, 1 << 29), kt));
   const long long units = (long long)p.a.batch * s.nkv * s.tiles;
-  return units <= pl.sms && keys_tiles + ceil_div(s.lb, kt) <= 4 * paged_stream_warps(s.rows, p.a.pg.format);
+  return units <= pl.sms && keys_tiles + ceil_div(s.lb, kt) <= 2 * paged_stream_warps(s.rows, p.a.pg.format);
 }
 
 template <int H>
@@ -177,9 +178,12 @@ PagedPlan paged_attn_plan(int batch, int L, int nq, int nkv, int format, int t_c
   PagedPlan pl{};
   pl.sms = num_sms;
   const int grp = nq / nkv, n = L * grp;
+  // 16 rows, us by the stream kernel and by tcgen05: one context of 65536 73 and 70 (4 bits 55 and 63), 8 to 2048 28 and 24 (22 and 23),
+  // 64 to 4096 109 and 121 (76 and 114), 16 to 16384 109 and 116 (69 and 105)
   pl.kernel = n <= 16 ? kPagedStream : kPagedTc;
-  // tcgen05: one lane's rows (4 bits: 96, so that warps are left to decode for either lane), or as few row tiles of two lanes as there
-  // can be, of even sizes
+  // tcgen05: units of one lane's rows (4 bits: 96, so that warps are left to decode for either lane), or as few of two lanes as there can
+  // be, of even sizes.  128 rows of 64 requests: 137 us as one lane each, 164 as two (96 rows, 4 bits: 144 and 201); 1540 rows of 4 requests:
+  // 154 us in units of one lane, each with its own copies of K and V, 119 in units of two (with a window 85 and 78).
   const int npt = 128 / grp, tiles = ceil_div(L, 2 * npt);
   pl.solo = pl.kernel == kPagedTc && L <= npt && n <= (format == FPD_PAGE_INT4 ? 96 : 128);
   pl.rows = n <= 8 ? 8 : n <= 16 ? 16 : pl.solo ? n : 2 * grp * ceil_div(L, 2 * tiles);
