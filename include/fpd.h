@@ -489,7 +489,8 @@ fpd_status fpd_paged_read(int batch, int total_rows, const fpd_paged_store* stor
  * A row that sees no key (or scores of -inf alone) gives out 0 and lse -inf.  What a row does not see does not touch it, finite or
  * not (rows beside which a mask hides something that is not finite take the sum twice, slowly).
  * Sums are fp32; weights of bf16 pages enter the second product as two bf16 terms, those of 4-bit pages as fp16; out is rounded
- * once.  batch * block_len * n_q_heads <= 2^26, at most 128 query heads per kv head.  Lengths outside [0, table_width page_size]
+ * once.  batch * block_len * n_q_heads <= 2^26, at most 128 query heads per kv head, and the keys that the tables can name must not
+ * come to more than 2^31 tiles of 64 in all (FPD_ERR_SHAPE).  Lengths outside [0, table_width page_size]
  * are clamped (FPD_CHECK_BAD_CONTEXT).  Calls that share a workspace must not overlap on the GPU.
  *   q, out       device [batch * block_len, n_q_heads, h] bf16; q normed and rotated
  *   k_blk, v_blk device [batch, n_kv_heads, block_len, h] bf16, or both NULL: no block keys (the block's own have been appended)
