@@ -169,6 +169,9 @@ cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
   if (e != cudaSuccess || alone) return e;
   const int rows = std::min(pl.rows, p.a.L * p.s.grp);
   if (pl.kernel == kPagedStream) return launch_k(paged_merge_kernel<H, 1>, dim3(pl.runs, ceil_div(rows, kMergeWarps)), kMergeWarps * 32, 0, st, p);
+  // two partials a unit, mostly: more rows a warp (windows at four trajectories 78 -> 74 us, 3 blocks of few units 16.6 -> 17.3)
+  if (pl.runs <= 2ll * p.a.batch * p.s.nkv * p.s.tiles)
+    return launch_k(paged_merge_kernel<H, 4>, dim3(pl.runs, ceil_div(rows, 4 * kMergeWarps)), kMergeWarps * 32, 0, st, p);
   return launch_k(paged_merge_kernel<H, 2>, dim3(pl.runs, ceil_div(rows, 2 * kMergeWarps)), kMergeWarps * 32, 0, st, p);
 }
 

@@ -641,8 +641,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
             const bool need = mx > m_ref + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {   // tcgen05.ld/st are warp-wide: every lane takes part
               // by a power of two where there is something to bring along: exact, for the weights of the first half too
-              const float up = need ? ceilf(mx - m_ref) : 0.f, m_new = m_ref == -INFINITY ? (need ? mx : m_ref) : m_ref + up;
-              const float cf = m_ref == -INFINITY || !(up < 127.f) ? 0.f : __uint_as_float((127u - (uint32_t)up) << 23);   // 2^-up
+              const float m_new = !need ? m_ref : m_ref == -INFINITY ? mx : m_ref + ceilf(mx - m_ref);
+              const float cf = (m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);
               if (!first_tile) {
                 // O may only be rescaled once every product into it has finished
                 if (!wait_bar(bar(B_PV + t), (cnt - 1) & 1)) *abort_flag = 1;
@@ -662,7 +662,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
                 lq[0] = pack2(la * cf, lb * cf);
                 unpack2(lq[1], la, lb);
                 lq[1] = pack2(la * cf, lb * cf);
-                const uint32_t by = half ? pack_f16(cf, cf) : __float_as_uint(cf) >> 16 | (__float_as_uint(cf) & 0xFFFF0000u);
+                uint32_t by = pack_f16(cf, cf);   // rounded, the power of two itself
+                if (!half) asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(by) : "f"(cf));
 #pragma unroll 1
                 for (int c0 = 0; c0 < (half ? k0 / 2 : k0); c0 += 16) {
                   float w[16];
