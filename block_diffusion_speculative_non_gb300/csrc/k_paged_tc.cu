@@ -13,10 +13,10 @@
 // together are dims i and i + 4 of 8, so Q is stored in that order too, and O comes out in it.  P enters as one fp16 term, p 2^7 (p
 // stays below 2^8; weights down to 2^-31 count); the block's own keys are bf16 and take the bf16 products.
 //
-// Bound by a lane's chain, S -> softmax -> P -> product -> next S: about 2.1 us a tile of 128 keys, 1.2 to 1.4 of them softmax (its
+// Bound by a lane's chain, S -> softmax -> P -> product -> next S: 2.1 to 2.8 us a tile of 128 keys, 1.2 to 1.5 of them softmax (its
 // instructions, at one to two softmax warps a scheduler), and for 4-bit pages by the decoding beside it (0.7 us of a team's four warps for
 // K or V of a tile).  8 texts of 16 positions, contexts to 2048: 27 us; 64 texts over 4-bit pages to 4096: 121 us (0.28 PFLOP/s of the
-// formula); 4 trajectories of 385 positions with a window of 1024: 78 us (0.41).
+// formula); 4 trajectories of 385 positions with a window of 1024: 74 us (0.43).
 #include <cstring>
 
 #include "attn_tc_prims.cuh"
@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(Roles<INT4>::THREADS, 1) paged_tc_kernel(const
   const PagedAttn& a = p.a;
   const PagedShape& sh = p.s;
   const int grp = sh.grp, nrows = a.L * grp;
-  // 4 bits: quarters of the lanes that no unit's rows reach (a text block's 64) decode instead (64 texts: 177 us without them, 168 with)
+  // 4 bits: quarters of the lanes that no unit's rows reach (a text block's 64) decode instead (64 texts, when the lanes
+  // still shared a unit: 177 us without them, 168 with)
   const int live = INT4 ? (min(nrows, p.rpt) + 31) / 32 : 4;
   const bool solo = p.solo;
   const int quarter = warp & 3;
