@@ -338,6 +338,40 @@ def test_workspace_at_any_16_byte_offset(pkg):
 
 
 @pytest.mark.parametrize("form", ["bf16", "int4"])
+def test_two_graphs_share_a_workspace(pkg, form):
+    ps = [Problem(pkg, form, **CASES[name], causal=True) for name in ("many_texts", "primitive", "tokens_128")]
+    want = [tuple(t.clone() for t in p.run()) for p in ps]
+    ws = torch.full((max(p.workspace().numel() for p in ps),), 0xFF, dtype=torch.uint8, device=DEV)
+    graphs, s = [], torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for p in ps:
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=s):
+                p.run(ws)
+    torch.cuda.current_stream().wait_stream(s)
+    for turn in ((0, 1, 2), (2, 0, 1), (1, 0, 0, 2)):
+        for p in ps:
+            p.out.fill_(math.nan)
+        for i in turn:
+            graphs[i].replay()
+        for p, (out, lse) in zip(ps, want):
+            assert torch.equal(p.out, out) and torch.equal(p.lse, lse)
+
+
+def test_more_key_tiles_than_31_bits_are_refused(pkg):
+    B, nkv, h = 64, 8, 64
+    pages = torch.zeros(pkg.fpd_page_bytes(pkg.FPD_PAGE_BF16, 16, nkv, h) // 2, dtype=BF, device=DEV)
+    table = i32([[0]] * B)   # never read: the sizes are refused before a launch
+    st = pkg.paged_store(pages, pkg.FPD_PAGE_BF16, 1, 1, 16, nkv, h, table.data_ptr(), table_width=2 ** 30 // 16)
+    assert pkg.fpd_paged_attention_workspace_bytes(B, 1, nkv, st) == 0
+    q = torch.zeros(B, nkv, h, dtype=BF, device=DEV)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    with pytest.raises(pkg.FpdError, match="31 bits"):
+        pkg.fpd_paged_attention(B, 1, nkv, st, 0, q, None, None, i32([0] * B), 0, 0, False, torch.empty_like(q), None, ws, ws.numel())
+
+
+@pytest.mark.parametrize("form", ["bf16", "int4"])
 def test_two_streams_two_workspaces(pkg, form):
     ps = [Problem(pkg, form, **CASES[n], seed=i) for i, n in enumerate(("text", "primitive"))]
     want = [[t.clone() for t in p.run()] for p in ps]
