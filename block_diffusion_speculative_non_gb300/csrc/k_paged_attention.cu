@@ -20,7 +20,7 @@ struct Args {
   int runs, spoilt_words;   // words of `spoilt` of a run
 };
 
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 4, kMergeWays = 8;
 
 // A row of a unit summed over the keys it sees, by one warp (paged_repair.cuh).
 template <int H>
@@ -43,7 +43,7 @@ __device__ __noinline__ void repair_run(const Args& p, int c, unsigned bad) {
   int t0, t1, last;
   for (int n = 0; walk.next(u, t0, t1, last); n++) {
     if (t0 != 0 || t1 != u.len() || !(bad >> min(n, 31) & 1)) continue;
-    for (int qi = u.rt * p.s.rows + warp; qi < min(a.L * grp, (u.rt + 1) * p.s.rows); qi += kMergeWarps) {
+    for (int qi = u.rt * p.s.rows + warp; qi < min(a.L * grp, (u.rt + 1) * p.s.rows); qi += blockDim.x >> 5) {
       const int j = p.s.by_grp.div(qi);
       const bf16* row = a.out + ((size_t)(u.b * a.L + j) * a.nq + u.g * grp + qi - j * grp) * H;
       bool spoilt = false;
@@ -55,21 +55,41 @@ __device__ __noinline__ void repair_run(const Args& p, int c, unsigned bad) {
 
 // The units that runs share: CTA (c, y) puts together rows of the unit that run c starts and leaves unfinished, from slots
 // 2 c + 1, 2 (c + 1), .. in that order; a warp has RPW rows.  The partials are requested with their weights, not behind them.
-template <int H, int RPW>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ Args p) {
+// WAYS > 1, few units cut into many parts: CTA (u, y) has row y of unit u, whose first run it looks for, and its warps share the
+// partials (one context of 39520 positions, 82 rows, 304 parts: 24 us in all, 87 with a
+// warp for two rows; one token of a context of 65536 in 8 kv heads, 152 parts each: 55 and 70, in 4 bits 33 and 56).
+template <int H, int RPW, int WAYS = 1>
+__global__ void __launch_bounds__((WAYS > 1 ? WAYS : kMergeWarps) * 32) paged_merge_kernel(const __grid_constant__ Args p) {
+  static_assert(WAYS == 1 || RPW == 1, "a CTA shares one row");
   constexpr int DPL = H / 32, U = 8 / RPW;
   pdl_wait();
   pdl_trigger();
   const PagedAttn& a = p.a;
-  const int c = blockIdx.x, lane = threadIdx.x & 31, R = p.s.rows, grp = p.s.grp;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = p.s.rows, grp = p.s.grp;
   const bool masks = p.s.window || p.s.causal;
-  if (masks && blockIdx.y == 0) {   // units that run c finished by itself and that came out with something that is no number
-    unsigned bad = 0;
-    for (int i = 0; i < p.spoilt_words; i++) bad |= a.spoilt[c * p.spoilt_words + i];
-    if (bad) repair_run<H>(p, c, bad);
+  if (masks && blockIdx.y == 0) {   // units that a run finished by itself and that came out with something that is no number
+    for (int run = blockIdx.x; run < p.runs; run += gridDim.x) {
+      unsigned bad = 0;
+      for (int i = 0; i < p.spoilt_words; i++) bad |= a.spoilt[run * p.spoilt_words + i];
+      if (bad) repair_run<H>(p, run, bad);
+    }
+  }
+  int c = blockIdx.x;
+  if constexpr (WAYS > 1) {
+    __shared__ int first;
+    if (threadIdx.x == 0) first = -1;
+    __syncthreads();
+    const int rt = blockIdx.x % p.s.tiles, bg = blockIdx.x / p.s.tiles, g = bg % p.s.nkv, b = bg / p.s.nkv;
+    for (int run = threadIdx.x; run < p.runs; run += WAYS * 32) {
+      const int4 d = a.desc[run];
+      if (d.x == b && d.y == g && d.z == rt) first = run;
+    }
+    __syncthreads();
+    c = first;
+    if (c < 0) return;   // a run has finished it
   }
   const int4 d = a.desc[c];
-  const int r0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * RPW, rows = min(R, a.L * grp - d.z * R);
+  const int r0 = WAYS > 1 ? blockIdx.y : (blockIdx.y * kMergeWarps + warp) * RPW, rows = min(R, a.L * grp - d.z * R);
   if (d.x < 0 || r0 >= rows) return;
   const int pieces = d.w - c + 1;
   auto slot = [&](int i, int r) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * R + min(r, rows - 1); };
@@ -81,7 +101,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
 #pragma unroll
     for (int e = 0; e < DPL; e++) num[q][e] = 0.f;
   }
-  for (int i0 = 0; i0 < pieces; i0 += U) {   // the softmax of the partials, U at a time
+  for (int i0 = WAYS > 1 ? warp * U : 0; i0 < pieces; i0 += WAYS * U) {   // the softmax of the partials, U at a time
     float t[RPW][U][DPL];
     float2 v[RPW][U];
 #pragma unroll
@@ -121,6 +141,28 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
       }
     }
   }
+  if constexpr (WAYS > 1) {   // the warps' sums, in their order
+    __shared__ float2 stat[WAYS];
+    __shared__ float part[WAYS][H];
+    if (lane == 0) stat[warp] = make_float2(mx[0], den[0]);
+#pragma unroll
+    for (int e = 0; e < DPL; e++) part[warp][lane * DPL + e] = num[0][e];
+    __syncthreads();
+    if (warp > 0) return;
+    float m = -INFINITY;
+    for (int w = 0; w < WAYS; w++)
+      if (stat[w].y != 0.f) m = fmaxf(m, stat[w].x);
+    den[0] = 0.f;
+#pragma unroll
+    for (int e = 0; e < DPL; e++) num[0][e] = 0.f;
+    for (int w = 0; w < WAYS; w++) {
+      const float by = stat[w].y == 0.f ? 0.f : ex2_approx(stat[w].x - m);
+      den[0] += stat[w].y == 0.f ? 0.f : stat[w].y * by;
+#pragma unroll
+      for (int e = 0; e < DPL; e++) num[0][e] += by != 0.f ? part[w][lane * DPL + e] * by : 0.f;
+    }
+    mx[0] = m;
+  }
 #pragma unroll
   for (int q = 0; q < RPW; q++) {
     if (r0 + q >= rows) break;
@@ -147,7 +189,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
   }
 }
 
+// parts of a unit from which on a CTA merges one row (blocks of 16, 38 parts a unit: 41.5 us against 48.7; 19 parts: 31.3 against 30.7; 10:
+// 36.9 against 28.8)
+constexpr int kManyParts = 24;
 constexpr int kUnitCost = 3;   // what a unit costs besides its tiles, in tiles (0, 2 and 3: 103, 97 and 95 us at four trajectories with a window)
+
+// The most tiles that a unit can have.
+long long most_tiles(const Args& p) {
+  const PagedShape& s = p.s;
+  const int kt = s.kt();
+  long long n = ceil_div(p.a.pg.cap(), kt);
+  if (s.window) n = std::min(n, ((long long)s.window + s.L) / kt + 2 + ceil_div(std::min(s.sinks, 1 << 29), kt));
+  return n + ceil_div(s.lb, kt);
+}
 
 // Few short units: a CTA each, whose warps have at most two tiles, does without partials and the merge's launch.  (Rows of one position
 // see the same keys, so nothing needs a repair.)  4 tokens, 8 kv heads, us in runs and so: contexts to 512 16.4 and 11.1, to 1024 (three
@@ -155,11 +209,8 @@ constexpr int kUnitCost = 3;   // what a unit costs besides its tiles, in tiles 
 bool unit_per_cta(const Args& p, const PagedPlan& pl) {
   const PagedShape& s = p.s;
   if (s.L > 1 && (s.window || s.causal)) return false;
-  const int kt = s.kt();
-  long long keys_tiles = ceil_div(p.a.pg.cap(), kt);
-  if (s.window) keys_tiles = std::min(keys_tiles, ((long long)s.window + s.L) / kt + 2 + ceil_div(std::min(s.sinks, 1 << 29), kt));
   const long long units = (long long)p.a.batch * s.nkv * s.tiles;
-  return units <= pl.sms && keys_tiles + ceil_div(s.lb, kt) <= 2 * paged_stream_warps(s.rows, p.a.pg.format);
+  return units <= pl.sms && most_tiles(p) <= 2 * paged_stream_warps(s.rows, p.a.pg.format);
 }
 
 template <int H>
@@ -168,11 +219,13 @@ cudaError_t launch(const Args& p, const PagedPlan& pl, cudaStream_t st) {
   const cudaError_t e = pl.kernel == kPagedStream ? launch_paged_stream(p.a, p.s, pl, alone, st) : launch_paged_tc(p.a, p.s, pl, st);
   if (e != cudaSuccess || alone) return e;
   const int rows = std::min(pl.rows, p.a.L * p.s.grp);
-  if (pl.kernel == kPagedStream) return launch_k(paged_merge_kernel<H, 1>, dim3(pl.runs, ceil_div(rows, kMergeWarps)), kMergeWarps * 32, 0, st, p);
+  const long long units = (long long)p.a.batch * p.s.nkv * p.s.tiles;
+  if (pl.runs > kManyParts * units && most_tiles(p) > kManyParts)
+    return launch_k(paged_merge_kernel<H, 1, kMergeWays>, dim3((unsigned)units, rows), kMergeWays * 32, 0, st, p);
+  auto merge = [&](auto kernel, int rpw) { return launch_k(kernel, dim3(pl.runs, ceil_div(rows, rpw * kMergeWarps)), kMergeWarps * 32, 0, st, p); };
+  if (pl.kernel == kPagedStream) return merge(paged_merge_kernel<H, 1>, 1);
   // two partials a unit, mostly: more rows a warp (windows at four trajectories 78 -> 74 us, 3 blocks of few units 16.6 -> 17.3)
-  if (pl.runs <= 2ll * p.a.batch * p.s.nkv * p.s.tiles)
-    return launch_k(paged_merge_kernel<H, 4>, dim3(pl.runs, ceil_div(rows, 4 * kMergeWarps)), kMergeWarps * 32, 0, st, p);
-  return launch_k(paged_merge_kernel<H, 2>, dim3(pl.runs, ceil_div(rows, 2 * kMergeWarps)), kMergeWarps * 32, 0, st, p);
+  return pl.runs <= 2 * units ? merge(paged_merge_kernel<H, 4>, 4) : merge(paged_merge_kernel<H, 2>, 2);
 }
 
 }  // namespace
