@@ -162,6 +162,8 @@ CASES = {
     "many_rows_24": dict(lens=[(61 * i) % 400 for i in range(60)], L=6, nq=16, nkv=4, h=64, page=32),
     "many_rows_96": dict(lens=[(47 * i) % 500 for i in range(40)], L=12, nq=32, nkv=4, h=128, page=16),
     "many_rows_160": dict(lens=[(83 * i) % 700 for i in range(30)], L=40, nq=16, nkv=4, h=64, page=128),
+    "long_text": dict(lens=[7013], L=16, nq=4, nkv=1, h=128, page=64),
+    "long_ragged": dict(lens=[8190, 0, 65], L=3, nq=4, nkv=1, h=64, page=16),
     "many": dict(lens=[(37 * i) % 90 for i in range(200)], L=2, nq=4, nkv=2, h=64, page=16),
 }
 MASKS = {"all": {}, "causal": dict(causal=True), "window": dict(window=50), "window_sinks": dict(window=33, sinks=5),
@@ -225,7 +227,7 @@ def test_what_is_not_finite_reaches_rows_that_see_it_and_no_other_request(pkg, n
 
 @pytest.mark.parametrize("form", ["bf16", "int4"])
 @pytest.mark.parametrize("mask", ["window_sinks", "sinks_causal", "causal", "appended_window"])
-@pytest.mark.parametrize("name", ["tokens_128", "text", "group_5", "primitive_64", "group_16"])
+@pytest.mark.parametrize("name", ["tokens_128", "text", "group_5", "primitive_64", "group_16", "long_text", "long_ragged"])
 def test_values_that_are_not_finite_stay_where_they_are_seen(pkg, name, mask, form):
     """Infinite and NaN values behind a window's start and later in a causal block: rows that do not see them are as they were, rows
     that do have no number in those dims."""
